@@ -57,8 +57,10 @@ typedef enum {
   MARLIN_ERR_WORKSPACE_TOO_SMALL = 4,  /* workspace smaller than required        */
   MARLIN_ERR_CUDA = 5,                 /* a CUDA runtime call or launch failed    */
   MARLIN_ERR_TIMEOUT = 6,              /* a bounded wait inside a kernel gave up  */
-  MARLIN_ERR_BOUNDS = 7                /* bounds-checked build only: a kernel
-                                          formed an address outside its buffer    */
+  MARLIN_ERR_BOUNDS = 7                /* a device-side index (adapter, page, length)
+                                          is out of range; in the bounds-checked
+                                          build also: a kernel formed an address
+                                          outside its buffer                      */
 } marlin_status_t;
 
 /* Human-readable name of a status code (static string, never NULL).  No page
@@ -318,15 +320,157 @@ marlin_status_t marlin_sparse_gemm(const uint16_t* X, const void* packed, const 
                                    marlin_stream_t stream);
 
 /*
+ * ---- Low-rank adapters beside the shared product -----------------------------
+ *
+ * Y[m] = X[m] . dequant(W) + scaling[a] * (X[m] . A[a]^T) . B[a]^T,  a = index[m],
+ *
+ * for many requests at once: every row has the adapter of its request, or none.
+ * The pages have no counterpart; the operation is the usual low-rank update of a
+ * frozen (here 4-bit) projection.
+ */
+
+/*
+ * Bytes of device workspace marlin_lora_gemm needs: marlin_workspace_bytes'
+ * and the fp32 partial sums of X . A^T.  A buffer sized for M also serves every
+ * smaller M with the same K, N, group, r, adapters (or fewer).  r: a multiple
+ * of 8 up to 128, else MARLIN_ERR_UNSUPPORTED (pad A and B with zeros).
+ * Host-only.  bytes: host pointer, written.
+ */
+marlin_status_t marlin_lora_workspace_bytes(int M, int K, int N, int group, int r, int adapters,
+                                            int device, size_t* bytes);
+
+/*
+ * The product with adapters: three launches on `stream` (X . A^T, marlin_gemm,
+ * the adapters' part added to Y).
+ *
+ * X, packed, scales, zeros, Y, M, K, N, group  as for marlin_gemm, except that
+ *            Y is 16-byte aligned.
+ * A          device, fp16 [adapters][r][K], 16-byte aligned (read only).
+ * B          device, fp16 [adapters][N][r], 16-byte aligned (read only).
+ * scaling    device, fp32 [adapters].
+ * index      device, int32 [M]: the row's adapter, negative for none.  An entry
+ *            >= adapters gives the row no adapter and is reported by
+ *            marlin_last_device_status as MARLIN_ERR_BOUNDS.  Rows may come in
+ *            any order; blocks of 16 or 32 rows that share adapters are fastest.
+ * workspace  device, >= marlin_lora_workspace_bytes(...) bytes, 16-byte aligned,
+ *            zeroed once; ordering as for marlin_gemm.
+ * X . A^T is summed in fp32, scaled, and rounded once to fp16 (normalised row by
+ * row, so that its range is fp32's) for the product with B; that is summed in
+ * fp32 and added to the fp16 base product, so Y is rounded twice.
+ * Deterministic.  Errors: INVALID_ARG, UNSUPPORTED (r), MISALIGNED,
+ * WORKSPACE_TOO_SMALL (host checks, nothing launched); CUDA.
+ */
+marlin_status_t marlin_lora_gemm(const uint16_t* X, const void* packed, const uint16_t* scales,
+                                 const int32_t* zeros, const uint16_t* A, const uint16_t* B,
+                                 const float* scaling, const int32_t* index, int adapters, int r,
+                                 uint16_t* Y, int M, int K, int N, int group, void* workspace,
+                                 size_t workspace_bytes, marlin_stream_t stream);
+
+/*
+ * ---- 4-bit paged key/value cache ------------------------------------------------
+ *
+ * The pages have no counterpart: once the weights are 4-bit, the cache is what
+ * a long decode step reads.  Every vector (one token, one key head, head_dim
+ * channels of a key or a value) is held as 4-bit codes c in 0..15 and two fp16
+ * numbers, and stands for
+ *     s * (c - 8) + o,   s = fp16((max - min) * fp32(1/15)),  o = fp16(min + 8 s),
+ *     c = 8 + clamp(round_to_even((x - o) / s), -8, 7)   (8 where s = 0),
+ * in fp32 arithmetic.  A vector that holds an infinity or a NaN reads back as
+ * NaN in every channel.
+ *
+ * Arguments the entry points share
+ *   cache       device, marlin_kv_cache_bytes(...) bytes, 16-byte aligned.  Its
+ *               bytes are this library's own layout (pages of page_size tokens
+ *               of every key head); unwritten tokens may hold anything.
+ *   head_dim    64 or 128; page_size a multiple of 16 up to 1024 (others ->
+ *               MARLIN_ERR_UNSUPPORTED).
+ *   page_table  device, int32 [requests][max_pages]: token t of request b lives in
+ *               page page_table[b][t / page_size].  max_pages * page_size <= 2^30.
+ *   lengths     device, int32 [requests]: cached tokens, the new ones included.
+ *   q_start     device, int32 [requests + 1], ascending from >= 0 to <= tokens: the
+ *               new tokens of request b are rows q_start[b] .. q_start[b+1] - 1 of
+ *               the [tokens][heads][head_dim] tensors, and they are its last ones:
+ *               row q_start[b] + i is at position lengths[b] - new + i.
+ *   workspace   device, marlin_kv_workspace_bytes(...) bytes, 16-byte aligned, zeroed
+ *               once; ordering as for marlin_gemm.
+ * Entries of page_table, lengths and q_start that contradict each other or lie
+ * out of range are found on the device, skipped, and reported by
+ * marlin_last_device_status as MARLIN_ERR_BOUNDS (that call's results are not
+ * valid); they are never followed.
+ * Strides are in elements; the last dimension is contiguous.
+ */
+
+/* Bytes of a cache of n_pages pages: n_pages * kv_heads * page_size * (head_dim + 8).
+ * Host-only. */
+marlin_status_t marlin_kv_cache_bytes(int n_pages, int kv_heads, int head_dim, int page_size,
+                                      size_t* bytes);
+
+/* Bytes of device workspace for the calls below with this many query heads and up
+ * to this many requests and tokens on `device` (the status word and the partial
+ * results of split requests; append and read use the first 256 bytes only).
+ * Host-only. */
+marlin_status_t marlin_kv_workspace_bytes(int heads, int kv_heads, int head_dim, int requests,
+                                          int tokens, int device, size_t* bytes);
+
+/*
+ * Quantises the new tokens' keys and values and writes them into the cache.
+ * k, v: device, fp16 [tokens][kv_heads][head_dim], 8-byte aligned, strides
+ * multiples of 4 (e.g. views of one QKV product).  One launch.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED; CUDA.
+ */
+marlin_status_t marlin_kv_append(const uint16_t* k, int64_t k_token_stride, int64_t k_head_stride,
+                                 const uint16_t* v, int64_t v_token_stride, int64_t v_head_stride,
+                                 void* cache, int n_pages, int kv_heads, int head_dim, int page_size,
+                                 const int32_t* page_table, int max_pages, const int32_t* lengths,
+                                 const int32_t* q_start, int requests, int tokens, void* workspace,
+                                 marlin_stream_t stream);
+
+/*
+ * The values the cache holds for the same tokens: k, v device, fp16
+ * [tokens][kv_heads][head_dim] contiguous, 8-byte aligned, written (rows that no
+ * request owns are left alone).  Errors as for marlin_kv_append.
+ */
+marlin_status_t marlin_kv_read(uint16_t* k, uint16_t* v, const void* cache, int n_pages, int kv_heads,
+                               int head_dim, int page_size, const int32_t* page_table, int max_pages,
+                               const int32_t* lengths, const int32_t* q_start, int requests, int tokens,
+                               void* workspace, marlin_stream_t stream);
+
+/*
+ * Causal attention of the new tokens over the cache (which holds their own keys
+ * and values already):
+ *     out[i][h] = softmax_t(scale * q[i][h] . K_t[h / G]) . V_t[h / G],
+ * G = heads / kv_heads, over the positions t <= position(i) and, if window > 0,
+ * t > position(i) - window.
+ * q       device, fp16 [tokens][heads][head_dim], 16-byte aligned, strides
+ *         multiples of 8.
+ * out     device, fp16 [tokens][heads][head_dim] contiguous, 16-byte aligned,
+ *         written.  A row that sees no token (more new tokens than the length)
+ *         is zero, and reported as above.
+ * max_q   most new tokens of any request; a request with more is served too, but
+ *         may be slower.
+ * Scores, softmax statistics and sums are fp32; q, the codes, scales and offsets
+ * enter the products exactly.  Deterministic for given lengths.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE_TOO_SMALL; CUDA.
+ */
+marlin_status_t marlin_kv_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
+                                    int heads, const void* cache, int n_pages, int kv_heads,
+                                    int head_dim, int page_size, const int32_t* page_table,
+                                    int max_pages, const int32_t* lengths, const int32_t* q_start,
+                                    int requests, int tokens, int max_q, float scale, int window,
+                                    uint16_t* out, void* workspace, size_t workspace_bytes,
+                                    marlin_stream_t stream);
+
+/*
  * No page passage: failure reporting of this library's bounded waits.
  * Synchronises `stream`, reads and clears the device status word that
  * marlin_gemm keeps in `workspace`, and returns MARLIN_OK,
  * MARLIN_ERR_TIMEOUT (a bounded wait in a kernel expired; that call's Y is
- * not valid) or, from a library built with -DMARLIN_DEBUG (which checks
+ * not valid) or MARLIN_ERR_BOUNDS: the adapter or cache kernels met an index
+ * out of range, or a library built with -DMARLIN_DEBUG (which checks
  * every address its kernels form against the extent of its buffer and skips
- * the access instead of faulting), MARLIN_ERR_BOUNDS; the 32-bit word at byte
+ * the access instead of faulting) met such an address; the 32-bit word at byte
  * 4 of the workspace then names the first failed check (cleared too).
- * workspace: device, as passed to marlin_gemm.
+ * workspace: device, as passed to marlin_gemm or to the adapter and cache calls.
  */
 marlin_status_t marlin_last_device_status(void* workspace, marlin_stream_t stream);
 

@@ -22,7 +22,9 @@ from ._binding import MarlinError, status_string  # noqa: F401
 
 __all__ = ["PackedWeights", "Workspace", "repack", "gemm", "gemm_into", "gemm_host", "device_status",
            "MarlinError", "status_string", "packed_layout", "SparsePackedWeights", "sparse_repack",
-           "sparse_gemm", "sparse_gemm_into"]
+           "sparse_gemm", "sparse_gemm_into", "LoraBank", "LoraWorkspace", "lora_gemm", "lora_gemm_into",
+           "Kv4Cache", "Kv4Batch", "Kv4Workspace", "kv4_append", "kv4_read", "kv4_attention",
+           "kv4_attention_into"]
 
 
 def _stream() -> int:
@@ -248,3 +250,10 @@ def sparse_gemm_into(x: torch.Tensor, w: SparsePackedWeights, ws: Workspace, y: 
 def sparse_gemm(x: torch.Tensor, w: SparsePackedWeights, ws: Workspace) -> torch.Tensor:
     y = torch.empty((x.shape[0], w.N), dtype=torch.float16, device=x.device)
     return sparse_gemm_into(x, w, ws, y)
+
+
+# ---- operators beside the product ------------------------------------------------
+
+from .lora import LoraBank, LoraWorkspace, lora_gemm, lora_gemm_into  # noqa: E402
+from .kv4 import (Kv4Batch, Kv4Cache, Kv4Workspace, kv4_append, kv4_attention, kv4_attention_into,  # noqa: E402
+                  kv4_read)

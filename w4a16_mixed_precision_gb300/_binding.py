@@ -39,6 +39,13 @@ EXPORTS = (
     "marlin_sparse_packed_layout",
     "marlin_sparse_repack",
     "marlin_sparse_gemm",
+    "marlin_lora_workspace_bytes",
+    "marlin_lora_gemm",
+    "marlin_kv_cache_bytes",
+    "marlin_kv_workspace_bytes",
+    "marlin_kv_append",
+    "marlin_kv_read",
+    "marlin_kv_attention",
 )
 
 
@@ -89,6 +96,17 @@ def open_library(path: str) -> ctypes.CDLL:
         lib.marlin_sparse_repack.argtypes = [P, P, P, I, I, I, P, P, P]
         lib.marlin_sparse_gemm.argtypes = [P, P, P, P, P, P, I, I, I, I, P, SZ, P]
         for f in ("marlin_sparse_packed_layout", "marlin_sparse_repack", "marlin_sparse_gemm"):
+            getattr(lib, f).restype = I
+        L, F, PSZ = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(SZ)
+        kv = [P, I, I, I, I, P, I, P, P, I, I]  # cache .. page_size, page_table, max_pages, lengths, q_start, B, T
+        lib.marlin_lora_workspace_bytes.argtypes = [I] * 7 + [PSZ]
+        lib.marlin_lora_gemm.argtypes = [P] * 8 + [I, I, P, I, I, I, I, P, SZ, P]
+        lib.marlin_kv_cache_bytes.argtypes = [I, I, I, I, PSZ]
+        lib.marlin_kv_workspace_bytes.argtypes = [I] * 6 + [PSZ]
+        lib.marlin_kv_append.argtypes = [P, L, L, P, L, L] + kv + [P, P]
+        lib.marlin_kv_read.argtypes = [P, P] + kv + [P, P]
+        lib.marlin_kv_attention.argtypes = [P, L, L, I] + kv + [I, F, I, P, P, SZ, P]
+        for f in EXPORTS[-7:]:
             getattr(lib, f).restype = I
         for f in ("marlin_packed_layout", "marlin_repack", "marlin_workspace_bytes", "marlin_gemm",
                   "marlin_last_device_status"):
@@ -186,3 +204,24 @@ def sparse_gemm_raw(x_ptr: int, packed_ptr: int, meta_ptr: int | None, scales_pt
     """Raw call of the 2:4-sparse multiply; returns the status code."""
     return load().marlin_sparse_gemm(x_ptr, packed_ptr, meta_ptr or None, scales_ptr, zeros_ptr or None,
                                      y_ptr, M, K, N, group, ws_ptr, ws_bytes, stream or None)
+
+
+def lora_workspace_bytes(M: int, K: int, N: int, group: int, r: int, adapters: int, device: int = 0) -> int:
+    b = ctypes.c_size_t()
+    _check(load().marlin_lora_workspace_bytes(M, K, N, group, r, adapters, device, ctypes.byref(b)),
+           "marlin_lora_workspace_bytes")
+    return b.value
+
+
+def kv_cache_bytes(n_pages: int, kv_heads: int, head_dim: int, page_size: int) -> int:
+    b = ctypes.c_size_t()
+    _check(load().marlin_kv_cache_bytes(n_pages, kv_heads, head_dim, page_size, ctypes.byref(b)),
+           "marlin_kv_cache_bytes")
+    return b.value
+
+
+def kv_workspace_bytes(heads: int, kv_heads: int, head_dim: int, requests: int, tokens: int, device: int = 0) -> int:
+    b = ctypes.c_size_t()
+    _check(load().marlin_kv_workspace_bytes(heads, kv_heads, head_dim, requests, tokens, device, ctypes.byref(b)),
+           "marlin_kv_workspace_bytes")
+    return b.value

@@ -396,6 +396,13 @@ marlin_status_t run_gemm(const uint16_t* X, const void* packed, const void* meta
 
 namespace w4a16 {
 
+int device_sms(int device, int* sms) {
+  DeviceState* d;
+  const marlin_status_t s = device_state(device, &d);
+  if (s == MARLIN_OK) *sms = d->sms;
+  return s;
+}
+
 // Workspace bytes of the plan marlin_gemm (automatic kernel choice) uses for
 // this call on the current device; a marlin_status_t value.
 int call_workspace_bytes(int M, int K, int N, int group, bool has_zeros, size_t* bytes) {

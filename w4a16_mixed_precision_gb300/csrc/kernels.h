@@ -91,6 +91,9 @@ cudaError_t launch_small_m(const CUtensorMap& x_map, const GemmParams& p, int gr
                            uint32_t smem_bytes, bool sparse, cudaStream_t stream);
 cudaError_t small_m_set_smem_limit(int bytes);
 
+// SM count of a device (queried once); returns a marlin_status_t value.
+int device_sms(int device, int* sms);
+
 // Workspace bytes of the plan marlin_gemm uses for this call on the current
 // device (not the worst case over kernels and smaller M that
 // marlin_workspace_bytes reports); returns a marlin_status_t value.

@@ -1,0 +1,98 @@
+"""Low-rank adapters of many requests beside a shared W4A16 product:
+
+    y[m] = x[m] . dequant(W) + scaling[a] * (x[m] . A[a]^T) . B[a]^T,  a = index[m] (none if negative).
+
+One call (marlin_lora_gemm) per projection; see include/marlin.h.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _binding, _need_cuda, _on_current_device, _stream
+from ._binding import MarlinError
+
+MAX_RANK = 128
+
+
+class LoraBank:
+    """The adapters of one projection, on the device: a fp16 [n, r, K], b fp16
+    [n, N, r], scaling fp32 [n].  A rank that is not a multiple of 8 is padded
+    with zeros (a copy)."""
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scaling: torch.Tensor):
+        if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+            raise ValueError(f"expected a [n, r, K] and b [n, N, r], got {tuple(a.shape)} and {tuple(b.shape)}")
+        if tuple(scaling.shape) != (a.shape[0],):
+            raise ValueError(f"expected scaling [{a.shape[0]}], got {tuple(scaling.shape)}")
+        for name, t, dtype in (("a", a, torch.float16), ("b", b, torch.float16), ("scaling", scaling, torch.float32)):
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            if t.dtype != dtype:
+                raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if not a.device == b.device == scaling.device:
+            raise ValueError("a, b and scaling must be on one device")
+        n, r, K = a.shape
+        if not 0 < n or not 0 < r <= MAX_RANK:
+            raise ValueError(f"at least one adapter, of a rank up to {MAX_RANK}, is wanted: got {n} of rank {r}")
+        pad = -r % 8
+        if pad:
+            a, b = torch.nn.functional.pad(a, (0, 0, 0, pad)), torch.nn.functional.pad(b, (0, pad))
+        self.a, self.b, self.scaling = a.contiguous(), b.contiguous(), scaling.contiguous()
+        self.n, self.r, self.K, self.N = n, r + pad, K, b.shape[1]
+
+    @classmethod
+    def stack(cls, adapters) -> "LoraBank":
+        """From (a [r, K], b [N, r], scaling) of each adapter; lower ranks are padded with zeros."""
+        adapters = list(adapters)
+        if not adapters:
+            raise ValueError("at least one adapter is wanted")
+        r = max(a.shape[0] for a, _, _ in adapters)
+        pad = torch.nn.functional.pad
+        return cls(torch.stack([pad(a, (0, 0, 0, r - a.shape[0])) for a, _, _ in adapters]),
+                   torch.stack([pad(b, (0, r - b.shape[1])) for _, b, _ in adapters]),
+                   torch.tensor([float(s) for _, _, s in adapters], dtype=torch.float32, device=adapters[0][0].device))
+
+
+class LoraWorkspace:
+    """Device workspace of lora_gemm for up to max_M rows, zeroed once; also a
+    workspace for gemm with the same shapes."""
+
+    def __init__(self, max_M: int, K: int, N: int, group: int, r: int, adapters: int = 1 << 20, device=None):
+        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        if dev.type != "cuda":
+            raise ValueError("a workspace lives on a CUDA device")
+        if dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.nbytes = _binding.lora_workspace_bytes(max(max_M, 1), K, N, K if group == -1 else group, r + -r % 8,
+                                                    adapters, dev.index)
+        self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=dev)
+
+    @property
+    def ptr(self) -> int:
+        return self.buf.data_ptr()
+
+
+def lora_gemm_into(x: torch.Tensor, w, bank: LoraBank, index: torch.Tensor, ws: LoraWorkspace,
+                   y: torch.Tensor) -> torch.Tensor:
+    """y[M, N] = x[M, K] . dequant(W) + the part of each row's adapter, fp16, on
+    the current stream.  index: int32 [M], negative for no adapter."""
+    _need_cuda(x, "x", torch.float16)
+    _need_cuda(y, "y", torch.float16)
+    _need_cuda(index, "index", torch.int32)
+    M, K = x.shape
+    if K != w.K or K != bank.K or w.N != bank.N or tuple(y.shape) != (M, w.N) or tuple(index.shape) != (M,):
+        raise ValueError("shape mismatch")
+    _on_current_device(("x", x), ("weights", w.buf), ("adapters", bank.a), ("index", index), ("workspace", ws.buf),
+                       ("y", y))
+    rc = _binding.load().marlin_lora_gemm(
+        x.data_ptr(), w.codes_ptr, w.scales_ptr, w.zeros_ptr, bank.a.data_ptr(), bank.b.data_ptr(),
+        bank.scaling.data_ptr(), index.data_ptr(), bank.n, bank.r, y.data_ptr(), M, K, w.N, w.group, ws.ptr, ws.nbytes,
+        _stream() or None)
+    if rc != _binding.OK:
+        raise MarlinError(rc, "marlin_lora_gemm")
+    return y
+
+
+def lora_gemm(x: torch.Tensor, w, bank: LoraBank, index: torch.Tensor, ws: LoraWorkspace) -> torch.Tensor:
+    y = torch.empty((x.shape[0], w.N), dtype=torch.float16, device=x.device)
+    return lora_gemm_into(x, w, bank, index, ws, y)
