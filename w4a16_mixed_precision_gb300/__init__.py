@@ -28,7 +28,8 @@ __all__ = ["PackedWeights", "Workspace", "repack", "gemm", "gemm_into", "gemm_ho
 
 
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    # the current stream's handle without building a Stream object (2.9 us of a call on the host)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _on_current_device(*named) -> None:

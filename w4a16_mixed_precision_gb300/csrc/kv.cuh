@@ -92,6 +92,7 @@ struct KvAttnParams {
   int heads, group;         // query heads, and of them per key head
   int window;               // > 0: a query sees that many positions, its own included
   float scale_log2;         // softmax scale * log2(e)
+  int whole_blocks;         // pages hold whole blocks: one copy each
   int max_rows;             // requests with more query rows per key head are left to another launch
   int* counters;            // [grid], zero between calls
   float* partials;          // [2 grid][rows][D + 2]

@@ -4,14 +4,13 @@
 // over the cached tokens t <= position(i) (and t > position(i) - window).
 //
 // Bound: streaming the cache, 2 (D/2 + 4) bytes per token and key head, once.
-//   * The work is (request, key head, block of 8 NB query rows) segments of
-//     16-token granules; the rows of a block are the G query heads that share
-//     the key head, for one or more query tokens, so that a granule is read
-//     once for all of them.  Every CTA (one per SM) takes an equal contiguous
-//     stripe of granules, found on the device from the lengths.
-//   * Its W warps take granules in turn, each with its own ring of bulk copies
-//     (one per granule), its own running maximum, sum and accumulators: no
-//     barrier inside a segment.
+//   * The work is (request, key head, group of 8 NB query rows) segments of
+//     blocks of 64 tokens; the rows of a group are the query heads that share
+//     the key head, for one or more query tokens, so that a block is read once
+//     for all of them.  Every warp of the card takes an equal contiguous stripe
+//     of blocks, found on the device from the lengths, with its own ring of
+//     bulk copies, running maximum, sum and accumulators: no barrier until the
+//     stripe is done.
 //   * Both products run on mma.sync with the cache as the 16-row operand and the
 //     query rows as the 8 columns: S^T[16 tokens x 8 rows] = K Q^T and
 //     O^T[16 channels x 8 rows] += V^T P^T.  A code c is fed as the fp16
@@ -23,10 +22,12 @@
 //     the rounding of the fp16 output.  s_t is normalised by a running power of
 //     two so that neither half falls below fp16's range.
 //   * The maximum is only moved when a score exceeds it by 2^8 (one vote per
-//     granule instead of shuffles and a rescaling).
-// A segment cut by stripe boundaries is finished by whichever of its CTAs
-// arrives last, summing all parts in stripe order (so the result does not
-// depend on the order of arrival).  Nothing waits for another CTA.
+//     block instead of shuffles and a rescaling).
+// A segment that is one warp's alone is written by that warp; the parts of one
+// that is cut between warps meet in shared memory; one that is cut between CTAs
+// is finished by whichever of them arrives last, summing all parts in stripe
+// order (so the result does not depend on the order of arrival).  Nothing waits
+// for another CTA.
 #include "kv.cuh"
 
 namespace w4a16 {
@@ -34,6 +35,7 @@ namespace w4a16 {
 namespace {
 
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kLowest = -1e30f;       // the running maximum before the first score
 constexpr float kLazy = 8.f;            // log2 of how far a score may exceed the reference
 constexpr float kCodeUnit = 16777216.f;  // 2^24: an fp16 subnormal's unit is 2^-24
 constexpr float kMinSref = 9.313225746154785e-10f;  // 2^-30
@@ -42,15 +44,6 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -84,35 +77,89 @@ __device__ __forceinline__ void store_row(const KvAttnParams& p, const KvSeq& s,
   *reinterpret_cast<uint2*>(p.out + ((long long)(s.q0 + i) * p.heads + head) * D + ch) = v;
 }
 
-// One request's share of the work: its granules [g_lo, g_lo + n) and the
-// number of its blocks of query rows.
-struct SeqWork {
-  KvSeq s;
-  int g_lo, n, rbs;
+// Pairs of fp32 values: sm_103a multiplies and adds two at a time.
+struct F2 {
+  float x, y;
+};
+__device__ __forceinline__ void mma16816(F2 (&d)[2], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0].x), "+f"(d[0].y), "+f"(d[1].x), "+f"(d[1].y)
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ F2 dup(float v) { return {v, v}; }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("{\n\t.reg .b64 ta, tb, tc, td;\n\tmov.b64 ta, {%2, %3};\n\tmov.b64 tb, {%4, %5};\n\tmov.b64 tc, {%6, %7};\n\t"
+      "fma.rn.f32x2 td, ta, tb, tc;\n\tmov.b64 {%0, %1}, td;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 d;
+  asm("{\n\t.reg .b64 ta, tb, td;\n\tmov.b64 ta, {%2, %3};\n\tmov.b64 tb, {%4, %5};\n\t"
+      "mul.rn.f32x2 td, ta, tb;\n\tmov.b64 {%0, %1}, td;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 d;
+  asm("{\n\t.reg .b64 ta, tb, td;\n\tmov.b64 ta, {%2, %3};\n\tmov.b64 tb, {%4, %5};\n\t"
+      "add.rn.f32x2 td, ta, tb;\n\tmov.b64 {%0, %1}, td;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// W warps; blocks of GB granules; S blocks in a warp's ring.
+template <int D, int NB>
+struct Shape {
+  static constexpr int W = 8, GB = NB == 1 ? 4 : 2, S = 8 / GB * (D == 128 ? 1 : 2);
+  static constexpr int kBlock = GB * kGranule;  // tokens
+  static constexpr int RB = 8 * NB;             // query rows
+  static constexpr int GR = kv_granule_bytes(D);
+  static constexpr int BB = GB * GR;            // bytes of a block
+  static constexpr int kOStride = D + 4;        // floats of a row of a part in shared memory
+  static constexpr int kPart = RB * (kOStride + 2) * 4;  // rows, then (maximum, sum) of each
+  static constexpr int kRing = 2048;           // after the control block
+  static constexpr int kFirst = kRing + W * S * BB;      // the warps' first parts; the last ones go to their rings
+  static constexpr int kSmem = kFirst + W * kPart;
+  static_assert(kPart <= S * BB && kPart % 16 == 0, "a part has to fit a warp's ring");
 };
 
-template <int RB>
+// One request's share of the work: its blocks [lo, lo + n) and the number of
+// its groups of query rows.
+struct SeqWork {
+  KvSeq s;
+  int lo, n, rbs;
+};
+
+template <typename Sh>
 __device__ __forceinline__ SeqWork seq_work(const KvAttnParams& p, int b, bool report) {
   SeqWork w;
   w.s = kv_seq(p.kv, b, report);
   if (w.s.nq > w.s.len && report) kv_fail(p.kv, kKvSiteLen);
   const int rows = w.s.nq * p.group;
-  w.rbs = rows > p.max_rows ? 0 : (rows + RB - 1) / RB;
+  w.rbs = rows > p.max_rows ? 0 : (rows + Sh::RB - 1) / Sh::RB;
   const int first = w.s.len - w.s.nq;  // position of the first query token
   const int lo = p.window > 0 ? max(0, first - p.window + 1) : 0;
-  w.g_lo = lo >> 4;
-  w.n = max(1, ((w.s.len + 15) >> 4) - w.g_lo);
+  w.lo = lo / Sh::kBlock;
+  w.n = max(1, (w.s.len + Sh::kBlock - 1) / Sh::kBlock - w.lo);
   return w;
 }
 
-// A place in the stripe: granule g of segment seg (key head * rbs + row block)
-// of request b.
+// A place in the stripe: block g of segment seg (key head * rbs + row group) of
+// request b.
 struct Cursor {
   int b, seg, g;
   SeqWork w;
 };
 
-template <int RB>
+template <typename Sh>
 __device__ __forceinline__ void advance(const KvAttnParams& p, Cursor& c, int by) {
   c.g += by;
   while (c.g >= c.w.n) {
@@ -121,158 +168,206 @@ __device__ __forceinline__ void advance(const KvAttnParams& p, Cursor& c, int by
       c.seg = 0;
       do {
         if (++c.b >= p.kv.B) { c.g = 0; return; }
-        c.w = seq_work<RB>(p, c.b, false);
+        c.w = seq_work<Sh>(p, c.b, false);
       } while (c.w.rbs == 0);
     }
   }
 }
 
-// Largest W that the shared memory of an SM holds with a useful ring.
-template <int D, int NB>
-struct Shape {
-  static constexpr int W = NB == 1 ? 16 : 8;    // warps
-  static constexpr int S = NB == 1 ? 4 : 8;     // granules in a warp's ring
-  static constexpr int RB = 8 * NB;             // query rows
-  static constexpr int GR = kv_granule_bytes(D);
-  static constexpr int kOStride = D + 4;        // floats of a row in the merge buffer
-  static constexpr int kRing = 1024;
-  static constexpr int kMerge = kRing + W * S * GR;
-  static constexpr int kMl = kMerge + W * RB * kOStride * 4;
-  static constexpr int kSmem = kMl + W * RB * 2 * 4;
+// What a warp left in shared memory: the end of a segment that began before its
+// stripe (or a middle of one), and the beginning of one that goes on after it.
+struct Parts {
+  int idle;                // the warp has no blocks
+  int first, last;         // whether there is one
+  int first_ends;          // the segment ends in this warp
+  int b[2], seg[2];        // of first and last
+  long long s0[2];         // the segment's first unit
 };
+
+// Joins row `row`, channels ch .. ch + 3 of one part: rows of `stride` floats,
+// then (maximum, sum) of each.
+template <int RB, bool kGlobal>
+__device__ __forceinline__ void join(const float* part, int stride, int row, int ch, float& top, float& sum,
+                                     float4& acc) {
+  const float2* mp = reinterpret_cast<const float2*>(part + RB * stride) + row;
+  const float4* ap = reinterpret_cast<const float4*>(part + row * stride + ch);
+  const float2 ml = kGlobal ? __ldcg(mp) : *mp;
+  const float4 a = kGlobal ? __ldcg(ap) : *ap;
+  if (ml.y == 0.f) return;  // saw no token
+  const float nt = fmaxf(top, ml.x);
+  const float fo = top == nt ? 1.f : ex2(top - nt), fn = ml.x == nt ? 1.f : ex2(ml.x - nt);
+  top = nt;
+  sum = fmaf(sum, fo, ml.y * fn);
+  acc.x = fmaf(acc.x, fo, a.x * fn);
+  acc.y = fmaf(acc.y, fo, a.y * fn);
+  acc.z = fmaf(acc.z, fo, a.z * fn);
+  acc.w = fmaf(acc.w, fo, a.w * fn);
+}
 
 struct AttnCtrl {
   uint64_t full[64];       // [W][S]
-  long long scan[16];
-  long long total;
-  long long start_off;     // first unit's offset in its request
+  long long scan[8], scan_segs[8];
+  int longest[8];
+  long long start_off;     // the first unit's offset in its request
   int start_b;
   int abort;
-  int last;
+  int arrived;
+  Parts parts[8];
 };
-static_assert(sizeof(AttnCtrl) <= 1024, "control block too large");
+static_assert(sizeof(AttnCtrl) <= 2048, "control block too large");
 
 template <int D, int NB>
 __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const KvAttnParams p) {
   using Sh = Shape<D, NB>;
-  constexpr int W = Sh::W, S = Sh::S, RB = Sh::RB, GR = Sh::GR, CW = D / 32;
+  constexpr int W = Sh::W, S = Sh::S, GB = Sh::GB, RB = Sh::RB, GR = Sh::GR, BB = Sh::BB, CW = D / 32;
   extern __shared__ __align__(128) uint8_t smem[];
   AttnCtrl* ctrl = reinterpret_cast<AttnCtrl*>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
-  const uint32_t ring = smem_addr(smem) + Sh::kRing + warp * (S * GR);
-  float* const merge = reinterpret_cast<float*>(smem + Sh::kMerge);
-  float* const ml = reinterpret_cast<float*>(smem + Sh::kMl);
+  uint8_t* const ring_ptr = smem + Sh::kRing + warp * (S * BB);
+  const uint32_t ring = smem_addr(ring_ptr);
 
   if (lane == 0) {
     for (int s = 0; s < S; ++s) mbar_init(smem_addr(&ctrl->full[warp * S + s]), 1);
-    if (warp == 0) {
-      ctrl->abort = 0;
-      ctrl->start_b = -1;
-    }
+    ctrl->parts[warp].first = ctrl->parts[warp].last = 0;
+    if (warp == 0) ctrl->abort = 0;
     fence_mbarrier_init();
   }
   if (tid == 0) griddep_launch_dependents();
   griddep_wait();
 
-  // ---- this CTA's stripe of granules -----------------------------------------
+  // ---- the stripes: all blocks, and this CTA's and this warp's -----------------
   const int per = (p.kv.B + W * 32 - 1) / (W * 32);
   const int b0 = min(tid * per, p.kv.B), b1 = min(b0 + per, p.kv.B);
-  long long mine = 0;
+  long long mine = 0, mine_segs = 0;
+  int longest = 0;
   for (int b = b0; b < b1; ++b) {
-    const SeqWork w = seq_work<RB>(p, b, blockIdx.x == 0);
-    mine += (long long)p.kv.hkv * w.rbs * w.n;
+    const SeqWork w = seq_work<Sh>(p, b, blockIdx.x == 0);
+    const long long segs = (long long)p.kv.hkv * w.rbs;
+    mine += segs * w.n;
+    mine_segs += segs;
+    if (segs) longest = max(longest, w.n);
   }
-  long long before = mine;
+  long long before = mine, before_segs = mine_segs;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, before, m);
-    if (lane >= m) before += o;
+    const long long o = __shfl_up_sync(0xffffffffu, before, m), os = __shfl_up_sync(0xffffffffu, before_segs, m);
+    if (lane >= m) {
+      before += o;
+      before_segs += os;
+    }
+    longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, m));
   }
-  if (lane == 31) ctrl->scan[warp] = before;
+  if (lane == 31) {
+    ctrl->scan[warp] = before;
+    ctrl->scan_segs[warp] = before_segs;
+    ctrl->longest[warp] = longest;
+  }
   __syncthreads();
-  long long U = 0, base = 0;
+  long long U = 0, segs = 0;
+#pragma unroll
   for (int w = 0; w < W; ++w) {
-    if (w == warp) base = U;
+    if (w == warp) {
+      before += U - mine;
+      before_segs += segs - mine_segs;
+    }
     U += ctrl->scan[w];
+    segs += ctrl->scan_segs[w];
+    longest = max(longest, ctrl->longest[w]);
   }
-  before += base - mine;
   if (U == 0) return;
-  // small problems: at least a granule per warp for every CTA that takes part
-  const long long G = min((long long)gridDim.x, (U + W - 1) / W);
+  // Few segments of moderate length: a CTA each (by_seg), so that none is cut
+  // between CTAs.  Publishing and joining parts costs about as much as six
+  // blocks of a warp.
+  const long long even = (U + (long long)gridDim.x * W - 1) / ((long long)gridDim.x * W);
+  const bool by_seg = segs <= (long long)gridDim.x && (longest + W - 1) / W <= even + 6;
+  // otherwise an equal share of all blocks for every warp, at least one
+  const long long G = by_seg ? segs : min((long long)gridDim.x, (U + W - 1) / W);
   if (blockIdx.x >= G) return;
-  const long long u_begin = stripe_begin(blockIdx.x, U, G), u_end = stripe_begin(blockIdx.x + 1, U, G);
-  if (u_begin >= before && u_begin < before + mine) {
-    long long off = u_begin - before;
-    for (int b = b0; b < b1; ++b) {
-      const SeqWork w = seq_work<RB>(p, b, false);
-      const long long n = (long long)p.kv.hkv * w.rbs * w.n;
-      if (off < n) {
-        ctrl->start_b = b;
-        ctrl->start_off = off;
-        break;
+  const long long u_cta = stripe_begin(blockIdx.x, U, G);
+  {
+    const long long at = by_seg ? blockIdx.x : u_cta;
+    const long long from = by_seg ? before_segs : before;
+    if (at >= from && at < from + (by_seg ? mine_segs : mine)) {
+      long long off = at - from;
+      for (int b = b0; b < b1; ++b) {
+        const SeqWork w = seq_work<Sh>(p, b, false);
+        const long long n = (long long)p.kv.hkv * w.rbs * (by_seg ? 1 : w.n);
+        if (off < n) {
+          ctrl->start_b = b;
+          ctrl->start_off = by_seg ? off * w.n : off;
+          break;
+        }
+        off -= n;
       }
-      off -= n;
     }
   }
   __syncthreads();
   Cursor cur;
   cur.b = ctrl->start_b;
-  cur.w = seq_work<RB>(p, cur.b, false);
+  cur.w = seq_work<Sh>(p, cur.b, false);
   cur.seg = (int)(ctrl->start_off / cur.w.n);
   cur.g = (int)(ctrl->start_off - (long long)cur.seg * cur.w.n);
+  int total;           // this warp's blocks
+  long long from = 0;  // and the first of them
+  if (by_seg) {
+    from = (long long)cur.w.n * warp / W;
+    total = (int)((long long)cur.w.n * (warp + 1) / W - from);
+    cur.g += (int)from;  // inside the segment, or at its end where there is nothing left to do
+  } else {
+    const long long gw = (long long)blockIdx.x * W + warp;
+    from = stripe_begin(gw, U, G * W);
+    total = (int)(stripe_begin(gw + 1, U, G * W) - from);
+    if (total > 0) advance<Sh>(p, cur, (int)(from - u_cta));
+  }
 
+  if (lane == 0) ctrl->parts[warp].idle = total == 0;
   const WaitCtx wc{&ctrl->abort, p.kv.status, p.timeout_ns};
-  const int total = (int)(u_end - u_begin);
-  const int mine_n = total > warp ? (total - warp + W - 1) / W : 0;  // this warp's granules: warp, warp + W, ...
 
-  // ---- the ring's producer (all lanes keep the cursor, lane 0 copies) ------------
+  // ---- the ring's producer: lane i < GB finds the place of granule i ----------------
   Cursor pc = cur;
-  advance<RB>(p, pc, warp);
-  int issued = 0;
-  auto page_of = [&](const Cursor& k) {
-    return p.kv.table[(long long)k.b * p.kv.max_pages + kv_div_page(p.kv, k.w.g_lo + k.g)];
+  int issued = 0, next_page = 0;
+  auto look_up = [&]() {  // the page of this lane's granule of the block at pc
+    const int gi = (pc.w.lo + pc.g) * GB + lane;
+    if (lane < GB && gi * kGranule < pc.w.s.len)
+      next_page = p.kv.table[(long long)pc.b * p.kv.max_pages + kv_div_page(p.kv, gi)];
   };
-  int next_page = 0;
-  if (mine_n > 0 && pc.w.s.len > 0) next_page = page_of(pc);
-  auto issue = [&](int stage) {  // copies the granule at pc and moves on
-    const int gi = pc.w.g_lo + pc.g;
-    const bool inside = gi * kGranule < pc.w.s.len;  // else nothing is cached there (an empty request)
+  auto issue = [&](int stage) {
+    const int gi = (pc.w.lo + pc.g) * GB + lane;
+    const bool inside = lane < GB && gi * kGranule < pc.w.s.len;
     const bool ok = next_page >= 0 && next_page < p.kv.n_pages;
+    if (inside && !ok) kv_fail(p.kv, kKvSitePage);  // no copy: the block's results are not valid, and reported
+    const int n = __popc(__ballot_sync(0xffffffffu, inside && ok));
     const uint32_t bar = smem_addr(&ctrl->full[warp * S + stage]);
-    if (lane == 0) {
-      if (inside && ok) {
-        const int h = pc.seg / pc.w.rbs;
-        mbar_arrive_expect_tx(bar, GR);
-        bulk_g2s(ring + stage * GR,
-                 p.kv.cache + next_page * p.kv.page_bytes + h * p.kv.head_bytes +
-                     (long long)(gi - kv_div_page(p.kv, gi) * p.kv.page16) * GR,
-                 GR, bar, policy_evict_first());
-      } else {
-        if (inside) kv_fail(p.kv, kKvSitePage);
-        mbar_arrive(bar);  // no copy: nobody sees the granule, or its page is reported as missing
-      }
+    if (lane == 0) mbar_arrive_expect_tx(bar, n * GR);
+    __syncwarp();
+    if (inside && ok && (p.whole_blocks ? lane == 0 : true)) {
+      const int h = pc.seg / pc.w.rbs;
+      bulk_g2s(ring + stage * BB + lane * GR,
+               p.kv.cache + next_page * p.kv.page_bytes + h * p.kv.head_bytes +
+                   (long long)(gi - kv_div_page(p.kv, gi) * p.kv.page16) * GR,
+               p.whole_blocks ? n * GR : GR, bar, policy_evict_first());
     }
-    ++issued;
-    if (issued < mine_n) {
-      advance<RB>(p, pc, W);
-      if (pc.w.s.len > 0) next_page = page_of(pc);
+    if (++issued < total) {
+      advance<Sh>(p, pc, 1);
+      look_up();
     }
   };
-  while (issued < min(S, mine_n)) issue(issued);
+  if (total > 0) look_up();
+  while (issued < min(S, total)) issue(issued);
 
-  int done = 0;  // granules of this warp consumed
-  int u = 0;     // units of the stripe passed
-  while (u < total) {
+  int done = 0;  // blocks of this warp consumed
+  bool ok = true;
+  while (ok && done < total) {
     const SeqWork& w = cur.w;
-    const int cnt = min(total - u, w.n - cur.g);
+    const int cnt = min(total - done, w.n - cur.g);
     const int h = cur.seg / w.rbs, rb = cur.seg - h * w.rbs;
     const int rows = w.s.nq * p.group;
     const int first = w.s.len - w.s.nq;
 
     // ---- queries: B operands in the channel order of the codes, and their sums ----
     uint32_t qf[NB][CW * 4];
-    float qs[NB][2];
+    F2 qs[NB];
     int hi_pos[NB][2], lo_pos[NB][2];  // tokens seen by rows 2c, 2c + 1: [lo, hi)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
@@ -302,9 +397,10 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
       }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      qs[nb].x = __shfl_sync(0xffffffffu, sum, 8 * c) * p.scale_log2;
+      qs[nb].y = __shfl_sync(0xffffffffu, sum, 8 * c + 4) * p.scale_log2;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        qs[nb][e] = __shfl_sync(0xffffffffu, sum, (2 * c + e) * 4) * p.scale_log2;
         const int rr = rb * RB + nb * 8 + 2 * c + e;
         const int pos = first + rr / p.group;
         hi_pos[nb][e] = rr < rows ? pos + 1 : 0;
@@ -317,278 +413,314 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
     const int all_lo = p.window > 0 ? first + i_last - p.window + 1 : 0;
     const int any_lo = p.window > 0 ? first + i_first - p.window + 1 : 0;
 
-    float m[NB][2], l[NB][2], pz[NB][2], o[CW * 2][NB][4];
-    float sref = kMinSref, rs = 64.f / kMinSref;
+    F2 m[NB], l[NB], pz[NB], o[CW * 2][NB][2];  // o: rows g and g + 8 of the tile
+    float sref = kMinSref;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      m[nb] = dup(kLowest);
+      l[nb] = pz[nb] = dup(0.f);
+#pragma unroll
+      for (int t = 0; t < CW * 2; ++t) o[t][nb][0] = o[t][nb][1] = dup(0.f);
+    }
+
+    for (int x = 0; x < cnt; ++x) {
+      const int t0 = (w.lo + cur.g + x) * Sh::kBlock;
+      const int stage = done % S;
+      const uint32_t st = ring + stage * BB;
+      if (!wait_warp(smem_addr(&ctrl->full[warp * S + stage]), (uint32_t)((done / S) & 1), wc)) {
+        ok = false;
+        break;
+      }
+      if (t0 < any_hi && t0 + Sh::kBlock > any_lo) {
+        const bool full = t0 + Sh::kBlock <= all_hi && t0 >= all_lo;
+
+        // ---- S^T = K Q^T on the codes: low nibbles and high (x 16) apart -----------
+        F2 raw[GB][NB][2];                        // tokens g and g + 8 of each granule
+        float ks[GB][2], kz[GB][2], vs[GB][2], vz[GB][2];
+#pragma unroll
+        for (int q = 0; q < GB; ++q) {
+          const uint32_t sg = st + q * GR;
+          uint32_t k0[CW], k1[CW];
+          lds_words<CW>(sg + g * (D / 2) + c * (D / 8), k0);
+          lds_words<CW>(sg + (g + 8) * (D / 2) + c * (D / 8), k1);
+          uint32_t pr[2][2];
+          lds_words<2>(sg + 16 * D + g * 8, pr[0]);
+          lds_words<2>(sg + 16 * D + (g + 8) * 8, pr[1]);
+          F2 sl[NB][2], sh[NB][2];
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) sl[nb][0] = sl[nb][1] = sh[nb][0] = sh[nb][1] = dup(0.f);
+#pragma unroll
+          for (int j = 0; j < CW; ++j) {
+            const uint32_t a0 = k0[j], a1 = k1[j], a2 = k0[j] >> 8, a3 = k1[j] >> 8;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              mma16816(sl[nb], a0 & 0x000F000Fu, a1 & 0x000F000Fu, a2 & 0x000F000Fu, a3 & 0x000F000Fu,
+                       qf[nb][4 * j], qf[nb][4 * j + 1]);
+              mma16816(sh[nb], a0 & 0x00F000F0u, a1 & 0x00F000F0u, a2 & 0x00F000F0u, a3 & 0x00F000F0u,
+                       qf[nb][4 * j + 2], qf[nb][4 * j + 3]);
+            }
+          }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              raw[q][nb][e] = fma2(sh[nb][e], dup(0.0625f), sl[nb][e]);
+          // scales and offsets of tokens g and g + 8; nothing is taken from slots
+          // that no row sees (they may hold anything)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(&pr[e][0]));
+            const float2 vf = __half22float2(*reinterpret_cast<const __half2*>(&pr[e][1]));
+            ks[q][e] = kf.x * (kCodeUnit * p.scale_log2);
+            kz[q][e] = fmaf(-8.f, kf.x, kf.y);
+            vs[q][e] = vf.x;
+            vz[q][e] = fmaf(-8.f, vf.x, vf.y);
+            const int t = t0 + 16 * q + g + 8 * e;
+            if (!full && (t >= any_hi || t < any_lo)) ks[q][e] = kz[q][e] = vs[q][e] = vz[q][e] = 0.f;
+          }
+        }
+        // scores in units of log2, less the running maximum; element (q, nb, e) holds
+        // token g + 8 e of granule q for rows 2c, 2c + 1
+        F2 xm[GB][NB][2];
+        float over = kNegInf, big = 0.f;
+        auto scores = [&]() {
+          over = kNegInf;
+#pragma unroll
+          for (int q = 0; q < GB; ++q)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                F2 v = fma2(dup(ks[q][e]), raw[q][nb][e],
+                            fma2(dup(kz[q][e]), qs[nb], {-m[nb].x, -m[nb].y}));
+                if (!full) {
+                  const int t = t0 + 16 * q + g + 8 * e;
+                  if (t >= hi_pos[nb][0] || t < lo_pos[nb][0]) v.x = kNegInf;
+                  if (t >= hi_pos[nb][1] || t < lo_pos[nb][1]) v.y = kNegInf;
+                }
+                xm[q][nb][e] = v;
+                over = fmaxf(over, fmaxf(v.x, v.y));
+              }
+        };
+        scores();
+#pragma unroll
+        for (int q = 0; q < GB; ++q) big = fmaxf(big, fmaxf(vs[q][0], vs[q][1]));
+        if (__any_sync(0xffffffffu, over > kLazy || big > sref)) {
+          // move the references: the rows' maxima and the power of two above the values' scales
+#pragma unroll
+          for (int q = 4; q < 32; q <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, q));
+          float ratio = 1.f;
+          if (big > sref) {  // 2^(exponent + 1); warp-uniform: vs depends on g alone
+            const float up = __uint_as_float(((__float_as_uint(big) >> 23) + 1) << 23);
+            ratio = sref / up;
+            sref = up;
+          }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            float top[2] = {kLowest, kLowest};
+#pragma unroll
+            for (int q = 0; q < GB; ++q)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {  // the scores again: less a first maximum of kLowest they are not kept
+                const F2 v = fma2(dup(ks[q][e]), raw[q][nb][e], mul2(dup(kz[q][e]), qs[nb]));
+                if (xm[q][nb][e].x != kNegInf) top[0] = fmaxf(top[0], v.x);
+                if (xm[q][nb][e].y != kNegInf) top[1] = fmaxf(top[1], v.y);
+              }
+#pragma unroll
+            for (int q = 4; q < 32; q <<= 1) {
+              top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], q));
+              top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], q));
+            }
+            const F2 nm = {fmaxf(m[nb].x, top[0]), fmaxf(m[nb].y, top[1])};
+            const F2 f = {m[nb].x == nm.x ? 1.f : ex2(m[nb].x - nm.x), m[nb].y == nm.y ? 1.f : ex2(m[nb].y - nm.y)};
+            m[nb] = nm;
+            l[nb] = mul2(l[nb], f);
+            pz[nb] = mul2(pz[nb], f);
+            const F2 fo = mul2(f, dup(ratio));
+#pragma unroll
+            for (int t = 0; t < CW * 2; ++t) {
+              o[t][nb][0] = mul2(o[t][nb][0], fo);
+              o[t][nb][1] = mul2(o[t][nb][1], fo);
+            }
+          }
+          scores();
+        }
+        // ---- probabilities, and O^T += V^T P^T --------------------------------------
+        const float rs = 64.f / sref;
+#pragma unroll
+        for (int q = 0; q < GB; ++q) {
+          const uint32_t sg = st + q * GR;
+          uint32_t v0[CW], v1[CW];
+          lds_words<CW>(sg + 8 * D + lane * (D / 8), v0);
+          lds_words<CW>(sg + 12 * D + lane * (D / 8), v1);
+          uint32_t ph[NB][2], pl[NB][2];
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const F2 pe = {ex2(xm[q][nb][e].x), ex2(xm[q][nb][e].y)};
+              l[nb] = add2(l[nb], pe);
+              F2 y = mul2(pe, dup(vs[q][e] * rs));
+              if (full) {
+                pz[nb] = fma2(pe, dup(vz[q][e]), pz[nb]);
+              } else {  // a token that is masked for one row alone may have a NaN scale
+                const int t = t0 + 16 * q + g + 8 * e;
+                if (t >= hi_pos[nb][0] || t < lo_pos[nb][0]) y.x = 0.f;
+                else pz[nb].x = fmaf(pe.x, vz[q][e], pz[nb].x);
+                if (t >= hi_pos[nb][1] || t < lo_pos[nb][1]) y.y = 0.f;
+                else pz[nb].y = fmaf(pe.y, vz[q][e], pz[nb].y);
+              }
+              const __half2 hi = __floats2half2_rn(y.x, y.y);
+              const float2 back = __half22float2(hi);
+              ph[nb][e] = transpose8x8(h2_bits(hi));
+              pl[nb][e] = transpose8x8(h2_bits(__floats2half2_rn(y.x - back.x, y.y - back.y)));
+            }
+#pragma unroll
+          for (int j = 0; j < CW; ++j) {
+            const uint32_t a0 = v0[j], a1 = v0[j] >> 8, a2 = v1[j], a3 = v1[j] >> 8;
+            const uint32_t l0 = a0 & 0x000F000Fu, l1 = a1 & 0x000F000Fu, l2 = a2 & 0x000F000Fu, l3 = a3 & 0x000F000Fu;
+            const uint32_t h0 = a0 & 0x00F000F0u, h1 = a1 & 0x00F000F0u, h2 = a2 & 0x00F000F0u, h3 = a3 & 0x00F000F0u;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              mma16816(o[2 * j][nb], l0, l1, l2, l3, ph[nb][0], ph[nb][1]);
+              mma16816(o[2 * j + 1][nb], h0, h1, h2, h3, ph[nb][0], ph[nb][1]);
+              mma16816(o[2 * j][nb], l0, l1, l2, l3, pl[nb][0], pl[nb][1]);
+              mma16816(o[2 * j + 1][nb], h0, h1, h2, h3, pl[nb][0], pl[nb][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      ++done;
+      if (issued < total) issue(stage);
+    }
+    if (!ok) break;
+
+    // ---- the end of the segment, or of the stripe --------------------------------------
+    const float unit = kCodeUnit * sref * (1.f / 64.f);
+    const bool whole = cnt == w.n;
+    const bool tail = cur.g != 0;  // a segment that began before: this warp's first part, else its last
+    float* part = reinterpret_cast<float*>(tail ? smem + Sh::kFirst + warp * Sh::kPart : ring_ptr);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        m[nb][e] = kNegInf;
-        l[nb][e] = pz[nb][e] = 0.f;
+      for (int q = 4; q < 32; q <<= 1) {
+        l[nb] = add2(l[nb], {__shfl_xor_sync(0xffffffffu, l[nb].x, q), __shfl_xor_sync(0xffffffffu, l[nb].y, q)});
+        pz[nb] = add2(pz[nb], {__shfl_xor_sync(0xffffffffu, pz[nb].x, q), __shfl_xor_sync(0xffffffffu, pz[nb].y, q)});
       }
-#pragma unroll
-      for (int t = 0; t < CW * 2; ++t)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[t][nb][k] = 0.f;
-    }
-
-    // this warp's granules of the segment: units u + x with (u + x) % W == warp
-    for (int x = (warp - u % W + W) % W; x < cnt; x += W) {
-      const int t0 = (w.g_lo + cur.g + x) * kGranule;
-      const int stage = done % S;
-      const uint32_t st = ring + stage * GR;
-      const uint32_t ph = (uint32_t)((done / S) & 1);
-      if (!wait_warp(smem_addr(&ctrl->full[warp * S + stage]), ph, wc)) break;
-      uint32_t k0[CW], k1[CW], v0[CW], v1[CW];
-      lds_words<CW>(st + g * (D / 2) + c * (D / 8), k0);
-      lds_words<CW>(st + (g + 8) * (D / 2) + c * (D / 8), k1);
-      lds_words<CW>(st + 8 * D + lane * (D / 8), v0);
-      lds_words<CW>(st + 12 * D + lane * (D / 8), v1);
-      uint32_t pa[2], pb[2];
-      lds_words<2>(st + 16 * D + g * 8, pa);
-      lds_words<2>(st + 16 * D + (g + 8) * 8, pb);
-      __syncwarp();
-      ++done;
-      if (issued < mine_n) issue(stage);
-      if (t0 >= any_hi || t0 + kGranule <= any_lo) continue;
-      const bool full = t0 + kGranule <= all_hi && t0 >= all_lo;
-
-      // scales and offsets of tokens g (index 0) and g + 8 (1); nothing is
-      // taken from slots that no row sees (they may hold anything)
-      float ks[2], kz[2], vs[2], vz[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const uint32_t* pr = e ? pb : pa;
-        const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(&pr[0]));
-        const float2 vf = __half22float2(*reinterpret_cast<const __half2*>(&pr[1]));
-        const int t = t0 + g + 8 * e;
-        const bool seen = full || (t < any_hi && t >= any_lo);
-        ks[e] = seen ? kf.x * (kCodeUnit * p.scale_log2) : 0.f;
-        kz[e] = seen ? kf.y - 8.f * kf.x : 0.f;
-        vs[e] = seen ? vf.x : 0.f;
-        vz[e] = seen ? vf.y - 8.f * vf.x : 0.f;
-      }
-
-      // ---- S^T = K Q^T on the codes: low nibbles and high (x 16) apart -----------
-      float sl[NB][4], sh[NB][4];
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sl[nb][k] = sh[nb][k] = 0.f;
-#pragma unroll
-      for (int j = 0; j < CW; ++j) {
-        const uint32_t a0 = k0[j], a1 = k1[j], a2 = k0[j] >> 8, a3 = k1[j] >> 8;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          mma16816(sl[nb], a0 & 0x000F000Fu, a1 & 0x000F000Fu, a2 & 0x000F000Fu, a3 & 0x000F000Fu,
-                   qf[nb][4 * j], qf[nb][4 * j + 1]);
-          mma16816(sh[nb], a0 & 0x00F000F0u, a1 & 0x00F000F0u, a2 & 0x00F000F0u, a3 & 0x00F000F0u,
-                   qf[nb][4 * j + 2], qf[nb][4 * j + 3]);
-        }
-      }
-      // scores in units of log2: element k is token g + 8 (k >> 1), row 2c + (k & 1)
-      bool over = vs[0] > sref || vs[1] > sref;
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int tt = k >> 1, e = k & 1;
-          const float raw = fmaf(sh[nb][k], 0.0625f, sl[nb][k]);
-          float xs = fmaf(ks[tt], raw, kz[tt] * qs[nb][e]);
-          if (!full) {
-            const int t = t0 + g + 8 * tt;
-            if (t >= hi_pos[nb][e] || t < lo_pos[nb][e]) xs = kNegInf;
-          }
-          sl[nb][k] = xs;
-          over = over || xs > m[nb][e] + kLazy;
-        }
-      if (__any_sync(0xffffffffu, over)) {
-        // move the references: the rows' maxima and the power of two above the values' scales
-        float sm = fmaxf(vs[0], vs[1]);
-#pragma unroll
-        for (int q = 4; q < 32; q <<= 1) sm = fmaxf(sm, __shfl_xor_sync(0xffffffffu, sm, q));
-        float ratio = 1.f;
-        if (sm > sref) {  // 2^(exponent + 1); warp-uniform: vs depends on g alone
-          const float up = __uint_as_float(((__float_as_uint(sm) >> 23) + 1) << 23);
-          ratio = sref / up;
-          sref = up;
-          rs = 64.f / up;
-        }
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(sl[nb][e], sl[nb][2 + e]);
-#pragma unroll
-            for (int q = 4; q < 32; q <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, q));
-            top = fmaxf(top, m[nb][e]);
-            const float f = m[nb][e] == top ? 1.f : ex2(m[nb][e] - top);
-            m[nb][e] = top;
-            l[nb][e] *= f;
-            pz[nb][e] *= f;
-            const float fo = f * ratio;
-#pragma unroll
-            for (int t = 0; t < CW * 2; ++t) {
-              o[t][nb][e] *= fo;
-              o[t][nb][2 + e] *= fo;
-            }
-          }
-      }
-      // ---- probabilities; P^T's operand halves ------------------------------------
-      uint32_t ph0[NB], ph1[NB], pl0[NB], pl1[NB];
-      const float w0 = vs[0] * rs, w1 = vs[1] * rs;
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        float y[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int tt = k >> 1, e = k & 1;
-          const float ref = m[nb][e] == kNegInf ? 0.f : m[nb][e];
-          const float pe = ex2(sl[nb][k] - ref);
-          l[nb][e] += pe;
-          float zz = pe * vz[tt];
-          y[k] = pe * (tt ? w1 : w0);
-          if (!full) {  // a masked token's scale may be NaN
-            const int t = t0 + g + 8 * tt;
-            if (t >= hi_pos[nb][e] || t < lo_pos[nb][e]) zz = y[k] = 0.f;
-          }
-          pz[nb][e] += zz;
-        }
-        const __half2 h0 = __floats2half2_rn(y[0], y[1]), h1 = __floats2half2_rn(y[2], y[3]);
-        const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
-        ph0[nb] = transpose8x8(h2_bits(h0));
-        ph1[nb] = transpose8x8(h2_bits(h1));
-        pl0[nb] = transpose8x8(h2_bits(__floats2half2_rn(y[0] - f0.x, y[1] - f0.y)));
-        pl1[nb] = transpose8x8(h2_bits(__floats2half2_rn(y[2] - f1.x, y[3] - f1.y)));
-      }
-      // ---- O^T += V^T P^T -----------------------------------------------------------
-#pragma unroll
-      for (int j = 0; j < CW; ++j) {
-        const uint32_t a0 = v0[j], a1 = v0[j] >> 8, a2 = v1[j], a3 = v1[j] >> 8;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const uint32_t l0 = a0 & 0x000F000Fu, l1 = a1 & 0x000F000Fu, l2 = a2 & 0x000F000Fu, l3 = a3 & 0x000F000Fu;
-          const uint32_t h0 = a0 & 0x00F000F0u, h1 = a1 & 0x00F000F0u, h2 = a2 & 0x00F000F0u, h3 = a3 & 0x00F000F0u;
-          mma16816(o[2 * j][nb], l0, l1, l2, l3, ph0[nb], ph1[nb]);
-          mma16816(o[2 * j + 1][nb], h0, h1, h2, h3, ph0[nb], ph1[nb]);
-          mma16816(o[2 * j][nb], l0, l1, l2, l3, pl0[nb], pl1[nb]);
-          mma16816(o[2 * j + 1][nb], h0, h1, h2, h3, pl0[nb], pl1[nb]);
-        }
-      }
-    }
-
-    // ---- the warps' parts -> shared memory -------------------------------------------
-    const float unit = kCodeUnit * sref * (1.f / 64.f);
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int q = 4; q < 32; q <<= 1) {
-          l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], q);
-          pz[nb][e] += __shfl_xor_sync(0xffffffffu, pz[nb][e], q);
-        }
         const int row = nb * 8 + 2 * c + e;
-        if (g == 0) {
-          ml[(warp * RB + row) * 2] = m[nb][e];
-          ml[(warp * RB + row) * 2 + 1] = l[nb][e];
+        const float ll = e ? l[nb].y : l[nb].x, zz = e ? pz[nb].y : pz[nb].x;
+        if (!whole && g == 0) {
+          part[RB * Sh::kOStride + 2 * row] = e ? m[nb].y : m[nb].x;
+          part[RB * Sh::kOStride + 2 * row + 1] = ll;
         }
-        float* dst = merge + (warp * RB + row) * Sh::kOStride + g * (D / 8);
 #pragma unroll
         for (int j = 0; j < CW; ++j) {
+          const F2 a = o[2 * j][nb][0], b = o[2 * j + 1][nb][0], d = o[2 * j][nb][1], f = o[2 * j + 1][nb][1];
           float4 v;
-          v.x = fmaf(o[2 * j][nb][e], unit, pz[nb][e]);
-          v.y = fmaf(o[2 * j + 1][nb][e], unit * 0.0625f, pz[nb][e]);
-          v.z = fmaf(o[2 * j][nb][2 + e], unit, pz[nb][e]);
-          v.w = fmaf(o[2 * j + 1][nb][2 + e], unit * 0.0625f, pz[nb][e]);
-          *reinterpret_cast<float4*>(dst + 4 * j) = v;
+          v.x = fmaf(e ? a.y : a.x, unit, zz);
+          v.y = fmaf(e ? b.y : b.x, unit * 0.0625f, zz);
+          v.z = fmaf(e ? d.y : d.x, unit, zz);
+          v.w = fmaf(e ? f.y : f.x, unit * 0.0625f, zz);
+          if (!whole)
+            *reinterpret_cast<float4*>(part + row * Sh::kOStride + g * (D / 8) + 4 * j) = v;
+          else if (rb * RB + row < rows)
+            store_row(p, w.s, h, rb * RB + row, g * (D / 8) + 4 * j, D, v, ll);
         }
       }
-    __syncthreads();
-
-    // ---- the CTA's part; whole segments are finished, others published ---------------
-    const bool whole = cnt == w.n;
-    const long long s0 = u_begin + u - cur.g;  // the segment's first unit
-    const int slot = 2 * blockIdx.x + (cur.g == 0 ? 1 : 0);
-    float* part = p.partials + (long long)slot * (RB * (D + 2));
-    constexpr int kVec = RB * D / 4;
-    for (int v = tid; v < kVec; v += W * 32) {
-      const int row = v / (D / 4), ch = (v - row * (D / 4)) * 4;
-      float top = kNegInf;
-#pragma unroll
-      for (int q = 0; q < W; ++q) top = fmaxf(top, ml[(q * RB + row) * 2]);
-      float sum = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int q = 0; q < W; ++q) {
-        const float mq = ml[(q * RB + row) * 2], lq = ml[(q * RB + row) * 2 + 1];
-        if (lq == 0.f) continue;
-        const float f = mq == top ? 1.f : ex2(mq - top);
-        const float4 a = *reinterpret_cast<const float4*>(merge + (q * RB + row) * Sh::kOStride + ch);
-        sum = fmaf(lq, f, sum);
-        acc.x = fmaf(a.x, f, acc.x);
-        acc.y = fmaf(a.y, f, acc.y);
-        acc.z = fmaf(a.z, f, acc.z);
-        acc.w = fmaf(a.w, f, acc.w);
-      }
-      if (whole) {
-        const int rr = rb * RB + row;
-        if (rr < rows) store_row(p, w.s, h, rr, ch, D, acc, sum);
+    }
+    if (!whole && lane == 0) {
+      Parts& q = ctrl->parts[warp];
+      if (tail) {
+        q.first = 1;
+        q.first_ends = cur.g + cnt == w.n;
       } else {
-        __stcg(reinterpret_cast<float4*>(part + row * D + ch), acc);
-        if (ch == 0) {
-          __stcg(part + RB * D + 2 * row, top);
-          __stcg(part + RB * D + 2 * row + 1, sum);
-        }
+        q.last = 1;
       }
+      q.b[tail ? 0 : 1] = cur.b;
+      q.seg[tail ? 0 : 1] = cur.seg;
+      q.s0[tail ? 0 : 1] = from + done - cnt - cur.g;
     }
-    if (!whole) {
-      const long long c0 = stripe_owner(s0, U, G), c1 = stripe_owner(s0 + w.n - 1, U, G);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        int* counter = p.counters + c0;
-        const int arrived = atomicAdd(counter, 1);
-        ctrl->last = arrived == (int)(c1 - c0);
-        if (ctrl->last) *counter = 0;  // everyone has arrived: ready for the next call
-        __threadfence();
-      }
-      __syncthreads();
-      if (ctrl->last) {
-        for (int v = tid; v < kVec; v += W * 32) {
-          const int row = v / (D / 4), ch = (v - row * (D / 4)) * 4;
-          const int rr = rb * RB + row;
-          if (rr >= rows) continue;
-          // the parts in stripe order: the first CTA's is its last segment's (slot
-          // 1), the others' their first (slot 0)
-          float top = kNegInf, sum = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (long long q = c0; q <= c1; ++q) {
-            const float* src = p.partials + (2 * q + (q == c0 ? 1 : 0)) * (RB * (D + 2));
-            const float mq = __ldcg(src + RB * D + 2 * row), lq = __ldcg(src + RB * D + 2 * row + 1);
-            const float4 a = __ldcg(reinterpret_cast<const float4*>(src + row * D + ch));
-            if (lq == 0.f) continue;
-            const float nt = fmaxf(top, mq);
-            const float fo = top == nt ? 1.f : ex2(top - nt), fn = mq == nt ? 1.f : ex2(mq - nt);
-            top = nt;
-            sum = fmaf(sum, fo, lq * fn);
-            acc.x = fmaf(acc.x, fo, a.x * fn);
-            acc.y = fmaf(acc.y, fo, a.y * fn);
-            acc.z = fmaf(acc.z, fo, a.z * fn);
-            acc.w = fmaf(acc.w, fo, a.w * fn);
-          }
-          store_row(p, w.s, h, rr, ch, D, acc, sum);
-        }
-      }
-    }
-    __syncthreads();  // the merge buffer is free again
-    u += cnt;
-    advance<RB>(p, cur, cnt);
+    advance<Sh>(p, cur, cnt);
   }
   // nothing may still be in flight into this CTA's shared memory
   for (; done < issued; ++done)
     if (lane == 0) wait_drain(smem_addr(&ctrl->full[warp * S + done % S]), (uint32_t)((done / S) & 1), wc);
+  __syncthreads();
+  if (ctrl->abort) return;
+
+  // ---- segments cut between warps: the parts of consecutive warps --------------------
+  // A run begins with a warp's last part, or (start = -1) with the first part of
+  // the CTA's first warp that has any blocks: a segment that began in an earlier
+  // CTA.  It goes on with the next warps' first parts until the segment ends.
+  constexpr int kVec = RB * D / 4;
+  int lead0 = 0;
+  while (lead0 < W - 1 && ctrl->parts[lead0].idle) ++lead0;
+  for (int start = -1; start < W; ++start) {
+    const bool head = start >= 0;  // the segment begins in this CTA
+    const int q0 = head ? start : lead0;
+    const Parts& lead = ctrl->parts[q0];
+    if (head ? !lead.last : !lead.first) continue;
+    const int sb = lead.b[head], sseg = lead.seg[head];
+    int end = q0 + 1;  // one past the last warp of the run
+    bool ends = !head && lead.first_ends;
+    while (!ends && end < W && (ctrl->parts[end].first || ctrl->parts[end].idle)) {
+      ends = ctrl->parts[end].first && ctrl->parts[end].first_ends;
+      ++end;
+    }
+    const SeqWork w = seq_work<Sh>(p, sb, false);
+    const int h = sseg / w.rbs, rb = sseg - h * w.rbs, rows = w.s.nq * p.group;
+    const bool here = head && ends;
+    const int slot = 2 * blockIdx.x + (head ? 1 : 0);
+    float* part = p.partials + (long long)slot * (RB * (D + 2));
+    for (int v = tid; v < kVec; v += W * 32) {
+      const int row = v / (D / 4), ch = (v - row * (D / 4)) * 4;
+      float top = kLowest, sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int q = q0; q < end; ++q) {
+        if (ctrl->parts[q].idle) continue;
+        const uint8_t* at = head && q == q0 ? smem + Sh::kRing + q * (S * BB) : smem + Sh::kFirst + q * Sh::kPart;
+        join<RB, false>(reinterpret_cast<const float*>(at), Sh::kOStride, row, ch, top, sum, acc);
+      }
+      if (here) {
+        if (rb * RB + row < rows) store_row(p, w.s, h, rb * RB + row, ch, D, acc, sum);
+      } else {
+        __stcg(reinterpret_cast<float4*>(part + row * D + ch), acc);
+        if (ch == 0) __stcg(reinterpret_cast<float2*>(part + RB * D + 2 * row), make_float2(top, sum));
+      }
+    }
+    if (here) continue;
+
+    // ---- cut between CTAs: the last to arrive joins the parts in stripe order --------
+    const long long s0 = lead.s0[head];
+    const long long c0 = stripe_owner(s0, U, G), c1 = stripe_owner(s0 + w.n - 1, U, G);
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+      int* counter = p.counters + c0;
+      const int arrived = atomicAdd(counter, 1);
+      ctrl->arrived = arrived == (int)(c1 - c0);
+      if (ctrl->arrived) *counter = 0;  // everyone has arrived: ready for the next call
+      __threadfence();
+    }
+    __syncthreads();
+    if (ctrl->arrived) {
+      for (int v = tid; v < kVec; v += W * 32) {
+        const int row = v / (D / 4), ch = (v - row * (D / 4)) * 4;
+        if (rb * RB + row >= rows) continue;
+        float top = kLowest, sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        // the first CTA's part is in its slot 1, the others' in slot 0
+#pragma unroll 4
+        for (long long q = c0; q <= c1; ++q)
+          join<RB, true>(p.partials + (2 * q + (q == c0 ? 1 : 0)) * (RB * (D + 2)), D, row, ch, top, sum, acc);
+        store_row(p, w.s, h, rb * RB + row, ch, D, acc, sum);
+      }
+    }
+    __syncthreads();
+  }
 }
 
 template <int D, int NB>

@@ -261,6 +261,7 @@ marlin_status_t marlin_kv_attention(const uint16_t* q, int64_t q_token_stride, i
   p.group = group;
   p.window = window;
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.whole_blocks = p.kv.page16 % 4 == 0;
   p.max_rows = 0x7FFFFFFF;
   p.counters = reinterpret_cast<int*>(ws + a.counters_off);
   p.partials = reinterpret_cast<float*>(ws + a.partials_off);
