@@ -48,19 +48,21 @@ __device__ __forceinline__ float ex2(float x) {
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
 
+// Plain loads from shared memory (the compiler may move them up to the wait).
 template <int N>
-__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
+__device__ __forceinline__ void load_words(const uint8_t* at, uint32_t (&w)[N]) {
   if constexpr (N == 4) {
-    const uint4 v = lds128(addr);
+    const uint4 v = *reinterpret_cast<const uint4*>(at);
     w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
   } else {
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+    const uint2 v = *reinterpret_cast<const uint2*>(at);
+    w[0] = v.x; w[1] = v.y;
   }
 }
 
@@ -83,7 +85,7 @@ struct F2 {
 };
 __device__ __forceinline__ void mma16816(F2 (&d)[2], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0].x), "+f"(d[0].y), "+f"(d[1].x), "+f"(d[1].y)
@@ -129,6 +131,7 @@ struct Shape {
   static constexpr int kFirst = kRing + W * S * BB;      // the warps' first parts; the last ones go to their rings
   static constexpr int kSmem = kFirst + W * kPart;
   static_assert(kPart <= S * BB && kPart % 16 == 0, "a part has to fit a warp's ring");
+  static_assert(W <= 16 && W * S <= 64, "the control block holds 16 warps and 64 barriers");
 };
 
 // One request's share of the work: its blocks [lo, lo + n) and the number of
@@ -184,18 +187,11 @@ struct Parts {
   long long s0[2];         // the segment's first unit
 };
 
-// Joins row `row`, channels ch .. ch + 3 of one part: rows of `stride` floats,
-// then (maximum, sum) of each.
-template <int RB, bool kGlobal>
-__device__ __forceinline__ void join(const float* part, int stride, int row, int ch, float& top, float& sum,
-                                     float4& acc) {
-  const float2* mp = reinterpret_cast<const float2*>(part + RB * stride) + row;
-  const float4* ap = reinterpret_cast<const float4*>(part + row * stride + ch);
-  const float2 ml = kGlobal ? __ldcg(mp) : *mp;
-  const float4 a = kGlobal ? __ldcg(ap) : *ap;
-  if (ml.y == 0.f) return;  // saw no token
-  const float nt = fmaxf(top, ml.x);
-  const float fo = top == nt ? 1.f : ex2(top - nt), fn = ml.x == nt ? 1.f : ex2(ml.x - nt);
+// Joins one part's (maximum, sum) and values of four channels.  A part that saw
+// no token has sum 0 and zeros.
+__device__ __forceinline__ void join(float2 ml, float4 a, float& top, float& sum, float4& acc) {
+  const float nt = ml.y == 0.f ? top : fmaxf(top, ml.x);
+  const float fo = top == nt ? 1.f : ex2(top - nt), fn = ml.x == nt ? 1.f : ml.y == 0.f ? 0.f : ex2(ml.x - nt);
   top = nt;
   sum = fmaf(sum, fo, ml.y * fn);
   acc.x = fmaf(acc.x, fo, a.x * fn);
@@ -204,15 +200,24 @@ __device__ __forceinline__ void join(const float* part, int stride, int row, int
   acc.w = fmaf(acc.w, fo, a.w * fn);
 }
 
+// stripe_begin and stripe_owner, in 32 bits where the products fit.
+__device__ __forceinline__ long long begin_of(long long i, long long U, long long N) {
+  return U * N < (1ll << 32) ? (long long)((uint32_t)(i * U) / (uint32_t)N) : stripe_begin(i, U, N);
+}
+__device__ __forceinline__ long long owner_of(long long u, long long U, long long N) {
+  return U * N < (1ll << 32) ? (long long)((uint32_t)((u + 1) * N - 1) / (uint32_t)U) : stripe_owner(u, U, N);
+}
+
 struct AttnCtrl {
   uint64_t full[64];       // [W][S]
-  long long scan[8], scan_segs[8];
-  int longest[8];
+  long long scan[16], scan_segs[16];
+  int longest[16];
   long long start_off;     // the first unit's offset in its request
   int start_b;
   int abort;
-  int arrived;
-  Parts parts[8];
+  int arrived[2];
+  SeqWork start_w;
+  Parts parts[16];
 };
 static_assert(sizeof(AttnCtrl) <= 2048, "control block too large");
 
@@ -284,7 +289,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
   // otherwise an equal share of all blocks for every warp, at least one
   const long long G = by_seg ? segs : min((long long)gridDim.x, (U + W - 1) / W);
   if (blockIdx.x >= G) return;
-  const long long u_cta = stripe_begin(blockIdx.x, U, G);
+  const long long u_cta = begin_of(blockIdx.x, U, G);
   {
     const long long at = by_seg ? blockIdx.x : u_cta;
     const long long from = by_seg ? before_segs : before;
@@ -295,6 +300,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
         const long long n = (long long)p.kv.hkv * w.rbs * (by_seg ? 1 : w.n);
         if (off < n) {
           ctrl->start_b = b;
+          ctrl->start_w = w;
           ctrl->start_off = by_seg ? off * w.n : off;
           break;
         }
@@ -305,9 +311,10 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
   __syncthreads();
   Cursor cur;
   cur.b = ctrl->start_b;
-  cur.w = seq_work<Sh>(p, cur.b, false);
-  cur.seg = (int)(ctrl->start_off / cur.w.n);
-  cur.g = (int)(ctrl->start_off - (long long)cur.seg * cur.w.n);
+  cur.w = ctrl->start_w;
+  const long long start_off = ctrl->start_off;
+  cur.seg = start_off < (1ll << 32) ? (int)((uint32_t)start_off / (uint32_t)cur.w.n) : (int)(start_off / cur.w.n);
+  cur.g = (int)(start_off - (long long)cur.seg * cur.w.n);
   int total;           // this warp's blocks
   long long from = 0;  // and the first of them
   if (by_seg) {
@@ -316,8 +323,8 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
     cur.g += (int)from;  // inside the segment, or at its end where there is nothing left to do
   } else {
     const long long gw = (long long)blockIdx.x * W + warp;
-    from = stripe_begin(gw, U, G * W);
-    total = (int)(stripe_begin(gw + 1, U, G * W) - from);
+    from = begin_of(gw, U, G * W);
+    total = (int)(begin_of(gw + 1, U, G * W) - from);
     if (total > 0) advance<Sh>(p, cur, (int)(from - u_cta));
   }
 
@@ -423,10 +430,10 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
       for (int t = 0; t < CW * 2; ++t) o[t][nb][0] = o[t][nb][1] = dup(0.f);
     }
 
-    for (int x = 0; x < cnt; ++x) {
-      const int t0 = (w.lo + cur.g + x) * Sh::kBlock;
+    for (int i = 0; i < cnt; ++i) {
+      const int t0 = (w.lo + cur.g + i) * Sh::kBlock;
       const int stage = done % S;
-      const uint32_t st = ring + stage * BB;
+      const uint8_t* st = ring_ptr + stage * BB;
       if (!wait_warp(smem_addr(&ctrl->full[warp * S + stage]), (uint32_t)((done / S) & 1), wc)) {
         ok = false;
         break;
@@ -435,77 +442,69 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
         const bool full = t0 + Sh::kBlock <= all_hi && t0 >= all_lo;
 
         // ---- S^T = K Q^T on the codes: low nibbles and high (x 16) apart -----------
-        F2 raw[GB][NB][2];                        // tokens g and g + 8 of each granule
-        float ks[GB][2], kz[GB][2], vs[GB][2], vz[GB][2];
+        // x: scores in units of log2; element (q, nb, e) is token g + 8 e of granule
+        // q for rows 2c, 2c + 1
+        F2 x[GB][NB][2], top[NB];
+        float vs[GB][2], vz[GB][2], big = 0.f;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) top[nb] = dup(kLowest);
+        uint32_t k0[GB][CW], k1[GB][CW];
+        F2 sl[GB][NB][2], sh[GB][NB][2];
 #pragma unroll
         for (int q = 0; q < GB; ++q) {
-          const uint32_t sg = st + q * GR;
-          uint32_t k0[CW], k1[CW];
-          lds_words<CW>(sg + g * (D / 2) + c * (D / 8), k0);
-          lds_words<CW>(sg + (g + 8) * (D / 2) + c * (D / 8), k1);
-          uint32_t pr[2][2];
-          lds_words<2>(sg + 16 * D + g * 8, pr[0]);
-          lds_words<2>(sg + 16 * D + (g + 8) * 8, pr[1]);
-          F2 sl[NB][2], sh[NB][2];
+          load_words<CW>(st + q * GR + g * (D / 2) + c * (D / 8), k0[q]);
+          load_words<CW>(st + q * GR + (g + 8) * (D / 2) + c * (D / 8), k1[q]);
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) sl[nb][0] = sl[nb][1] = sh[nb][0] = sh[nb][1] = dup(0.f);
+          for (int nb = 0; nb < NB; ++nb) sl[q][nb][0] = sl[q][nb][1] = sh[q][nb][0] = sh[q][nb][1] = dup(0.f);
+        }
+        // the granules in turn, so that no product waits for the one before
 #pragma unroll
-          for (int j = 0; j < CW; ++j) {
-            const uint32_t a0 = k0[j], a1 = k1[j], a2 = k0[j] >> 8, a3 = k1[j] >> 8;
+        for (int j = 0; j < CW; ++j)
+#pragma unroll
+          for (int q = 0; q < GB; ++q) {
+            const uint32_t a0 = k0[q][j], a1 = k1[q][j], a2 = k0[q][j] >> 8, a3 = k1[q][j] >> 8;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-              mma16816(sl[nb], a0 & 0x000F000Fu, a1 & 0x000F000Fu, a2 & 0x000F000Fu, a3 & 0x000F000Fu,
+              mma16816(sl[q][nb], a0 & 0x000F000Fu, a1 & 0x000F000Fu, a2 & 0x000F000Fu, a3 & 0x000F000Fu,
                        qf[nb][4 * j], qf[nb][4 * j + 1]);
-              mma16816(sh[nb], a0 & 0x00F000F0u, a1 & 0x00F000F0u, a2 & 0x00F000F0u, a3 & 0x00F000F0u,
+              mma16816(sh[q][nb], a0 & 0x00F000F0u, a1 & 0x00F000F0u, a2 & 0x00F000F0u, a3 & 0x00F000F0u,
                        qf[nb][4 * j + 2], qf[nb][4 * j + 3]);
             }
           }
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              raw[q][nb][e] = fma2(sh[nb][e], dup(0.0625f), sl[nb][e]);
+        for (int q = 0; q < GB; ++q) {
+          uint32_t pr[2][2];
+          load_words<2>(st + q * GR + 16 * D + g * 8, pr[0]);
+          load_words<2>(st + q * GR + 16 * D + (g + 8) * 8, pr[1]);
           // scales and offsets of tokens g and g + 8; nothing is taken from slots
           // that no row sees (they may hold anything)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(&pr[e][0]));
             const float2 vf = __half22float2(*reinterpret_cast<const __half2*>(&pr[e][1]));
-            ks[q][e] = kf.x * (kCodeUnit * p.scale_log2);
-            kz[q][e] = fmaf(-8.f, kf.x, kf.y);
+            float ks = kf.x * (kCodeUnit * p.scale_log2), kz = fmaf(-8.f, kf.x, kf.y);
             vs[q][e] = vf.x;
             vz[q][e] = fmaf(-8.f, vf.x, vf.y);
             const int t = t0 + 16 * q + g + 8 * e;
-            if (!full && (t >= any_hi || t < any_lo)) ks[q][e] = kz[q][e] = vs[q][e] = vz[q][e] = 0.f;
+            if (!full && (t >= any_hi || t < any_lo)) ks = kz = vs[q][e] = vz[q][e] = 0.f;
+            big = fmaxf(big, vs[q][e]);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              F2 v = fma2(dup(ks), fma2(sh[q][nb][e], dup(0.0625f), sl[q][nb][e]), mul2(dup(kz), qs[nb]));
+              if (!full) {
+                if (t >= hi_pos[nb][0] || t < lo_pos[nb][0]) v.x = kNegInf;
+                if (t >= hi_pos[nb][1] || t < lo_pos[nb][1]) v.y = kNegInf;
+              }
+              x[q][nb][e] = v;
+              top[nb].x = fmaxf(top[nb].x, v.x);
+              top[nb].y = fmaxf(top[nb].y, v.y);
+            }
           }
         }
-        // scores in units of log2, less the running maximum; element (q, nb, e) holds
-        // token g + 8 e of granule q for rows 2c, 2c + 1
-        F2 xm[GB][NB][2];
-        float over = kNegInf, big = 0.f;
-        auto scores = [&]() {
-          over = kNegInf;
+        bool over = big > sref;
 #pragma unroll
-          for (int q = 0; q < GB; ++q)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                F2 v = fma2(dup(ks[q][e]), raw[q][nb][e],
-                            fma2(dup(kz[q][e]), qs[nb], {-m[nb].x, -m[nb].y}));
-                if (!full) {
-                  const int t = t0 + 16 * q + g + 8 * e;
-                  if (t >= hi_pos[nb][0] || t < lo_pos[nb][0]) v.x = kNegInf;
-                  if (t >= hi_pos[nb][1] || t < lo_pos[nb][1]) v.y = kNegInf;
-                }
-                xm[q][nb][e] = v;
-                over = fmaxf(over, fmaxf(v.x, v.y));
-              }
-        };
-        scores();
-#pragma unroll
-        for (int q = 0; q < GB; ++q) big = fmaxf(big, fmaxf(vs[q][0], vs[q][1]));
-        if (__any_sync(0xffffffffu, over > kLazy || big > sref)) {
+        for (int nb = 0; nb < NB; ++nb) over = over || top[nb].x > m[nb].x + kLazy || top[nb].y > m[nb].y + kLazy;
+        if (__any_sync(0xffffffffu, over)) {
           // move the references: the rows' maxima and the power of two above the values' scales
 #pragma unroll
           for (int q = 4; q < 32; q <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, q));
@@ -517,21 +516,12 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
           }
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            float top[2] = {kLowest, kLowest};
-#pragma unroll
-            for (int q = 0; q < GB; ++q)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {  // the scores again: less a first maximum of kLowest they are not kept
-                const F2 v = fma2(dup(ks[q][e]), raw[q][nb][e], mul2(dup(kz[q][e]), qs[nb]));
-                if (xm[q][nb][e].x != kNegInf) top[0] = fmaxf(top[0], v.x);
-                if (xm[q][nb][e].y != kNegInf) top[1] = fmaxf(top[1], v.y);
-              }
 #pragma unroll
             for (int q = 4; q < 32; q <<= 1) {
-              top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], q));
-              top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], q));
+              top[nb].x = fmaxf(top[nb].x, __shfl_xor_sync(0xffffffffu, top[nb].x, q));
+              top[nb].y = fmaxf(top[nb].y, __shfl_xor_sync(0xffffffffu, top[nb].y, q));
             }
-            const F2 nm = {fmaxf(m[nb].x, top[0]), fmaxf(m[nb].y, top[1])};
+            const F2 nm = {fmaxf(m[nb].x, top[nb].x), fmaxf(m[nb].y, top[nb].y)};
             const F2 f = {m[nb].x == nm.x ? 1.f : ex2(m[nb].x - nm.x), m[nb].y == nm.y ? 1.f : ex2(m[nb].y - nm.y)};
             m[nb] = nm;
             l[nb] = mul2(l[nb], f);
@@ -543,22 +533,22 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
               o[t][nb][1] = mul2(o[t][nb][1], fo);
             }
           }
-          scores();
         }
         // ---- probabilities, and O^T += V^T P^T --------------------------------------
         const float rs = 64.f / sref;
 #pragma unroll
         for (int q = 0; q < GB; ++q) {
-          const uint32_t sg = st + q * GR;
+          const uint8_t* sg = st + q * GR;
           uint32_t v0[CW], v1[CW];
-          lds_words<CW>(sg + 8 * D + lane * (D / 8), v0);
-          lds_words<CW>(sg + 12 * D + lane * (D / 8), v1);
+          load_words<CW>(sg + 8 * D + lane * (D / 8), v0);
+          load_words<CW>(sg + 12 * D + lane * (D / 8), v1);
           uint32_t ph[NB][2], pl[NB][2];
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const F2 pe = {ex2(xm[q][nb][e].x), ex2(xm[q][nb][e].y)};
+              const F2 xm = add2(x[q][nb][e], {-m[nb].x, -m[nb].y});
+              const F2 pe = {ex2(xm.x), ex2(xm.y)};
               l[nb] = add2(l[nb], pe);
               F2 y = mul2(pe, dup(vs[q][e] * rs));
               if (full) {
@@ -575,19 +565,20 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
               ph[nb][e] = transpose8x8(h2_bits(hi));
               pl[nb][e] = transpose8x8(h2_bits(__floats2half2_rn(y.x - back.x, y.y - back.y)));
             }
+          // first halves of all tiles, then second halves: no result waits for the one before
 #pragma unroll
-          for (int j = 0; j < CW; ++j) {
-            const uint32_t a0 = v0[j], a1 = v0[j] >> 8, a2 = v1[j], a3 = v1[j] >> 8;
-            const uint32_t l0 = a0 & 0x000F000Fu, l1 = a1 & 0x000F000Fu, l2 = a2 & 0x000F000Fu, l3 = a3 & 0x000F000Fu;
-            const uint32_t h0 = a0 & 0x00F000F0u, h1 = a1 & 0x00F000F0u, h2 = a2 & 0x00F000F0u, h3 = a3 & 0x00F000F0u;
+          for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              mma16816(o[2 * j][nb], l0, l1, l2, l3, ph[nb][0], ph[nb][1]);
-              mma16816(o[2 * j + 1][nb], h0, h1, h2, h3, ph[nb][0], ph[nb][1]);
-              mma16816(o[2 * j][nb], l0, l1, l2, l3, pl[nb][0], pl[nb][1]);
-              mma16816(o[2 * j + 1][nb], h0, h1, h2, h3, pl[nb][0], pl[nb][1]);
+            for (int j = 0; j < CW; ++j) {
+              const uint32_t a0 = v0[j], a1 = v0[j] >> 8, a2 = v1[j], a3 = v1[j] >> 8;
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                const uint32_t p0 = half ? pl[nb][0] : ph[nb][0], p1 = half ? pl[nb][1] : ph[nb][1];
+                mma16816(o[2 * j][nb], a0 & 0x000F000Fu, a1 & 0x000F000Fu, a2 & 0x000F000Fu, a3 & 0x000F000Fu, p0, p1);
+                mma16816(o[2 * j + 1][nb], a0 & 0x00F000F0u, a1 & 0x00F000F0u, a2 & 0x00F000F0u, a3 & 0x00F000F0u, p0,
+                         p1);
+              }
             }
-          }
         }
       }
       __syncwarp();
@@ -656,6 +647,10 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
   // the CTA's first warp that has any blocks: a segment that began in an earlier
   // CTA.  It goes on with the next warps' first parts until the segment ends.
   constexpr int kVec = RB * D / 4;
+  struct Cut {
+    int on, b, seg;
+    long long s0;
+  } cut[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};  // runs cut between CTAs: one that began before, one that goes on
   int lead0 = 0;
   while (lead0 < W - 1 && ctrl->parts[lead0].idle) ++lead0;
   for (int start = -1; start < W; ++start) {
@@ -681,8 +676,10 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int q = q0; q < end; ++q) {
         if (ctrl->parts[q].idle) continue;
-        const uint8_t* at = head && q == q0 ? smem + Sh::kRing + q * (S * BB) : smem + Sh::kFirst + q * Sh::kPart;
-        join<RB, false>(reinterpret_cast<const float*>(at), Sh::kOStride, row, ch, top, sum, acc);
+        const float* at = reinterpret_cast<const float*>(head && q == q0 ? smem + Sh::kRing + q * (S * BB)
+                                                                         : smem + Sh::kFirst + q * Sh::kPart);
+        join(*reinterpret_cast<const float2*>(at + RB * Sh::kOStride + 2 * row),
+             *reinterpret_cast<const float4*>(at + row * Sh::kOStride + ch), top, sum, acc);
       }
       if (here) {
         if (rb * RB + row < rows) store_row(p, w.s, h, rb * RB + row, ch, D, acc, sum);
@@ -691,35 +688,56 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
         if (ch == 0) __stcg(reinterpret_cast<float2*>(part + RB * D + 2 * row), make_float2(top, sum));
       }
     }
-    if (here) continue;
+    if (!here) {
+      if (head) cut[1] = {1, sb, sseg, lead.s0[1]};
+      else cut[0] = {1, sb, sseg, lead.s0[0]};
+    }
+  }
+  if (!cut[0].on && !cut[1].on) return;
 
-    // ---- cut between CTAs: the last to arrive joins the parts in stripe order --------
-    const long long s0 = lead.s0[head];
-    const long long c0 = stripe_owner(s0, U, G), c1 = stripe_owner(s0 + w.n - 1, U, G);
+  // ---- segments cut between CTAs: the last to arrive joins the parts in stripe order ---
+  __threadfence();
+  __syncthreads();
+  if (tid < 2 && (tid ? cut[1].on : cut[0].on)) {
+    const long long s0 = tid ? cut[1].s0 : cut[0].s0;
+    const int n = seq_work<Sh>(p, tid ? cut[1].b : cut[0].b, false).n;
+    const int c0 = (int)owner_of(s0, U, G), c1 = (int)owner_of(s0 + n - 1, U, G);
+    const int arrived = atomicAdd(p.counters + c0, 1);
+    ctrl->arrived[tid] = arrived == c1 - c0;
+    if (arrived == c1 - c0) p.counters[c0] = 0;  // everyone has arrived: ready for the next call
     __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-      int* counter = p.counters + c0;
-      const int arrived = atomicAdd(counter, 1);
-      ctrl->arrived = arrived == (int)(c1 - c0);
-      if (ctrl->arrived) *counter = 0;  // everyone has arrived: ready for the next call
-      __threadfence();
-    }
-    __syncthreads();
-    if (ctrl->arrived) {
-      for (int v = tid; v < kVec; v += W * 32) {
-        const int row = v / (D / 4), ch = (v - row * (D / 4)) * 4;
-        if (rb * RB + row >= rows) continue;
-        float top = kLowest, sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        // the first CTA's part is in its slot 1, the others' in slot 0
-#pragma unroll 4
-        for (long long q = c0; q <= c1; ++q)
-          join<RB, true>(p.partials + (2 * q + (q == c0 ? 1 : 0)) * (RB * (D + 2)), D, row, ch, top, sum, acc);
-        store_row(p, w.s, h, rb * RB + row, ch, D, acc, sum);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (!cut[k].on || !ctrl->arrived[k]) continue;
+    const SeqWork w = seq_work<Sh>(p, cut[k].b, false);
+    const int h = cut[k].seg / w.rbs, rb = cut[k].seg - h * w.rbs, rows = w.s.nq * p.group;
+    const int c0 = (int)owner_of(cut[k].s0, U, G), c1 = (int)owner_of(cut[k].s0 + w.n - 1, U, G);
+    for (int v = tid; v < kVec; v += W * 32) {
+      const int row = v / (D / 4), ch = (v - row * (D / 4)) * 4;
+      if (rb * RB + row >= rows) continue;
+      float top = kLowest, sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      constexpr int kAhead = 8;  // parts loaded together
+      for (int q0 = c0; q0 <= c1; q0 += kAhead) {
+        float2 ml[kAhead];
+        float4 a[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          ml[i] = make_float2(kLowest, 0.f);
+          a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (q0 + i <= c1) {  // the first CTA's part is in its slot 1, the others' in slot 0
+            const float* src = p.partials + (2ll * (q0 + i) + (q0 + i == c0 ? 1 : 0)) * (RB * (D + 2));
+            ml[i] = __ldcg(reinterpret_cast<const float2*>(src + RB * D + 2 * row));
+            a[i] = __ldcg(reinterpret_cast<const float4*>(src + row * D + ch));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) join(ml[i], a[i], top, sum, acc);
       }
+      store_row(p, w.s, h, rb * RB + row, ch, D, acc, sum);
     }
-    __syncthreads();
   }
 }
 
