@@ -95,7 +95,8 @@ struct KvAttnParams {
   int whole_blocks;         // pages hold whole blocks: one copy each
   int max_rows;             // requests with more query rows per key head are left to another launch
   int* counters;            // [grid], zero between calls
-  float* partials;          // [2 grid][rows][D + 2]
+  float* partials;          // [2 grid] parts of segments cut between CTAs, kv_attn_part_floats(D) at most
+  float* firsts;            // [grid][warps] parts that a warp leaves before its stripe is done
   unsigned long long timeout_ns;
 };
 
@@ -106,5 +107,8 @@ cudaError_t launch_kv_read(const KvParams& p, int D, uint16_t* k, uint16_t* v, c
 // nb: blocks of 8 query rows that share a pass over the cache (1 or 2)
 cudaError_t launch_kv_attn(const KvAttnParams& p, int D, int nb, int grid, cudaStream_t stream);
 cudaError_t kv_attn_set_smem_limit();
+// Warps of a CTA at most, and floats of a part in the workspace at most (16 rows).
+constexpr int kKvAttnWarps = 8;
+constexpr int kv_attn_part_floats(int D) { return 16 * (D + 4 + 2); }
 
 }  // namespace w4a16

@@ -28,6 +28,8 @@
 // is finished by whichever of them arrives last, summing all parts in stripe
 // order (so the result does not depend on the order of arrival).  Nothing waits
 // for another CTA.
+#include <type_traits>
+
 #include "kv.cuh"
 
 namespace w4a16 {
@@ -79,7 +81,9 @@ __device__ __forceinline__ void store_row(const KvAttnParams& p, const KvSeq& s,
   *reinterpret_cast<uint2*>(p.out + ((long long)(s.q0 + i) * p.heads + head) * D + ch) = v;
 }
 
-// Pairs of fp32 values: sm_103a multiplies and adds two at a time.
+// Pairs of fp32 values: one instruction for two operations, where both
+// operands are pairs already (at two cycles it costs the pipe what two scalar
+// operations do, and duplicating an operand would cost moves on the busier one).
 struct F2 {
   float x, y;
 };
@@ -120,18 +124,17 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 // W warps; blocks of GB granules; S blocks in a warp's ring.
 template <int D, int NB>
 struct Shape {
-  static constexpr int W = 8, GB = NB == 1 ? 4 : 2, S = 8 / GB * (D == 128 ? 1 : 2);
+  static constexpr int W = 8, GB = NB == 1 ? 4 : 2, S = NB == 1 ? 2 : D == 128 ? 4 : 8;
   static constexpr int kBlock = GB * kGranule;  // tokens
   static constexpr int RB = 8 * NB;             // query rows
   static constexpr int GR = kv_granule_bytes(D);
   static constexpr int BB = GB * GR;            // bytes of a block
   static constexpr int kOStride = D + 4;        // floats of a row of a part in shared memory
   static constexpr int kPart = RB * (kOStride + 2) * 4;  // rows, then (maximum, sum) of each
-  static constexpr int kRing = 2048;           // after the control block
-  static constexpr int kFirst = kRing + W * S * BB;      // the warps' first parts; the last ones go to their rings
-  static constexpr int kSmem = kFirst + W * kPart;
+  static constexpr int kRing = 3072;           // after the control block
+  static constexpr int kSmem = kRing + W * S * BB;
   static_assert(kPart <= S * BB && kPart % 16 == 0, "a part has to fit a warp's ring");
-  static_assert(W <= 16 && W * S <= 64, "the control block holds 16 warps and 64 barriers");
+  static_assert(W <= kKvAttnWarps && W * S <= 64, "the control block's and the workspace's room");
 };
 
 // One request's share of the work: its blocks [lo, lo + n) and the number of
@@ -179,12 +182,17 @@ __device__ __forceinline__ void advance(const KvAttnParams& p, Cursor& c, int by
 
 // What a warp left in shared memory: the end of a segment that began before its
 // stripe (or a middle of one), and the beginning of one that goes on after it.
+struct Segment {
+  KvSeq s;                 // its request's rows and length
+  int h, rb, n;            // key head, group of query rows, blocks
+  long long s0;            // first unit
+};
 struct Parts {
   int idle;                // the warp has no blocks
   int first, last;         // whether there is one
   int first_ends;          // the segment ends in this warp
-  int b[2], seg[2];        // of first and last
-  long long s0[2];         // the segment's first unit
+  int first_last;          // nothing comes after it in the stripe: it is in the ring, else in the workspace
+  Segment seg[2];          // of first and last
 };
 
 // Joins one part's (maximum, sum) and values of four channels.  A part that saw
@@ -217,9 +225,9 @@ struct AttnCtrl {
   int abort;
   int arrived[2];
   SeqWork start_w;
-  Parts parts[16];
+  Parts parts[kKvAttnWarps];
 };
-static_assert(sizeof(AttnCtrl) <= 2048, "control block too large");
+static_assert(sizeof(AttnCtrl) <= 3072, "control block too large");
 
 template <int D, int NB>
 __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const KvAttnParams p) {
@@ -329,38 +337,48 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
   }
 
   if (lane == 0) ctrl->parts[warp].idle = total == 0;
+  const uint64_t policy = policy_evict_first();  // the cache is read once
   const WaitCtx wc{&ctrl->abort, p.kv.status, p.timeout_ns};
 
-  // ---- the ring's producer: lane i < GB finds the place of granule i ----------------
+  // ---- the ring's producer: lane i < GB copies granule i of the next block -------------
   Cursor pc = cur;
-  int issued = 0, next_page = 0;
-  auto look_up = [&]() {  // the page of this lane's granule of the block at pc
-    const int gi = (pc.w.lo + pc.g) * GB + lane;
-    if (lane < GB && gi * kGranule < pc.w.s.len)
-      next_page = p.kv.table[(long long)pc.b * p.kv.max_pages + kv_div_page(p.kv, gi)];
+  const int* table = nullptr;  // the request's pages
+  uint8_t* heads = nullptr;    // the key head's place in page 0
+  int gi = 0, issued = 0, next_page = 0;  // this lane's granule, blocks copied, the granule's page
+  auto enter = [&]() {  // a new segment
+    table = p.kv.table + (long long)pc.b * p.kv.max_pages;
+    heads = p.kv.cache + (pc.seg / pc.w.rbs) * p.kv.head_bytes;
+    gi = (pc.w.lo + pc.g) * GB + lane;
+  };
+  auto look_up = [&]() {
+    if (lane < GB && gi * kGranule < pc.w.s.len) next_page = table[kv_div_page(p.kv, gi)];
   };
   auto issue = [&](int stage) {
-    const int gi = (pc.w.lo + pc.g) * GB + lane;
     const bool inside = lane < GB && gi * kGranule < pc.w.s.len;
-    const bool ok = next_page >= 0 && next_page < p.kv.n_pages;
-    if (inside && !ok) kv_fail(p.kv, kKvSitePage);  // no copy: the block's results are not valid, and reported
-    const int n = __popc(__ballot_sync(0xffffffffu, inside && ok));
+    const bool there = inside && (uint32_t)next_page < (uint32_t)p.kv.n_pages;
+    if (inside && !there) kv_fail(p.kv, kKvSitePage);  // no copy: the block's results are not valid, and reported
+    const int n = __popc(__ballot_sync(0xffffffffu, there));
     const uint32_t bar = smem_addr(&ctrl->full[warp * S + stage]);
     if (lane == 0) mbar_arrive_expect_tx(bar, n * GR);
     __syncwarp();
-    if (inside && ok && (p.whole_blocks ? lane == 0 : true)) {
-      const int h = pc.seg / pc.w.rbs;
+    if (there && (lane == 0 || !p.whole_blocks))
       bulk_g2s(ring + stage * BB + lane * GR,
-               p.kv.cache + next_page * p.kv.page_bytes + h * p.kv.head_bytes +
-                   (long long)(gi - kv_div_page(p.kv, gi) * p.kv.page16) * GR,
-               p.whole_blocks ? n * GR : GR, bar, policy_evict_first());
-    }
+               heads + next_page * p.kv.page_bytes + (gi - kv_div_page(p.kv, gi) * p.kv.page16) * GR,
+               p.whole_blocks ? n * GR : GR, bar, policy);
     if (++issued < total) {
-      advance<Sh>(p, pc, 1);
+      gi += GB;
+      if (++pc.g == pc.w.n) {
+        pc.g -= 1;
+        advance<Sh>(p, pc, 1);
+        enter();
+      }
       look_up();
     }
   };
-  if (total > 0) look_up();
+  if (total > 0) {
+    enter();
+    look_up();
+  }
   while (issued < min(S, total)) issue(issued);
 
   int done = 0;  // blocks of this warp consumed
@@ -430,6 +448,152 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
       for (int t = 0; t < CW * 2; ++t) o[t][nb][0] = o[t][nb][1] = dup(0.f);
     }
 
+    auto block = [&](auto masked, const int t0, const uint8_t* st) {
+      using Masked = decltype(masked);
+
+      // ---- S^T = K Q^T on the codes: low nibbles and high (x 16) apart -----------
+      // x: scores in units of log2; element (q, nb, e) is token g + 8 e of granule
+      // q for rows 2c, 2c + 1
+      F2 x[GB][NB][2], top[NB];
+      float vs[GB][2], vz[GB][2], big = 0.f;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) top[nb] = dup(kLowest);
+      uint32_t k0[GB][CW], k1[GB][CW];
+      F2 sl[GB][NB][2], sh[GB][NB][2];
+#pragma unroll
+      for (int q = 0; q < GB; ++q) {
+        load_words<CW>(st + q * GR + g * (D / 2) + c * (D / 8), k0[q]);
+        load_words<CW>(st + q * GR + (g + 8) * (D / 2) + c * (D / 8), k1[q]);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) sl[q][nb][0] = sl[q][nb][1] = sh[q][nb][0] = sh[q][nb][1] = dup(0.f);
+      }
+      // the granules in turn, so that no product waits for the one before
+#pragma unroll
+      for (int j = 0; j < CW; ++j)
+#pragma unroll
+        for (int q = 0; q < GB; ++q) {
+          const uint32_t a0 = k0[q][j], a1 = k1[q][j], a2 = k0[q][j] >> 8, a3 = k1[q][j] >> 8;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            mma16816(sl[q][nb], a0 & 0x000F000Fu, a1 & 0x000F000Fu, a2 & 0x000F000Fu, a3 & 0x000F000Fu,
+                     qf[nb][4 * j], qf[nb][4 * j + 1]);
+            mma16816(sh[q][nb], a0 & 0x00F000F0u, a1 & 0x00F000F0u, a2 & 0x00F000F0u, a3 & 0x00F000F0u,
+                     qf[nb][4 * j + 2], qf[nb][4 * j + 3]);
+          }
+        }
+#pragma unroll
+      for (int q = 0; q < GB; ++q) {
+        uint32_t pr[2][2];
+        load_words<2>(st + q * GR + 16 * D + g * 8, pr[0]);
+        load_words<2>(st + q * GR + 16 * D + (g + 8) * 8, pr[1]);
+        // scales and offsets of tokens g and g + 8; nothing is taken from slots
+        // that no row sees (they may hold anything)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(&pr[e][0]));
+          const float2 vf = __half22float2(*reinterpret_cast<const __half2*>(&pr[e][1]));
+          float ks = kf.x * (kCodeUnit * p.scale_log2), kz = fmaf(-8.f, kf.x, kf.y);
+          vs[q][e] = vf.x;
+          vz[q][e] = fmaf(-8.f, vf.x, vf.y);
+          const int t = t0 + 16 * q + g + 8 * e;
+          if (Masked::value && (t >= any_hi || t < any_lo)) ks = kz = vs[q][e] = vz[q][e] = 0.f;
+          big = fmaxf(big, vs[q][e]);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const F2 raw = fma2(sh[q][nb][e], dup(0.0625f), sl[q][nb][e]);
+            F2 v = {fmaf(ks, raw.x, kz * qs[nb].x), fmaf(ks, raw.y, kz * qs[nb].y)};
+            if (Masked::value) {
+              if (t >= hi_pos[nb][0] || t < lo_pos[nb][0]) v.x = kNegInf;
+              if (t >= hi_pos[nb][1] || t < lo_pos[nb][1]) v.y = kNegInf;
+            }
+            x[q][nb][e] = v;
+            top[nb].x = fmaxf(top[nb].x, v.x);
+            top[nb].y = fmaxf(top[nb].y, v.y);
+          }
+        }
+      }
+      bool over = big > sref;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) over = over || top[nb].x > m[nb].x + kLazy || top[nb].y > m[nb].y + kLazy;
+      if (__any_sync(0xffffffffu, over)) {
+        // move the references: the rows' maxima and the power of two above the values' scales
+#pragma unroll
+        for (int q = 4; q < 32; q <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, q));
+        float ratio = 1.f;
+        if (big > sref) {  // 2^(exponent + 1); warp-uniform: vs depends on g alone
+          const float up = __uint_as_float(((__float_as_uint(big) >> 23) + 1) << 23);
+          ratio = sref / up;
+          sref = up;
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+          for (int q = 4; q < 32; q <<= 1) {
+            top[nb].x = fmaxf(top[nb].x, __shfl_xor_sync(0xffffffffu, top[nb].x, q));
+            top[nb].y = fmaxf(top[nb].y, __shfl_xor_sync(0xffffffffu, top[nb].y, q));
+          }
+          const F2 nm = {fmaxf(m[nb].x, top[nb].x), fmaxf(m[nb].y, top[nb].y)};
+          const F2 f = {m[nb].x == nm.x ? 1.f : ex2(m[nb].x - nm.x), m[nb].y == nm.y ? 1.f : ex2(m[nb].y - nm.y)};
+          m[nb] = nm;
+          l[nb] = mul2(l[nb], f);
+          pz[nb] = mul2(pz[nb], f);
+          const F2 fo = mul2(f, dup(ratio));
+#pragma unroll
+          for (int t = 0; t < CW * 2; ++t) {
+            o[t][nb][0] = mul2(o[t][nb][0], fo);
+            o[t][nb][1] = mul2(o[t][nb][1], fo);
+          }
+        }
+      }
+      // ---- probabilities, and O^T += V^T P^T --------------------------------------
+      const float rs = 64.f / sref;
+#pragma unroll
+      for (int q = 0; q < GB; ++q) {
+        const uint8_t* sg = st + q * GR;
+        uint32_t v0[CW], v1[CW];
+        load_words<CW>(sg + 8 * D + lane * (D / 8), v0);
+        load_words<CW>(sg + 12 * D + lane * (D / 8), v1);
+        uint32_t ph[NB][2], pl[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const F2 xm = add2(x[q][nb][e], {-m[nb].x, -m[nb].y});
+            const F2 pe = {ex2(xm.x), ex2(xm.y)};
+            l[nb] = add2(l[nb], pe);
+            const float wt = vs[q][e] * rs;
+            F2 y = {pe.x * wt, pe.y * wt};
+            if (!Masked::value) {
+              pz[nb] = {fmaf(pe.x, vz[q][e], pz[nb].x), fmaf(pe.y, vz[q][e], pz[nb].y)};
+            } else {  // a token that is masked for one row alone may have a NaN scale
+              const int t = t0 + 16 * q + g + 8 * e;
+              if (t >= hi_pos[nb][0] || t < lo_pos[nb][0]) y.x = 0.f;
+              else pz[nb].x = fmaf(pe.x, vz[q][e], pz[nb].x);
+              if (t >= hi_pos[nb][1] || t < lo_pos[nb][1]) y.y = 0.f;
+              else pz[nb].y = fmaf(pe.y, vz[q][e], pz[nb].y);
+            }
+            const __half2 hi = __floats2half2_rn(y.x, y.y);
+            const float2 back = __half22float2(hi);
+            ph[nb][e] = transpose8x8(h2_bits(hi));
+            pl[nb][e] = transpose8x8(h2_bits(__floats2half2_rn(y.x - back.x, y.y - back.y)));
+          }
+        // first halves of all tiles, then second halves: no result waits for the one before
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int j = 0; j < CW; ++j) {
+            const uint32_t a0 = v0[j], a1 = v0[j] >> 8, a2 = v1[j], a3 = v1[j] >> 8;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              const uint32_t p0 = half ? pl[nb][0] : ph[nb][0], p1 = half ? pl[nb][1] : ph[nb][1];
+              mma16816(o[2 * j][nb], a0 & 0x000F000Fu, a1 & 0x000F000Fu, a2 & 0x000F000Fu, a3 & 0x000F000Fu, p0, p1);
+              mma16816(o[2 * j + 1][nb], a0 & 0x00F000F0u, a1 & 0x00F000F0u, a2 & 0x00F000F0u, a3 & 0x00F000F0u, p0,
+                       p1);
+            }
+          }
+      }
+    };
+
     for (int i = 0; i < cnt; ++i) {
       const int t0 = (w.lo + cur.g + i) * Sh::kBlock;
       const int stage = done % S;
@@ -438,149 +602,9 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
         ok = false;
         break;
       }
-      if (t0 < any_hi && t0 + Sh::kBlock > any_lo) {
-        const bool full = t0 + Sh::kBlock <= all_hi && t0 >= all_lo;
-
-        // ---- S^T = K Q^T on the codes: low nibbles and high (x 16) apart -----------
-        // x: scores in units of log2; element (q, nb, e) is token g + 8 e of granule
-        // q for rows 2c, 2c + 1
-        F2 x[GB][NB][2], top[NB];
-        float vs[GB][2], vz[GB][2], big = 0.f;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) top[nb] = dup(kLowest);
-        uint32_t k0[GB][CW], k1[GB][CW];
-        F2 sl[GB][NB][2], sh[GB][NB][2];
-#pragma unroll
-        for (int q = 0; q < GB; ++q) {
-          load_words<CW>(st + q * GR + g * (D / 2) + c * (D / 8), k0[q]);
-          load_words<CW>(st + q * GR + (g + 8) * (D / 2) + c * (D / 8), k1[q]);
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) sl[q][nb][0] = sl[q][nb][1] = sh[q][nb][0] = sh[q][nb][1] = dup(0.f);
-        }
-        // the granules in turn, so that no product waits for the one before
-#pragma unroll
-        for (int j = 0; j < CW; ++j)
-#pragma unroll
-          for (int q = 0; q < GB; ++q) {
-            const uint32_t a0 = k0[q][j], a1 = k1[q][j], a2 = k0[q][j] >> 8, a3 = k1[q][j] >> 8;
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              mma16816(sl[q][nb], a0 & 0x000F000Fu, a1 & 0x000F000Fu, a2 & 0x000F000Fu, a3 & 0x000F000Fu,
-                       qf[nb][4 * j], qf[nb][4 * j + 1]);
-              mma16816(sh[q][nb], a0 & 0x00F000F0u, a1 & 0x00F000F0u, a2 & 0x00F000F0u, a3 & 0x00F000F0u,
-                       qf[nb][4 * j + 2], qf[nb][4 * j + 3]);
-            }
-          }
-#pragma unroll
-        for (int q = 0; q < GB; ++q) {
-          uint32_t pr[2][2];
-          load_words<2>(st + q * GR + 16 * D + g * 8, pr[0]);
-          load_words<2>(st + q * GR + 16 * D + (g + 8) * 8, pr[1]);
-          // scales and offsets of tokens g and g + 8; nothing is taken from slots
-          // that no row sees (they may hold anything)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(&pr[e][0]));
-            const float2 vf = __half22float2(*reinterpret_cast<const __half2*>(&pr[e][1]));
-            float ks = kf.x * (kCodeUnit * p.scale_log2), kz = fmaf(-8.f, kf.x, kf.y);
-            vs[q][e] = vf.x;
-            vz[q][e] = fmaf(-8.f, vf.x, vf.y);
-            const int t = t0 + 16 * q + g + 8 * e;
-            if (!full && (t >= any_hi || t < any_lo)) ks = kz = vs[q][e] = vz[q][e] = 0.f;
-            big = fmaxf(big, vs[q][e]);
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              F2 v = fma2(dup(ks), fma2(sh[q][nb][e], dup(0.0625f), sl[q][nb][e]), mul2(dup(kz), qs[nb]));
-              if (!full) {
-                if (t >= hi_pos[nb][0] || t < lo_pos[nb][0]) v.x = kNegInf;
-                if (t >= hi_pos[nb][1] || t < lo_pos[nb][1]) v.y = kNegInf;
-              }
-              x[q][nb][e] = v;
-              top[nb].x = fmaxf(top[nb].x, v.x);
-              top[nb].y = fmaxf(top[nb].y, v.y);
-            }
-          }
-        }
-        bool over = big > sref;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) over = over || top[nb].x > m[nb].x + kLazy || top[nb].y > m[nb].y + kLazy;
-        if (__any_sync(0xffffffffu, over)) {
-          // move the references: the rows' maxima and the power of two above the values' scales
-#pragma unroll
-          for (int q = 4; q < 32; q <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, q));
-          float ratio = 1.f;
-          if (big > sref) {  // 2^(exponent + 1); warp-uniform: vs depends on g alone
-            const float up = __uint_as_float(((__float_as_uint(big) >> 23) + 1) << 23);
-            ratio = sref / up;
-            sref = up;
-          }
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-            for (int q = 4; q < 32; q <<= 1) {
-              top[nb].x = fmaxf(top[nb].x, __shfl_xor_sync(0xffffffffu, top[nb].x, q));
-              top[nb].y = fmaxf(top[nb].y, __shfl_xor_sync(0xffffffffu, top[nb].y, q));
-            }
-            const F2 nm = {fmaxf(m[nb].x, top[nb].x), fmaxf(m[nb].y, top[nb].y)};
-            const F2 f = {m[nb].x == nm.x ? 1.f : ex2(m[nb].x - nm.x), m[nb].y == nm.y ? 1.f : ex2(m[nb].y - nm.y)};
-            m[nb] = nm;
-            l[nb] = mul2(l[nb], f);
-            pz[nb] = mul2(pz[nb], f);
-            const F2 fo = mul2(f, dup(ratio));
-#pragma unroll
-            for (int t = 0; t < CW * 2; ++t) {
-              o[t][nb][0] = mul2(o[t][nb][0], fo);
-              o[t][nb][1] = mul2(o[t][nb][1], fo);
-            }
-          }
-        }
-        // ---- probabilities, and O^T += V^T P^T --------------------------------------
-        const float rs = 64.f / sref;
-#pragma unroll
-        for (int q = 0; q < GB; ++q) {
-          const uint8_t* sg = st + q * GR;
-          uint32_t v0[CW], v1[CW];
-          load_words<CW>(sg + 8 * D + lane * (D / 8), v0);
-          load_words<CW>(sg + 12 * D + lane * (D / 8), v1);
-          uint32_t ph[NB][2], pl[NB][2];
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const F2 xm = add2(x[q][nb][e], {-m[nb].x, -m[nb].y});
-              const F2 pe = {ex2(xm.x), ex2(xm.y)};
-              l[nb] = add2(l[nb], pe);
-              F2 y = mul2(pe, dup(vs[q][e] * rs));
-              if (full) {
-                pz[nb] = fma2(pe, dup(vz[q][e]), pz[nb]);
-              } else {  // a token that is masked for one row alone may have a NaN scale
-                const int t = t0 + 16 * q + g + 8 * e;
-                if (t >= hi_pos[nb][0] || t < lo_pos[nb][0]) y.x = 0.f;
-                else pz[nb].x = fmaf(pe.x, vz[q][e], pz[nb].x);
-                if (t >= hi_pos[nb][1] || t < lo_pos[nb][1]) y.y = 0.f;
-                else pz[nb].y = fmaf(pe.y, vz[q][e], pz[nb].y);
-              }
-              const __half2 hi = __floats2half2_rn(y.x, y.y);
-              const float2 back = __half22float2(hi);
-              ph[nb][e] = transpose8x8(h2_bits(hi));
-              pl[nb][e] = transpose8x8(h2_bits(__floats2half2_rn(y.x - back.x, y.y - back.y)));
-            }
-          // first halves of all tiles, then second halves: no result waits for the one before
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int j = 0; j < CW; ++j) {
-              const uint32_t a0 = v0[j], a1 = v0[j] >> 8, a2 = v1[j], a3 = v1[j] >> 8;
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb) {
-                const uint32_t p0 = half ? pl[nb][0] : ph[nb][0], p1 = half ? pl[nb][1] : ph[nb][1];
-                mma16816(o[2 * j][nb], a0 & 0x000F000Fu, a1 & 0x000F000Fu, a2 & 0x000F000Fu, a3 & 0x000F000Fu, p0, p1);
-                mma16816(o[2 * j + 1][nb], a0 & 0x00F000F0u, a1 & 0x00F000F0u, a2 & 0x00F000F0u, a3 & 0x00F000F0u, p0,
-                         p1);
-              }
-            }
-        }
-      }
+      // one version for blocks that every row sees whole, one with masks
+      if (t0 + Sh::kBlock <= all_hi && t0 >= all_lo) block(std::false_type{}, t0, st);
+      else if (t0 < any_hi && t0 + Sh::kBlock > any_lo) block(std::true_type{}, t0, st);
       __syncwarp();
       ++done;
       if (issued < total) issue(stage);
@@ -591,7 +615,9 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
     const float unit = kCodeUnit * sref * (1.f / 64.f);
     const bool whole = cnt == w.n;
     const bool tail = cur.g != 0;  // a segment that began before: this warp's first part, else its last
-    float* part = reinterpret_cast<float*>(tail ? smem + Sh::kFirst + warp * Sh::kPart : ring_ptr);
+    // a part goes to the ring once the stream is done, else to the workspace
+    float* part = done == total ? reinterpret_cast<float*>(ring_ptr)
+                                : p.firsts + (long long)(blockIdx.x * W + warp) * (Sh::kPart / 4);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -627,12 +653,11 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
       if (tail) {
         q.first = 1;
         q.first_ends = cur.g + cnt == w.n;
+        q.first_last = done == total;
       } else {
         q.last = 1;
       }
-      q.b[tail ? 0 : 1] = cur.b;
-      q.seg[tail ? 0 : 1] = cur.seg;
-      q.s0[tail ? 0 : 1] = from + done - cnt - cur.g;
+      q.seg[tail ? 0 : 1] = {w.s, h, rb, w.n, from + done - cnt - cur.g};
     }
     advance<Sh>(p, cur, cnt);
   }
@@ -642,93 +667,99 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
   __syncthreads();
   if (ctrl->abort) return;
 
-  // ---- segments cut between warps: the parts of consecutive warps --------------------
-  // A run begins with a warp's last part, or (start = -1) with the first part of
-  // the CTA's first warp that has any blocks: a segment that began in an earlier
-  // CTA.  It goes on with the next warps' first parts until the segment ends.
-  constexpr int kVec = RB * D / 4;
-  struct Cut {
-    int on, b, seg;
-    long long s0;
-  } cut[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};  // runs cut between CTAs: one that began before, one that goes on
-  int lead0 = 0;
-  while (lead0 < W - 1 && ctrl->parts[lead0].idle) ++lead0;
-  for (int start = -1; start < W; ++start) {
-    const bool head = start >= 0;  // the segment begins in this CTA
-    const int q0 = head ? start : lead0;
-    const Parts& lead = ctrl->parts[q0];
-    if (head ? !lead.last : !lead.first) continue;
-    const int sb = lead.b[head], sseg = lead.seg[head];
-    int end = q0 + 1;  // one past the last warp of the run
-    bool ends = !head && lead.first_ends;
-    while (!ends && end < W && (ctrl->parts[end].first || ctrl->parts[end].idle)) {
-      ends = ctrl->parts[end].first && ctrl->parts[end].first_ends;
-      ++end;
-    }
-    const SeqWork w = seq_work<Sh>(p, sb, false);
-    const int h = sseg / w.rbs, rb = sseg - h * w.rbs, rows = w.s.nq * p.group;
-    const bool here = head && ends;
-    const int slot = 2 * blockIdx.x + (head ? 1 : 0);
-    float* part = p.partials + (long long)slot * (RB * (D + 2));
-    for (int v = tid; v < kVec; v += W * 32) {
-      const int row = v / (D / 4), ch = (v - row * (D / 4)) * 4;
-      float top = kLowest, sum = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int q = q0; q < end; ++q) {
-        if (ctrl->parts[q].idle) continue;
-        const float* at = reinterpret_cast<const float*>(head && q == q0 ? smem + Sh::kRing + q * (S * BB)
-                                                                         : smem + Sh::kFirst + q * Sh::kPart);
-        join(*reinterpret_cast<const float2*>(at + RB * Sh::kOStride + 2 * row),
-             *reinterpret_cast<const float4*>(at + row * Sh::kOStride + ch), top, sum, acc);
+  // ---- segments cut between warps: runs of parts of consecutive warps ------------------
+  // A run begins with a warp's last part, or with the first part of the CTA's
+  // first warp that has any blocks (a segment that began in an earlier CTA), and
+  // goes on with the next warps' first parts until the segment ends.  Lane 0
+  // looks at the run that began before, lane 1 + q at the one that warp q begins.
+  constexpr int kVec = RB * D / 4;  // a thread joins four channels of one row
+  int run_q0 = 0, run_end = 0, run_ends = 0, run_on = 0;
+  {
+    int q = lane - 1;
+    if (lane == 0)
+      for (q = 0; q < W - 1 && ctrl->parts[q].idle;) ++q;
+    if (q < W) {
+      run_on = lane ? ctrl->parts[q].last : ctrl->parts[q].first;
+      run_ends = lane == 0 && ctrl->parts[q].first_ends;
+      run_q0 = q;
+      for (run_end = q + 1; run_on && !run_ends && run_end < W; ++run_end) {
+        const Parts& next = ctrl->parts[run_end];
+        if (!next.idle && !next.first) break;
+        run_ends = !next.idle && next.first_ends;
       }
-      if (here) {
-        if (rb * RB + row < rows) store_row(p, w.s, h, rb * RB + row, ch, D, acc, sum);
-      } else {
-        __stcg(reinterpret_cast<float4*>(part + row * D + ch), acc);
-        if (ch == 0) __stcg(reinterpret_cast<float2*>(part + RB * D + 2 * row), make_float2(top, sum));
-      }
-    }
-    if (!here) {
-      if (head) cut[1] = {1, sb, sseg, lead.s0[1]};
-      else cut[0] = {1, sb, sseg, lead.s0[0]};
     }
   }
-  if (!cut[0].on && !cut[1].on) return;
+  const uint32_t runs = __ballot_sync(0xffffffffu, run_on);
+  // the (at most two) runs whose segments other CTAs share: that of lane 0, and
+  // the last one if its segment goes on
+  const uint32_t shared = runs & ~__ballot_sync(0xffffffffu, lane != 0 && run_ends);
+  for (int v = tid; v < __popc(runs) * kVec; v += W * 32) {
+    const int lead = (int)__fns(runs, 0, v / kVec + 1);  // the same for the whole warp
+    const int q0 = __shfl_sync(0xffffffffu, run_q0, lead), end = __shfl_sync(0xffffffffu, run_end, lead);
+    const Segment& sg = ctrl->parts[q0].seg[lead != 0];
+    const int row = (v % kVec) / (D / 4), ch = (v % (D / 4)) * 4;
+    float top = kLowest, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int q = q0; q < end; ++q) {
+      if (ctrl->parts[q].idle) continue;
+      const bool in_ring = (lead != 0 && q == q0) || ctrl->parts[q].first_last;
+      const float* at = in_ring ? reinterpret_cast<const float*>(smem + Sh::kRing + q * (S * BB))
+                                : p.firsts + (long long)(blockIdx.x * W + q) * (Sh::kPart / 4);
+      join(*reinterpret_cast<const float2*>(at + RB * Sh::kOStride + 2 * row),
+           *reinterpret_cast<const float4*>(at + row * Sh::kOStride + ch), top, sum, acc);
+    }
+    if ((shared >> lead) & 1u) {
+      float* part = p.partials + (2ll * blockIdx.x + (lead != 0)) * (RB * (D + 2));
+      __stcg(reinterpret_cast<float4*>(part + row * D + ch), acc);
+      if (ch == 0) __stcg(reinterpret_cast<float2*>(part + RB * D + 2 * row), make_float2(top, sum));
+    } else if (sg.rb * RB + row < sg.s.nq * p.group) {
+      store_row(p, sg.s, sg.h, sg.rb * RB + row, ch, D, acc, sum);
+    }
+  }
+  if (shared == 0) return;
 
   // ---- segments cut between CTAs: the last to arrive joins the parts in stripe order ---
+  // k = 0: the one that began before, k = 1: the one that goes on
+  const bool on[2] = {(shared & 1u) != 0, (shared & ~1u) != 0};
+  const int goes_on = 31 - __clz((int)(shared | 1u));
+  const Segment* seg[2] = {&ctrl->parts[__shfl_sync(0xffffffffu, run_q0, 0)].seg[0],
+                           &ctrl->parts[__shfl_sync(0xffffffffu, run_q0, goes_on)].seg[1]};
+  int c0[2] = {0, 0}, c1[2] = {0, 0};  // the CTAs that share it
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (on[k]) {
+      c0[k] = (int)owner_of(seg[k]->s0, U, G);
+      c1[k] = (int)owner_of(seg[k]->s0 + seg[k]->n - 1, U, G);
+    }
   __threadfence();
   __syncthreads();
-  if (tid < 2 && (tid ? cut[1].on : cut[0].on)) {
-    const long long s0 = tid ? cut[1].s0 : cut[0].s0;
-    const int n = seq_work<Sh>(p, tid ? cut[1].b : cut[0].b, false).n;
-    const int c0 = (int)owner_of(s0, U, G), c1 = (int)owner_of(s0 + n - 1, U, G);
-    const int arrived = atomicAdd(p.counters + c0, 1);
-    ctrl->arrived[tid] = arrived == c1 - c0;
-    if (arrived == c1 - c0) p.counters[c0] = 0;  // everyone has arrived: ready for the next call
+  if (tid < 2 && on[tid]) {
+    const int first_cta = tid ? c0[1] : c0[0], last_cta = tid ? c1[1] : c1[0];
+    const int arrived = atomicAdd(p.counters + first_cta, 1);
+    ctrl->arrived[tid] = arrived == last_cta - first_cta;
+    if (arrived == last_cta - first_cta) p.counters[first_cta] = 0;  // all are here: ready for the next call
     __threadfence();
   }
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    if (!cut[k].on || !ctrl->arrived[k]) continue;
-    const SeqWork w = seq_work<Sh>(p, cut[k].b, false);
-    const int h = cut[k].seg / w.rbs, rb = cut[k].seg - h * w.rbs, rows = w.s.nq * p.group;
-    const int c0 = (int)owner_of(cut[k].s0, U, G), c1 = (int)owner_of(cut[k].s0 + w.n - 1, U, G);
+    if (!on[k] || !ctrl->arrived[k]) continue;
+    const Segment sg = *seg[k];
     for (int v = tid; v < kVec; v += W * 32) {
       const int row = v / (D / 4), ch = (v - row * (D / 4)) * 4;
-      if (rb * RB + row >= rows) continue;
+      if (sg.rb * RB + row >= sg.s.nq * p.group) continue;
       float top = kLowest, sum = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       constexpr int kAhead = 8;  // parts loaded together
-      for (int q0 = c0; q0 <= c1; q0 += kAhead) {
+      for (int q0 = c0[k]; q0 <= c1[k]; q0 += kAhead) {
         float2 ml[kAhead];
         float4 a[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
           ml[i] = make_float2(kLowest, 0.f);
           a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (q0 + i <= c1) {  // the first CTA's part is in its slot 1, the others' in slot 0
-            const float* src = p.partials + (2ll * (q0 + i) + (q0 + i == c0 ? 1 : 0)) * (RB * (D + 2));
+          if (q0 + i <= c1[k]) {  // the first CTA's part is in its slot 1, the others' in slot 0
+            const float* src = p.partials + (2ll * (q0 + i) + (q0 + i == c0[k] ? 1 : 0)) * (RB * (D + 2));
             ml[i] = __ldcg(reinterpret_cast<const float2*>(src + RB * D + 2 * row));
             a[i] = __ldcg(reinterpret_cast<const float4*>(src + row * D + ch));
           }
@@ -736,7 +767,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) join(ml[i], a[i], top, sum, acc);
       }
-      store_row(p, w.s, h, rb * RB + row, ch, D, acc, sum);
+      store_row(p, sg.s, sg.h, sg.rb * RB + row, ch, D, acc, sum);
     }
   }
 }

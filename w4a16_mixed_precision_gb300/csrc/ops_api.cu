@@ -114,7 +114,7 @@ marlin_status_t kv_copy(bool append, uint16_t* k, int64_t k_ts, int64_t k_hs, ui
 
 struct AttnPlan {
   int grid, nb;
-  size_t counters_off, partials_off, bytes;
+  size_t counters_off, partials_off, firsts_off, bytes;
 };
 
 AttnPlan attn_plan(int sms, int D, int group, int max_q) {
@@ -123,7 +123,9 @@ AttnPlan attn_plan(int sms, int D, int group, int max_q) {
   a.nb = (long long)group * max_q > 8 ? 2 : 1;
   a.counters_off = 256;
   a.partials_off = round_up(a.counters_off + sizeof(int) * (size_t)sms, 256);
-  a.bytes = a.partials_off + (size_t)2 * sms * 16 * (D + 2) * sizeof(float);  // 16 rows: either nb
+  const size_t part = kv_attn_part_floats(D) * sizeof(float);
+  a.firsts_off = a.partials_off + 2 * sms * part;
+  a.bytes = a.firsts_off + kKvAttnWarps * sms * part;
   return a;
 }
 
@@ -265,6 +267,7 @@ marlin_status_t marlin_kv_attention(const uint16_t* q, int64_t q_token_stride, i
   p.max_rows = 0x7FFFFFFF;
   p.counters = reinterpret_cast<int*>(ws + a.counters_off);
   p.partials = reinterpret_cast<float*>(ws + a.partials_off);
+  p.firsts = reinterpret_cast<float*>(ws + a.firsts_off);
   p.timeout_ns = kTimeoutNs;
   return launch_kv_attn(p, head_dim, a.nb, a.grid, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MARLIN_OK
