@@ -330,14 +330,14 @@ marlin_status_t marlin_sparse_gemm(const uint16_t* X, const void* packed, const 
  */
 
 /*
- * Bytes of device workspace marlin_lora_gemm needs: marlin_workspace_bytes'
- * and the fp32 partial sums of X . A^T.  A buffer sized for M also serves every
- * smaller M with the same K, N, group, r, adapters (or fewer).  r: a multiple
- * of 8 up to 128, else MARLIN_ERR_UNSUPPORTED (pad A and B with zeros).
- * Host-only.  bytes: host pointer, written.
+ * Bytes of device workspace marlin_lora_gemm needs: marlin_workspace_bytes' and
+ * X . A^T of every row.  A buffer sized for M also serves every smaller M with
+ * the same K, N, group, r.  r: a multiple of 8 up to 128, else
+ * MARLIN_ERR_UNSUPPORTED (pad A and B with zeros).  Host-only.  bytes: host
+ * pointer, written.
  */
-marlin_status_t marlin_lora_workspace_bytes(int M, int K, int N, int group, int r, int adapters,
-                                            int device, size_t* bytes);
+marlin_status_t marlin_lora_workspace_bytes(int M, int K, int N, int group, int r, int device,
+                                            size_t* bytes);
 
 /*
  * The product with adapters: three launches on `stream` (X . A^T, marlin_gemm,

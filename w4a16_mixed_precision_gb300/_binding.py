@@ -99,7 +99,7 @@ def open_library(path: str) -> ctypes.CDLL:
             getattr(lib, f).restype = I
         L, F, PSZ = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(SZ)
         kv = [P, I, I, I, I, P, I, P, P, I, I]  # cache .. page_size, page_table, max_pages, lengths, q_start, B, T
-        lib.marlin_lora_workspace_bytes.argtypes = [I] * 7 + [PSZ]
+        lib.marlin_lora_workspace_bytes.argtypes = [I] * 6 + [PSZ]
         lib.marlin_lora_gemm.argtypes = [P] * 8 + [I, I, P, I, I, I, I, P, SZ, P]
         lib.marlin_kv_cache_bytes.argtypes = [I, I, I, I, PSZ]
         lib.marlin_kv_workspace_bytes.argtypes = [I] * 6 + [PSZ]
@@ -206,9 +206,9 @@ def sparse_gemm_raw(x_ptr: int, packed_ptr: int, meta_ptr: int | None, scales_pt
                                      y_ptr, M, K, N, group, ws_ptr, ws_bytes, stream or None)
 
 
-def lora_workspace_bytes(M: int, K: int, N: int, group: int, r: int, adapters: int, device: int = 0) -> int:
+def lora_workspace_bytes(M: int, K: int, N: int, group: int, r: int, device: int = 0) -> int:
     b = ctypes.c_size_t()
-    _check(load().marlin_lora_workspace_bytes(M, K, N, group, r, adapters, device, ctypes.byref(b)),
+    _check(load().marlin_lora_workspace_bytes(M, K, N, group, r, device, ctypes.byref(b)),
            "marlin_lora_workspace_bytes")
     return b.value
 

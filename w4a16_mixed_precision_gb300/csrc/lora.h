@@ -13,18 +13,20 @@ struct LoraParams {
   const float* scaling;    // [adapters]
   const int* index;        // [M]: the row's adapter, negative for none
   uint16_t* y;             // fp16 [M][N], the base product; the adapters' part is added to it
-  float* v;                // fp32 [splits][M][r]: x . A^T, a partial sum per K split
+  uint16_t* v;             // fp16 [M][rp]: scaling * x . A^T of the row, over unit[m]
+  float* unit;             // [M]: a power of two
   int* status;
   int M, K, N, r, adapters;
-  int splits;              // K splits of the first product
-  int passes;              // CTAs that share the adapters of a block of rows
+  int rp;                  // r rounded up to 16
+  int splits;              // CTAs of a cluster, each a part of K (first product)
+  int passes;              // CTAs that share the adapters of a block of rows (first product)
+  int groups;              // the same for the second product
 };
 
 constexpr int kLoraMaxRank = 128;
-constexpr int kLoraMaxSplits = 16;
 
-// K splits and CTAs per block of rows for this problem.
-void lora_plan(int M, int K, int adapters, int sms, int* splits, int* passes);
+// Fills splits, passes and groups.
+void lora_plan(LoraParams* p, int sms);
 cudaError_t launch_lora_down(const LoraParams& p, cudaStream_t stream);
 cudaError_t launch_lora_up(const LoraParams& p, cudaStream_t stream);
 

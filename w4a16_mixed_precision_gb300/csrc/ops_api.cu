@@ -28,23 +28,17 @@ marlin_status_t current_sms(int* sms) {
 // ---- adapters ---------------------------------------------------------------------
 
 struct LoraSizes {
-  size_t gemm, v_off, total;
-  int splits, passes;
+  size_t gemm, v_off, unit_off, total;
 };
 
-marlin_status_t lora_sizes(int M, int K, int N, int group, int r, int adapters, int device, LoraSizes* z) {
-  if (M < 0 || r <= 0 || adapters <= 0) return MARLIN_ERR_INVALID_ARG;
+marlin_status_t lora_sizes(int M, int K, int N, int group, int r, int device, LoraSizes* z) {
+  if (M < 0 || r <= 0) return MARLIN_ERR_INVALID_ARG;
   if (r % 8 != 0 || r > kLoraMaxRank) return MARLIN_ERR_UNSUPPORTED;
-  marlin_status_t s = marlin_workspace_bytes(M, K, N, group, device, &z->gemm);
+  const marlin_status_t s = marlin_workspace_bytes(M, K, N, group, device, &z->gemm);
   if (s != MARLIN_OK) return s;
-  int sms;
-  if ((s = static_cast<marlin_status_t>(device_sms(device, &sms))) != MARLIN_OK) return s;
-  const int m = M > 0 ? M : 1;
-  lora_plan(m, K, adapters, sms, &z->splits, &z->passes);
   z->v_off = round_up(z->gemm, 256);
-  // room for every M' <= M: fewer rows may be split more often along K
-  const size_t rows = (size_t)m * z->splits, small = (size_t)(m < 1024 ? m : 1024) * kLoraMaxSplits;
-  z->total = z->v_off + (rows > small ? rows : small) * (size_t)r * sizeof(float);
+  z->unit_off = z->v_off + round_up((size_t)M * round_up(r, 16) * sizeof(uint16_t), 256);
+  z->total = z->unit_off + (size_t)M * sizeof(float);
   return MARLIN_OK;
 }
 
@@ -133,11 +127,10 @@ AttnPlan attn_plan(int sms, int D, int group, int max_q) {
 
 extern "C" {
 
-marlin_status_t marlin_lora_workspace_bytes(int M, int K, int N, int group, int r, int adapters, int device,
-                                            size_t* bytes) {
+marlin_status_t marlin_lora_workspace_bytes(int M, int K, int N, int group, int r, int device, size_t* bytes) {
   if (!bytes) return MARLIN_ERR_INVALID_ARG;
   LoraSizes z;
-  const marlin_status_t s = lora_sizes(M, K, N, group, r, adapters, device, &z);
+  const marlin_status_t s = lora_sizes(M, K, N, group, r, device, &z);
   if (s == MARLIN_OK) *bytes = z.total;
   return s;
 }
@@ -157,9 +150,11 @@ marlin_status_t marlin_lora_gemm(const uint16_t* X, const void* packed, const ui
   int dev;
   if (cudaGetDevice(&dev) != cudaSuccess) return MARLIN_ERR_CUDA;
   LoraSizes z;
-  marlin_status_t s = lora_sizes(M, K, N, group, r, adapters, dev, &z);
+  marlin_status_t s = lora_sizes(M, K, N, group, r, dev, &z);
   if (s != MARLIN_OK) return s;
-  if (workspace_bytes < z.v_off + (size_t)M * z.splits * r * sizeof(float)) return MARLIN_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < z.total) return MARLIN_ERR_WORKSPACE_TOO_SMALL;
+  int sms;
+  if ((s = static_cast<marlin_status_t>(device_sms(dev, &sms))) != MARLIN_OK) return s;
 
   LoraParams p{};
   p.x = X;
@@ -168,15 +163,15 @@ marlin_status_t marlin_lora_gemm(const uint16_t* X, const void* packed, const ui
   p.scaling = scaling;
   p.index = index;
   p.y = Y;
-  p.v = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + z.v_off);
+  p.v = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + z.v_off);
+  p.unit = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + z.unit_off);
   p.status = static_cast<int*>(workspace);
   p.M = M;
   p.K = K;
   p.N = N;
   p.r = r;
   p.adapters = adapters;
-  p.splits = z.splits;
-  p.passes = z.passes;
+  lora_plan(&p, sms);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (launch_lora_down(p, st) != cudaSuccess) return MARLIN_ERR_CUDA;
   s = marlin_gemm(X, packed, scales, zeros, Y, M, K, N, group, workspace, z.gemm, stream);

@@ -57,14 +57,14 @@ class LoraWorkspace:
     """Device workspace of lora_gemm for up to max_M rows, zeroed once; also a
     workspace for gemm with the same shapes."""
 
-    def __init__(self, max_M: int, K: int, N: int, group: int, r: int, adapters: int = 1 << 20, device=None):
+    def __init__(self, max_M: int, K: int, N: int, group: int, r: int, device=None):
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         if dev.type != "cuda":
             raise ValueError("a workspace lives on a CUDA device")
         if dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
         self.nbytes = _binding.lora_workspace_bytes(max(max_M, 1), K, N, K if group == -1 else group, r + -r % 8,
-                                                    adapters, dev.index)
+                                                    dev.index)
         self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=dev)
 
     @property
