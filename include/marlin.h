@@ -330,18 +330,17 @@ marlin_status_t marlin_sparse_gemm(const uint16_t* X, const void* packed, const 
  */
 
 /*
- * Bytes of device workspace marlin_lora_gemm needs: marlin_workspace_bytes' and
- * X . A^T of every row.  A buffer sized for M also serves every smaller M with
- * the same K, N, group, r.  r: a multiple of 8 up to 128, else
- * MARLIN_ERR_UNSUPPORTED (pad A and B with zeros).  Host-only.  bytes: host
- * pointer, written.
+ * Bytes of device workspace marlin_lora_gemm needs: marlin_workspace_bytes' and,
+ * for many rows, X . A^T of every row.  A buffer sized for M also serves every
+ * smaller M with the same K, N, group, r, and marlin_gemm.  Host-only.  bytes:
+ * host pointer, written.  r as below.
  */
 marlin_status_t marlin_lora_workspace_bytes(int M, int K, int N, int group, int r, int device,
                                             size_t* bytes);
 
 /*
- * The product with adapters: three launches on `stream` (X . A^T, marlin_gemm,
- * the adapters' part added to Y).
+ * The product with adapters: marlin_gemm and the adapters' part, added to Y (one
+ * launch after it; from 128 rows on X . A^T has a launch before it).
  *
  * X, packed, scales, zeros, Y, M, K, N, group  as for marlin_gemm, except that
  *            Y is 16-byte aligned.
@@ -352,8 +351,10 @@ marlin_status_t marlin_lora_workspace_bytes(int M, int K, int N, int group, int 
  *            >= adapters gives the row no adapter and is reported by
  *            marlin_last_device_status as MARLIN_ERR_BOUNDS.  Rows may come in
  *            any order; blocks of 16 or 32 rows that share adapters are fastest.
- * workspace  device, >= marlin_lora_workspace_bytes(...) bytes, 16-byte aligned,
- *            zeroed once; ordering as for marlin_gemm.
+ * r          a multiple of 8 up to 128, else MARLIN_ERR_UNSUPPORTED (pad A and B
+ *            with zeros).
+ * workspace  device, >= marlin_lora_workspace_bytes(...) bytes; else as for
+ *            marlin_gemm.
  * X . A^T is summed in fp32, scaled, and rounded once to fp16 (normalised row by
  * row, so that its range is fp32's) for the product with B; that is summed in
  * fp32 and added to the fp16 base product, so Y is rounded twice.

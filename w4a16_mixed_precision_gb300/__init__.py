@@ -111,9 +111,11 @@ class Workspace:
             raise ValueError("a workspace lives on a CUDA device")
         if dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
-        self.nbytes = _binding.workspace_bytes(max(max_M, 1), K, N, K if group == -1 else group,
-                                               dev.index)
+        self.nbytes = self._bytes(max(max_M, 1), K, N, K if group == -1 else group, dev.index)
         self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=dev)
+
+    def _bytes(self, M: int, K: int, N: int, group: int, device: int) -> int:
+        return _binding.workspace_bytes(M, K, N, group, device)
 
     @property
     def ptr(self) -> int:

@@ -1,24 +1,27 @@
 // lora.cu -- low-rank adapters of many requests beside a shared product:
 //     y[m] += scaling[a] * (x[m] . A[a]^T) . B[a]^T,   a = index[m] (none if negative),
-// A[a] r x K and B[a] N x r in fp16.  Two kernels: down (v = scaling x . A^T) and
-// up (y += v . B^T).
+// A[a] r x K and B[a] N x r in fp16.  Below 128 rows one kernel after the product,
+// v = scaling x . A^T staying in shared memory between its two halves; from 128
+// rows on two, so that the second can take 128 rows at a time.
 //
 // Bound: for few rows reading the adapters in use, r (K + N) fp16 each; for
 // many rows reading x, and reading and writing y.
-//   * Rows are taken in blocks of 16 or 32.  A block makes one pass for each
-//     different adapter among its rows (one, for the rows of a prompt), with the
-//     other rows' operand zeroed, so any order of rows is right and runs of
-//     equal adapters are fast.  Which rows share an adapter is found in the
-//     kernel by a vote; for small batches the passes of a block go to
-//     different CTAs.
+//   * Rows are taken in blocks.  A block makes one pass for each different adapter
+//     among its rows (one, for the rows of a prompt), with the other rows masked,
+//     so any order of rows is right and runs of equal adapters are fast.  Which
+//     rows share an adapter is found in the kernel by votes; for small batches
+//     the passes of a block go to different clusters.
 //   * mma.sync with the rows as the 16-row operand.  The k order is permuted
 //     alike in both operands so that every lane loads 16 consecutive bytes.
-//   * down splits K over the warps of a CTA and the CTAs of a cluster, whose sums
-//     meet in the first CTA's shared memory in a fixed order: no partial sums in
-//     global memory and no second reduction.
-//   * v is scaled, normalised by a power of two per row (so that no magnitude
-//     of x leaves fp16's range) and rounded to fp16 for the second product: one
-//     rounding of 2^-12 per term of a sum that is itself an addition to y.
+//   * First product: K is split over the warps of a CTA and the CTAs of a
+//     cluster; all parts are summed through distributed shared memory, in the
+//     same order.  Second product, few rows: the cluster's warps split the N
+//     columns, with the operands of the next four groups of columns in flight.
+//     Many rows: a warp keeps its operand columns in registers and passes over
+//     the block's rows.
+//   * v is normalised by a power of two per row (so that no magnitude of x leaves
+//     fp16's range) and rounded to fp16 for the second product: one rounding of
+//     2^-12 per term of a sum that is itself an addition to y.
 #include "lora.h"
 
 #include <cuda_fp16.h>
@@ -30,8 +33,7 @@ namespace w4a16 {
 
 namespace {
 
-constexpr int kDownWarps = 8;
-constexpr int kUpWarps = 4;
+constexpr int kWarps = 8;
 constexpr int kLoraSite = 104;  // the word after the status word: an adapter index out of range
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -67,8 +69,20 @@ __device__ __forceinline__ Block block_adapters(const LoraParams& p, int row0, i
   return k;
 }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
+// y (eight columns of a row, loaded before) + u * acc, rounded, to its place.
+// e: the row of the tile's pair (g or g + 8).
+__device__ __forceinline__ void add_row(uint16_t* at, uint4 y, const float (&acc)[4][4], int e, float u) {
+  uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&yw[t]));
+    const __half2 h = __floats2half2_rn(fmaf(acc[t][2 * e], u, f.x), fmaf(acc[t][2 * e + 1], u, f.y));
+    yw[t] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(at) = y;
 }
 
 // The fp32 value at this CTA-local shared address in CTA `rank` of the cluster.
@@ -82,228 +96,324 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-// v and unit of the rows whose pass is one of this cluster's.  MT: 16-row tiles
-// per block; NT: 8-rank tiles (r <= 8 NT).  CTA rank in the cluster: the part of K.
-template <int MT, int NT>
-__global__ void __launch_bounds__(kDownWarps * 32) lora_down_kernel(const LoraParams p) {
-  constexpr int kRows = 16 * MT, kRanks = 8 * NT, kAcc = MT * NT * 4;
+// MT: 16-row tiles per block; NT: 8-rank tiles (r <= 8 NT).  Grid: blocks of rows;
+// CTAs of the cluster (parts of K, then of N); clusters that share the passes.
+// kBoth: both products (MT = 1); else v and unit go to the workspace.
+template <int MT, int NT, bool kBoth>
+__global__ void __launch_bounds__(kWarps * 32, NT <= 8 ? 2 : 1) lora_kernel(const LoraParams p) {
+  constexpr int kRows = 16 * MT, kRanks = 8 * NT, kRp = (kRanks + 15) / 16 * 16, kAcc = MT * NT * 4;
   // half of the warps leave their sums to the other half, three times; then the CTA's sum
-  __shared__ float red[kDownWarps / 2][kAcc][32];
+  __shared__ float red[kWarps / 2][kAcc][32];
   __shared__ float total[kRows][kRanks + 1];
+  __shared__ __half v[kRows][kRp + 8];
+  __shared__ float unit[kRows];
   if (threadIdx.x == 0) griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int row0 = blockIdx.x * kRows;
+  const int row0 = blockIdx.x * kRows, rank = blockIdx.y;
   const Block k = block_adapters(p, row0, kRows);
   const int count = __popc(k.leaders);
   if ((int)blockIdx.z >= count) return;  // alike in all CTAs of the cluster
+  // this cluster's passes: lane i holds the adapter of the i-th and its rows
+  const int passes = (count - (int)blockIdx.z + p.passes - 1) / p.passes;
+  int pass_ad = 0;
+  uint32_t pass_rows = 0;
+  {
+    uint32_t left = k.leaders;
+    for (int q = 0; q < count; ++q, left &= left - 1) {
+      const int ad = __shfl_sync(0xffffffffu, k.mine, __ffs(left) - 1);
+      const uint32_t rows = __ballot_sync(0xffffffffu, k.mine == ad);
+      if (q % p.passes == (int)blockIdx.z && q / p.passes == lane) {
+        pass_ad = ad;
+        pass_rows = rows;
+      }
+    }
+  }
+  const bool row_mine = k.pass >= 0 && k.pass % p.passes == (int)blockIdx.z;  // this lane's row
+  const uint32_t rows_mine = __ballot_sync(0xffffffffu, row_mine);
 
-  // this warp's 32-wide K steps
-  const int steps = p.K / 32, parts = p.splits * kDownWarps, part = blockIdx.y * kDownWarps + warp;
-  const int s0 = steps * part / parts, s1 = steps * (part + 1) / parts;
-
-  float acc[MT][NT][4];
+  // ---- x . A^T: this warp's 32-wide K steps --------------------------------------------
+  {
+    const int steps = p.K / 32, parts = p.splits * kWarps, part = rank * kWarps + warp;
+    const int s0 = steps * part / parts, s1 = steps * (part + 1) / parts;
+    float acc[MT][NT][4];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-
-  uint32_t left = k.leaders;
-  for (int pass = 0; pass < count; ++pass, left &= left - 1) {
-    if (pass % p.passes != (int)blockIdx.z) continue;
-    const int ad = __shfl_sync(0xffffffffu, k.mine, __ffs(left) - 1);
-    const uint32_t rows = __ballot_sync(0xffffffffu, k.mine == ad);
-    const uint16_t* a = p.a + (long long)ad * p.r * p.K + c * 8;
-    const uint16_t* x = p.x + (long long)row0 * p.K + c * 8;
-    constexpr int kTogether = 2 * MT + NT <= 4 ? 4 : 2 * MT + NT <= 8 ? 2 : 1;  // steps whose loads go out together
-#pragma unroll kTogether
-    for (int s = s0; s < s1; ++s) {
-      uint4 xr[MT][2], ar[NT];
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        ar[j] = j * 8 + g < p.r ? __ldg(reinterpret_cast<const uint4*>(a + (long long)(j * 8 + g) * p.K + s * 32))
-                                : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+    for (int q = 0; q < passes; ++q) {
+      const int ad = __shfl_sync(0xffffffffu, pass_ad, q);
+      const uint32_t rows = __shfl_sync(0xffffffffu, pass_rows, q);
+      const uint16_t* a = p.a + (long long)ad * p.r * p.K + c * 8;
+      const uint16_t* x = p.x + (long long)row0 * p.K + c * 8;
+      constexpr int kTogether = 2 * MT + NT <= 4 ? 4 : 2 * MT + NT <= 8 ? 2 : 1;  // steps whose loads go out together
+#pragma unroll kTogether
+      for (int s = s0; s < s1; ++s) {
+        uint4 xr[MT][2], ar[NT];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int row = 16 * i + 8 * e + g;
-          xr[i][e] = (rows >> row) & 1u ? *reinterpret_cast<const uint4*>(x + (long long)row * p.K + s * 32)
-                                        : make_uint4(0u, 0u, 0u, 0u);
-        }
+        for (int j = 0; j < NT; ++j)
+          ar[j] = j * 8 + g < p.r ? __ldg(reinterpret_cast<const uint4*>(a + (long long)(j * 8 + g) * p.K + s * 32))
+                                  : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          mma16816(acc[i][j], xr[i][0].x, xr[i][1].x, xr[i][0].y, xr[i][1].y, ar[j].x, ar[j].y);
-          mma16816(acc[i][j], xr[i][0].z, xr[i][1].z, xr[i][0].w, xr[i][1].w, ar[j].z, ar[j].w);
-        }
+          for (int e = 0; e < 2; ++e) {
+            const int row = 16 * i + 8 * e + g;
+            xr[i][e] = (rows >> row) & 1u ? *reinterpret_cast<const uint4*>(x + (long long)row * p.K + s * 32)
+                                          : make_uint4(0u, 0u, 0u, 0u);
+          }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            mma16816(acc[i][j], xr[i][0].x, xr[i][1].x, xr[i][0].y, xr[i][1].y, ar[j].x, ar[j].y);
+            mma16816(acc[i][j], xr[i][0].z, xr[i][1].z, xr[i][0].w, xr[i][1].w, ar[j].z, ar[j].w);
+          }
+      }
+    }
+    // the sum over the warps, in a fixed order
+#pragma unroll
+    for (int half = kWarps / 2; half >= 1; half >>= 1) {
+      if (warp >= half && warp < 2 * half) {
+#pragma unroll
+        for (int t = 0; t < kAcc; ++t) red[warp - half][t][lane] = acc[t / (NT * 4)][t / 4 % NT][t % 4];
+      }
+      __syncthreads();
+      if (warp < half) {
+#pragma unroll
+        for (int t = 0; t < kAcc; ++t) acc[t / (NT * 4)][t / 4 % NT][t % 4] += red[warp][t][lane];
+      }
+      __syncthreads();
+    }
+    if (warp == 0) {
+#pragma unroll
+      for (int t = 0; t < kAcc; ++t) {
+        const int i = t / (NT * 4), j = t / 4 % NT, e = t % 4;
+        total[16 * i + g + 8 * (e >> 1)][8 * j + 2 * c + (e & 1)] = acc[i][j][e];
+      }
     }
   }
-  // ---- the sum over the warps, then over the cluster's CTAs, each in order -------------
-#pragma unroll
-  for (int half = kDownWarps / 2; half >= 1; half >>= 1) {
-    if (warp >= half && warp < 2 * half) {
-#pragma unroll
-      for (int t = 0; t < kAcc; ++t) red[warp - half][t][lane] = acc[t / (NT * 4)][t / 4 % NT][t % 4];
-    }
+  if (p.splits > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
     __syncthreads();
-    if (warp < half) {
-#pragma unroll
-      for (int t = 0; t < kAcc; ++t) acc[t / (NT * 4)][t / 4 % NT][t % 4] += red[warp][t][lane];
-    }
-    __syncthreads();
   }
-  if (warp == 0) {
+  // ---- v: the sum over the cluster, scaled, normalised, fp16 (every CTA for itself, or
+  // each a share of the rows for the workspace) --------------------------------------------
+  const int by = kBoth ? kWarps : kWarps * p.splits;
+  for (int row = kBoth ? warp : rank * kWarps + warp; row < kRows; row += by) {
+    const int ad = __shfl_sync(0xffffffffu, k.mine, row);
+    const bool on = (rows_mine >> row) & 1u;
+    const float scaling = on ? p.scaling[ad] : 0.f;
+    float s[(kRp + 31) / 32], top = 0.f;
 #pragma unroll
-    for (int t = 0; t < kAcc; ++t) {
-      const int i = t / (NT * 4), j = t / 4 % NT, e = t % 4;
-      total[16 * i + g + 8 * (e >> 1)][8 * j + 2 * c + (e & 1)] = acc[i][j][e];
-    }
-  }
-  if (p.splits > 1) cluster_sync();
-  else __syncthreads();
-  if (blockIdx.y == 0) {
-    for (int row = warp; row < kRows; row += kDownWarps) {
-      const int pass = __shfl_sync(0xffffffffu, k.pass, row), ad = __shfl_sync(0xffffffffu, k.mine, row);
-      if (pass < 0 || pass % p.passes != (int)blockIdx.z) continue;
-      const float scaling = p.scaling[ad];
-      float s[(kRanks + 31) / 32], top = 0.f;
-#pragma unroll
-      for (int i = 0; i < (kRanks + 31) / 32; ++i) {
-        const int j = 32 * i + lane;
-        s[i] = 0.f;
-        if (j < p.r) {
+    for (int i = 0; i < (kRp + 31) / 32; ++i) {
+      const int j = 32 * i + lane;
+      s[i] = 0.f;
+      if (on && j < p.r) {
+        if (p.splits == 1) {
           s[i] = total[row][j];
-          for (int q = 1; q < p.splits; ++q) s[i] += ld_cluster(smem_addr(&total[row][j]), (uint32_t)q);
-          s[i] *= scaling;
+        } else {
+          float part[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) part[q] = q < p.splits ? ld_cluster(smem_addr(&total[row][j]), (uint32_t)q) : 0.f;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) s[i] += part[q];
         }
-        top = fmaxf(top, fabsf(s[i]));
+        s[i] *= scaling;
       }
-#pragma unroll
-      for (int q = 1; q < 32; q <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, q));
-      // 2^exponent of the row's largest magnitude
-      const float u = top > 1e-30f ? __uint_as_float(__float_as_uint(top) & 0x7F800000u) : 1.f;
-#pragma unroll
-      for (int i = 0; i < (kRanks + 31) / 32; ++i) {
-        const int j = 32 * i + lane;
-        if (j < p.rp) p.v[(long long)(row0 + row) * p.rp + j] = __half_as_ushort(__float2half_rn(s[i] / u));
-      }
-      if (lane == 0) p.unit[row0 + row] = u;
+      top = fmaxf(top, fabsf(s[i]));
     }
+#pragma unroll
+    for (int q = 1; q < 32; q <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, q));
+    // 2^exponent of the row's largest magnitude
+    const float u = top > 1e-30f ? __uint_as_float(__float_as_uint(top) & 0x7F800000u) : 1.f;
+#pragma unroll
+    for (int i = 0; i < (kRp + 31) / 32; ++i)
+      if (kBoth) {
+        if (32 * i + lane < kRp) v[row][32 * i + lane] = __float2half_rn(s[i] / u);
+      } else if (on && 32 * i + lane < p.rp) {
+        p.v[(long long)(row0 + row) * p.rp + 32 * i + lane] = __half_as_ushort(__float2half_rn(s[i] / u));
+      }
+    if (lane == 0 && kBoth) unit[row] = u;
+    if (lane == 0 && !kBoth && on) p.unit[row0 + row] = u;
   }
-  if (p.splits > 1) cluster_sync();  // the sums stay until they are read
-}
+  if (p.splits > 1) cluster_arrive();  // this CTA has read the others' sums
+  if constexpr (!kBoth) {
+    if (p.splits > 1) cluster_wait();
+    return;
+  }
+  __syncthreads();
 
-// y += v . B^T for the rows whose pass is one of this CTA's; every warp takes 32
-// columns of the CTA's 128.
-template <int MT>
-__global__ void __launch_bounds__(kUpWarps * 32) lora_up_kernel(const LoraParams p) {
-  if (threadIdx.x == 0) griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int row0 = blockIdx.x * (16 * MT), n0 = blockIdx.y * (kUpWarps * 32) + warp * 32;
-  griddep_wait();
-  const Block k = block_adapters(p, row0, 16 * MT);
-  const int count = __popc(k.leaders);
-  if ((int)blockIdx.z >= count) return;
-
-  // this lane's pieces of y: rows g and g + 8 of each tile, columns 8c .. 8c + 7
-  uint4 y[MT][2];
-  float unit[MT][2];
-  bool mine[MT][2];
+  // ---- y += v . B^T: this warp's groups of 32 columns ------------------------------------
+  if constexpr (kBoth) {
+    constexpr int kAhead = 4;  // (group, pass, step) triples whose loads are in flight
+    const int groups = p.N / 32, parts = p.splits * kWarps, part = rank * kWarps + warp;
+    const int n_first = groups * part / parts, n_last = groups * (part + 1) / parts;
+    const int steps = (p.r + 15) / 16;
+    // operand column g of tile t is output column 8 (g / 2) + 2 t + g % 2 of the
+    // group's 32, so that a lane's results are 8 consecutive columns of y
+    const uint16_t* b = p.b + (long long)(8 * (g >> 1) + (g & 1)) * p.r + 4 * c;
+    uint16_t* y0 = p.y + (long long)row0 * p.N + 8 * c;
+    uint2 br[kAhead][4];
+    uint4 y[kAhead][2];  // with a group's last triple: its rows g and g + 8
+    int load_n = n_first, load_pass = 0, load_step = 0;
+    auto load = [&](uint2(&bq)[4], uint4(&yq)[2]) {
+      if (load_n >= n_last) return;
+      const int ad = __shfl_sync(0xffffffffu, pass_ad, load_pass);
+      const bool in = 16 * load_step + 4 * c < p.r;
+      const uint16_t* src = b + ((long long)ad * p.N + 32 * load_n) * p.r + 16 * load_step;
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+      for (int t = 0; t < 4; ++t)
+        bq[t] = in ? __ldg(reinterpret_cast<const uint2*>(src + 2 * t * p.r)) : make_uint2(0u, 0u);
+      if (++load_step < steps) return;
+      load_step = 0;
+      if (++load_pass < passes) return;
+      load_pass = 0;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int row = 16 * i + 8 * e + g;
-      const int pass = __shfl_sync(0xffffffffu, k.pass, row);
-      mine[i][e] = pass >= 0 && pass % p.groups == (int)blockIdx.z;
-      y[i][e] = make_uint4(0u, 0u, 0u, 0u);
-      unit[i][e] = 0.f;
-      if (mine[i][e]) {
-        y[i][e] = *reinterpret_cast<const uint4*>(p.y + (long long)(row0 + row) * p.N + n0 + 8 * c);
-        unit[i][e] = p.unit[row0 + row];
-      }
-    }
-
-  float acc[MT][4][4];
+      for (int e = 0; e < 2; ++e)
+        if ((rows_mine >> (8 * e + g)) & 1u)
+          yq[e] = *reinterpret_cast<const uint4*>(y0 + (long long)(8 * e + g) * p.N + 32 * load_n);
+      ++load_n;
+    };
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+    for (int q = 0; q < kAhead; ++q) load(br[q], y[q]);
+    int n = n_first, pass = 0, step = 0;
+    float acc[4][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][t][e] = 0.f;
-  // operand column g of tile t is output column 8 (g / 2) + 2 t + g % 2 of the
-  // warp's 32, so that a lane's results are 8 consecutive columns of y
-  const uint16_t* b0 = p.b + (long long)(n0 + 8 * (g >> 1) + (g & 1)) * p.r + 4 * c;
-  const int steps = p.rp / 16;
-  // (pass, step) pairs, several at a time so that their loads are in flight together
-  int pass = blockIdx.z, step = 0;
-  uint32_t left = k.leaders;
-  for (int q = 0; q < pass; ++q) left &= left - 1;
-  constexpr int kAhead = 4;
-  while (pass < count) {
-    uint2 br[kAhead][4], v[kAhead][MT][2];
+      for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+    while (n < n_last) {
 #pragma unroll
-    for (int q = 0; q < kAhead; ++q) {
-      const bool on = pass < count;
-      const int ad = __shfl_sync(0xffffffffu, k.mine, on ? __ffs(left) - 1 : 0);
-      const uint32_t rows = on ? __ballot_sync(0xffffffffu, k.mine == ad) : 0u;
-      const bool in = on && 16 * step + 4 * c < p.r;
+      for (int q = 0; q < kAhead; ++q) {
+        if (n < n_last) {  // uniform
+          const uint32_t rows = __shfl_sync(0xffffffffu, pass_rows, pass);
+          uint2 v0 = make_uint2(0u, 0u), v1 = v0;
+          if ((rows >> g) & 1u) v0 = *reinterpret_cast<const uint2*>(&v[g][16 * step + 4 * c]);
+          if ((rows >> (g + 8)) & 1u) v1 = *reinterpret_cast<const uint2*>(&v[g + 8][16 * step + 4 * c]);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) mma16816(acc[t], v0.x, v1.x, v0.y, v1.y, br[q][t].x, br[q][t].y);
+          if (++step == steps) {
+            step = 0;
+            if (++pass == passes) {
+              pass = 0;
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if ((rows_mine >> (8 * e + g)) & 1u)
+                  add_row(y0 + (long long)(8 * e + g) * p.N + 32 * n, y[q][e], acc, e, unit[8 * e + g]);
+#pragma unroll
+              for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+              ++n;
+            }
+          }
+          load(br[q], y[q]);
+        }
+      }
+    }
+  }
+  if (p.splits > 1) cluster_wait();  // nobody reads this CTA's shared memory any more
+}
+
+// y += v . B^T for blocks of 128 rows: a warp keeps 32 columns of B in registers
+// (a step of 16 ranks at a time beyond 64) and passes over the rows.  ST: steps
+// of 16 ranks (r <= 16 ST).
+template <int ST>
+__global__ void __launch_bounds__(kWarps * 32, ST <= 4 ? 2 : 1) lora_up_kernel(const LoraParams p) {
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int row0 = blockIdx.x * 128, n0 = (blockIdx.y * kWarps + warp) * 32;
+  if (n0 >= p.N) return;
+  int mine[4];  // the adapters of rows lane, lane + 32, ...
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = row0 + 32 * i + lane;
+    const int ad = row < p.M ? p.index[row] : -1;
+    mine[i] = ad < 0 || ad >= p.adapters ? -1 : ad;  // out of range: reported by the first kernel
+  }
+  const uint16_t* b = p.b + ((long long)n0 + 8 * (g >> 1) + (g & 1)) * p.r + 4 * c;
+  while (true) {
+    // the next adapter, and its rows
+    int ad = -1;
+    uint32_t rows[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t left = __ballot_sync(0xffffffffu, mine[i] >= 0);
+      if (ad < 0 && left) ad = __shfl_sync(0xffffffffu, mine[i], __ffs(left) - 1);
+    }
+    if (ad < 0) break;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      rows[i] = __ballot_sync(0xffffffffu, mine[i] == ad);
+      if (mine[i] == ad) mine[i] = -1;
+    }
+    uint2 br[ST][4];
+#pragma unroll
+    for (int s = 0; s < ST; ++s)
 #pragma unroll
       for (int t = 0; t < 4; ++t)
-        br[q][t] = in ? __ldg(reinterpret_cast<const uint2*>(b0 + ((long long)ad * p.N + 2 * t) * p.r + 16 * step))
-                      : make_uint2(0u, 0u);
+        br[s][t] = 16 * s + 4 * c < p.r
+                       ? __ldg(reinterpret_cast<const uint2*>(b + ((long long)ad * p.N + 2 * t) * p.r + 16 * s))
+                       : make_uint2(0u, 0u);
+    // tiles of 16 rows, kTogether at a time with their loads in flight
+    constexpr int kTogether = ST <= 2 ? 4 : 2;
+#pragma unroll 1
+    for (int i0 = 0; i0 < 8; i0 += kTogether) {
+      uint4 y[kTogether][2];
+      uint2 v[kTogether][ST][2];
+      float u[kTogether][2];
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int q = 0; q < kTogether; ++q)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int row = 16 * i + 8 * e + g;
-          v[q][i][e] = make_uint2(0u, 0u);
-          if ((rows >> row) & 1u)
-            v[q][i][e] = *reinterpret_cast<const uint2*>(p.v + (long long)(row0 + row) * p.rp + 16 * step + 4 * c);
-        }
-      if (on && ++step == steps) {
-        step = 0;
-        for (int d = 0; d < p.groups; ++d) {
-          ++pass;
-          left &= left - 1;
-        }
-      }
-    }
+          const int tile = i0 + q;
+          const uint32_t word = tile < 2 ? rows[0] : tile < 4 ? rows[1] : tile < 6 ? rows[2] : rows[3];
+          const bool on = (word >> (16 * (tile & 1) + 8 * e + g)) & 1u;
+          const long long row = row0 + 16 * tile + 8 * e + g;
+          u[q][e] = 0.f;  // 0 marks a row that is not this adapter's
 #pragma unroll
-    for (int q = 0; q < kAhead; ++q)
+          for (int s = 0; s < ST; ++s) v[q][s][e] = make_uint2(0u, 0u);
+          if (on) {
+            y[q][e] = *reinterpret_cast<const uint4*>(p.y + row * p.N + n0 + 8 * c);
+            u[q][e] = p.unit[row];
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+            for (int s = 0; s < ST; ++s)
+              if (16 * s < p.rp) v[q][s][e] = *reinterpret_cast<const uint2*>(p.v + row * p.rp + 16 * s + 4 * c);
+          }
+        }
+#pragma unroll
+      for (int q = 0; q < kTogether; ++q) {
+        float acc[4][4];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-          mma16816(acc[i][t], v[q][i][0].x, v[q][i][1].x, v[q][i][0].y, v[q][i][1].y, br[q][t].x, br[q][t].y);
-  }
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+          for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (!mine[i][e]) continue;
-      uint32_t* yw = reinterpret_cast<uint32_t*>(&y[i][e]);
+        for (int s = 0; s < ST; ++s)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&yw[t]));
-        const __half2 h = __floats2half2_rn(fmaf(acc[i][t][2 * e], unit[i][e], f.x),
-                                            fmaf(acc[i][t][2 * e + 1], unit[i][e], f.y));
-        yw[t] = *reinterpret_cast<const uint32_t*>(&h);
+          for (int t = 0; t < 4; ++t)
+            mma16816(acc[t], v[q][s][0].x, v[q][s][1].x, v[q][s][0].y, v[q][s][1].y, br[s][t].x, br[s][t].y);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (u[q][e] != 0.f)
+            add_row(p.y + (long long)(row0 + 16 * (i0 + q) + 8 * e + g) * p.N + n0 + 8 * c, y[q][e], acc, e, u[q][e]);
       }
-      *reinterpret_cast<uint4*>(p.y + (long long)(row0 + 16 * i + 8 * e + g) * p.N + n0 + 8 * c) = y[i][e];
     }
+  }
 }
 
 template <typename F>
-cudaError_t launch(F kernel, dim3 grid, int threads, int cluster, const LoraParams& p, cudaStream_t stream) {
+cudaError_t launch(F kernel, dim3 grid, int cluster, const LoraParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
+  cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -316,44 +426,39 @@ cudaError_t launch(F kernel, dim3 grid, int threads, int cluster, const LoraPara
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// Blocks of 32 rows from 128 rows on: enough blocks to fill the card, and each
-// adapter operand is used for twice as many rows (where the registers hold the
-// sums of 32 rows, in the first product).
-int row_tiles(int M) { return M >= 128 ? 2 : 1; }
-int down_tiles(int M, int r) { return r <= 64 ? row_tiles(M) : 1; }
-
 }  // namespace
 
-void lora_plan(LoraParams* p, int sms) {
-  const int rows = 16 * down_tiles(p->M, p->r), blocks = (p->M + rows - 1) / rows;
-  int most = p->M < rows ? p->M : rows;  // different adapters in a block
-  if (p->adapters < most) most = p->adapters;
-  p->rp = (p->r + 15) / 16 * 16;
-  p->passes = p->M >= 128 ? 1 : most;
-  p->groups = p->M >= 128 ? 1 : (most + 3) / 4;
-  // clusters of up to 8 CTAs, while there are few CTAs and a step for every warp
-  int s = 1;
-  while (s < 8 && 2 * s * blocks * p->passes <= 4 * sms && p->K / 32 >= 2 * s * kDownWarps) s *= 2;
-  p->splits = s;
-}
+// From 128 rows on the first product is before marlin_gemm in the stream (its
+// launch and tail overlap the product's start) and only the second after it.
+bool lora_two_kernels(int M) { return M >= 128; }
 
-cudaError_t launch_lora_down(const LoraParams& p, cudaStream_t stream) {
+cudaError_t launch_lora(LoraParams p, int half, int sms, cudaStream_t stream) {
   const int nt = p.r <= 8 ? 1 : p.r <= 16 ? 2 : p.r <= 32 ? 4 : p.r <= 64 ? 8 : 16;
-  const int mt = down_tiles(p.M, p.r);
-  const dim3 grid((p.M + 16 * mt - 1) / (16 * mt), p.splits, p.passes);
-#define W4A16_DOWN(MT, NT) \
-  if (mt == MT && nt == NT) return launch(lora_down_kernel<MT, NT>, grid, kDownWarps * 32, p.splits, p, stream);
-  W4A16_DOWN(1, 1) W4A16_DOWN(1, 2) W4A16_DOWN(1, 4) W4A16_DOWN(1, 8) W4A16_DOWN(1, 16)
-  W4A16_DOWN(2, 1) W4A16_DOWN(2, 2) W4A16_DOWN(2, 4) W4A16_DOWN(2, 8)
-#undef W4A16_DOWN
+  const bool both = !lora_two_kernels(p.M);
+  if (!both && half == 1) {
+    const dim3 grid((p.M + 127) / 128, (p.N / 32 + kWarps - 1) / kWarps);
+    return p.r <= 16   ? launch(lora_up_kernel<1>, grid, 1, p, stream)
+           : p.r <= 32 ? launch(lora_up_kernel<2>, grid, 1, p, stream)
+           : p.r <= 64 ? launch(lora_up_kernel<4>, grid, 1, p, stream)
+                       : launch(lora_up_kernel<8>, grid, 1, p, stream);
+  }
+  const int mt = both || p.r > 64 ? 1 : 2;  // 32 rows where the registers hold their sums
+  const int blocks = (p.M + 16 * mt - 1) / (16 * mt);
+  int most = p.M < 16 ? p.M : 16;  // different adapters in a block
+  if (p.adapters < most) most = p.adapters;
+  p.passes = both ? most : 1;
+  // clusters of up to 8 CTAs, while there is room on the card and a step for every warp
+  p.splits = 1;
+  while (p.splits < 8 && 2 * p.splits * blocks * p.passes <= 2 * sms && p.K / 32 >= 2 * p.splits * kWarps)
+    p.splits *= 2;
+  const dim3 grid(blocks, p.splits, p.passes);
+#define W4A16_LORA(MT, NT, BOTH) \
+  if (mt == MT && nt == NT && both == BOTH) return launch(lora_kernel<MT, NT, BOTH>, grid, p.splits, p, stream);
+  W4A16_LORA(1, 1, true) W4A16_LORA(1, 2, true) W4A16_LORA(1, 4, true) W4A16_LORA(1, 8, true)
+  W4A16_LORA(1, 16, true) W4A16_LORA(2, 1, false) W4A16_LORA(2, 2, false) W4A16_LORA(2, 4, false)
+  W4A16_LORA(2, 8, false) W4A16_LORA(1, 16, false)
+#undef W4A16_LORA
   return cudaErrorInvalidValue;
-}
-
-cudaError_t launch_lora_up(const LoraParams& p, cudaStream_t stream) {
-  const int mt = row_tiles(p.M), blocks = (p.M + 16 * mt - 1) / (16 * mt);
-  const dim3 grid(blocks, p.N / (kUpWarps * 32), p.groups);
-  return mt == 1 ? launch(lora_up_kernel<1>, grid, kUpWarps * 32, 1, p, stream)
-                 : launch(lora_up_kernel<2>, grid, kUpWarps * 32, 1, p, stream);
 }
 
 }  // namespace w4a16

@@ -13,21 +13,20 @@ struct LoraParams {
   const float* scaling;    // [adapters]
   const int* index;        // [M]: the row's adapter, negative for none
   uint16_t* y;             // fp16 [M][N], the base product; the adapters' part is added to it
-  uint16_t* v;             // fp16 [M][rp]: scaling * x . A^T of the row, over unit[m]
-  float* unit;             // [M]: a power of two
+  uint16_t* v;             // workspace, from 128 rows on: fp16 [M][rp], scaling * x . A^T of the row over unit[m]
+  float* unit;             // workspace: [M], a power of two
+  int rp;                  // r rounded up to 16
   int* status;
   int M, K, N, r, adapters;
-  int rp;                  // r rounded up to 16
-  int splits;              // CTAs of a cluster, each a part of K (first product)
-  int passes;              // CTAs that share the adapters of a block of rows (first product)
-  int groups;              // the same for the second product
+  int splits;              // CTAs of a cluster (filled in by launch_lora, like passes)
+  int passes;              // clusters that share the adapters of a block of rows
 };
 
 constexpr int kLoraMaxRank = 128;
 
-// Fills splits, passes and groups.
-void lora_plan(LoraParams* p, int sms);
-cudaError_t launch_lora_down(const LoraParams& p, cudaStream_t stream);
-cudaError_t launch_lora_up(const LoraParams& p, cudaStream_t stream);
+// half: 0 the first product, 1 the second; where lora_two_kernels is false half 0
+// is not launched and half 1 does both.
+bool lora_two_kernels(int M);
+cudaError_t launch_lora(LoraParams p, int half, int sms, cudaStream_t stream);
 
 }  // namespace w4a16

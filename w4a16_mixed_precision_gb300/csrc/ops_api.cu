@@ -27,13 +27,13 @@ marlin_status_t current_sms(int* sms) {
 
 // ---- adapters ---------------------------------------------------------------------
 
+// ---- adapters: the product's workspace, then v and unit for many rows ---------------
+
 struct LoraSizes {
   size_t gemm, v_off, unit_off, total;
 };
 
 marlin_status_t lora_sizes(int M, int K, int N, int group, int r, int device, LoraSizes* z) {
-  if (M < 0 || r <= 0) return MARLIN_ERR_INVALID_ARG;
-  if (r % 8 != 0 || r > kLoraMaxRank) return MARLIN_ERR_UNSUPPORTED;
   const marlin_status_t s = marlin_workspace_bytes(M, K, N, group, device, &z->gemm);
   if (s != MARLIN_OK) return s;
   z->v_off = round_up(z->gemm, 256);
@@ -128,7 +128,8 @@ AttnPlan attn_plan(int sms, int D, int group, int max_q) {
 extern "C" {
 
 marlin_status_t marlin_lora_workspace_bytes(int M, int K, int N, int group, int r, int device, size_t* bytes) {
-  if (!bytes) return MARLIN_ERR_INVALID_ARG;
+  if (!bytes || M < 0 || r <= 0) return MARLIN_ERR_INVALID_ARG;
+  if (r % 8 != 0 || r > kLoraMaxRank) return MARLIN_ERR_UNSUPPORTED;
   LoraSizes z;
   const marlin_status_t s = lora_sizes(M, K, N, group, r, device, &z);
   if (s == MARLIN_OK) *bytes = z.total;
@@ -140,22 +141,20 @@ marlin_status_t marlin_lora_gemm(const uint16_t* X, const void* packed, const ui
                                  int adapters, int r, uint16_t* Y, int M, int K, int N, int group, void* workspace,
                                  size_t workspace_bytes, marlin_stream_t stream) {
   if (M < 0 || r <= 0 || adapters <= 0) return MARLIN_ERR_INVALID_ARG;
-  if (r % 8 != 0 || r > kLoraMaxRank) return MARLIN_ERR_UNSUPPORTED;
   if (const marlin_status_t c = marlin_packed_layout(K, N, group, 0, nullptr, nullptr, nullptr)) return c;
+  if (r % 8 != 0 || r > kLoraMaxRank) return MARLIN_ERR_UNSUPPORTED;
   if (M == 0) return MARLIN_OK;
   if (!X || !packed || !scales || !A || !B || !scaling || !index || !Y || !workspace) return MARLIN_ERR_INVALID_ARG;
   if (!aligned(X, 16) || !aligned(packed, 16) || !aligned(scales, 16) || !aligned(zeros, 16) || !aligned(A, 16) ||
       !aligned(B, 16) || !aligned(scaling, 4) || !aligned(index, 4) || !aligned(Y, 16) || !aligned(workspace, 16))
     return MARLIN_ERR_MISALIGNED;
-  int dev;
+  int dev, sms;
   if (cudaGetDevice(&dev) != cudaSuccess) return MARLIN_ERR_CUDA;
-  LoraSizes z;
-  marlin_status_t s = lora_sizes(M, K, N, group, r, dev, &z);
+  marlin_status_t s = static_cast<marlin_status_t>(device_sms(dev, &sms));
   if (s != MARLIN_OK) return s;
+  LoraSizes z;
+  if ((s = lora_sizes(M, K, N, group, r, dev, &z)) != MARLIN_OK) return s;
   if (workspace_bytes < z.total) return MARLIN_ERR_WORKSPACE_TOO_SMALL;
-  int sms;
-  if ((s = static_cast<marlin_status_t>(device_sms(dev, &sms))) != MARLIN_OK) return s;
-
   LoraParams p{};
   p.x = X;
   p.a = A;
@@ -165,18 +164,18 @@ marlin_status_t marlin_lora_gemm(const uint16_t* X, const void* packed, const ui
   p.y = Y;
   p.v = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + z.v_off);
   p.unit = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + z.unit_off);
+  p.rp = (int)round_up(r, 16);
   p.status = static_cast<int*>(workspace);
   p.M = M;
   p.K = K;
   p.N = N;
   p.r = r;
   p.adapters = adapters;
-  lora_plan(&p, sms);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (launch_lora_down(p, st) != cudaSuccess) return MARLIN_ERR_CUDA;
+  if (lora_two_kernels(M) && launch_lora(p, 0, sms, st) != cudaSuccess) return MARLIN_ERR_CUDA;
   s = marlin_gemm(X, packed, scales, zeros, Y, M, K, N, group, workspace, z.gemm, stream);
   if (s != MARLIN_OK) return s;
-  return launch_lora_up(p, st) == cudaSuccess ? MARLIN_OK : MARLIN_ERR_CUDA;
+  return launch_lora(p, 1, sms, st) == cudaSuccess ? MARLIN_OK : MARLIN_ERR_CUDA;
 }
 
 marlin_status_t marlin_kv_cache_bytes(int n_pages, int kv_heads, int head_dim, int page_size, size_t* bytes) {

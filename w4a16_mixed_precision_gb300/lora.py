@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import torch
 
-from . import _binding, _need_cuda, _on_current_device, _stream
+from . import Workspace, _binding, _need_cuda, _on_current_device, _stream
 from ._binding import MarlinError
 
 MAX_RANK = 128
@@ -53,23 +53,16 @@ class LoraBank:
                    torch.tensor([float(s) for _, _, s in adapters], dtype=torch.float32, device=adapters[0][0].device))
 
 
-class LoraWorkspace:
-    """Device workspace of lora_gemm for up to max_M rows, zeroed once; also a
-    workspace for gemm with the same shapes."""
+class LoraWorkspace(Workspace):
+    """Device workspace of lora_gemm for up to max_M rows and adapters of rank r,
+    zeroed once; serves gemm with the same shapes too."""
 
     def __init__(self, max_M: int, K: int, N: int, group: int, r: int, device=None):
-        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-        if dev.type != "cuda":
-            raise ValueError("a workspace lives on a CUDA device")
-        if dev.index is None:
-            dev = torch.device("cuda", torch.cuda.current_device())
-        self.nbytes = _binding.lora_workspace_bytes(max(max_M, 1), K, N, K if group == -1 else group, r + -r % 8,
-                                                    dev.index)
-        self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=dev)
+        self.r = r + -r % 8
+        super().__init__(max_M, K, N, group, device)
 
-    @property
-    def ptr(self) -> int:
-        return self.buf.data_ptr()
+    def _bytes(self, M: int, K: int, N: int, group: int, device: int) -> int:
+        return _binding.lora_workspace_bytes(M, K, N, group, self.r, device)
 
 
 def lora_gemm_into(x: torch.Tensor, w, bank: LoraBank, index: torch.Tensor, ws: LoraWorkspace,
