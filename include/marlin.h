@@ -415,8 +415,8 @@ marlin_status_t marlin_kv_workspace_bytes(int heads, int kv_heads, int head_dim,
 
 /*
  * Quantises the new tokens' keys and values and writes them into the cache.
- * k, v: device, fp16 [tokens][kv_heads][head_dim], 8-byte aligned, strides
- * multiples of 4 (e.g. views of one QKV product).  One launch.
+ * k, v: device, fp16 [tokens][kv_heads][head_dim], 16-byte aligned, strides
+ * multiples of 8 (e.g. views of one QKV product).  One launch.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED; CUDA.
  */
 marlin_status_t marlin_kv_append(const uint16_t* k, int64_t k_token_stride, int64_t k_head_stride,
@@ -428,7 +428,7 @@ marlin_status_t marlin_kv_append(const uint16_t* k, int64_t k_token_stride, int6
 
 /*
  * The values the cache holds for the same tokens: k, v device, fp16
- * [tokens][kv_heads][head_dim] contiguous, 8-byte aligned, written (rows that no
+ * [tokens][kv_heads][head_dim] contiguous, 16-byte aligned, written (rows that no
  * request owns are left alone).  Errors as for marlin_kv_append.
  */
 marlin_status_t marlin_kv_read(uint16_t* k, uint16_t* v, const void* cache, int n_pages, int kv_heads,

@@ -96,7 +96,7 @@ marlin_status_t kv_copy(bool append, uint16_t* k, int64_t k_ts, int64_t k_hs, ui
       make_kv(&p, cache, n_pages, hkv, D, page, table, max_pages, lens, q_start, B, T, workspace);
   if (s != MARLIN_OK || B == 0 || T == 0) return s;
   if (!k || !v) return MARLIN_ERR_INVALID_ARG;
-  if (!aligned(k, 8) || !aligned(v, 8) || !strides_ok(k_ts, k_hs, 4) || !strides_ok(v_ts, v_hs, 4))
+  if (!aligned(k, 16) || !aligned(v, 16) || !strides_ok(k_ts, k_hs, 8) || !strides_ok(v_ts, v_hs, 8))
     return MARLIN_ERR_MISALIGNED;
   const long long st[4] = {k_ts, k_hs, v_ts, v_hs};
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
