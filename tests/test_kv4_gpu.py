@@ -148,6 +148,15 @@ ATTENTION = [
     ([64, 0, 5], [1, 0, 1], 4, 2, 128, 16, 0),            # a request without tokens
     ([20000], [1], 8, 1, 128, 64, 0),                     # split over many CTAs
     ([9000], [2], 16, 2, 64, 256, 5000),
+    # many query rows per key head: tiles of 128 rows, blocks of 64 tokens
+    ([65], [65], 1, 1, 64, 16, 0),                        # one row more than the streaming kernel takes
+    ([128], [128], 2, 2, 128, 64, 0),                     # exactly one tile
+    ([129, 1, 300], [129, 1, 300], 3, 3, 128, 32, 0),     # tiles of one row; one request beside them
+    ([500], [100], 7, 1, 128, 16, 0),                     # a later part of a prompt, 7 heads share a key head
+    ([777], [777], 4, 1, 64, 48, 0),
+    ([1000], [300], 4, 2, 128, 128, 100),                 # window shorter than a block pair
+    ([400], [400], 2, 1, 64, 16, 1),                      # every token sees itself alone
+    ([640, 64], [200, 64], 8, 8, 128, 64, 64),
 ]
 
 
@@ -205,6 +214,37 @@ def test_attention_nan_stays_where_it_is_seen():
     for b, (qq, yy, bad) in enumerate(zip(split(q, nq), split(y, nq), split(nan, nq))):
         ref = kv_ref.attention(qq, kv[b], vv[b], nq[b], D ** -0.5)
         close(yy[~bad], ref[~bad], vv[b])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_nan_and_large_scores(D):
+    """The same on tiles of 128 rows: NaN keys, values and queries stay where they are seen; a block whose
+    scores and value scales are far above the earlier ones moves the rows' references."""
+    import w4a16_mixed_precision_gb300 as w4
+    lens, nq, hq, hkv, page = [400], [200], 4, 2, 16
+    k, v, cache, batch, hist = make(lens, nq, hkv, D, page, seed=21)
+    k[250:270] *= np.float16(30)     # scores up to a few hundred, from the fourth block on
+    v[64:128] *= np.float16(1e-3)
+    v[300:310] *= np.float16(200)
+    k[390, 0, 3] = np.nan
+    v[395, 1, 7] = np.inf
+    q = np.random.default_rng(22).standard_normal((sum(nq), hq, D)).astype(np.float16)
+    q[17, 2, 0] = np.nan
+    ws = w4.Kv4Workspace(batch, hq, cache)
+    w4.kv4_append(torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), cache, hist, ws)
+    y = w4.kv4_attention(torch.from_numpy(q).cuda(), cache, batch, ws).cpu().numpy()
+    assert w4.device_status(ws) == 0
+    nan = np.zeros(y.shape[:2], bool)
+    nan[190:, 0:2] = True
+    nan[195:, 2:4] = True
+    nan[17, 2] = True
+    assert np.array_equal(np.isnan(y).any(-1), nan) and np.array_equal(np.isnan(y).all(-1), nan)
+    vals = kv_ref.values(v)
+    ref = kv_ref.attention(q, kv_ref.values(k), vals, 200, D ** -0.5)
+    # by how much the seen values can move a row: the larger scores' fp32 error grows with them
+    mag = np.abs(q.astype(np.float64)).sum(-1) * 15 * np.abs(k[:390].astype(np.float64)).max() * D ** -0.5
+    tol = (2.0 ** -11 * np.abs(ref) + (2.0 ** -12 + 2.0 ** -20 * mag[:, :, None]) * np.abs(vals[:390]).max() + 2.0 ** -24)
+    assert (np.abs(y - ref)[~nan] <= tol[~nan]).all()
 
 
 def test_bad_entries_are_reported_and_not_followed():

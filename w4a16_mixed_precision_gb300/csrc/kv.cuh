@@ -93,6 +93,7 @@ struct KvAttnParams {
   int window;               // > 0: a query sees that many positions, its own included
   float scale_log2;         // softmax scale * log2(e)
   int whole_blocks;         // pages hold whole blocks: one copy each
+  int min_rows;             // requests with up to so many query rows per key head are left to another launch
   int max_rows;             // requests with more query rows per key head are left to another launch
   int* counters;            // [grid], zero between calls
   float* partials;          // [2 grid] parts of segments cut between CTAs, kv_attn_part_floats(D) at most
@@ -107,6 +108,8 @@ cudaError_t launch_kv_read(const KvParams& p, int D, uint16_t* k, uint16_t* v, c
 // nb: blocks of 8 query rows that share a pass over the cache (1 or 2)
 cudaError_t launch_kv_attn(const KvAttnParams& p, int D, int nb, int grid, cudaStream_t stream);
 cudaError_t kv_attn_set_smem_limit();
+cudaError_t launch_kv_prefill(const KvAttnParams& p, int D, cudaStream_t stream);
+cudaError_t kv_prefill_set_smem_limit();
 // Warps of a CTA at most, and floats of a part in the workspace at most (16 rows).
 constexpr int kKvAttnWarps = 8;
 constexpr int kv_attn_part_floats(int D) { return 16 * (D + 4 + 2); }

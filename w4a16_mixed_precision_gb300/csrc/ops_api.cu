@@ -106,6 +106,9 @@ marlin_status_t kv_copy(bool append, uint16_t* k, int64_t k_ts, int64_t k_hs, ui
 
 // ---- attention ----------------------------------------------------------------------
 
+// More query rows per key head than this go to the tcgen05 kernel.
+constexpr int kPrefillRows = 64;
+
 struct AttnPlan {
   int grid, nb;
   size_t counters_off, partials_off, firsts_off, bytes;
@@ -244,7 +247,7 @@ marlin_status_t marlin_kv_attention(const uint16_t* q, int64_t q_token_stride, i
     std::lock_guard<std::mutex> hold(lock);
     if (dev < 0 || dev >= 64) return MARLIN_ERR_INVALID_ARG;
     if (!set[dev]) {
-      if (kv_attn_set_smem_limit() != cudaSuccess) return MARLIN_ERR_CUDA;
+      if (kv_attn_set_smem_limit() != cudaSuccess || kv_prefill_set_smem_limit() != cudaSuccess) return MARLIN_ERR_CUDA;
       set[dev] = true;
     }
   }
@@ -258,14 +261,27 @@ marlin_status_t marlin_kv_attention(const uint16_t* q, int64_t q_token_stride, i
   p.window = window;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.whole_blocks = p.kv.page16 % 4 == 0;
+  p.min_rows = 0;
   p.max_rows = 0x7FFFFFFF;
   p.counters = reinterpret_cast<int*>(ws + a.counters_off);
   p.partials = reinterpret_cast<float*>(ws + a.partials_off);
   p.firsts = reinterpret_cast<float*>(ws + a.firsts_off);
   p.timeout_ns = kTimeoutNs;
-  return launch_kv_attn(p, head_dim, a.nb, a.grid, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? MARLIN_OK
-             : MARLIN_ERR_CUDA;
+  // Which kernel: by the query rows that share a key head.  The streaming kernel
+  // takes 8 or 16 rows a pass over the cache, the tcgen05 kernel 128.  Where every
+  // request has the same number of new tokens one launch serves them all (each
+  // kernel is right for any number); else both are launched and each takes its
+  // side of the bound, request by request.
+  const bool uniform = requests == 1 || (long long)requests * max_q == tokens;
+  const bool some_large = (long long)(requests == 1 ? tokens : max_q) * group > kPrefillRows;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (some_large) {
+    if (!uniform) p.min_rows = kPrefillRows;
+    if (launch_kv_prefill(p, head_dim, st) != cudaSuccess) return MARLIN_ERR_CUDA;
+    if (uniform) return MARLIN_OK;
+    p.max_rows = kPrefillRows;
+  }
+  return launch_kv_attn(p, head_dim, a.nb, a.grid, st) == cudaSuccess ? MARLIN_OK : MARLIN_ERR_CUDA;
 }
 
 }  // extern "C"
