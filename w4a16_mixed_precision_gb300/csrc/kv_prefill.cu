@@ -124,18 +124,34 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
                : "memory");
 }
 
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* at, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(at);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(at);
+    w[0] = v.x; w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(at);
+  }
+}
+
 template <int D>
 struct ShapeP {
   static constexpr int kK = kBlock * D * 2, kV = D * kBlock * 2;  // bytes of a block's operands
   static constexpr int kPar = kBlock * 16;                        // and of its scales and offsets
   static constexpr int kStages = 2;
-  static constexpr int kOffV = kStages * kK, kOffPar = kOffV + kStages * kV;
-  static constexpr int kSmem = 1024 + kOffPar + kStages * kPar;   // alignment slack first
+  static constexpr int kRaw = 4 * kv_granule_bytes(D);            // a block as it lies in the cache
+  static constexpr int kRing = 4;                                 // of them in flight
+  static constexpr int kOffV = kStages * kK, kOffPar = kOffV + kStages * kV, kOffRaw = kOffPar + kStages * kPar;
+  static constexpr int kSmem = 1024 + kOffRaw + kRing * kRaw;     // alignment slack first
+  static_assert(2 * (kSmem + 1024 + 512) <= 228 * 1024, "two CTAs share an SM");
   static constexpr int kColO = 0, kColS = D, kColQ = D + kBlock;  // columns of tensor memory; P is in S's place
 };
 
 struct CtrlP {
-  uint64_t kv_full[2], kv_empty[2], s_full, p_full, q_full, o_full, drain;
+  uint64_t kv_full[2], kv_empty[2], raw_full[4], raw_empty[4], s_full, p_full, q_full, o_full, drain;
   uint32_t tmem;
   int abort;
   int b, local;
@@ -158,6 +174,10 @@ __global__ void __launch_bounds__(kThreadsP, 2) kv_prefill_kernel(const KvAttnPa
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(ctrl.kv_full[s]), kDequantWarps);
       mbar_init(bar(ctrl.kv_empty[s]), 1);
+    }
+    for (int s = 0; s < Sh::kRing; ++s) {
+      mbar_init(bar(ctrl.raw_full[s]), 1);
+      mbar_init(bar(ctrl.raw_empty[s]), kDequantWarps);
     }
     mbar_init(bar(ctrl.s_full), 1);
     mbar_init(bar(ctrl.p_full), kSoftmaxWarps);
@@ -282,7 +302,8 @@ __global__ void __launch_bounds__(kThreadsP, 2) kv_prefill_kernel(const KvAttnPa
       uint32_t P[32];
       F2 lt, pzt;
       float over;
-      // one pass over the block's scores; Masked: some row does not see all of it
+      // one pass over the block's scores; Masked: some row does not see all of it.  A
+      // second one where a reference had to be moved.
       auto pass = [&](auto masked) {
         using Masked = decltype(masked);
         lt = pzt = dup(0.f);
@@ -318,10 +339,13 @@ __global__ void __launch_bounds__(kThreadsP, 2) kv_prefill_kernel(const KvAttnPa
           }
         }
       };
-      if (__any_sync(0xffffffffu, R == kUnset)) over = 2.f * kMost;
-      else if (full) pass(std::false_type{});
-      else pass(std::true_type{});
-      if (__any_sync(0xffffffffu, over > kMost)) {
+      over = 2.f * kMost;
+      for (int attempt = 0; attempt < 2; ++attempt) {
+        if (attempt > 0 || !__any_sync(0xffffffffu, R == kUnset)) {
+          if (full) pass(std::false_type{});
+          else pass(std::true_type{});
+        }
+        if (attempt > 0 || !__any_sync(0xffffffffu, over > kMost)) break;
         // move the reference of the rows that need it, rescale what they have
         float top = kNegInf;
 #pragma unroll 1
@@ -364,7 +388,6 @@ __global__ void __launch_bounds__(kThreadsP, 2) kv_prefill_kernel(const KvAttnPa
           }
           tmem_wait_st();
         }
-        pass(std::true_type{});
       }
       l = add2(l, lt);
       pz = add2(pz, pzt);
@@ -402,62 +425,50 @@ __global__ void __launch_bounds__(kThreadsP, 2) kv_prefill_kernel(const KvAttnPa
     // ================= dequantisation =================
     const int dw = warp - kSoftmaxWarps, g = lane >> 2, c = lane & 3;
     const int half = dw >> 1, wp = dw & 1;  // this warp's part of the values
+    // warp 0 of the four keeps kRing blocks in flight: lane q < 4 copies granule q
     const int* table = p.kv.table + (long long)b * p.kv.max_pages;
     const uint8_t* heads = p.kv.cache + h * p.kv.head_bytes;
-    uint32_t k0[CW], k1[CW], vv[4][CW / 2];
-    uint2 pr;
-    auto load = [&](int j) {
-      // lane q < 4 finds granule q
-      const int gi = (blk0 + j) * 4 + lane;
-      unsigned long long at = 0;
-      if (lane < 4 && gi * kGranule < seq.len) {
-        const int page = table[kv_div_page(p.kv, gi)];
-        if ((uint32_t)page < (uint32_t)p.kv.n_pages)
-          at = (unsigned long long)(uintptr_t)(heads + page * p.kv.page_bytes +
-                                               (gi - kv_div_page(p.kv, gi) * p.kv.page16) * GR);
-        else
-          kv_fail(p.kv, kKvSitePage);
-      }
-      const uint8_t* mine = reinterpret_cast<const uint8_t*>((uintptr_t)__shfl_sync(0xffffffffu, at, dw));
-      pr = make_uint2(0u, 0u);
-#pragma unroll
-      for (int w = 0; w < CW; ++w) k0[w] = k1[w] = 0u;
-      if (mine) {
-        if constexpr (CW == 4) {
-          const uint4 a = *reinterpret_cast<const uint4*>(mine + g * (D / 2) + c * (D / 8));
-          const uint4 d = *reinterpret_cast<const uint4*>(mine + (g + 8) * (D / 2) + c * (D / 8));
-          k0[0] = a.x; k0[1] = a.y; k0[2] = a.z; k0[3] = a.w;
-          k1[0] = d.x; k1[1] = d.y; k1[2] = d.z; k1[3] = d.w;
-        } else {
-          const uint2 a = *reinterpret_cast<const uint2*>(mine + g * (D / 2) + c * (D / 8));
-          const uint2 d = *reinterpret_cast<const uint2*>(mine + (g + 8) * (D / 2) + c * (D / 8));
-          k0[0] = a.x; k0[1] = a.y;
-          k1[0] = d.x; k1[1] = d.y;
-        }
-        // nothing is taken from tokens that are not written (they may hold anything)
-        if (lane < 16 && ((blk0 + j) * 4 + dw) * kGranule + lane < seq.len)
-          pr = *reinterpret_cast<const uint2*>(mine + 16 * D + 8 * lane);
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint8_t* from = reinterpret_cast<const uint8_t*>((uintptr_t)__shfl_sync(0xffffffffu, at, q));
-#pragma unroll
-        for (int w = 0; w < CW / 2; ++w) vv[q][w] = 0u;
-        if (from) {
-          from += 8 * D + half * (4 * D) + lane * (D / 8) + wp * (D / 16);
-          if constexpr (CW == 4) {
-            const uint2 a = *reinterpret_cast<const uint2*>(from);
-            vv[q][0] = a.x;
-            vv[q][1] = a.y;
-          } else {
-            vv[q][0] = *reinterpret_cast<const uint32_t*>(from);
-          }
-        }
-      }
+    const uint64_t policy = policy_evict_last();  // other CTAs read the same blocks
+    const uint32_t raw = base + Sh::kOffRaw;
+    int next_page = 0, issued = 0;
+    auto look_up = [&]() {
+      const int gi = (blk0 + issued) * 4 + lane;
+      if (lane < 4 && gi * kGranule < seq.len) next_page = table[kv_div_page(p.kv, gi)];
     };
-    load(0);
-    for (int j = 0; j < n; ++j) {
+    auto issue = [&]() {
+      const int gi = (blk0 + issued) * 4 + lane, slot = issued % Sh::kRing;
+      const bool inside = lane < 4 && gi * kGranule < seq.len;
+      const bool there = inside && (uint32_t)next_page < (uint32_t)p.kv.n_pages;
+      if (inside && !there) kv_fail(p.kv, kKvSitePage);  // no copy: the results are not valid, and reported
+      const int copies = __popc(__ballot_sync(0xffffffffu, there));
+      if (lane == 0) mbar_arrive_expect_tx(bar(ctrl.raw_full[slot]), copies * GR);
+      __syncwarp();
+      if (there && (lane == 0 || !p.whole_blocks))
+        bulk_g2s(raw + slot * Sh::kRaw + lane * GR,
+                 heads + next_page * p.kv.page_bytes + (gi - kv_div_page(p.kv, gi) * p.kv.page16) * GR,
+                 p.whole_blocks ? copies * GR : GR, bar(ctrl.raw_full[slot]), policy);
+      if (++issued < n) look_up();
+    };
+    if (dw == 0) {
+      look_up();
+      while (issued < min(Sh::kRing, n)) issue();
+    }
+    const uint8_t* raw_ptr = smem_raw + (base - smem_addr(smem_raw)) + Sh::kOffRaw;
+    int j = 0;
+    for (; j < n; ++j) {
       const int stage = j & 1;
+      if (!wait_warp(bar(ctrl.raw_full[j % Sh::kRing]), (uint32_t)((j / Sh::kRing) & 1), wc)) break;
+      const uint8_t* in = raw_ptr + (j % Sh::kRing) * Sh::kRaw;
+      uint32_t k0[CW], k1[CW], vv[4][CW / 2];
+      load_words<CW>(in + dw * GR + g * (D / 2) + c * (D / 8), k0);
+      load_words<CW>(in + dw * GR + (g + 8) * (D / 2) + c * (D / 8), k1);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        load_words<CW / 2>(in + q * GR + 8 * D + half * (4 * D) + lane * (D / 8) + wp * (D / 16), vv[q]);
+      // nothing is taken from tokens that are not written (they may hold anything)
+      uint2 pr = make_uint2(0u, 0u);
+      if (lane < 16 && ((blk0 + j) * 4 + dw) * kGranule + lane < seq.len)
+        pr = *reinterpret_cast<const uint2*>(in + dw * GR + 16 * D + 8 * lane);
       if (j >= 2 && !wait_warp(bar(ctrl.kv_empty[stage]), (uint32_t)((j / 2 - 1) & 1), wc)) break;
       const uint32_t kt = base + stage * Sh::kK, vt = base + Sh::kOffV + stage * Sh::kV;
       // keys: row = token, 16-byte unit = 8 channels; lanes with c >= 2 take their words
@@ -512,11 +523,25 @@ __global__ void __launch_bounds__(kThreadsP, 2) kv_prefill_kernel(const KvAttnPa
         }
         if (lane == 0) ctrl.vmax[stage][dw] = big;
       }
-      if (j + 1 < n) load(j + 1);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(ctrl.kv_full[stage]));
+      if (lane == 0) {
+        mbar_arrive(bar(ctrl.kv_full[stage]));
+        mbar_arrive(bar(ctrl.raw_empty[j % Sh::kRing]));
+      }
+      // the slot of the block before this one, which the others are done with by now
+      if (dw == 0 && j > 0 && issued < n) {
+        if (!wait_warp(bar(ctrl.raw_empty[(j - 1) % Sh::kRing]), (uint32_t)(((j - 1) / Sh::kRing) & 1), wc)) {
+          ++j;
+          break;
+        }
+        issue();
+      }
     }
+    // nothing may still be in flight into this CTA's shared memory
+    if (dw == 0 && lane == 0)
+      for (; j < issued; ++j)
+        wait_drain(bar(ctrl.raw_full[j % Sh::kRing]), (uint32_t)((j / Sh::kRing) & 1), wc);
   } else {
     // ================= products =================
     const uint32_t id_s = umma_idesc_f16_f32(kBlock), id_o = umma_idesc_f16_f32(D);
