@@ -5,16 +5,16 @@
 // it sees, on the tensor cores; beside them one exponential and about ten other
 // instructions per pair on the fp32 pipes, and the dequantisation of every
 // block once per CTA that reads it.
-//   * A CTA owns 128 query rows of one key head (the query heads that share it,
-//     for consecutive tokens) and passes over the tokens in blocks of 64.  Two
-//     CTAs share an SM (256 columns of tensor memory each), so that one's
-//     softmax runs under the other's products.
+//   * A CTA (one per SM) owns two tiles of 128 query rows of one key head (the
+//     query heads that share it, for consecutive tokens) and passes over the
+//     tokens in blocks of 64, dequantised once for both.  The tiles take turns:
+//     one's softmax runs under the other's products.
 //   * Q stays in tensor memory as the A operand of S = Q K^T; P replaces S in
 //     tensor memory as the A operand of O += P V; O stays in tensor memory.
 //   * Operands are the codes less 8, exact in fp16; the scales and offsets of
 //     keys enter the fp32 scores, those of values P and an fp32 sum per row
 //     (kv.cuh has the algebra).  What is rounded is p_t s_t, once, to fp16.
-//   * Four warps own a quarter of the rows each, a row per thread; four
+//   * Eight warps own the rows, one per thread; four
 //     dequantise the next block into 128-byte-swizzled shared memory; one
 //     issues the products.  Channels within groups of eight, and tokens within a
 //     block, are in the order in which the codes unpack, in both operands alike.
@@ -31,11 +31,11 @@ namespace {
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kUnset = -1e30f;   // a row's reference before it has seen a token
 constexpr float kMost = 16384.f;   // 2^14
-constexpr int kRows = 128;         // query rows of a CTA
+constexpr int kTile = 128, kTiles = 2, kRows = kTile * kTiles;  // query rows of a tile and of a CTA
 constexpr int kBlock = 64;         // tokens of a block
-constexpr int kSoftmaxWarps = 4, kDequantWarps = 4;
+constexpr int kTileWarps = 4, kSoftmaxWarps = kTiles * kTileWarps, kDequantWarps = 4;
 constexpr int kThreadsP = (kSoftmaxWarps + kDequantWarps + 1) * 32;
-constexpr int kTmem = 256;         // columns
+constexpr int kTmem = 512, kTileCols = kTmem / kTiles;  // columns, and of a tile
 
 struct F2 {
   float x, y;
@@ -141,26 +141,26 @@ template <int D>
 struct ShapeP {
   static constexpr int kK = kBlock * D * 2, kV = D * kBlock * 2;  // bytes of a block's operands
   static constexpr int kPar = kBlock * 16;                        // and of its scales and offsets
-  static constexpr int kStages = 2;
+  static constexpr int kStages = 3;                              // blocks of operands
   static constexpr int kRaw = 4 * kv_granule_bytes(D);            // a block as it lies in the cache
   static constexpr int kRing = 4;                                 // of them in flight
   static constexpr int kOffV = kStages * kK, kOffPar = kOffV + kStages * kV, kOffRaw = kOffPar + kStages * kPar;
   static constexpr int kSmem = 1024 + kOffRaw + kRing * kRaw;     // alignment slack first
-  static_assert(2 * (kSmem + 1024 + 512) <= 228 * 1024, "two CTAs share an SM");
+  static_assert(D + kBlock + D / 2 <= kTileCols, "O, S and Q of a tile");
   static constexpr int kColO = 0, kColS = D, kColQ = D + kBlock;  // columns of tensor memory; P is in S's place
 };
 
 struct CtrlP {
-  uint64_t kv_full[2], kv_empty[2], raw_full[4], raw_empty[4], s_full, p_full, q_full, o_full, drain;
+  uint64_t kv_full[3], kv_empty[3], raw_full[4], raw_empty[4], s_full[kTiles], p_full[kTiles], q_full, o_full, drain;
   uint32_t tmem;
   int abort;
   int b, local;
   KvSeq seq;
-  alignas(16) float vmax[2][4];  // largest value scale of each granule of a block
+  alignas(16) float vmax[3][4];  // largest value scale of each granule of a block
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreadsP, 2) kv_prefill_kernel(const KvAttnParams p) {
+__global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnParams p) {
   using Sh = ShapeP<D>;
   constexpr int CW = D / 32, GR = kv_granule_bytes(D);
   extern __shared__ uint8_t smem_raw[];
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreadsP, 2) kv_prefill_kernel(const KvAttnPa
   auto bar = [&](uint64_t& b) { return smem_addr(&b); };
 
   if (tid == 0) {
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < Sh::kStages; ++s) {
       mbar_init(bar(ctrl.kv_full[s]), kDequantWarps);
       mbar_init(bar(ctrl.kv_empty[s]), 1);
     }
@@ -179,8 +179,10 @@ __global__ void __launch_bounds__(kThreadsP, 2) kv_prefill_kernel(const KvAttnPa
       mbar_init(bar(ctrl.raw_full[s]), 1);
       mbar_init(bar(ctrl.raw_empty[s]), kDequantWarps);
     }
-    mbar_init(bar(ctrl.s_full), 1);
-    mbar_init(bar(ctrl.p_full), kSoftmaxWarps);
+    for (int t = 0; t < kTiles; ++t) {
+      mbar_init(bar(ctrl.s_full[t]), 1);
+      mbar_init(bar(ctrl.p_full[t]), kTileWarps);
+    }
     mbar_init(bar(ctrl.q_full), kSoftmaxWarps);
     mbar_init(bar(ctrl.o_full), 1);
     mbar_init(bar(ctrl.drain), 1);
@@ -244,23 +246,36 @@ __global__ void __launch_bounds__(kThreadsP, 2) kv_prefill_kernel(const KvAttnPa
   const int rows = seq.nq * p.group, tiles = (rows + kRows - 1) / kRows;
   const int h = ctrl.local % p.kv.hkv, row0 = (tiles - 1 - ctrl.local / p.kv.hkv) * kRows;
   const int first = seq.len - seq.nq;  // position of the first new token
-  const int i_first = row0 / p.group, i_last = (min(rows, row0 + kRows) - 1) / p.group;
-  // tokens any row sees [any_lo, any_hi), and that every row sees [all_lo, all_hi)
-  const int any_hi = first + i_last + 1, all_hi = first + i_first + 1;
-  const int any_lo = p.window > 0 ? max(0, first + i_first - p.window + 1) : 0;
-  const int all_lo = p.window > 0 ? first + i_last - p.window + 1 : 0;
-  const int blk0 = any_lo / kBlock;
-  const int n = max(1, (any_hi + kBlock - 1) / kBlock - blk0);  // one masked block where nothing is seen
+  // per tile: tokens any row sees [any_lo, any_hi), tokens every row sees [all_lo,
+  // all_hi), and the blocks of the former [from, to)
+  int all_lo[kTiles], all_hi[kTiles], from[kTiles], to[kTiles];
+  int blk0 = 0x7FFFFFFF, end = 0;
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) {
+    const int r0 = row0 + t * kTile, r1 = min(rows, r0 + kTile) - 1;  // first and last row
+    const int i0 = r0 / p.group, i1 = r1 / p.group;
+    const int any_lo = p.window > 0 ? max(0, first + i0 - p.window + 1) : 0, any_hi = first + i1 + 1;
+    all_lo[t] = p.window > 0 ? first + i1 - p.window + 1 : 0;
+    all_hi[t] = first + i0 + 1;
+    from[t] = any_lo / kBlock;
+    to[t] = r0 < rows && any_hi > 0 ? (any_hi + kBlock - 1) / kBlock : from[t];
+    if (to[t] > from[t]) {
+      blk0 = min(blk0, from[t]);
+      end = max(end, to[t]);
+    }
+  }
+  const int n = end > 0 ? end - blk0 : 0;  // blocks of the CTA; 0 where no row sees anything
 
   if (warp < kSoftmaxWarps) {
     // ================= softmax: a query row per thread =================
+    const int tile = warp / kTileWarps;
     const int row = row0 + warp * 32 + lane;
     const bool live = row < rows;
     const int i = live ? row / p.group : 0;
     const int head = h * p.group + (live ? row - i * p.group : 0);
     const int pos = first + i;
     const int hi = live ? pos + 1 : 0, lo = p.window > 0 ? pos - p.window + 1 : 0;  // tokens seen
-    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    const uint32_t lanes = tmem + (uint32_t)(tile * kTileCols) + ((uint32_t)((warp % kTileWarps) * 32) << 16);
 
     // Q to tensor memory, channels in the codes' order; the row's sum
     float qsum = 0.f;
@@ -290,15 +305,18 @@ __global__ void __launch_bounds__(kThreadsP, 2) kv_prefill_kernel(const KvAttnPa
     float R = live ? kUnset : 0.f;
     F2 l = dup(0.f), pz = dup(0.f);
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const int t0 = (blk0 + j) * kBlock, stage = j & 1;
-      if (!wait_warp(bar(ctrl.s_full), (uint32_t)(j & 1), wc)) {
+    const int my_from = tile ? from[1] : from[0], my_n = (tile ? to[1] : to[0]) - my_from;
+    const int my_all_lo = tile ? all_lo[1] : all_lo[0], my_all_hi = tile ? all_hi[1] : all_hi[0];
+    int stage = my_n > 0 ? (my_from - blk0) % Sh::kStages : 0;
+    for (int j = 0; j < my_n; ++j) {
+      const int t0 = (my_from + j) * kBlock;
+      if (!wait_warp(bar(ctrl.s_full[tile]), (uint32_t)(j & 1), wc)) {
         ok = false;
         break;
       }
       tc_fence_after();
       const float4* par = reinterpret_cast<const float4*>(par0 + stage * (Sh::kPar / 4));
-      const bool full = t0 >= all_lo && t0 + kBlock <= all_hi;
+      const bool full = t0 >= my_all_lo && t0 + kBlock <= my_all_hi;
       uint32_t P[32];
       F2 lt, pzt;
       float over;
@@ -394,13 +412,14 @@ __global__ void __launch_bounds__(kThreadsP, 2) kv_prefill_kernel(const KvAttnPa
       tmem_st32(lanes + Sh::kColS, P);
       tmem_wait_st();
       tc_fence_before();
-      if (lane == 0) mbar_arrive(bar(ctrl.p_full));
+      if (lane == 0) mbar_arrive(bar(ctrl.p_full[tile]));
+      if (++stage == Sh::kStages) stage = 0;
     }
     // ---- the rows' results ----
     if (ok && wait_warp(bar(ctrl.o_full), 0, wc)) {
       tc_fence_after();
       const float sum = l.x + l.y, off = pz.x + pz.y;
-      const float inv = hi > lo && hi > 0 ? 1.f / sum : 0.f;  // a row that sees no token is zero
+      const float inv = hi > 0 ? 1.f / sum : 0.f;  // a row that sees no token is zero
       uint16_t* dst = p.out + ((long long)(seq.q0 + i) * p.heads + head) * D;
 #pragma unroll 1
       for (int part = 0; part < D / 32; ++part) {
@@ -454,9 +473,9 @@ __global__ void __launch_bounds__(kThreadsP, 2) kv_prefill_kernel(const KvAttnPa
       while (issued < min(Sh::kRing, n)) issue();
     }
     const uint8_t* raw_ptr = smem_raw + (base - smem_addr(smem_raw)) + Sh::kOffRaw;
-    int j = 0;
+    int j = 0, stage = 0;
+    uint32_t ph = 0;
     for (; j < n; ++j) {
-      const int stage = j & 1;
       if (!wait_warp(bar(ctrl.raw_full[j % Sh::kRing]), (uint32_t)((j / Sh::kRing) & 1), wc)) break;
       const uint8_t* in = raw_ptr + (j % Sh::kRing) * Sh::kRaw;
       uint32_t k0[CW], k1[CW], vv[4][CW / 2];
@@ -469,7 +488,7 @@ __global__ void __launch_bounds__(kThreadsP, 2) kv_prefill_kernel(const KvAttnPa
       uint2 pr = make_uint2(0u, 0u);
       if (lane < 16 && ((blk0 + j) * 4 + dw) * kGranule + lane < seq.len)
         pr = *reinterpret_cast<const uint2*>(in + dw * GR + 16 * D + 8 * lane);
-      if (j >= 2 && !wait_warp(bar(ctrl.kv_empty[stage]), (uint32_t)((j / 2 - 1) & 1), wc)) break;
+      if (!wait_warp(bar(ctrl.kv_empty[stage]), ph ^ 1u, wc)) break;
       const uint32_t kt = base + stage * Sh::kK, vt = base + Sh::kOffV + stage * Sh::kV;
       // keys: row = token, 16-byte unit = 8 channels; lanes with c >= 2 take their words
       // in another order, so that eight lanes write eight different units
@@ -537,6 +556,10 @@ __global__ void __launch_bounds__(kThreadsP, 2) kv_prefill_kernel(const KvAttnPa
         }
         issue();
       }
+      if (++stage == Sh::kStages) {
+        stage = 0;
+        ph ^= 1u;
+      }
     }
     // nothing may still be in flight into this CTA's shared memory
     if (dw == 0 && lane == 0)
@@ -545,26 +568,56 @@ __global__ void __launch_bounds__(kThreadsP, 2) kv_prefill_kernel(const KvAttnPa
   } else {
     // ================= products =================
     const uint32_t id_s = umma_idesc_f16_f32(kBlock), id_o = umma_idesc_f16_f32(D);
-    bool ok = wait_warp(bar(ctrl.q_full), 0, wc);
-    for (int j = 0; ok && j < n; ++j) {
-      const int stage = j & 1;
-      if (!(ok = wait_warp(bar(ctrl.kv_full[stage]), (uint32_t)((j / 2) & 1), wc))) break;
-      tc_fence_after();
-      // S = Q K^T: both block's earlier readers of S's place are done (P was consumed by
-      // the product before, which these follow in order)
+    int stage = 0, next = Sh::kStages > 1 ? 1 : 0;  // of block j and of the one after it
+    uint32_t next_ph = 0;
+    // S = Q K^T of a tile.  S's place is free: P was consumed by a product before,
+    // which these follow in order.
+    auto scores = [&](int t, int st) {
+      const uint32_t cols = tmem + t * kTileCols;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        mma_f16_ts_elect(tmem + Sh::kColS, tmem + Sh::kColQ + kk * 8,
-                         umma_desc_sw128(base + stage * Sh::kK + (kk / 4) * (kBlock * 128)) + (uint64_t)(2 * (kk & 3)), id_s,
+        mma_f16_ts_elect(cols + Sh::kColS, cols + Sh::kColQ + kk * 8,
+                         umma_desc_sw128(base + st * Sh::kK + (kk / 4) * (kBlock * 128)) + (uint64_t)(2 * (kk & 3)), id_s,
                          kk > 0);
-      mma_commit_elect(bar(ctrl.s_full));
-      if (!(ok = wait_warp(bar(ctrl.p_full), (uint32_t)(j & 1), wc))) break;
+      mma_commit_elect(bar(ctrl.s_full[t]));
+    };
+    bool ok = wait_warp(bar(ctrl.q_full), 0, wc);
+    if (ok && n > 0 && (ok = wait_warp(bar(ctrl.kv_full[0]), 0, wc))) {
       tc_fence_after();
 #pragma unroll
-      for (int kk = 0; kk < kBlock / 16; ++kk)
-        mma_f16_ts_elect(tmem + Sh::kColO, tmem + Sh::kColS + kk * 8,
-                         umma_desc_sw128(base + Sh::kOffV + stage * Sh::kV) + (uint64_t)(2 * kk), id_o, j > 0 || kk > 0);
-      mma_commit_elect(bar(ctrl.kv_empty[stage]));
+      for (int t = 0; t < kTiles; ++t)
+        if (from[t] == blk0 && to[t] > blk0) scores(t, 0);
+    }
+    for (int j = 0; ok && j < n; ++j) {
+      const int blk = blk0 + j;
+      bool ready = j + 1 >= n;  // whether the next block's operands are there
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        if (ok && blk >= from[t] && blk < to[t]) {
+          if (!(ok = wait_warp(bar(ctrl.p_full[t]), (uint32_t)((blk - from[t]) & 1), wc))) break;
+          tc_fence_after();
+          const uint32_t cols = tmem + t * kTileCols;
+#pragma unroll
+          for (int kk = 0; kk < kBlock / 16; ++kk)
+            mma_f16_ts_elect(cols + Sh::kColO, cols + Sh::kColS + kk * 8,
+                             umma_desc_sw128(base + Sh::kOffV + stage * Sh::kV) + (uint64_t)(2 * kk), id_o,
+                             blk > from[t] || kk > 0);
+        }
+        if (t == kTiles - 1) mma_commit_elect(bar(ctrl.kv_empty[stage]));
+        if (ok && blk + 1 >= from[t] && blk + 1 < to[t]) {
+          if (!ready) {
+            if (!(ok = wait_warp(bar(ctrl.kv_full[next]), next_ph, wc))) break;
+            tc_fence_after();
+            ready = true;
+          }
+          scores(t, next);
+        }
+      }
+      stage = next;
+      if (++next == Sh::kStages) {
+        next = 0;
+        next_ph ^= 1u;
+      }
     }
     if (ok) mma_commit_elect(bar(ctrl.o_full));
     mma_commit_elect(bar(ctrl.drain));
@@ -602,7 +655,7 @@ cudaError_t kv_prefill_set_smem_limit() {
 }
 
 cudaError_t launch_kv_prefill(const KvAttnParams& p, int D, cudaStream_t stream) {
-  // tiles of 128 rows: at most one part-filled for each request
+  // groups of 256 rows: at most one part-filled for each request
   const long long grid = ((long long)p.kv.T * p.group / kRows + p.kv.B) * p.kv.hkv;
   return D == 128 ? launch<128>(p, grid, stream) : launch<64>(p, grid, stream);
 }
