@@ -9,8 +9,10 @@
 //     query heads that share it, for consecutive tokens) and passes over the
 //     tokens in blocks of 64, dequantised once for both.  The tiles take turns:
 //     one's softmax runs under the other's products.
-//   * Q stays in tensor memory as the A operand of S = Q K^T; P replaces S in
-//     tensor memory as the A operand of O += P V; O stays in tensor memory.
+//   * Q stays in shared memory as the A operand of S = Q K^T; S has two places in
+//     tensor memory, so that the next block's scores are there when a block's
+//     softmax is done; P replaces S as the A operand of O += P V; O stays in
+//     tensor memory.
 //   * Operands are the codes less 8, exact in fp16; the scales and offsets of
 //     keys enter the fp32 scores, those of values P and an fp32 sum per row
 //     (kv.cuh has the algebra).  What is rounded is p_t s_t, once, to fp16.
@@ -91,7 +93,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
                : "r"(taddr)
                : "memory");
 #undef W4A16_OUT
-  tmem_wait_ld();
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
 #define W4A16_IN(i) "r"(v[i])
@@ -124,6 +125,18 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
                : "memory");
 }
 
+// D[tmem] (+)= A[smem desc] * B[smem desc], kind::f16, issued by an elected lane.
+__device__ __forceinline__ void mma_f16_ss_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                 uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* at, uint32_t (&w)[N]) {
   if constexpr (N == 4) {
@@ -144,14 +157,17 @@ struct ShapeP {
   static constexpr int kStages = 3;                              // blocks of operands
   static constexpr int kRaw = 4 * kv_granule_bytes(D);            // a block as it lies in the cache
   static constexpr int kRing = 4;                                 // of them in flight
-  static constexpr int kOffV = kStages * kK, kOffPar = kOffV + kStages * kV, kOffRaw = kOffPar + kStages * kPar;
+  static constexpr int kQ = kTile * D * 2;                        // Q of a tile
+  static constexpr int kOffV = kStages * kK, kOffQ = kOffV + kStages * kV, kOffPar = kOffQ + kTiles * kQ,
+                       kOffRaw = kOffPar + kStages * kPar;
   static constexpr int kSmem = 1024 + kOffRaw + kRing * kRaw;     // alignment slack first
-  static_assert(D + kBlock + D / 2 <= kTileCols, "O, S and Q of a tile");
-  static constexpr int kColO = 0, kColS = D, kColQ = D + kBlock;  // columns of tensor memory; P is in S's place
+  static_assert(D + 2 * kBlock <= kTileCols, "O and two S of a tile");
+  static constexpr int kColO = 0, kColS = D;                      // columns of a tile; P is in S's place
 };
 
 struct CtrlP {
-  uint64_t kv_full[3], kv_empty[3], raw_full[4], raw_empty[4], s_full[kTiles], p_full[kTiles], q_full, o_full, drain;
+  uint64_t kv_full[3], kv_empty[3], raw_full[4], raw_empty[4], s_full[kTiles][2], p_full[kTiles][2], pv_done[kTiles], q_full,
+      o_full, drain;
   uint32_t tmem;
   int abort;
   int b, local;
@@ -180,8 +196,11 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       mbar_init(bar(ctrl.raw_empty[s]), kDequantWarps);
     }
     for (int t = 0; t < kTiles; ++t) {
-      mbar_init(bar(ctrl.s_full[t]), 1);
-      mbar_init(bar(ctrl.p_full[t]), kTileWarps);
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(bar(ctrl.s_full[t][s]), 1);
+        mbar_init(bar(ctrl.p_full[t][s]), kTileWarps);
+      }
+      mbar_init(bar(ctrl.pv_done[t]), 1);
     }
     mbar_init(bar(ctrl.q_full), kSoftmaxWarps);
     mbar_init(bar(ctrl.o_full), 1);
@@ -277,27 +296,23 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
     const int hi = live ? pos + 1 : 0, lo = p.window > 0 ? pos - p.window + 1 : 0;  // tokens seen
     const uint32_t lanes = tmem + (uint32_t)(tile * kTileCols) + ((uint32_t)((warp % kTileWarps) * 32) << 16);
 
-    // Q to tensor memory, channels in the codes' order; the row's sum
+    // Q to shared memory, channels in the codes' order; the row's sum
     float qsum = 0.f;
     {
       const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(seq.q0 + i) * p.q_ts + (long long)head * p.q_hs);
+      const int r = row - row0 - tile * kTile;
+      const uint32_t qt = base + Sh::kOffQ + tile * Sh::kQ + r * 128;
 #pragma unroll
-      for (int part = 0; part < D / 64; ++part) {
-        uint32_t q[32];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint4 v = live ? src[part * 8 + j] : make_uint4(0u, 0u, 0u, 0u);
-          q[4 * j] = __byte_perm(v.x, v.z, 0x5410);
-          q[4 * j + 1] = __byte_perm(v.y, v.w, 0x5410);
-          q[4 * j + 2] = __byte_perm(v.x, v.z, 0x7632);
-          q[4 * j + 3] = __byte_perm(v.y, v.w, 0x7632);
-          const float2 a = unpack(v.x), bb = unpack(v.y), cc = unpack(v.z), dd = unpack(v.w);
-          qsum += ((a.x + a.y) + (bb.x + bb.y)) + ((cc.x + cc.y) + (dd.x + dd.y));
-        }
-        tmem_st32(lanes + Sh::kColQ + part * 32, q);
+      for (int j = 0; j < D / 8; ++j) {
+        const uint4 v = live ? src[j] : make_uint4(0u, 0u, 0u, 0u);
+        const float2 a = unpack(v.x), bb = unpack(v.y), cc = unpack(v.z), dd = unpack(v.w);
+        qsum += ((a.x + a.y) + (bb.x + bb.y)) + ((cc.x + cc.y) + (dd.x + dd.y));
+        sts128(qt + (j / 8) * (kTile * 128) + (((j & 7) ^ (r & 7)) << 4),
+               make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                          __byte_perm(v.y, v.w, 0x7632)));
       }
-      tmem_wait_st();
-      tc_fence_before();
+      fence_proxy_async_smem();
+      __syncwarp();
       if (lane == 0) mbar_arrive(bar(ctrl.q_full));
     }
     const F2 qs = dup(qsum);
@@ -310,7 +325,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
     int stage = my_n > 0 ? (my_from - blk0) % Sh::kStages : 0;
     for (int j = 0; j < my_n; ++j) {
       const int t0 = (my_from + j) * kBlock;
-      if (!wait_warp(bar(ctrl.s_full[tile]), (uint32_t)(j & 1), wc)) {
+      const uint32_t s_col = lanes + Sh::kColS + (j & 1) * kBlock;
+      if (!wait_warp(bar(ctrl.s_full[tile][j & 1]), (uint32_t)((j >> 1) & 1), wc)) {
         ok = false;
         break;
       }
@@ -327,10 +343,14 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
         lt = pzt = dup(0.f);
         over = 0.f;
         const F2 nr = dup(-R);
+        uint32_t sc[2][32];
+        tmem_ld32(s_col, sc[0]);
+        tmem_wait_ld();
+        tmem_ld32(s_col + 32, sc[1]);  // under the first half's arithmetic
 #pragma unroll
         for (int half = 0; half < 2; ++half) {  // 32 tokens
-          uint32_t s[32];
-          tmem_ld32(lanes + Sh::kColS + half * 32, s);
+          if (half) tmem_wait_ld();
+          uint32_t(&s)[32] = sc[half];
 #pragma unroll
           for (int t = 0; t < 32; t += 2) {
             const float4 kp = par[(half * 32 + t)], vp = par[(half * 32 + t) + 1];  // (ks, ks, ko, ko), (vs, vs, vo, vo)
@@ -369,7 +389,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           uint32_t s[32];
-          tmem_ld32(lanes + Sh::kColS + half * 32, s);
+          tmem_ld32(s_col + half * 32, s);
+          tmem_wait_ld();
 #pragma unroll
           for (int t = 0; t < 32; t += 2) {
             const float4 kp = par[half * 32 + t];
@@ -395,11 +416,14 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
         l = mul2(l, dup(f));
         pz = mul2(pz, dup(f));
         if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-          // all earlier products are done: they were committed before this block's scores
+          // once the products of the blocks before are done (this one's follow P)
+          if (!wait_warp(bar(ctrl.pv_done[tile]), (uint32_t)((j - 1) & 1), wc)) break;
+          tc_fence_after();
 #pragma unroll 1
           for (int part = 0; part < D / 32; ++part) {
             uint32_t v[32];
             tmem_ld32(lanes + Sh::kColO + part * 32, v);
+            tmem_wait_ld();
 #pragma unroll
             for (int t = 0; t < 32; ++t) v[t] = __float_as_uint(__uint_as_float(v[t]) * f);
             tmem_st32(lanes + Sh::kColO + part * 32, v);
@@ -409,10 +433,10 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       }
       l = add2(l, lt);
       pz = add2(pz, pzt);
-      tmem_st32(lanes + Sh::kColS, P);
+      tmem_st32(s_col, P);
       tmem_wait_st();
       tc_fence_before();
-      if (lane == 0) mbar_arrive(bar(ctrl.p_full[tile]));
+      if (lane == 0) mbar_arrive(bar(ctrl.p_full[tile][j & 1]));
       if (++stage == Sh::kStages) stage = 0;
     }
     // ---- the rows' results ----
@@ -425,6 +449,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       for (int part = 0; part < D / 32; ++part) {
         uint32_t v[32];
         tmem_ld32(lanes + Sh::kColO + part * 32, v);
+        tmem_wait_ld();
         if (live) {
 #pragma unroll
           for (int t = 0; t < 32; t += 8) {
@@ -570,49 +595,48 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
     const uint32_t id_s = umma_idesc_f16_f32(kBlock), id_o = umma_idesc_f16_f32(D);
     int stage = 0, next = Sh::kStages > 1 ? 1 : 0;  // of block j and of the one after it
     uint32_t next_ph = 0;
-    // S = Q K^T of a tile.  S's place is free: P was consumed by a product before,
-    // which these follow in order.
-    auto scores = [&](int t, int st) {
-      const uint32_t cols = tmem + t * kTileCols;
+    // S = Q K^T of a tile's i-th block.  The place is free: the P that was there was
+    // consumed by a product before, which these follow in order.
+    auto scores = [&](int t, int i, int st) {
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        mma_f16_ts_elect(cols + Sh::kColS, cols + Sh::kColQ + kk * 8,
+        mma_f16_ss_elect(tmem + t * kTileCols + Sh::kColS + (i & 1) * kBlock,
+                         umma_desc_sw128(base + Sh::kOffQ + t * Sh::kQ + (kk / 4) * (kTile * 128)) + (uint64_t)(2 * (kk & 3)),
                          umma_desc_sw128(base + st * Sh::kK + (kk / 4) * (kBlock * 128)) + (uint64_t)(2 * (kk & 3)), id_s,
                          kk > 0);
-      mma_commit_elect(bar(ctrl.s_full[t]));
+      mma_commit_elect(bar(ctrl.s_full[t][i & 1]));
     };
     bool ok = wait_warp(bar(ctrl.q_full), 0, wc);
     if (ok && n > 0 && (ok = wait_warp(bar(ctrl.kv_full[0]), 0, wc))) {
       tc_fence_after();
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
-        if (from[t] == blk0 && to[t] > blk0) scores(t, 0);
+        if (from[t] == blk0 && to[t] > blk0) scores(t, 0, 0);
     }
     for (int j = 0; ok && j < n; ++j) {
       const int blk = blk0 + j;
-      bool ready = j + 1 >= n;  // whether the next block's operands are there
+      if (j + 1 < n) {  // the next block's scores go before this one's products with V
+        if (!(ok = wait_warp(bar(ctrl.kv_full[next]), next_ph, wc))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+          if (blk + 1 >= from[t] && blk + 1 < to[t]) scores(t, blk + 1 - from[t], next);
+      }
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
-        if (ok && blk >= from[t] && blk < to[t]) {
-          if (!(ok = wait_warp(bar(ctrl.p_full[t]), (uint32_t)((blk - from[t]) & 1), wc))) break;
-          tc_fence_after();
-          const uint32_t cols = tmem + t * kTileCols;
+        const int i = blk - from[t];
+        if (!ok || i < 0 || blk >= to[t]) continue;
+        if (!(ok = wait_warp(bar(ctrl.p_full[t][i & 1]), (uint32_t)((i >> 1) & 1), wc))) continue;
+        tc_fence_after();
+        const uint32_t cols = tmem + t * kTileCols;
 #pragma unroll
-          for (int kk = 0; kk < kBlock / 16; ++kk)
-            mma_f16_ts_elect(cols + Sh::kColO, cols + Sh::kColS + kk * 8,
-                             umma_desc_sw128(base + Sh::kOffV + stage * Sh::kV) + (uint64_t)(2 * kk), id_o,
-                             blk > from[t] || kk > 0);
-        }
-        if (t == kTiles - 1) mma_commit_elect(bar(ctrl.kv_empty[stage]));
-        if (ok && blk + 1 >= from[t] && blk + 1 < to[t]) {
-          if (!ready) {
-            if (!(ok = wait_warp(bar(ctrl.kv_full[next]), next_ph, wc))) break;
-            tc_fence_after();
-            ready = true;
-          }
-          scores(t, next);
-        }
+        for (int kk = 0; kk < kBlock / 16; ++kk)
+          mma_f16_ts_elect(cols + Sh::kColO, cols + Sh::kColS + (i & 1) * kBlock + kk * 8,
+                           umma_desc_sw128(base + Sh::kOffV + stage * Sh::kV) + (uint64_t)(2 * kk), id_o, i > 0 || kk > 0);
+        mma_commit_elect(bar(ctrl.pv_done[t]));
       }
+      if (!ok) break;
+      mma_commit_elect(bar(ctrl.kv_empty[stage]));
       stage = next;
       if (++next == Sh::kStages) {
         next = 0;
