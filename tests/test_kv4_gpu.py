@@ -157,6 +157,9 @@ ATTENTION = [
     ([1000], [300], 4, 2, 128, 128, 100),                 # window shorter than a block pair
     ([400], [400], 2, 1, 64, 16, 1),                      # every token sees itself alone
     ([640, 64], [200, 64], 8, 8, 128, 64, 64),
+    # many requests: more than threads of a CTA; several whole requests in a warp's stripe
+    ([i * 7 % 50 + 1 for i in range(300)], [1] * 300, 4, 1, 64, 16, 0),
+    ([i * 37 % 400 + 1 for i in range(60)], [1] * 60, 8, 2, 128, 32, 0),
 ]
 
 
@@ -349,6 +352,45 @@ def test_on_another_stream_and_in_a_graph():
     kv, vv = split(kv_ref.values(k), lens), split(kv_ref.values(v), lens)
     for b in range(2):
         close(out[b:b + 1].cpu().numpy(), kv_ref.attention(q[b:b + 1], kv[b], vv[b], 1, D ** -0.5), vv[b])
+
+
+def test_one_workspace_for_many_shapes():
+    """What a call leaves in the workspace (arrival counts, parts) does not reach the next one."""
+    import w4a16_mixed_precision_gb300 as w4
+    ws = None
+    for seed, (lens, nq, hq, hkv) in enumerate([([5000], [1], 8, 2), ([300, 20], [1, 1], 16, 2), ([7000, 6500], [2, 2], 16, 2),
+                                                ([200], [200], 4, 2), ([5000], [1], 8, 2), ([64] * 9, [1] * 9, 8, 2)]):
+        D, page = 64, 16
+        k, v, cache, batch, hist = make(lens, nq, hkv, D, page, seed=30 + seed)
+        ws = ws or w4.Kv4Workspace(batch, 16, cache)
+        w4.kv4_append(torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), cache, hist, ws)
+        q = np.random.default_rng(seed).standard_normal((sum(nq), hq, D)).astype(np.float16)
+        y = w4.kv4_attention(torch.from_numpy(q).cuda(), cache, batch, ws)
+        assert w4.device_status(ws) == 0
+        kv, vv = split(kv_ref.values(k), lens), split(kv_ref.values(v), lens)
+        for b, (qq, yy) in enumerate(zip(split(q, nq), split(y.cpu().numpy(), nq))):
+            close(yy, kv_ref.attention(qq, kv[b], vv[b], nq[b], D ** -0.5), vv[b])
+
+
+def test_strided_queries():
+    """Queries, keys and values as views of one QKV product."""
+    import w4a16_mixed_precision_gb300 as w4
+    lens, nq, hq, hkv, D, page = [90, 33], [90, 33], 8, 2, 64, 16
+    k, v, cache, batch, hist = make(lens, nq, hkv, D, page, seed=40)
+    T = sum(nq)
+    q = np.random.default_rng(41).standard_normal((T, hq, D)).astype(np.float16)
+    qkv = torch.from_numpy(np.concatenate([q, k, v], axis=1)).cuda()
+    ws = w4.Kv4Workspace(batch, hq, cache)
+    w4.kv4_append(qkv[:, hq:hq + hkv], qkv[:, hq + hkv:], cache, batch, ws)
+    y = w4.kv4_attention(qkv[:, :hq], cache, batch, ws)
+    few = w4.Kv4Batch(batch.page_table, batch.lengths, torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda"), 2, 1)
+    one = w4.kv4_attention(qkv[[89, 122]][:, :hq], cache, few, ws)
+    assert w4.device_status(ws) == 0
+    kv, vv = split(kv_ref.values(k), lens), split(kv_ref.values(v), lens)
+    for b, (qq, yy) in enumerate(zip(split(q, nq), split(y.cpu().numpy(), nq))):
+        ref = kv_ref.attention(qq, kv[b], vv[b], nq[b], D ** -0.5)
+        close(yy, ref, vv[b])
+        close(one[b:b + 1].cpu().numpy(), ref[-1:], vv[b])
 
 
 def test_refusals():

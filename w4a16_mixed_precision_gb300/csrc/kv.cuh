@@ -53,6 +53,20 @@ __device__ __forceinline__ void kv_fail(const KvParams& p, int site) {
 // Sites of failed checks of device-side inputs (the word after the status word).
 enum KvSite { kKvSiteQStart = 101, kKvSiteLen = 102, kKvSitePage = 103, kKvSiteAdapter = 104 };
 
+// Brings the lengths, starts and page table towards L2 before the wait for the
+// previous kernel (which may still be writing them: a prefetch takes no value).
+// thread: index among all threads of the grid, a 128-byte line each.
+__device__ __forceinline__ void kv_prefetch_plan(const KvParams& p, long long thread) {
+  const long long table = (long long)p.B * p.max_pages;
+  const char* at = nullptr;
+  if (thread * 32 < table) at = reinterpret_cast<const char*>(p.table) + thread * 128;
+  if (at) asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+  if (thread * 32 < p.B) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(p.lens) + thread * 128));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(p.q_start) + thread * 128));
+  }
+}
+
 // Page of a granule of a request (g16 / page16) and its place inside the page.
 // page16 <= 64 and g16 < 2^26, where the rounded-up reciprocal is exact.
 __device__ __forceinline__ int kv_div_page(const KvParams& p, int g16) {

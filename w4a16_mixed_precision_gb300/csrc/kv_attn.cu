@@ -121,11 +121,12 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   return d;
 }
 
-// W warps; blocks of GB granules; S blocks in a warp's ring.
+// W warps; blocks of GB granules, GI of them taken together; S blocks in a warp's ring.
 template <int D, int NB>
 struct Shape {
-  static constexpr int W = 8, GB = NB == 1 ? 4 : 2, S = NB == 1 ? 2 : D == 128 ? 4 : 8;
+  static constexpr int W = 8, GB = 4, GI = NB == 1 ? 4 : 2, S = D == 128 ? 2 : 4;
   static constexpr int kBlock = GB * kGranule;  // tokens
+  static constexpr int kStep = GI * kGranule;  // tokens taken together
   static constexpr int RB = 8 * NB;             // query rows
   static constexpr int GR = kv_granule_bytes(D);
   static constexpr int BB = GB * GR;            // bytes of a block
@@ -232,7 +233,7 @@ static_assert(sizeof(AttnCtrl) <= 3072, "control block too large");
 template <int D, int NB>
 __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const KvAttnParams p) {
   using Sh = Shape<D, NB>;
-  constexpr int W = Sh::W, S = Sh::S, GB = Sh::GB, RB = Sh::RB, GR = Sh::GR, BB = Sh::BB, CW = D / 32;
+  constexpr int W = Sh::W, S = Sh::S, GB = Sh::GB, GI = Sh::GI, RB = Sh::RB, GR = Sh::GR, BB = Sh::BB, CW = D / 32;
   extern __shared__ __align__(128) uint8_t smem[];
   AttnCtrl* ctrl = reinterpret_cast<AttnCtrl*>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -247,6 +248,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
     fence_mbarrier_init();
   }
   if (tid == 0) griddep_launch_dependents();
+  kv_prefetch_plan(p.kv, (long long)blockIdx.x * (W * 32) + tid);
   griddep_wait();
 
   // ---- the stripes: all blocks, and this CTA's and this warp's -----------------
@@ -454,14 +456,14 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
       // ---- S^T = K Q^T on the codes: low nibbles and high (x 16) apart -----------
       // x: scores in units of log2; element (q, nb, e) is token g + 8 e of granule
       // q for rows 2c, 2c + 1
-      F2 x[GB][NB][2], top[NB];
-      float vs[GB][2], vz[GB][2], big = 0.f;
+      F2 x[GI][NB][2], top[NB];
+      float vs[GI][2], vz[GI][2], big = 0.f;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) top[nb] = dup(kLowest);
-      uint32_t k0[GB][CW], k1[GB][CW];
-      F2 sl[GB][NB][2], sh[GB][NB][2];
+      uint32_t k0[GI][CW], k1[GI][CW];
+      F2 sl[GI][NB][2], sh[GI][NB][2];
 #pragma unroll
-      for (int q = 0; q < GB; ++q) {
+      for (int q = 0; q < GI; ++q) {
         load_words<CW>(st + q * GR + g * (D / 2) + c * (D / 8), k0[q]);
         load_words<CW>(st + q * GR + (g + 8) * (D / 2) + c * (D / 8), k1[q]);
 #pragma unroll
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
 #pragma unroll
       for (int j = 0; j < CW; ++j)
 #pragma unroll
-        for (int q = 0; q < GB; ++q) {
+        for (int q = 0; q < GI; ++q) {
           const uint32_t a0 = k0[q][j], a1 = k1[q][j], a2 = k0[q][j] >> 8, a3 = k1[q][j] >> 8;
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
           }
         }
 #pragma unroll
-      for (int q = 0; q < GB; ++q) {
+      for (int q = 0; q < GI; ++q) {
         uint32_t pr[2][2];
         load_words<2>(st + q * GR + 16 * D + g * 8, pr[0]);
         load_words<2>(st + q * GR + 16 * D + (g + 8) * 8, pr[1]);
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
       // ---- probabilities, and O^T += V^T P^T --------------------------------------
       const float rs = 64.f / sref;
 #pragma unroll
-      for (int q = 0; q < GB; ++q) {
+      for (int q = 0; q < GI; ++q) {
         const uint8_t* sg = st + q * GR;
         uint32_t v0[CW], v1[CW];
         load_words<CW>(sg + 8 * D + lane * (D / 8), v0);
@@ -577,20 +579,30 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
             ph[nb][e] = transpose8x8(h2_bits(hi));
             pl[nb][e] = transpose8x8(h2_bits(__floats2half2_rn(y.x - back.x, y.y - back.y)));
           }
-        // first halves of all tiles, then second halves: no result waits for the one before
+        // two words' operands at a time, the first halves of P before the second: four products lie
+        // between two that add to the same sums
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+        for (int j0 = 0; j0 < CW; j0 += 2) {
+          uint32_t lo[2][4], hi[2][4];
 #pragma unroll
-          for (int j = 0; j < CW; ++j) {
-            const uint32_t a0 = v0[j], a1 = v0[j] >> 8, a2 = v1[j], a3 = v1[j] >> 8;
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              const uint32_t p0 = half ? pl[nb][0] : ph[nb][0], p1 = half ? pl[nb][1] : ph[nb][1];
-              mma16816(o[2 * j][nb], a0 & 0x000F000Fu, a1 & 0x000F000Fu, a2 & 0x000F000Fu, a3 & 0x000F000Fu, p0, p1);
-              mma16816(o[2 * j + 1][nb], a0 & 0x00F000F0u, a1 & 0x00F000F0u, a2 & 0x00F000F0u, a3 & 0x00F000F0u, p0,
-                       p1);
-            }
+          for (int d = 0; d < 2; ++d) {
+            const uint32_t a0 = v0[j0 + d], a1 = v0[j0 + d] >> 8, a2 = v1[j0 + d], a3 = v1[j0 + d] >> 8;
+            lo[d][0] = a0 & 0x000F000Fu; lo[d][1] = a1 & 0x000F000Fu;
+            lo[d][2] = a2 & 0x000F000Fu; lo[d][3] = a3 & 0x000F000Fu;
+            hi[d][0] = a0 & 0x00F000F0u; hi[d][1] = a1 & 0x00F000F0u;
+            hi[d][2] = a2 & 0x00F000F0u; hi[d][3] = a3 & 0x00F000F0u;
           }
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                const uint32_t p0 = half ? pl[nb][0] : ph[nb][0], p1 = half ? pl[nb][1] : ph[nb][1];
+                mma16816(o[2 * (j0 + d)][nb], lo[d][0], lo[d][1], lo[d][2], lo[d][3], p0, p1);
+                mma16816(o[2 * (j0 + d) + 1][nb], hi[d][0], hi[d][1], hi[d][2], hi[d][3], p0, p1);
+              }
+        }
       }
     };
 
@@ -603,8 +615,12 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
         break;
       }
       // one version for blocks that every row sees whole, one with masks
-      if (t0 + Sh::kBlock <= all_hi && t0 >= all_lo) block(std::false_type{}, t0, st);
-      else if (t0 < any_hi && t0 + Sh::kBlock > any_lo) block(std::true_type{}, t0, st);
+#pragma unroll 1
+      for (int q = 0; q < GB; q += GI) {
+        const int t = t0 + q * kGranule;
+        if (t + Sh::kStep <= all_hi && t >= all_lo) block(std::false_type{}, t, st + q * GR);
+        else if (t < any_hi && t + Sh::kStep > any_lo) block(std::true_type{}, t, st + q * GR);
+      }
       __syncwarp();
       ++done;
       if (issued < total) issue(stage);
@@ -698,16 +714,25 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
     const int q0 = __shfl_sync(0xffffffffu, run_q0, lead), end = __shfl_sync(0xffffffffu, run_end, lead);
     const Segment& sg = ctrl->parts[q0].seg[lead != 0];
     const int row = (v % kVec) / (D / 4), ch = (v % (D / 4)) * 4;
+    // all parts' loads first, then the sums in order
+    float2 pml[W];
+    float4 pa[W];
+#pragma unroll
+    for (int q = 0; q < W; ++q) {
+      pml[q] = make_float2(kLowest, 0.f);
+      pa[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (q >= q0 && q < end && !ctrl->parts[q].idle) {
+        const bool in_ring = (lead != 0 && q == q0) || ctrl->parts[q].first_last;
+        const float* at = in_ring ? reinterpret_cast<const float*>(smem + Sh::kRing + q * (S * BB))
+                                  : p.firsts + (long long)(blockIdx.x * W + q) * (Sh::kPart / 4);
+        pml[q] = *reinterpret_cast<const float2*>(at + RB * Sh::kOStride + 2 * row);
+        pa[q] = *reinterpret_cast<const float4*>(at + row * Sh::kOStride + ch);
+      }
+    }
     float top = kLowest, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int q = q0; q < end; ++q) {
-      if (ctrl->parts[q].idle) continue;
-      const bool in_ring = (lead != 0 && q == q0) || ctrl->parts[q].first_last;
-      const float* at = in_ring ? reinterpret_cast<const float*>(smem + Sh::kRing + q * (S * BB))
-                                : p.firsts + (long long)(blockIdx.x * W + q) * (Sh::kPart / 4);
-      join(*reinterpret_cast<const float2*>(at + RB * Sh::kOStride + 2 * row),
-           *reinterpret_cast<const float4*>(at + row * Sh::kOStride + ch), top, sum, acc);
-    }
+#pragma unroll
+    for (int q = 0; q < W; ++q) join(pml[q], pa[q], top, sum, acc);
     if ((shared >> lead) & 1u) {
       float* part = p.partials + (2ll * blockIdx.x + (lead != 0)) * (RB * (D + 2));
       __stcg(reinterpret_cast<float4*>(part + row * D + ch), acc);
@@ -731,11 +756,12 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
       c0[k] = (int)owner_of(seg[k]->s0, U, G);
       c1[k] = (int)owner_of(seg[k]->s0 + seg[k]->n - 1, U, G);
     }
-  __threadfence();
   __syncthreads();
   if (tid < 2 && on[tid]) {
     const int first_cta = tid ? c0[1] : c0[0], last_cta = tid ? c1[1] : c1[0];
-    const int arrived = atomicAdd(p.counters + first_cta, 1);
+    // release and acquire at the card's scope, for the whole CTA by way of the barriers
+    int arrived;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(arrived) : "l"(p.counters + first_cta) : "memory");
     ctrl->arrived[tid] = arrived == last_cta - first_cta;
     if (arrived == last_cta - first_cta) p.counters[first_cta] = 0;  // all are here: ready for the next call
     __threadfence();

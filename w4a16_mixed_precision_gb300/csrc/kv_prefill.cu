@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
     fence_mbarrier_init();
     griddep_launch_dependents();
   }
+  kv_prefetch_plan(p.kv, (long long)blockIdx.x * kThreadsP + tid);
   griddep_wait();
   // ---- this CTA's rows: the requests' tiles in order, the last (longest) tile first ------
   if (warp == 0) {

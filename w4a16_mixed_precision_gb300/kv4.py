@@ -13,7 +13,7 @@ from dataclasses import dataclass
 
 import torch
 
-from . import _binding, _on_current_device, _stream
+from . import _binding, _on_current_device
 from ._binding import MarlinError
 
 
@@ -28,6 +28,9 @@ class Kv4Cache:
         self.nbytes = _binding.kv_cache_bytes(n_pages, kv_heads, head_dim, page_size)
         self.n_pages, self.kv_heads, self.head_dim, self.page_size = n_pages, kv_heads, head_dim, page_size
         self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=dev)
+        self._device, self._like = self.buf.get_device(), self.buf.new_empty(0, dtype=torch.float16)
+        self._scale = 1.0 / math.sqrt(head_dim)
+        self._args = (self.buf.data_ptr(), n_pages, kv_heads, head_dim, page_size)
 
 
 @dataclass
@@ -55,6 +58,7 @@ class Kv4Batch:
             raise ValueError("expected page_table [B, pages], lengths [B], q_start [B + 1], tokens >= 0, max_q >= 0")
         if not self.page_table.device == self.lengths.device == self.q_start.device:
             raise ValueError("page_table, lengths and q_start must be on one device")
+        self._device = self.lengths.get_device()
         self._args = (self.page_table.data_ptr(), self.page_table.shape[1], self.lengths.data_ptr(),
                       self.q_start.data_ptr(), B, self.tokens)
 
@@ -68,48 +72,57 @@ class Kv4Workspace:
         self.nbytes = _binding.kv_workspace_bytes(heads, cache.kv_heads, cache.head_dim, batch.lengths.shape[0],
                                                   batch.tokens, dev.index)
         self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=dev)
+        self._device, self._ptr = self.buf.get_device(), self.buf.data_ptr()
 
     @property
     def ptr(self) -> int:
-        return self.buf.data_ptr()
+        return self._ptr
 
 
-def _check_heads(t: torch.Tensor, name: str, tokens: int, heads: int | None, cache: Kv4Cache) -> None:
+def _explain(name: str, t: torch.Tensor, tokens: int, heads, cache: Kv4Cache) -> None:
+    """Raises for a tensor that is not fp16 [tokens, heads, head_dim] on the cache's device."""
     if not t.is_cuda or t.dtype != torch.float16:
         raise ValueError(f"{name} must be an fp16 CUDA tensor, got {t.dtype} on {t.device}")
-    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != cache.head_dim or (heads is not None and t.shape[1] != heads):
+    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != cache.head_dim or (heads and t.shape[1] != heads):
         raise ValueError(f"{name}: expected [{tokens}, {heads or 'heads'}, {cache.head_dim}], got {tuple(t.shape)}")
-    if t.stride(2) != 1 and t.shape[2] > 1:
+    if t.stride(2) != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
+
+
+def _on_device(cache: Kv4Cache, batch: Kv4Batch, ws: Kv4Workspace, *named) -> int:
+    """The current device, on which every tensor of a call has to be."""
+    cur = torch._C._cuda_getDevice()
+    if not (cache._device == batch._device == ws._device == cur and all(t.get_device() == cur for _, t in named)):
+        _on_current_device(("cache", cache.buf), ("page_table", batch.page_table), ("workspace", ws.buf), *named)
+    return cur
 
 
 def kv4_append(k: torch.Tensor, v: torch.Tensor, cache: Kv4Cache, batch: Kv4Batch, ws: Kv4Workspace) -> None:
     """Quantise the batch's new keys and values, fp16 [tokens, kv_heads,
     head_dim] (views of one QKV product are fine), into the cache, on the
     current stream."""
-    table, max_pages, lengths, q_start, B, T = batch._args
-    _check_heads(k, "k", T, cache.kv_heads, cache)
-    _check_heads(v, "v", T, cache.kv_heads, cache)
-    _on_current_device(("k", k), ("v", v), ("cache", cache.buf), ("page_table", batch.page_table), ("workspace", ws.buf))
-    rc = _binding.load().marlin_kv_append(
-        k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), cache.buf.data_ptr(),
-        cache.n_pages, cache.kv_heads, cache.head_dim, cache.page_size, table, max_pages, lengths, q_start, B, T,
-        ws.ptr, _stream() or None)
-    if rc != _binding.OK:
+    want = (batch.tokens, cache.kv_heads, cache.head_dim)
+    ks, vs = k.stride(), v.stride()
+    for name, t, st in (("k", k, ks), ("v", v, vs)):
+        if t.dtype is not torch.float16 or t.shape != want or st[2] != 1 or not t.is_cuda:
+            _explain(name, t, batch.tokens, cache.kv_heads, cache)
+    cur = _on_device(cache, batch, ws, ("k", k), ("v", v))
+    rc = (_binding._lib or _binding.load()).marlin_kv_append(
+        k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], *cache._args, *batch._args, ws._ptr,
+        torch._C._cuda_getCurrentRawStream(cur))
+    if rc:
         raise MarlinError(rc, "marlin_kv_append")
 
 
 def kv4_read(cache: Kv4Cache, batch: Kv4Batch, ws: Kv4Workspace):
     """(k, v), fp16 [tokens, kv_heads, head_dim]: the values the cache holds for
     the batch's new tokens."""
-    table, max_pages, lengths, q_start, B, T = batch._args
-    _on_current_device(("cache", cache.buf), ("page_table", batch.page_table), ("workspace", ws.buf))
-    k = torch.empty((T, cache.kv_heads, cache.head_dim), dtype=torch.float16, device=cache.buf.device)
-    v = torch.empty_like(k)
-    rc = _binding.load().marlin_kv_read(
-        k.data_ptr(), v.data_ptr(), cache.buf.data_ptr(), cache.n_pages, cache.kv_heads, cache.head_dim,
-        cache.page_size, table, max_pages, lengths, q_start, B, T, ws.ptr, _stream() or None)
-    if rc != _binding.OK:
+    cur = _on_device(cache, batch, ws)
+    shape = (batch.tokens, cache.kv_heads, cache.head_dim)
+    k, v = cache._like.new_empty(shape), cache._like.new_empty(shape)
+    rc = (_binding._lib or _binding.load()).marlin_kv_read(
+        k.data_ptr(), v.data_ptr(), *cache._args, *batch._args, ws._ptr, torch._C._cuda_getCurrentRawStream(cur))
+    if rc:
         raise MarlinError(rc, "marlin_kv_read")
     return k, v
 
@@ -120,24 +133,24 @@ def kv4_attention_into(q: torch.Tensor, cache: Kv4Cache, batch: Kv4Batch, ws: Kv
     over the cache, which holds their own keys and values already.  scale:
     1 / sqrt(head_dim) by default; window > 0: a token sees that many positions,
     its own included."""
-    table, max_pages, lengths, q_start, B, T = batch._args
-    _check_heads(q, "q", T, None, cache)
-    _check_heads(out, "out", T, q.shape[1], cache)
-    if not out.is_contiguous():
+    qs, shape = q.stride(), q.shape
+    if (q.dtype is not torch.float16 or len(shape) != 3 or shape[0] != batch.tokens or shape[2] != cache.head_dim
+            or qs[2] != 1 or not q.is_cuda):
+        _explain("q", q, batch.tokens, None, cache)
+    if out.dtype is not torch.float16 or out.shape != shape or not out.is_contiguous() or not out.is_cuda:
+        _explain("out", out, batch.tokens, shape[1], cache)
         raise ValueError("out must be contiguous")
-    _on_current_device(("q", q), ("cache", cache.buf), ("page_table", batch.page_table), ("workspace", ws.buf),
-                       ("out", out))
-    rc = _binding.load().marlin_kv_attention(
-        q.data_ptr(), q.stride(0), q.stride(1), q.shape[1], cache.buf.data_ptr(), cache.n_pages, cache.kv_heads,
-        cache.head_dim, cache.page_size, table, max_pages, lengths, q_start, B, T, batch.max_q,
-        1.0 / math.sqrt(cache.head_dim) if scale is None else scale, window, out.data_ptr(), ws.ptr, ws.nbytes,
-        _stream() or None)
-    if rc != _binding.OK:
+    cur = _on_device(cache, batch, ws, ("q", q), ("out", out))
+    rc = (_binding._lib or _binding.load()).marlin_kv_attention(
+        q.data_ptr(), qs[0], qs[1], shape[1], *cache._args, *batch._args, batch.max_q,
+        cache._scale if scale is None else scale, window, out.data_ptr(), ws._ptr, ws.nbytes,
+        torch._C._cuda_getCurrentRawStream(cur))
+    if rc:
         raise MarlinError(rc, "marlin_kv_attention")
     return out
 
 
 def kv4_attention(q: torch.Tensor, cache: Kv4Cache, batch: Kv4Batch, ws: Kv4Workspace, scale: float | None = None,
                   window: int = 0) -> torch.Tensor:
-    out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+    out = q.new_empty(q.shape)
     return kv4_attention_into(q, cache, batch, ws, out, scale, window)

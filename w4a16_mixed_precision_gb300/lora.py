@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import torch
 
-from . import Workspace, _binding, _need_cuda, _on_current_device, _stream
+from . import Workspace, _binding, _need_cuda, _on_current_device
 from ._binding import MarlinError
 
 MAX_RANK = 128
@@ -39,6 +39,8 @@ class LoraBank:
             a, b = torch.nn.functional.pad(a, (0, 0, 0, pad)), torch.nn.functional.pad(b, (0, pad))
         self.a, self.b, self.scaling = a.contiguous(), b.contiguous(), scaling.contiguous()
         self.n, self.r, self.K, self.N = n, r + pad, K, b.shape[1]
+        self._device = self.a.get_device()
+        self._args = (self.a.data_ptr(), self.b.data_ptr(), self.scaling.data_ptr(), n, self.r)
 
     @classmethod
     def stack(cls, adapters) -> "LoraBank":
@@ -69,23 +71,30 @@ def lora_gemm_into(x: torch.Tensor, w, bank: LoraBank, index: torch.Tensor, ws: 
                    y: torch.Tensor) -> torch.Tensor:
     """y[M, N] = x[M, K] . dequant(W) + the part of each row's adapter, fp16, on
     the current stream.  index: int32 [M], negative for no adapter."""
-    _need_cuda(x, "x", torch.float16)
-    _need_cuda(y, "y", torch.float16)
-    _need_cuda(index, "index", torch.int32)
-    M, K = x.shape
-    if K != w.K or K != bank.K or w.N != bank.N or tuple(y.shape) != (M, w.N) or tuple(index.shape) != (M,):
+    f16, K = torch.float16, w.K
+    M = x.shape[0]
+    if x.dtype is not f16 or y.dtype is not f16 or index.dtype is not torch.int32 or not (
+            x.is_contiguous() and y.is_contiguous() and index.is_contiguous()):
+        _need_cuda(x, "x", f16)
+        _need_cuda(y, "y", f16)
+        _need_cuda(index, "index", torch.int32)
+    if x.shape != (M, K) or K != bank.K or w.N != bank.N or y.shape != (M, w.N) or index.shape != (M,):
         raise ValueError("shape mismatch")
-    _on_current_device(("x", x), ("weights", w.buf), ("adapters", bank.a), ("index", index), ("workspace", ws.buf),
-                       ("y", y))
-    rc = _binding.load().marlin_lora_gemm(
-        x.data_ptr(), w.codes_ptr, w.scales_ptr, w.zeros_ptr, bank.a.data_ptr(), bank.b.data_ptr(),
-        bank.scaling.data_ptr(), index.data_ptr(), bank.n, bank.r, y.data_ptr(), M, K, w.N, w.group, ws.ptr, ws.nbytes,
-        _stream() or None)
-    if rc != _binding.OK:
+    cur = torch._C._cuda_getDevice()
+    if not (x.get_device() == y.get_device() == index.get_device() == w.buf.get_device() == bank._device
+            == ws.buf.get_device() == cur):
+        for name, t in (("x", x), ("y", y), ("index", index)):
+            _need_cuda(t, name)
+        _on_current_device(("x", x), ("weights", w.buf), ("adapters", bank.a), ("index", index), ("workspace", ws.buf),
+                           ("y", y))
+    rc = (_binding._lib or _binding.load()).marlin_lora_gemm(
+        x.data_ptr(), w.codes_ptr, w.scales_ptr, w.zeros_ptr, *bank._args[:3], index.data_ptr(), *bank._args[3:],
+        y.data_ptr(), M, K, w.N, w.group, ws.buf.data_ptr(), ws.nbytes, torch._C._cuda_getCurrentRawStream(cur))
+    if rc:
         raise MarlinError(rc, "marlin_lora_gemm")
     return y
 
 
 def lora_gemm(x: torch.Tensor, w, bank: LoraBank, index: torch.Tensor, ws: LoraWorkspace) -> torch.Tensor:
-    y = torch.empty((x.shape[0], w.N), dtype=torch.float16, device=x.device)
+    y = x.new_empty((x.shape[0], w.N))
     return lora_gemm_into(x, w, bank, index, ws, y)
