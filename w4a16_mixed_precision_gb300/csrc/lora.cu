@@ -100,7 +100,7 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
 // CTAs of the cluster (parts of K, then of N); clusters that share the passes.
 // kBoth: both products (MT = 1); else v and unit go to the workspace.
 template <int MT, int NT, bool kBoth>
-__global__ void __launch_bounds__(kWarps * 32, NT <= 8 ? 2 : 1) lora_kernel(const LoraParams p) {
+__global__ void __launch_bounds__(kWarps * 32, NT <= 2 || !kBoth && NT <= 8 ? 2 : 1) lora_kernel(const LoraParams p) {
   constexpr int kRows = 16 * MT, kRanks = 8 * NT, kRp = (kRanks + 15) / 16 * 16, kAcc = MT * NT * 4;
   // half of the warps leave their sums to the other half, three times; then the CTA's sum
   __shared__ float red[kWarps / 2][kAcc][32];
@@ -250,25 +250,33 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 8 ? 2 : 1) lora_kernel(cons
 
   // ---- y += v . B^T: this warp's groups of 32 columns ------------------------------------
   if constexpr (kBoth) {
-    constexpr int kAhead = 4;  // (group, pass, step) triples whose loads are in flight
+    constexpr int kAhead = 4;                  // (group, pass, step) triples whose loads are in flight
+    constexpr int kRanksStep = NT >= 4 ? 32 : 16, kHalves = kRanksStep / 16;  // ranks of a step: 8 or 16 bytes a lane
     const int groups = p.N / 32, parts = p.splits * kWarps, part = rank * kWarps + warp;
     const int n_first = groups * part / parts, n_last = groups * (part + 1) / parts;
-    const int steps = (p.r + 15) / 16;
+    const int steps = (p.r + kRanksStep - 1) / kRanksStep;
     // operand column g of tile t is output column 8 (g / 2) + 2 t + g % 2 of the
     // group's 32, so that a lane's results are 8 consecutive columns of y
-    const uint16_t* b = p.b + (long long)(8 * (g >> 1) + (g & 1)) * p.r + 4 * c;
+    const uint16_t* b = p.b + (long long)(8 * (g >> 1) + (g & 1)) * p.r + 4 * kHalves * c;
     uint16_t* y0 = p.y + (long long)row0 * p.N + 8 * c;
-    uint2 br[kAhead][4];
+    uint32_t br[kAhead][4][2 * kHalves];
     uint4 y[kAhead][2];  // with a group's last triple: its rows g and g + 8
     int load_n = n_first, load_pass = 0, load_step = 0;
-    auto load = [&](uint2(&bq)[4], uint4(&yq)[2]) {
+    auto load = [&](uint32_t(&bq)[4][2 * kHalves], uint4(&yq)[2]) {
       if (load_n >= n_last) return;
       const int ad = __shfl_sync(0xffffffffu, pass_ad, load_pass);
-      const bool in = 16 * load_step + 4 * c < p.r;
-      const uint16_t* src = b + ((long long)ad * p.N + 32 * load_n) * p.r + 16 * load_step;
+      const bool in = kRanksStep * load_step + 4 * kHalves * c < p.r;
+      const uint16_t* src = b + ((long long)ad * p.N + 32 * load_n) * p.r + kRanksStep * load_step;
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-        bq[t] = in ? __ldg(reinterpret_cast<const uint2*>(src + 2 * t * p.r)) : make_uint2(0u, 0u);
+      for (int t = 0; t < 4; ++t) {
+        if constexpr (kHalves == 2) {
+          const uint4 q = in ? __ldg(reinterpret_cast<const uint4*>(src + 2 * t * p.r)) : make_uint4(0u, 0u, 0u, 0u);
+          bq[t][0] = q.x; bq[t][1] = q.y; bq[t][2] = q.z; bq[t][3] = q.w;
+        } else {
+          const uint2 q = in ? __ldg(reinterpret_cast<const uint2*>(src + 2 * t * p.r)) : make_uint2(0u, 0u);
+          bq[t][0] = q.x; bq[t][1] = q.y;
+        }
+      }
       if (++load_step < steps) return;
       load_step = 0;
       if (++load_pass < passes) return;
@@ -292,11 +300,16 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 8 ? 2 : 1) lora_kernel(cons
       for (int q = 0; q < kAhead; ++q) {
         if (n < n_last) {  // uniform
           const uint32_t rows = __shfl_sync(0xffffffffu, pass_rows, pass);
-          uint2 v0 = make_uint2(0u, 0u), v1 = v0;
-          if ((rows >> g) & 1u) v0 = *reinterpret_cast<const uint2*>(&v[g][16 * step + 4 * c]);
-          if ((rows >> (g + 8)) & 1u) v1 = *reinterpret_cast<const uint2*>(&v[g + 8][16 * step + 4 * c]);
 #pragma unroll
-          for (int t = 0; t < 4; ++t) mma16816(acc[t], v0.x, v1.x, v0.y, v1.y, br[q][t].x, br[q][t].y);
+          for (int d = 0; d < kHalves; ++d) {
+            const int at = kRanksStep * step + 4 * kHalves * c + 4 * d;
+            uint2 v0 = make_uint2(0u, 0u), v1 = v0;
+            if ((rows >> g) & 1u) v0 = *reinterpret_cast<const uint2*>(&v[g][at]);
+            if ((rows >> (g + 8)) & 1u) v1 = *reinterpret_cast<const uint2*>(&v[g + 8][at]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+              mma16816(acc[t], v0.x, v1.x, v0.y, v1.y, br[q][t][2 * d], br[q][t][2 * d + 1]);
+          }
           if (++step == steps) {
             step = 0;
             if (++pass == passes) {
