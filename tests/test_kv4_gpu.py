@@ -362,7 +362,7 @@ def test_one_workspace_for_many_shapes():
                                                 ([200], [200], 4, 2), ([5000], [1], 8, 2), ([64] * 9, [1] * 9, 8, 2)]):
         D, page = 64, 16
         k, v, cache, batch, hist = make(lens, nq, hkv, D, page, seed=30 + seed)
-        ws = ws or w4.Kv4Workspace(batch, 16, cache)
+        ws = ws or w4.Kv4Workspace(hist, 16, cache)  # the largest of them
         w4.kv4_append(torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), cache, hist, ws)
         q = np.random.default_rng(seed).standard_normal((sum(nq), hq, D)).astype(np.float16)
         y = w4.kv4_attention(torch.from_numpy(q).cuda(), cache, batch, ws)

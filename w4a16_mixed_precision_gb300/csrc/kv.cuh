@@ -122,7 +122,9 @@ cudaError_t launch_kv_read(const KvParams& p, int D, uint16_t* k, uint16_t* v, c
 // nb: blocks of 8 query rows that share a pass over the cache (1 or 2)
 cudaError_t launch_kv_attn(const KvAttnParams& p, int D, int nb, int grid, cudaStream_t stream);
 cudaError_t kv_attn_set_smem_limit();
-cudaError_t launch_kv_prefill(const KvAttnParams& p, int D, cudaStream_t stream);
+cudaError_t launch_kv_prefill(const KvAttnParams& p, int D, int grid, cudaStream_t stream);
+// Floats of a part of an item (256 rows) that stripes cut; two for every CTA.
+constexpr int kv_prefill_part_floats(int D) { return 256 * (D + 4); }
 cudaError_t kv_prefill_set_smem_limit();
 // Warps of a CTA at most, and floats of a part in the workspace at most (16 rows).
 constexpr int kKvAttnWarps = 8;

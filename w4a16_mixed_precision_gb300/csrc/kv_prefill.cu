@@ -5,10 +5,13 @@
 // it sees, on the tensor cores; beside them one exponential and about ten other
 // instructions per pair on the fp32 pipes, and the dequantisation of every
 // block once per CTA that reads it.
-//   * A CTA (one per SM) owns two tiles of 128 query rows of one key head (the
-//     query heads that share it, for consecutive tokens) and passes over the
-//     tokens in blocks of 64, dequantised once for both.  The tiles take turns:
-//     one's softmax runs under the other's products.
+//   * An item is 256 query rows, two tiles of 128, of one key head (the query heads
+//     that share it, for consecutive tokens), which passes over the tokens it
+//     sees in blocks of 64, dequantised once for both tiles.  Every CTA (one per
+//     SM) takes an equal stripe of all items' blocks, found on the device; an
+//     item that stripes cut is finished by the last of its CTAs to arrive, in
+//     stripe order.  The blocks of a stripe's next item arrive and are
+//     dequantised while the one before is finished.
 //   * Q stays in shared memory as the A operand of S = Q K^T; S has two places in
 //     tensor memory, so that the next block's scores are there when a block's
 //     softmax is done; P replaces S as the A operand of O += P V; O stays in
@@ -168,12 +171,104 @@ struct ShapeP {
 struct CtrlP {
   uint64_t kv_full[3], kv_empty[3], raw_full[4], raw_empty[4], s_full[kTiles][2], p_full[kTiles][2], pv_done[kTiles], q_full,
       o_full, drain;
+  uint64_t part_done, verdict;
   uint32_t tmem;
   int abort;
-  int b, local;
-  KvSeq seq;
+  int last;             // whether this CTA joins the parts of an item
+  int start_b, start_h, start_tile, start_x;
+  long long sums[16], items[16];  // blocks and items of the requests of each warp
+  int longest[16];                // blocks of their longest item
   alignas(16) float vmax[3][4];  // largest value scale of each granule of a block
 };
+
+// Blocks that the rows of an item see: [lo, lo + n), one (masked) block where
+// they see nothing.
+struct Span {
+  int lo, n;
+};
+__device__ __forceinline__ Span item_span(const KvAttnParams& p, const KvSeq& s, int rows, int tile) {
+  const int r0 = tile * kRows, r1 = min(rows, r0 + kRows) - 1, first = s.len - s.nq;
+  const int lo = p.window > 0 ? max(0, first + r0 / p.group - p.window + 1) / kBlock : 0;
+  const int hi = (max(0, first + r1 / p.group + 1) + kBlock - 1) / kBlock;
+  return {lo, max(1, hi - lo)};
+}
+
+// Rows of a request, 0 where another launch takes it.
+__device__ __forceinline__ int item_rows(const KvAttnParams& p, const KvSeq& s) {
+  const int rows = s.nq * p.group;
+  return rows > p.min_rows ? rows : 0;
+}
+
+// Blocks of all items of a request and one key head, by a warp; and its longest item's.
+__device__ __forceinline__ long long request_blocks(const KvAttnParams& p, const KvSeq& s, int* longest) {
+  const int rows = item_rows(p, s), tiles = (rows + kRows - 1) / kRows;
+  long long sum = 0;
+  int most = 0;
+  for (int t = threadIdx.x & 31; t < tiles; t += 32) {
+    const int n = item_span(p, s, rows, t).n;
+    sum += n;
+    most = max(most, n);
+  }
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, m));
+  }
+  *longest = max(*longest, most);
+  return sum;
+}
+
+// A place in the stripe: block x of an item; items in the order request, key
+// head, tile (the last, longest one first).
+struct Place {
+  int b, h, tile, x;
+  int left;            // blocks of the stripe from here on
+  KvSeq seq;
+  int rows;
+  Span span;           // of the item
+};
+
+__device__ __forceinline__ void enter_item(const KvAttnParams& p, Place& c) { c.span = item_span(p, c.seq, c.rows, c.tile); }
+
+// One of an item's two tiles, in blocks [from, to) of the piece [blk0, end): those
+// that any of its rows sees; and the tokens that all of them see.
+struct Half {
+  int from, to, all_lo, all_hi;
+};
+__device__ __forceinline__ Half tile_half(const KvAttnParams& p, const Place& c, int t, int blk0, int end) {
+  const int r0 = c.tile * kRows + t * kTile, r1 = min(c.rows, r0 + kTile) - 1, first = c.seq.len - c.seq.nq;
+  const int i0 = r0 / p.group, i1 = r1 / p.group;
+  Half f;
+  f.all_lo = p.window > 0 ? first + i1 - p.window + 1 : 0;
+  f.all_hi = first + i0 + 1;
+  f.from = max(blk0, p.window > 0 ? max(0, first + i0 - p.window + 1) / kBlock : 0);
+  f.to = r0 < c.rows ? min(end, (max(0, first + i1 + 1) + kBlock - 1) / kBlock) : f.from;
+  if (f.to < f.from) f.to = f.from;
+  return f;
+}
+
+// Moves on by `by` blocks, to the end of the item at most.
+__device__ __forceinline__ void move_on(const KvAttnParams& p, Place& c, int by) {
+  c.x += by;
+  c.left -= by;
+  if (c.x < c.span.n || c.left <= 0) return;
+  c.x = 0;
+  if (--c.tile < 0) {
+    if (++c.h == p.kv.hkv) {
+      c.h = 0;
+      do {
+        if (++c.b >= p.kv.B) {
+          c.left = 0;
+          return;
+        }
+        c.seq = kv_seq(p.kv, c.b, false);
+        c.rows = item_rows(p, c.seq);
+      } while (c.rows == 0);
+    }
+    c.tile = (c.rows + kRows - 1) / kRows - 1;
+  }
+  enter_item(p, c);
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnParams p) {
@@ -203,55 +298,34 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       mbar_init(bar(ctrl.pv_done[t]), 1);
     }
     mbar_init(bar(ctrl.q_full), kSoftmaxWarps);
+    mbar_init(bar(ctrl.part_done), kSoftmaxWarps);
+    mbar_init(bar(ctrl.verdict), 1);
     mbar_init(bar(ctrl.o_full), 1);
     mbar_init(bar(ctrl.drain), 1);
     ctrl.abort = 0;
+    ctrl.start_b = -1;
     fence_mbarrier_init();
     griddep_launch_dependents();
   }
   kv_prefetch_plan(p.kv, (long long)blockIdx.x * kThreadsP + tid);
   griddep_wait();
-  // ---- this CTA's rows: the requests' tiles in order, the last (longest) tile first ------
-  if (warp == 0) {
-    long long left = blockIdx.x;
-    int b = -1;
-    KvSeq mine{0, 0, 0};
-    for (int b0 = 0; b0 < p.kv.B && b < 0; b0 += 32) {
-      KvSeq s{0, 0, 0};
-      long long n = 0;
-      if (b0 + lane < p.kv.B) {
-        s = kv_seq(p.kv, b0 + lane, blockIdx.x == 0);
-        if (s.nq > s.len && blockIdx.x == 0) kv_fail(p.kv, kKvSiteLen);
-        const long long rows = (long long)s.nq * p.group;
-        if (rows > p.min_rows) n = (rows + kRows - 1) / kRows * p.kv.hkv;
-      }
-      long long upto = n;
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, upto, m);
-        if (lane >= m) upto += o;
-      }
-      const uint32_t hit = __ballot_sync(0xffffffffu, left < upto);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        b = b0 + src;
-        left -= __shfl_sync(0xffffffffu, upto - n, src);
-        mine.q0 = __shfl_sync(0xffffffffu, s.q0, src);
-        mine.nq = __shfl_sync(0xffffffffu, s.nq, src);
-        mine.len = __shfl_sync(0xffffffffu, s.len, src);
-      } else {
-        left -= __shfl_sync(0xffffffffu, upto, 31);
-      }
-    }
-    if (lane == 0) {
-      ctrl.b = b;
-      ctrl.local = (int)left;
-      ctrl.seq = mine;
-    }
+  // ---- this CTA's stripe ------------------------------------------------------------------
+  // every warp sums a run of requests; the warp whose run holds the stripe's first block finds it
+  constexpr int kWarps = kThreadsP / 32;
+  const int per = (p.kv.B + kWarps - 1) / kWarps, b_from = min(warp * per, p.kv.B), b_to = min(b_from + per, p.kv.B);
+  long long mine = 0, mine_items = 0;
+  int longest = 0;
+  for (int b = b_from; b < b_to; ++b) {
+    const KvSeq q = kv_seq(p.kv, b, blockIdx.x == 0 && lane == 0);
+    if (q.nq > q.len && blockIdx.x == 0 && lane == 0) kv_fail(p.kv, kKvSiteLen);
+    mine += p.kv.hkv * request_blocks(p, q, &longest);
+    mine_items += (long long)p.kv.hkv * ((item_rows(p, q) + kRows - 1) / kRows);
   }
-  __syncthreads();
-  const int b = ctrl.b;
-  if (b < 0) return;
+  if (lane == 0) {
+    ctrl.sums[warp] = mine;
+    ctrl.items[warp] = mine_items;
+    ctrl.longest[warp] = longest;
+  }
   if (warp == kSoftmaxWarps + kDequantWarps) {
     tmem_alloc(smem_addr(&ctrl.tmem), kTmem);
     tmem_relinquish();
@@ -260,80 +334,156 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctrl.tmem;
-  const KvSeq seq = ctrl.seq;
-  const WaitCtx wc{&ctrl.abort, p.kv.status, p.timeout_ns};
-
-  const int rows = seq.nq * p.group, tiles = (rows + kRows - 1) / kRows;
-  const int h = ctrl.local % p.kv.hkv, row0 = (tiles - 1 - ctrl.local / p.kv.hkv) * kRows;
-  const int first = seq.len - seq.nq;  // position of the first new token
-  // per tile: tokens any row sees [any_lo, any_hi), tokens every row sees [all_lo,
-  // all_hi), and the blocks of the former [from, to)
-  int all_lo[kTiles], all_hi[kTiles], from[kTiles], to[kTiles];
-  int blk0 = 0x7FFFFFFF, end = 0;
+  long long U = 0, before = 0, all_items = 0, items_before = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w == warp) {
+      before = U;
+      items_before = all_items;
+    }
+    U += ctrl.sums[w];
+    all_items += ctrl.items[w];
+    longest = max(longest, ctrl.longest[w]);
+  }
+  // Few items of moderate length: a CTA each, none is cut (publishing and joining
+  // parts costs about as much as four blocks).
+  const bool by_item = all_items <= (long long)gridDim.x && longest <= U / gridDim.x + 4;
+  const long long G = by_item ? all_items : min((long long)gridDim.x, U);
+  const bool works = (long long)blockIdx.x < G;
+  const long long u_begin = works && !by_item ? stripe_begin(blockIdx.x, U, G) : 0;
+  const long long u_end = works && !by_item ? stripe_begin(blockIdx.x + 1, U, G) : 0;
+  const long long at_unit = by_item ? blockIdx.x : u_begin;
+  const long long from_unit = by_item ? items_before : before;
+  if (works && at_unit >= from_unit && at_unit < from_unit + (by_item ? mine_items : mine)) {
+    long long off = at_unit - from_unit;
+    for (int b = b_from; b < b_to; ++b) {
+      const KvSeq q = kv_seq(p.kv, b, false);
+      const int rows = item_rows(p, q), tiles = (rows + kRows - 1) / kRows;
+      const long long one = by_item ? tiles : request_blocks(p, q, &longest);
+      if (off >= one * p.kv.hkv) {
+        off -= one * p.kv.hkv;
+        continue;
+      }
+      const int h = (int)(off / one);
+      off -= h * one;
+      if (by_item) {
+        if (lane == 0) {
+          ctrl.start_b = b;
+          ctrl.start_h = h;
+          ctrl.start_tile = tiles - 1 - (int)off;
+          ctrl.start_x = 0;
+        }
+        break;
+      }
+      for (int top = (rows + kRows - 1) / kRows - 1; top >= 0; top -= 32) {  // 32 tiles at a time, downwards
+        const int n = top >= lane ? item_span(p, q, rows, top - lane).n : 0;
+        int upto = n;
 #pragma unroll
-  for (int t = 0; t < kTiles; ++t) {
-    const int r0 = row0 + t * kTile, r1 = min(rows, r0 + kTile) - 1;  // first and last row
-    const int i0 = r0 / p.group, i1 = r1 / p.group;
-    const int any_lo = p.window > 0 ? max(0, first + i0 - p.window + 1) : 0, any_hi = first + i1 + 1;
-    all_lo[t] = p.window > 0 ? first + i1 - p.window + 1 : 0;
-    all_hi[t] = first + i0 + 1;
-    from[t] = any_lo / kBlock;
-    to[t] = r0 < rows && any_hi > 0 ? (any_hi + kBlock - 1) / kBlock : from[t];
-    if (to[t] > from[t]) {
-      blk0 = min(blk0, from[t]);
-      end = max(end, to[t]);
+        for (int m = 1; m < 32; m <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, upto, m);
+          if (lane >= m) upto += o;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, off < upto);
+        if (hit) {
+          if (lane == __ffs(hit) - 1) {
+            ctrl.start_b = b;
+            ctrl.start_h = h;
+            ctrl.start_tile = top - lane;
+            ctrl.start_x = (int)off - (upto - n);
+          }
+          break;
+        }
+        off -= __shfl_sync(0xffffffffu, upto, 31);
+      }
+      break;
     }
   }
-  const int n = end > 0 ? end - blk0 : 0;  // blocks of the CTA; 0 where no row sees anything
+  __syncthreads();
+  const WaitCtx wc{&ctrl.abort, p.kv.status, p.timeout_ns};
+  Place at{};
+  at.b = ctrl.start_b;
+  if (at.b >= 0) {
+    at.h = ctrl.start_h;
+    at.tile = ctrl.start_tile;
+    at.x = ctrl.start_x;
+    at.seq = kv_seq(p.kv, at.b, false);
+    at.rows = item_rows(p, at.seq);
+    enter_item(p, at);
+    at.left = by_item ? at.span.n : (int)(u_end - u_begin);
+  }
 
   if (warp < kSoftmaxWarps) {
     // ================= softmax: a query row per thread =================
     const int tile = warp / kTileWarps;
-    const int row = row0 + warp * 32 + lane;
-    const bool live = row < rows;
+    const uint32_t lanes = tmem + (uint32_t)(tile * kTileCols) + ((uint32_t)((warp % kTileWarps) * 32) << 16);
+    // a row of D fp16 is moved by kLanes lanes of 16 bytes
+    constexpr int kLanes = D / 8, kPerRound = 32 / kLanes, kRounds = 32 / kPerRound;
+    bool ok = true;
+    int stage = 0;          // of the next block of the stripe
+    int jt = 0;             // blocks of this tile so far: its places and phases
+    int items = 0, cuts = 0;
+    long long u = u_begin;  // first block of the piece
+    while (ok && at.left > 0) {
+    const KvSeq seq = at.seq;
+    const int x1 = min(at.span.n, at.x + at.left), pieces = x1 - at.x;  // blocks at.x .. x1 - 1 of the item
+    const int first = seq.len - seq.nq, row = at.tile * kRows + warp * 32 + lane;
+    const bool live = row < at.rows;
     const int i = live ? row / p.group : 0;
-    const int head = h * p.group + (live ? row - i * p.group : 0);
+    const int head = at.h * p.group + (live ? row - i * p.group : 0);
     const int pos = first + i;
     const int hi = live ? pos + 1 : 0, lo = p.window > 0 ? pos - p.window + 1 : 0;  // tokens seen
-    const uint32_t lanes = tmem + (uint32_t)(tile * kTileCols) + ((uint32_t)((warp % kTileWarps) * 32) << 16);
+    const Half half_ = tile_half(p, at, tile, at.span.lo + at.x, at.span.lo + x1);
 
-    // Q to shared memory, channels in the codes' order; the row's sum
+    // Q to shared memory, channels in the codes' order: the warp's 32 rows, kLanes lanes a
+    // row (whole lines of global memory); then every row's sum
+    const int wrow = (warp % kTileWarps) * 32;  // the warp's first row of the tile
+    const long long row_at = live ? (long long)(seq.q0 + i) * p.q_ts + (long long)head * p.q_hs : -1;
     float qsum = 0.f;
     {
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(seq.q0 + i) * p.q_ts + (long long)head * p.q_hs);
-      const int r = row - row0 - tile * kTile;
-      const uint32_t qt = base + Sh::kOffQ + tile * Sh::kQ + r * 128;
+      const uint32_t qt = base + Sh::kOffQ + tile * Sh::kQ;
+      constexpr int kTogether = 8;  // loads in flight
+#pragma unroll 1
+      for (int it = 0; it < kRounds; it += kTogether) {
+        uint4 v[kTogether];
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j) {
-        const uint4 v = live ? src[j] : make_uint4(0u, 0u, 0u, 0u);
-        const float2 a = unpack(v.x), bb = unpack(v.y), cc = unpack(v.z), dd = unpack(v.w);
-        qsum += ((a.x + a.y) + (bb.x + bb.y)) + ((cc.x + cc.y) + (dd.x + dd.y));
-        sts128(qt + (j / 8) * (kTile * 128) + (((j & 7) ^ (r & 7)) << 4),
-               make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                          __byte_perm(v.y, v.w, 0x7632)));
+        for (int k = 0; k < kTogether; ++k) {
+          const long long from = __shfl_sync(0xffffffffu, row_at, (it + k) * kPerRound + lane / kLanes);
+          v[k] = from >= 0 ? *reinterpret_cast<const uint4*>(p.q + from + 8 * (lane % kLanes)) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k) {
+          const int r = wrow + (it + k) * kPerRound + lane / kLanes, u = lane % kLanes;
+          sts128(qt + (u / 8) * (kTile * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4),
+                 make_uint4(__byte_perm(v[k].x, v[k].z, 0x5410), __byte_perm(v[k].y, v[k].w, 0x5410),
+                            __byte_perm(v[k].x, v[k].z, 0x7632), __byte_perm(v[k].y, v[k].w, 0x7632)));
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(ctrl.q_full));
+      const int r = wrow + lane;
+#pragma unroll
+      for (int u = 0; u < kLanes; ++u) {
+        const uint4 v = lds128(qt + (u / 8) * (kTile * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4));
+        const float2 a = unpack(v.x), bb = unpack(v.y), cc = unpack(v.z), dd = unpack(v.w);
+        qsum += ((a.x + a.y) + (bb.x + bb.y)) + ((cc.x + cc.y) + (dd.x + dd.y));
+      }
     }
     const F2 qs = dup(qsum);
 
     float R = live ? kUnset : 0.f;
     F2 l = dup(0.f), pz = dup(0.f);
-    bool ok = true;
-    const int my_from = tile ? from[1] : from[0], my_n = (tile ? to[1] : to[0]) - my_from;
-    const int my_all_lo = tile ? all_lo[1] : all_lo[0], my_all_hi = tile ? all_hi[1] : all_hi[0];
-    int stage = my_n > 0 ? (my_from - blk0) % Sh::kStages : 0;
-    for (int j = 0; j < my_n; ++j) {
-      const int t0 = (my_from + j) * kBlock;
-      const uint32_t s_col = lanes + Sh::kColS + (j & 1) * kBlock;
-      if (!wait_warp(bar(ctrl.s_full[tile][j & 1]), (uint32_t)((j >> 1) & 1), wc)) {
+    const int skipped = half_.to > half_.from ? half_.from - (at.span.lo + at.x) : 0;
+    int st = (stage + skipped) % Sh::kStages;
+    for (int blk = half_.from; ok && blk < half_.to; ++blk, ++jt) {
+      const int t0 = blk * kBlock;
+      const uint32_t s_col = lanes + Sh::kColS + (jt & 1) * kBlock;
+      if (!wait_warp(bar(ctrl.s_full[tile][jt & 1]), (uint32_t)((jt >> 1) & 1), wc)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const float4* par = reinterpret_cast<const float4*>(par0 + stage * (Sh::kPar / 4));
-      const bool full = t0 >= my_all_lo && t0 + kBlock <= my_all_hi;
+      const float4* par = reinterpret_cast<const float4*>(par0 + st * (Sh::kPar / 4));
+      const bool full = t0 >= half_.all_lo && t0 + kBlock <= half_.all_hi;
       uint32_t P[32];
       F2 lt, pzt;
       float over;
@@ -401,7 +551,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
             if (at + 1 < hi && at + 1 >= lo) top = fmaxf(top, x.y);
           }
         }
-        const float4 vm = *reinterpret_cast<const float4*>(ctrl.vmax[stage]);
+        const float4 vm = *reinterpret_cast<const float4*>(ctrl.vmax[st]);
         const float big = fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w));
         const float scale = (float)max((int)(__float_as_uint(big) >> 23) - 126, -30);  // log2 of a power of two above it
         float f = 1.f;
@@ -416,9 +566,9 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
         }
         l = mul2(l, dup(f));
         pz = mul2(pz, dup(f));
-        if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+        if (blk > half_.from && __any_sync(0xffffffffu, f != 1.f)) {
           // once the products of the blocks before are done (this one's follow P)
-          if (!wait_warp(bar(ctrl.pv_done[tile]), (uint32_t)((j - 1) & 1), wc)) break;
+          if (!wait_warp(bar(ctrl.pv_done[tile]), (uint32_t)((jt - 1) & 1), wc)) break;
           tc_fence_after();
 #pragma unroll 1
           for (int part = 0; part < D / 32; ++part) {
@@ -437,52 +587,144 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       tmem_st32(s_col, P);
       tmem_wait_st();
       tc_fence_before();
-      if (lane == 0) mbar_arrive(bar(ctrl.p_full[tile][j & 1]));
-      if (++stage == Sh::kStages) stage = 0;
+      if (lane == 0) mbar_arrive(bar(ctrl.p_full[tile][jt & 1]));
+      if (++st == Sh::kStages) st = 0;
     }
-    // ---- the rows' results ----
-    if (ok && wait_warp(bar(ctrl.o_full), 0, wc)) {
-      tc_fence_after();
-      const float sum = l.x + l.y, off = pz.x + pz.y;
+    // ---- the rows' results, or this CTA's part of them ----
+    if (!ok || !wait_warp(bar(ctrl.o_full), (uint32_t)(items & 1), wc)) break;
+    tc_fence_after();
+    const bool whole = at.x == 0 && x1 == at.span.n;
+    const float sum = l.x + l.y, off = pz.x + pz.y;
+    const bool any = half_.to > half_.from;  // else there is nothing of this tile in tensor memory
+    // a finished row's channels 32 part .. + 31 into Q's place, which no product reads any more
+    const uint32_t ot = base + Sh::kOffQ + tile * Sh::kQ;
+    auto keep = [&](int part, const float (&v)[32]) {
+      const int r = wrow + lane;
+#pragma unroll
+      for (int t = 0; t < 32; t += 8) {
+        const int u = part * 4 + t / 8;
+        sts128(ot + r * (D * 2) + ((u ^ (r & 7)) << 4), make_uint4(pack(v[t], v[t + 1]), pack(v[t + 2], v[t + 3]),
+                                                                   pack(v[t + 4], v[t + 5]), pack(v[t + 6], v[t + 7])));
+      }
+    };
+    // the warp's rows from there to the output, whole lines at a time
+    const long long out_at = live ? ((long long)(seq.q0 + i) * p.heads + head) * D : -1;
+    auto write_rows = [&]() {
+      __syncwarp();
+#pragma unroll 4
+      for (int it = 0; it < kRounds; ++it) {
+        const int r = it * kPerRound + lane / kLanes, u = lane % kLanes;
+        const long long to = __shfl_sync(0xffffffffu, out_at, r);
+        const uint4 v = lds128(ot + (wrow + r) * (D * 2) + ((u ^ (r & 7)) << 4));
+        if (to >= 0) *reinterpret_cast<uint4*>(p.out + to + 8 * u) = v;
+      }
+      __syncwarp();
+    };
+    if (whole) {
       const float inv = hi > 0 ? 1.f / sum : 0.f;  // a row that sees no token is zero
-      uint16_t* dst = p.out + ((long long)(seq.q0 + i) * p.heads + head) * D;
 #pragma unroll 1
       for (int part = 0; part < D / 32; ++part) {
         uint32_t v[32];
         tmem_ld32(lanes + Sh::kColO + part * 32, v);
         tmem_wait_ld();
-        if (live) {
+        float o[32];
 #pragma unroll
-          for (int t = 0; t < 32; t += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float a = (__uint_as_float(v[t + 2 * k]) + off) * inv, c = (__uint_as_float(v[t + 2 * k + 1]) + off) * inv;
-              if (inv == 0.f) a = c = 0.f;
-              w[k] = pack(a, c);
-            }
-            *reinterpret_cast<uint4*>(dst + part * 32 + t) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
+        for (int t = 0; t < 32; ++t) o[t] = inv == 0.f ? 0.f : (__uint_as_float(v[t]) + off) * inv;
+        keep(part, o);
       }
+      write_rows();
+    } else {
+      // slot 0: a piece of an item that began before this stripe; slot 1: the beginning of one.
+      // Channel-major, so that a warp's rows are written and read in whole lines.
+      constexpr int kSlot = kRows * (D + 4);
+      const int my_row = warp * 32 + lane;
+      float* slot = p.partials + (2ll * blockIdx.x + (at.x == 0 ? 1 : 0)) * kSlot + my_row;
+#pragma unroll 1
+      for (int part = 0; part < D / 32; ++part) {
+        uint32_t v[32];
+        tmem_ld32(lanes + Sh::kColO + part * 32, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int t = 0; t < 32; ++t) __stcg(slot + (part * 32 + t) * kRows, any ? __uint_as_float(v[t]) + off : 0.f);
+      }
+      __stcg(slot + D * kRows, R);
+      __stcg(slot + (D + 1) * kRows, sum);
+      // all warps have written; one thread counts this CTA in, with release and acquire for all of them
+      const long long s0 = u - at.x;  // the item's first block among all
+      const int c0 = (int)stripe_owner(s0, U, G), c1 = (int)stripe_owner(s0 + at.span.n - 1, U, G);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(ctrl.part_done));
+      if (warp == 0) {
+        if (!wait_warp(bar(ctrl.part_done), (uint32_t)(cuts & 1), wc)) break;
+        if (lane == 0) {
+          int arrived;
+          asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+                       : "=r"(arrived)
+                       : "l"(p.counters + c0)
+                       : "memory");
+          ctrl.last = arrived == c1 - c0;
+          if (ctrl.last) p.counters[c0] = 0;  // all are here: ready for the next call
+          mbar_arrive(bar(ctrl.verdict));
+        }
+        __syncwarp();
+      }
+      if (!wait_warp(bar(ctrl.verdict), (uint32_t)(cuts & 1), wc)) break;
+      ++cuts;
+      if (*reinterpret_cast<volatile int*>(&ctrl.last)) {
+        // the parts in stripe order: the first CTA's is its slot 1, the others' their slot 0
+        auto part_of = [&](int q) { return p.partials + (2ll * q + (q == c0 ? 1 : 0)) * kSlot + my_row; };
+        float top = kUnset, all = 0.f;
+        for (int q = c0; q <= c1; ++q) {
+          const float r = __ldcg(part_of(q) + D * kRows), lq = __ldcg(part_of(q) + (D + 1) * kRows);
+          const float nt = lq == 0.f ? top : fmaxf(top, r);
+          all = fmaf(all, top == nt ? 1.f : ex2(top - nt), lq == 0.f ? 0.f : r == nt ? lq : lq * ex2(r - nt));
+          top = nt;
+        }
+        const float inv = hi > 0 ? 1.f / all : 0.f;
+#pragma unroll 1
+        for (int part = 0; part < D / 32; ++part) {
+          float o[32];
+#pragma unroll
+          for (int t = 0; t < 32; ++t) o[t] = 0.f;
+#pragma unroll 1
+          for (int q = c0; q <= c1; ++q) {
+            const float r = __ldcg(part_of(q) + D * kRows), lq = __ldcg(part_of(q) + (D + 1) * kRows);
+            const float f = lq == 0.f ? 0.f : r == top ? 1.f : ex2(r - top);
+#pragma unroll
+            for (int t = 0; t < 32; ++t) o[t] = fmaf(__ldcg(part_of(q) + (part * 32 + t) * kRows), f, o[t]);
+          }
+#pragma unroll
+          for (int t = 0; t < 32; ++t) o[t] = inv == 0.f ? 0.f : o[t] * inv;
+          keep(part, o);
+        }
+        write_rows();
+      }
+    }
+    // on to the next item; its Q may replace this one's: o_full followed all products
+    tc_fence_before();
+    ++items;
+    stage = (stage + pieces) % Sh::kStages;
+    u += pieces;
+    move_on(p, at, pieces);
     }
   } else if (warp < kSoftmaxWarps + kDequantWarps) {
     // ================= dequantisation =================
     const int dw = warp - kSoftmaxWarps, g = lane >> 2, c = lane & 3;
     const int half = dw >> 1, wp = dw & 1;  // this warp's part of the values
     // warp 0 of the four keeps kRing blocks in flight: lane q < 4 copies granule q
-    const int* table = p.kv.table + (long long)b * p.kv.max_pages;
-    const uint8_t* heads = p.kv.cache + h * p.kv.head_bytes;
     const uint64_t policy = policy_evict_last();  // other CTAs read the same blocks
     const uint32_t raw = base + Sh::kOffRaw;
+    const int n = at.left;
+    Place ahead = at;  // the next block to copy
     int next_page = 0, issued = 0;
     auto look_up = [&]() {
-      const int gi = (blk0 + issued) * 4 + lane;
-      if (lane < 4 && gi * kGranule < seq.len) next_page = table[kv_div_page(p.kv, gi)];
+      const int gi = (ahead.span.lo + ahead.x) * 4 + lane;
+      if (lane < 4 && gi * kGranule < ahead.seq.len)
+        next_page = p.kv.table[(long long)ahead.b * p.kv.max_pages + kv_div_page(p.kv, gi)];
     };
     auto issue = [&]() {
-      const int gi = (blk0 + issued) * 4 + lane, slot = issued % Sh::kRing;
-      const bool inside = lane < 4 && gi * kGranule < seq.len;
+      const int gi = (ahead.span.lo + ahead.x) * 4 + lane, slot = issued % Sh::kRing;
+      const bool inside = lane < 4 && gi * kGranule < ahead.seq.len;
       const bool there = inside && (uint32_t)next_page < (uint32_t)p.kv.n_pages;
       if (inside && !there) kv_fail(p.kv, kKvSitePage);  // no copy: the results are not valid, and reported
       const int copies = __popc(__ballot_sync(0xffffffffu, there));
@@ -490,11 +732,15 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       __syncwarp();
       if (there && (lane == 0 || !p.whole_blocks))
         bulk_g2s(raw + slot * Sh::kRaw + lane * GR,
-                 heads + next_page * p.kv.page_bytes + (gi - kv_div_page(p.kv, gi) * p.kv.page16) * GR,
+                 p.kv.cache + ahead.h * p.kv.head_bytes + next_page * p.kv.page_bytes +
+                     (gi - kv_div_page(p.kv, gi) * p.kv.page16) * GR,
                  p.whole_blocks ? copies * GR : GR, bar(ctrl.raw_full[slot]), policy);
-      if (++issued < n) look_up();
+      if (++issued < n) {
+        move_on(p, ahead, 1);
+        look_up();
+      }
     };
-    if (dw == 0) {
+    if (dw == 0 && n > 0) {
       look_up();
       while (issued < min(Sh::kRing, n)) issue();
     }
@@ -512,7 +758,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
         load_words<CW / 2>(in + q * GR + 8 * D + half * (4 * D) + lane * (D / 8) + wp * (D / 16), vv[q]);
       // nothing is taken from tokens that are not written (they may hold anything)
       uint2 pr = make_uint2(0u, 0u);
-      if (lane < 16 && ((blk0 + j) * 4 + dw) * kGranule + lane < seq.len)
+      if (lane < 16 && ((at.span.lo + at.x) * 4 + dw) * kGranule + lane < at.seq.len)
         pr = *reinterpret_cast<const uint2*>(in + dw * GR + 16 * D + 8 * lane);
       if (!wait_warp(bar(ctrl.kv_empty[stage]), ph ^ 1u, wc)) break;
       const uint32_t kt = base + stage * Sh::kK, vt = base + Sh::kOffV + stage * Sh::kV;
@@ -582,6 +828,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
         }
         issue();
       }
+      move_on(p, at, 1);
       if (++stage == Sh::kStages) {
         stage = 0;
         ph ^= 1u;
@@ -594,8 +841,11 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
   } else {
     // ================= products =================
     const uint32_t id_s = umma_idesc_f16_f32(kBlock), id_o = umma_idesc_f16_f32(D);
-    int stage = 0, next = Sh::kStages > 1 ? 1 : 0;  // of block j and of the one after it
-    uint32_t next_ph = 0;
+    int stage = 0;           // of block blk
+    uint32_t ph = 0;
+    int jt[kTiles] = {0, 0};  // blocks of each tile whose products with V were issued: places and phases
+    int items = 0;
+    bool ok = true;
     // S = Q K^T of a tile's i-th block.  The place is free: the P that was there was
     // consumed by a product before, which these follow in order.
     auto scores = [&](int t, int i, int st) {
@@ -607,44 +857,57 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
                          kk > 0);
       mma_commit_elect(bar(ctrl.s_full[t][i & 1]));
     };
-    bool ok = wait_warp(bar(ctrl.q_full), 0, wc);
-    if (ok && n > 0 && (ok = wait_warp(bar(ctrl.kv_full[0]), 0, wc))) {
+    while (ok && at.left > 0) {
+      const int pieces = min(at.span.n - at.x, at.left), blk0 = at.span.lo + at.x, end = blk0 + pieces;
+      Half half_[kTiles];
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) half_[t] = tile_half(p, at, t, blk0, end);
+      // Q of this item, which the softmax warps write after the item before is done
+      if (!(ok = wait_warp(bar(ctrl.q_full), (uint32_t)(items & 1), wc))) break;
+      if (!(ok = wait_warp(bar(ctrl.kv_full[stage]), ph, wc))) break;
       tc_fence_after();
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
-        if (from[t] == blk0 && to[t] > blk0) scores(t, 0, 0);
-    }
-    for (int j = 0; ok && j < n; ++j) {
-      const int blk = blk0 + j;
-      if (j + 1 < n) {  // the next block's scores go before this one's products with V
-        if (!(ok = wait_warp(bar(ctrl.kv_full[next]), next_ph, wc))) break;
-        tc_fence_after();
+        if (half_[t].from == blk0 && half_[t].to > blk0) scores(t, jt[t], stage);
+      for (int blk = blk0; ok && blk < end; ++blk) {
+        int next = stage + 1;
+        uint32_t next_ph = ph;
+        if (next == Sh::kStages) {
+          next = 0;
+          next_ph ^= 1u;
+        }
+        if (blk + 1 < end) {  // the next block's scores go before this one's products with V
+          if (!(ok = wait_warp(bar(ctrl.kv_full[next]), next_ph, wc))) break;
+          tc_fence_after();
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
-          if (blk + 1 >= from[t] && blk + 1 < to[t]) scores(t, blk + 1 - from[t], next);
-      }
+          for (int t = 0; t < kTiles; ++t)
+            if (blk + 1 >= half_[t].from && blk + 1 < half_[t].to) scores(t, jt[t] + (blk >= half_[t].from), next);
+        }
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        const int i = blk - from[t];
-        if (!ok || i < 0 || blk >= to[t]) continue;
-        if (!(ok = wait_warp(bar(ctrl.p_full[t][i & 1]), (uint32_t)((i >> 1) & 1), wc))) continue;
-        tc_fence_after();
-        const uint32_t cols = tmem + t * kTileCols;
+        for (int t = 0; t < kTiles; ++t) {
+          if (!ok || blk < half_[t].from || blk >= half_[t].to) continue;
+          const int i = jt[t];
+          if (!(ok = wait_warp(bar(ctrl.p_full[t][i & 1]), (uint32_t)((i >> 1) & 1), wc))) continue;
+          tc_fence_after();
+          const uint32_t cols = tmem + t * kTileCols;
 #pragma unroll
-        for (int kk = 0; kk < kBlock / 16; ++kk)
-          mma_f16_ts_elect(cols + Sh::kColO, cols + Sh::kColS + (i & 1) * kBlock + kk * 8,
-                           umma_desc_sw128(base + Sh::kOffV + stage * Sh::kV) + (uint64_t)(2 * kk), id_o, i > 0 || kk > 0);
-        mma_commit_elect(bar(ctrl.pv_done[t]));
+          for (int kk = 0; kk < kBlock / 16; ++kk)
+            mma_f16_ts_elect(cols + Sh::kColO, cols + Sh::kColS + (i & 1) * kBlock + kk * 8,
+                             umma_desc_sw128(base + Sh::kOffV + stage * Sh::kV) + (uint64_t)(2 * kk), id_o,
+                             blk > half_[t].from || kk > 0);
+          mma_commit_elect(bar(ctrl.pv_done[t]));
+          ++jt[t];
+        }
+        if (!ok) break;
+        mma_commit_elect(bar(ctrl.kv_empty[stage]));
+        stage = next;
+        ph = next_ph;
       }
       if (!ok) break;
-      mma_commit_elect(bar(ctrl.kv_empty[stage]));
-      stage = next;
-      if (++next == Sh::kStages) {
-        next = 0;
-        next_ph ^= 1u;
-      }
+      mma_commit_elect(bar(ctrl.o_full));
+      ++items;
+      move_on(p, at, pieces);
     }
-    if (ok) mma_commit_elect(bar(ctrl.o_full));
     mma_commit_elect(bar(ctrl.drain));
     wait_drain(bar(ctrl.drain), 0, wc);
   }
@@ -655,10 +918,10 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
 }
 
 template <int D>
-cudaError_t launch(const KvAttnParams& p, long long grid, cudaStream_t stream) {
+cudaError_t launch(const KvAttnParams& p, int grid, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreadsP);
   cfg.dynamicSmemBytes = ShapeP<D>::kSmem;
   cfg.stream = stream;
@@ -679,9 +942,7 @@ cudaError_t kv_prefill_set_smem_limit() {
   return e;
 }
 
-cudaError_t launch_kv_prefill(const KvAttnParams& p, int D, cudaStream_t stream) {
-  // groups of 256 rows: at most one part-filled for each request
-  const long long grid = ((long long)p.kv.T * p.group / kRows + p.kv.B) * p.kv.hkv;
+cudaError_t launch_kv_prefill(const KvAttnParams& p, int D, int grid, cudaStream_t stream) {
   return D == 128 ? launch<128>(p, grid, stream) : launch<64>(p, grid, stream);
 }
 

@@ -111,18 +111,22 @@ constexpr int kPrefillRows = 64;
 
 struct AttnPlan {
   int grid, nb;
-  size_t counters_off, partials_off, firsts_off, bytes;
+  size_t counters_off, partials_off, firsts_off, prompt_off, bytes;
 };
 
-AttnPlan attn_plan(int sms, int D, int group, int max_q) {
+// [status 256 B][arrivals of both kernels][parts of the streaming kernel][parts of the
+// tcgen05 kernel, where a request can have enough rows for it]
+AttnPlan attn_plan(int sms, int D, int group, int max_q, int tokens) {
   AttnPlan a;
   a.grid = sms;
   a.nb = (long long)group * max_q > 8 ? 2 : 1;
   a.counters_off = 256;
-  a.partials_off = round_up(a.counters_off + sizeof(int) * (size_t)sms, 256);
+  a.partials_off = round_up(a.counters_off + 2 * sizeof(int) * (size_t)sms, 256);
   const size_t part = kv_attn_part_floats(D) * sizeof(float);
   a.firsts_off = a.partials_off + 2 * sms * part;
-  a.bytes = a.firsts_off + kKvAttnWarps * sms * part;
+  a.prompt_off = round_up(a.firsts_off + kKvAttnWarps * sms * part, 256);
+  a.bytes = a.prompt_off;
+  if ((long long)group * tokens > kPrefillRows) a.bytes += 2 * sms * kv_prefill_part_floats(D) * sizeof(float);
   return a;
 }
 
@@ -196,7 +200,7 @@ marlin_status_t marlin_kv_workspace_bytes(int heads, int kv_heads, int head_dim,
   int sms;
   const marlin_status_t s = static_cast<marlin_status_t>(device_sms(device, &sms));
   if (s != MARLIN_OK) return s;
-  *bytes = attn_plan(sms, head_dim, heads / kv_heads, 1).bytes;
+  *bytes = attn_plan(sms, head_dim, heads / kv_heads, 1, tokens).bytes;
   return MARLIN_OK;
 }
 
@@ -237,7 +241,8 @@ marlin_status_t marlin_kv_attention(const uint16_t* q, int64_t q_token_stride, i
   int sms;
   if ((s = current_sms(&sms)) != MARLIN_OK) return s;
   const int group = heads / kv_heads;
-  const AttnPlan a = attn_plan(sms, head_dim, group, max_q);
+  if ((long long)tokens * group > 0x7FFFFFFF) return MARLIN_ERR_UNSUPPORTED;
+  const AttnPlan a = attn_plan(sms, head_dim, group, max_q, tokens);
   if (workspace_bytes < a.bytes) return MARLIN_ERR_WORKSPACE_TOO_SMALL;
   {
     static std::mutex lock;
@@ -277,7 +282,10 @@ marlin_status_t marlin_kv_attention(const uint16_t* q, int64_t q_token_stride, i
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (some_large) {
     if (!uniform) p.min_rows = kPrefillRows;
-    if (launch_kv_prefill(p, head_dim, st) != cudaSuccess) return MARLIN_ERR_CUDA;
+    KvAttnParams f = p;
+    f.counters = p.counters + a.grid;
+    f.partials = reinterpret_cast<float*>(ws + a.prompt_off);
+    if (launch_kv_prefill(f, head_dim, a.grid, st) != cudaSuccess) return MARLIN_ERR_CUDA;
     if (uniform) return MARLIN_OK;
     p.max_rows = kPrefillRows;
   }

@@ -28,7 +28,7 @@ class Kv4Cache:
         self.nbytes = _binding.kv_cache_bytes(n_pages, kv_heads, head_dim, page_size)
         self.n_pages, self.kv_heads, self.head_dim, self.page_size = n_pages, kv_heads, head_dim, page_size
         self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=dev)
-        self._device, self._like = self.buf.get_device(), self.buf.new_empty(0, dtype=torch.float16)
+        self._device = self.buf.get_device()
         self._scale = 1.0 / math.sqrt(head_dim)
         self._args = (self.buf.data_ptr(), n_pages, kv_heads, head_dim, page_size)
 
@@ -119,7 +119,8 @@ def kv4_read(cache: Kv4Cache, batch: Kv4Batch, ws: Kv4Workspace):
     the batch's new tokens."""
     cur = _on_device(cache, batch, ws)
     shape = (batch.tokens, cache.kv_heads, cache.head_dim)
-    k, v = cache._like.new_empty(shape), cache._like.new_empty(shape)
+    k = torch.empty(shape, dtype=torch.float16, device=cache.buf.device)
+    v = torch.empty_like(k)
     rc = (_binding._lib or _binding.load()).marlin_kv_read(
         k.data_ptr(), v.data_ptr(), *cache._args, *batch._args, ws._ptr, torch._C._cuda_getCurrentRawStream(cur))
     if rc:
@@ -152,5 +153,5 @@ def kv4_attention_into(q: torch.Tensor, cache: Kv4Cache, batch: Kv4Batch, ws: Kv
 
 def kv4_attention(q: torch.Tensor, cache: Kv4Cache, batch: Kv4Batch, ws: Kv4Workspace, scale: float | None = None,
                   window: int = 0) -> torch.Tensor:
-    out = q.new_empty(q.shape)
+    out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
     return kv4_attention_into(q, cache, batch, ws, out, scale, window)

@@ -96,5 +96,5 @@ def lora_gemm_into(x: torch.Tensor, w, bank: LoraBank, index: torch.Tensor, ws: 
 
 
 def lora_gemm(x: torch.Tensor, w, bank: LoraBank, index: torch.Tensor, ws: LoraWorkspace) -> torch.Tensor:
-    y = x.new_empty((x.shape[0], w.N))
+    y = torch.empty((x.shape[0], w.N), dtype=torch.float16, device=x.device)
     return lora_gemm_into(x, w, bank, index, ws, y)
