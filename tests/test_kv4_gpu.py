@@ -181,6 +181,24 @@ def test_attention(lens, nq, hq, hkv, D, page, window):
         close(yy, kv_ref.attention(qq, kv[b], vv[b], nq[b], D ** -0.5, window), vv[b])
 
 
+LONG_PROMPTS = [
+    # few items of many tokens: cut over CTAs and joined
+    ([3000], [100], 7, 1, 128, 16, 0),
+    ([2500, 40, 3100], [70, 40, 90], 8, 2, 64, 32, 0),
+    ([4000, 2900], [150, 300], 2, 1, 128, 64, 2600),
+    ([6001], [65], 16, 1, 64, 48, 0),                     # one item but a little
+    # more items than SMs: a CTA for each, and CTAs without one
+    ([90] * 22, [80] * 22, 8, 8, 64, 16, 0),
+    ([200, 1, 75, 40] * 9, [100, 1, 75, 33] * 9, 8, 8, 128, 32, 0),
+    ([300] * 40, [70] * 40, 12, 6, 64, 64, 100),
+]
+
+
+@pytest.mark.parametrize("lens,nq,hq,hkv,D,page,window", LONG_PROMPTS)
+def test_prompts_cut_over_ctas_and_a_cta_each(lens, nq, hq, hkv, D, page, window):
+    test_attention(lens, nq, hq, hkv, D, page, window)
+
+
 @pytest.mark.parametrize("spread", [1e-3, 30.0])
 def test_attention_of_small_and_large_values(spread):
     """Value scales near fp16's small numbers, and scores so peaked that one token takes all."""

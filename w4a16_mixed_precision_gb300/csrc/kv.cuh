@@ -104,6 +104,8 @@ struct KvAttnParams {
   long long q_ts, q_hs;     // elements
   uint16_t* out;            // fp16 [T][heads][D]
   int heads, group;         // query heads, and of them per key head
+  int stripes;              // CTAs that share all items of the prompt kernel where these are cut
+  unsigned long long group_magic;  // floor(2^64 / group) + 1, 0 for group = 1
   int window;               // > 0: a query sees that many positions, its own included
   float scale_log2;         // softmax scale * log2(e)
   int whole_blocks;         // pages hold whole blocks: one copy each
@@ -115,6 +117,11 @@ struct KvAttnParams {
   unsigned long long timeout_ns;
 };
 
+// row / group, exact for 32-bit rows.
+__device__ __forceinline__ int kv_div_group(const KvAttnParams& p, int row) {
+  return p.group_magic ? (int)__umul64hi((unsigned long long)(uint32_t)row, p.group_magic) : row;
+}
+
 cudaError_t launch_kv_append(const KvParams& p, int D, const uint16_t* k, const uint16_t* v, const long long (&st)[4],
                              cudaStream_t stream);
 cudaError_t launch_kv_read(const KvParams& p, int D, uint16_t* k, uint16_t* v, const long long (&st)[4],
@@ -123,6 +130,10 @@ cudaError_t launch_kv_read(const KvParams& p, int D, uint16_t* k, uint16_t* v, c
 cudaError_t launch_kv_attn(const KvAttnParams& p, int D, int nb, int grid, cudaStream_t stream);
 cudaError_t kv_attn_set_smem_limit();
 cudaError_t launch_kv_prefill(const KvAttnParams& p, int D, int grid, cudaStream_t stream);
+// Items (256 rows of a request and key head) at most: one part-filled for each request.
+constexpr long long kv_prefill_items(long long tokens, int requests, int hkv, int group) {
+  return (tokens * group / 256 + requests) * hkv;
+}
 // Floats of a part of an item (256 rows) that stripes cut; two for every CTA.
 constexpr int kv_prefill_part_floats(int D) { return 256 * (D + 4); }
 cudaError_t kv_prefill_set_smem_limit();

@@ -7,11 +7,11 @@
 // block once per CTA that reads it.
 //   * An item is 256 query rows, two tiles of 128, of one key head (the query heads
 //     that share it, for consecutive tokens), which passes over the tokens it
-//     sees in blocks of 64, dequantised once for both tiles.  Every CTA (one per
-//     SM) takes an equal stripe of all items' blocks, found on the device; an
-//     item that stripes cut is finished by the last of its CTAs to arrive, in
-//     stripe order.  The blocks of a stripe's next item arrive and are
-//     dequantised while the one before is finished.
+//     sees in blocks of 64, dequantised once for both tiles.  A CTA (one per SM)
+//     takes one item, or, where there would be few or long ones, an equal stripe
+//     of all items' blocks; the rule is at find_item.  Either is found on the
+//     device.  An item that stripes cut is finished by the last of its CTAs to
+//     arrive, in stripe order.
 //   * Q stays in shared memory as the A operand of S = Q K^T; S has two places in
 //     tensor memory, so that the next block's scores are there when a block's
 //     softmax is done; P replaces S as the A operand of O += P V; O stays in
@@ -175,6 +175,7 @@ struct CtrlP {
   uint32_t tmem;
   int abort;
   int last;             // whether this CTA joins the parts of an item
+  int by_item;          // whether a CTA takes one whole item
   int start_b, start_h, start_tile, start_x;
   long long sums[16], items[16];  // blocks and items of the requests of each warp
   int longest[16];                // blocks of their longest item
@@ -188,8 +189,8 @@ struct Span {
 };
 __device__ __forceinline__ Span item_span(const KvAttnParams& p, const KvSeq& s, int rows, int tile) {
   const int r0 = tile * kRows, r1 = min(rows, r0 + kRows) - 1, first = s.len - s.nq;
-  const int lo = p.window > 0 ? max(0, first + r0 / p.group - p.window + 1) / kBlock : 0;
-  const int hi = (max(0, first + r1 / p.group + 1) + kBlock - 1) / kBlock;
+  const int lo = p.window > 0 ? max(0, first + kv_div_group(p, r0) - p.window + 1) / kBlock : 0;
+  const int hi = (max(0, first + kv_div_group(p, r1) + 1) + kBlock - 1) / kBlock;
   return {lo, max(1, hi - lo)};
 }
 
@@ -237,7 +238,7 @@ struct Half {
 };
 __device__ __forceinline__ Half tile_half(const KvAttnParams& p, const Place& c, int t, int blk0, int end) {
   const int r0 = c.tile * kRows + t * kTile, r1 = min(c.rows, r0 + kTile) - 1, first = c.seq.len - c.seq.nq;
-  const int i0 = r0 / p.group, i1 = r1 / p.group;
+  const int i0 = kv_div_group(p, r0), i1 = kv_div_group(p, r1);
   Half f;
   f.all_lo = p.window > 0 ? first + i1 - p.window + 1 : 0;
   f.all_hi = first + i0 + 1;
@@ -268,6 +269,70 @@ __device__ __forceinline__ void move_on(const KvAttnParams& p, Place& c, int by)
     c.tile = (c.rows + kRows - 1) / kRows - 1;
   }
   enter_item(p, c);
+}
+
+// The blockIdx.x-th item, each request's longest first, by a warp, where the grid has
+// a CTA for every item.  But not where stripes are expected to end before the last
+// of the items: these end after as many of the longest as an SM takes, or half of one
+// after the mean, whichever is less; stripes at the mean (U / S blocks), and what
+// starting, publishing and joining parts costs.  Measured with 128 channels, items
+// against stripes: 256 items of 16 blocks at most 47 against 77 us, 576 of 24 at most
+// 124 against 153, 1264 of 40 at most 325 against 442; 256 of 126 to 141 blocks 389
+// against 355, 376 of 94 to 141 506 against 462, 504 of 94 to 125 629 against 573.
+// The mean is taken as if a request's items grew evenly.
+constexpr int kCutCost = 20, kCutItemCost = 4;  // blocks
+__device__ __forceinline__ void find_item(const KvAttnParams& p, CtrlP& ctrl) {
+  const int lane = threadIdx.x & 31;
+  long long left = blockIdx.x, U = 0, items = 0;
+  int longest = 0;
+  bool found = false;
+  for (int b0 = 0; b0 < p.kv.B; b0 += 32) {
+    long long n = 0;
+    int tiles = 0;
+    if (b0 + lane < p.kv.B) {
+      const KvSeq s = kv_seq(p.kv, b0 + lane, blockIdx.x == 0);
+      if (s.nq > s.len && blockIdx.x == 0) kv_fail(p.kv, kKvSiteLen);
+      const int rows = item_rows(p, s);
+      tiles = (rows + kRows - 1) / kRows;
+      n = (long long)tiles * p.kv.hkv;
+      if (tiles > 0) {
+        const int n0 = item_span(p, s, rows, 0).n, n1 = item_span(p, s, rows, tiles - 1).n;
+        longest = max(longest, max(n0, n1));
+        U += n * (n0 + n1) / 2;
+      }
+    }
+    long long upto = n;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, upto, m);
+      if (lane >= m) upto += o;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, left < upto);
+    if (!found && hit && lane == __ffs(hit) - 1) {
+      const int k = (int)(left - (upto - n));
+      ctrl.start_b = b0 + lane;
+      ctrl.start_h = k % p.kv.hkv;
+      ctrl.start_tile = tiles - 1 - k / p.kv.hkv;
+      ctrl.start_x = 0;
+    }
+    found = found || hit;
+    const long long all = __shfl_sync(0xffffffffu, upto, 31);
+    left -= all;
+    items += all;
+  }
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    U += __shfl_xor_sync(0xffffffffu, U, m);
+    longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, m));
+  }
+  __syncwarp();
+  const long long S = p.stripes, mean = U / S;
+  const long long whole = min((items + S - 1) / S * longest, mean + longest / 2);
+  if (whole <= mean + kCutCost + kCutItemCost * items / S) {
+    if (lane == 0) ctrl.by_item = 1;
+  } else if (lane == 0) {
+    ctrl.start_b = -1;
+  }
 }
 
 template <int D>
@@ -303,101 +368,110 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
     mbar_init(bar(ctrl.o_full), 1);
     mbar_init(bar(ctrl.drain), 1);
     ctrl.abort = 0;
+    ctrl.by_item = 0;
     ctrl.start_b = -1;
     fence_mbarrier_init();
     griddep_launch_dependents();
   }
   kv_prefetch_plan(p.kv, (long long)blockIdx.x * kThreadsP + tid);
   griddep_wait();
-  // ---- this CTA's stripe ------------------------------------------------------------------
-  // every warp sums a run of requests; the warp whose run holds the stripe's first block finds it
-  constexpr int kWarps = kThreadsP / 32;
-  const int per = (p.kv.B + kWarps - 1) / kWarps, b_from = min(warp * per, p.kv.B), b_to = min(b_from + per, p.kv.B);
-  long long mine = 0, mine_items = 0;
-  int longest = 0;
-  for (int b = b_from; b < b_to; ++b) {
-    const KvSeq q = kv_seq(p.kv, b, blockIdx.x == 0 && lane == 0);
-    if (q.nq > q.len && blockIdx.x == 0 && lane == 0) kv_fail(p.kv, kKvSiteLen);
-    mine += p.kv.hkv * request_blocks(p, q, &longest);
-    mine_items += (long long)p.kv.hkv * ((item_rows(p, q) + kRows - 1) / kRows);
-  }
-  if (lane == 0) {
-    ctrl.sums[warp] = mine;
-    ctrl.items[warp] = mine_items;
-    ctrl.longest[warp] = longest;
-  }
   if (warp == kSoftmaxWarps + kDequantWarps) {
     tmem_alloc(smem_addr(&ctrl.tmem), kTmem);
     tmem_relinquish();
   }
+  // ---- this CTA's work: an item, or a stripe of all items ----------------------------------
+  const bool many = (int)gridDim.x > p.stripes;
+  if (many && warp == 0) find_item(p, ctrl);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctrl.tmem;
-  long long U = 0, before = 0, all_items = 0, items_before = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w == warp) {
-      before = U;
-      items_before = all_items;
-    }
-    U += ctrl.sums[w];
-    all_items += ctrl.items[w];
-    longest = max(longest, ctrl.longest[w]);
-  }
-  // Few items of moderate length: a CTA each, none is cut (publishing and joining
-  // parts costs about as much as four blocks).
-  const bool by_item = all_items <= (long long)gridDim.x && longest <= U / gridDim.x + 4;
-  const long long G = by_item ? all_items : min((long long)gridDim.x, U);
-  const bool works = (long long)blockIdx.x < G;
-  const long long u_begin = works && !by_item ? stripe_begin(blockIdx.x, U, G) : 0;
-  const long long u_end = works && !by_item ? stripe_begin(blockIdx.x + 1, U, G) : 0;
-  const long long at_unit = by_item ? blockIdx.x : u_begin;
-  const long long from_unit = by_item ? items_before : before;
-  if (works && at_unit >= from_unit && at_unit < from_unit + (by_item ? mine_items : mine)) {
-    long long off = at_unit - from_unit;
+  bool by_item = ctrl.by_item;
+  long long U = 0, G = 0, u_begin = 0, u_end = 0;
+  if (!by_item) {
+    // every warp sums a run of requests; the warp whose run holds the CTA's first block finds it
+    constexpr int kWarps = kThreadsP / 32;
+    const int per = (p.kv.B + kWarps - 1) / kWarps, b_from = min(warp * per, p.kv.B), b_to = min(b_from + per, p.kv.B);
+    long long mine = 0, mine_items = 0;
+    int longest = 0;
     for (int b = b_from; b < b_to; ++b) {
-      const KvSeq q = kv_seq(p.kv, b, false);
-      const int rows = item_rows(p, q), tiles = (rows + kRows - 1) / kRows;
-      const long long one = by_item ? tiles : request_blocks(p, q, &longest);
-      if (off >= one * p.kv.hkv) {
-        off -= one * p.kv.hkv;
-        continue;
+      const KvSeq q = kv_seq(p.kv, b, blockIdx.x == 0 && lane == 0);
+      if (q.nq > q.len && blockIdx.x == 0 && lane == 0) kv_fail(p.kv, kKvSiteLen);
+      mine += p.kv.hkv * request_blocks(p, q, &longest);
+      mine_items += (long long)p.kv.hkv * ((item_rows(p, q) + kRows - 1) / kRows);
+    }
+    if (lane == 0) {
+      ctrl.sums[warp] = mine;
+      ctrl.items[warp] = mine_items;
+      ctrl.longest[warp] = longest;
+    }
+    __syncthreads();
+    long long before = 0, all_items = 0, items_before = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w == warp) {
+        before = U;
+        items_before = all_items;
       }
-      const int h = (int)(off / one);
-      off -= h * one;
-      if (by_item) {
-        if (lane == 0) {
-          ctrl.start_b = b;
-          ctrl.start_h = h;
-          ctrl.start_tile = tiles - 1 - (int)off;
-          ctrl.start_x = 0;
+      U += ctrl.sums[w];
+      all_items += ctrl.items[w];
+      longest = max(longest, ctrl.longest[w]);
+    }
+    // no more items than SMs: a CTA each, unless stripes would end before the longest
+    by_item = !many && all_items <= (long long)gridDim.x && longest <= U / p.stripes + kCutCost;
+    G = by_item ? all_items : min((long long)p.stripes, U);
+    const bool works = (long long)blockIdx.x < G;
+    if (works && !by_item) {
+      u_begin = stripe_begin(blockIdx.x, U, G);
+      u_end = stripe_begin(blockIdx.x + 1, U, G);
+    }
+    const long long at_unit = by_item ? blockIdx.x : u_begin;
+    const long long from_unit = by_item ? items_before : before;
+    if (works && at_unit >= from_unit && at_unit < from_unit + (by_item ? mine_items : mine)) {
+      long long off = at_unit - from_unit;
+      for (int b = b_from; b < b_to; ++b) {
+        const KvSeq q = kv_seq(p.kv, b, false);
+        const int rows = item_rows(p, q), tiles = (rows + kRows - 1) / kRows;
+        const long long one = by_item ? tiles : request_blocks(p, q, &longest);
+        if (off >= one * p.kv.hkv) {
+          off -= one * p.kv.hkv;
+          continue;
         }
-        break;
-      }
-      for (int top = (rows + kRows - 1) / kRows - 1; top >= 0; top -= 32) {  // 32 tiles at a time, downwards
-        const int n = top >= lane ? item_span(p, q, rows, top - lane).n : 0;
-        int upto = n;
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-          const int o = __shfl_up_sync(0xffffffffu, upto, m);
-          if (lane >= m) upto += o;
-        }
-        const uint32_t hit = __ballot_sync(0xffffffffu, off < upto);
-        if (hit) {
-          if (lane == __ffs(hit) - 1) {
+        const int h = (int)(off / one);
+        off -= h * one;
+        if (by_item) {
+          if (lane == 0) {
             ctrl.start_b = b;
             ctrl.start_h = h;
-            ctrl.start_tile = top - lane;
-            ctrl.start_x = (int)off - (upto - n);
+            ctrl.start_tile = tiles - 1 - (int)off;
+            ctrl.start_x = 0;
           }
           break;
         }
-        off -= __shfl_sync(0xffffffffu, upto, 31);
+        for (int top = tiles - 1; top >= 0; top -= 32) {  // 32 tiles at a time, downwards
+          const int n = top >= lane ? item_span(p, q, rows, top - lane).n : 0;
+          int upto = n;
+#pragma unroll
+          for (int m = 1; m < 32; m <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, upto, m);
+            if (lane >= m) upto += o;
+          }
+          const uint32_t hit = __ballot_sync(0xffffffffu, off < upto);
+          if (hit) {
+            if (lane == __ffs(hit) - 1) {
+              ctrl.start_b = b;
+              ctrl.start_h = h;
+              ctrl.start_tile = top - lane;
+              ctrl.start_x = (int)off - (upto - n);
+            }
+            break;
+          }
+          off -= __shfl_sync(0xffffffffu, upto, 31);
+        }
+        break;
       }
-      break;
     }
+    __syncthreads();
   }
-  __syncthreads();
   const WaitCtx wc{&ctrl.abort, p.kv.status, p.timeout_ns};
   Place at{};
   at.b = ctrl.start_b;
@@ -427,7 +501,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
     const int x1 = min(at.span.n, at.x + at.left), pieces = x1 - at.x;  // blocks at.x .. x1 - 1 of the item
     const int first = seq.len - seq.nq, row = at.tile * kRows + warp * 32 + lane;
     const bool live = row < at.rows;
-    const int i = live ? row / p.group : 0;
+    const int i = live ? kv_div_group(p, row) : 0;
     const int head = at.h * p.group + (live ? row - i * p.group : 0);
     const int pos = first + i;
     const int hi = live ? pos + 1 : 0, lo = p.window > 0 ? pos - p.window + 1 : 0;  // tokens seen
@@ -512,15 +586,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
             if (!see1) x.y = kNegInf;
             const F2 e = {ex2(x.x), ex2(x.y)};
             lt = add2(lt, e);
-            F2 y = mul2(e, {vp.x, vp.y});
-            F2 z = Masked::value ? mul2(e, {vp.z, vp.w}) : F2{0.f, 0.f};
-            if (Masked::value) {  // a token that is masked for this row may have a NaN scale
-              if (!see0) y.x = z.x = 0.f;
-              if (!see1) y.y = z.y = 0.f;
-              pzt = add2(pzt, z);
-            } else {
-              pzt = fma2(e, {vp.z, vp.w}, pzt);
-            }
+            const F2 y = mul2(e, {vp.x, vp.y});  // the values' scales and offsets are finite
+            pzt = fma2(e, {vp.z, vp.w}, pzt);
             over = fmaxf(over, fmaxf(y.x, y.y));
             // token 16 q + 8 hf + 2 c is pair (4 hf + c) * 4 + q of the operand
             const int q = half * 2 + t / 16, hf = (t / 8) & 1, c = (t / 2) & 3;
@@ -621,7 +688,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       __syncwarp();
     };
     if (whole) {
-      const float inv = hi > 0 ? 1.f / sum : 0.f;  // a row that sees no token is zero
+      const float inv = hi > 0 ? 1.f / sum : 0.f, add = off * inv;  // a row that sees no token is zero
 #pragma unroll 1
       for (int part = 0; part < D / 32; ++part) {
         uint32_t v[32];
@@ -629,7 +696,11 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
         tmem_wait_ld();
         float o[32];
 #pragma unroll
-        for (int t = 0; t < 32; ++t) o[t] = inv == 0.f ? 0.f : (__uint_as_float(v[t]) + off) * inv;
+        for (int t = 0; t < 32; ++t) o[t] = fmaf(__uint_as_float(v[t]), inv, add);
+        if (inv == 0.f) {  // also where tensor memory holds nothing of this tile
+#pragma unroll
+          for (int t = 0; t < 32; ++t) o[t] = 0.f;
+        }
         keep(part, o);
       }
       write_rows();
@@ -800,10 +871,13 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       }
       // scales and offsets, by pairs of tokens: (ks, ks, ko, ko, vs, vs, vo, vo), keys' in log2 units
       {
-        const float2 kf = unpack(pr.x), vf = unpack(pr.y);
+        float2 kf = unpack(pr.x), vf = unpack(pr.y);
+        if (!(fabsf(vf.x) <= 65504.f)) {  // a value that holds NaN: by way of its score, which masks can take out
+          kf.x = vf.x;
+          vf.x = vf.y = 0.f;
+        }
         float big = lane < 16 ? vf.x : 0.f;
-        big = big > 0.f ? big : 0.f;  // also of a NaN
-#pragma unroll
+        #pragma unroll
         for (int m = 1; m < 16; m <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, m));
         if (lane < 16) {
           float* dst = par0 + stage * (Sh::kPar / 4) + (16 * dw + (lane & ~1)) * 4 + (lane & 1);

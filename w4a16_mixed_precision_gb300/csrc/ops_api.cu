@@ -1,6 +1,7 @@
 // ops_api.cu -- the C ABI of the operators beside the W4A16 product: low-rank
 // adapters, and the 4-bit paged key/value cache (argument checks, plans,
 // launches).
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 
@@ -263,6 +264,7 @@ marlin_status_t marlin_kv_attention(const uint16_t* q, int64_t q_token_stride, i
   p.out = out;
   p.heads = heads;
   p.group = group;
+  p.group_magic = group == 1 ? 0ull : ~0ull / (unsigned)group + 1;
   p.window = window;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.whole_blocks = p.kv.page16 % 4 == 0;
@@ -285,7 +287,10 @@ marlin_status_t marlin_kv_attention(const uint16_t* q, int64_t q_token_stride, i
     KvAttnParams f = p;
     f.counters = p.counters + a.grid;
     f.partials = reinterpret_cast<float*>(ws + a.prompt_off);
-    if (launch_kv_prefill(f, head_dim, a.grid, st) != cudaSuccess) return MARLIN_ERR_CUDA;
+    f.stripes = a.grid;
+    const long long items = kv_prefill_items(tokens, requests, kv_heads, group);
+    if (items > 0x7FFFFFFF) return MARLIN_ERR_UNSUPPORTED;
+    if (launch_kv_prefill(f, head_dim, std::max((int)items, a.grid), st) != cudaSuccess) return MARLIN_ERR_CUDA;
     if (uniform) return MARLIN_OK;
     p.max_rows = kPrefillRows;
   }
