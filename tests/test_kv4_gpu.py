@@ -199,6 +199,24 @@ def test_prompts_cut_over_ctas_and_a_cta_each(lens, nq, hq, hkv, D, page, window
     test_attention(lens, nq, hq, hkv, D, page, window)
 
 
+@pytest.mark.parametrize("nq", [1, 80])
+def test_long_context_is_as_accurate_as_its_rounding(nq):
+    """The mean of many values is small beside each: what is lost on the way to it, in root mean square, is no
+    more than rounding the result itself (2^-11 / sqrt(3) of it at most), on few rows and on tiles of 128;
+    the two together are sqrt(2) times that."""
+    import w4a16_mixed_precision_gb300 as w4
+    lens, hq, hkv, D, page = [131001], 4, 1, 128, 64
+    k, v, cache, batch, hist = make(lens, [nq], hkv, D, page, seed=30)
+    ws = w4.Kv4Workspace(batch, hq, cache)
+    w4.kv4_append(torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), cache, hist, ws)
+    q = np.random.default_rng(31).standard_normal((nq, hq, D)).astype(np.float16)
+    y = w4.kv4_attention(torch.from_numpy(q).cuda(), cache, batch, ws).cpu().numpy().astype(np.float64)
+    assert w4.device_status(ws) == 0
+    some = slice(max(0, nq - 3), nq)
+    ref = kv_ref.attention(q[some], kv_ref.values(k), kv_ref.values(v), some.stop - some.start, D ** -0.5)
+    assert np.sqrt(((y[some] - ref) ** 2).mean()) <= 2.0 ** 0.5 * 2.0 ** -11 / 3 ** 0.5 * np.sqrt((ref ** 2).mean())
+
+
 @pytest.mark.parametrize("spread", [1e-3, 30.0])
 def test_attention_of_small_and_large_values(spread):
     """Value scales near fp16's small numbers, and scores so peaked that one token takes all."""
