@@ -63,6 +63,10 @@ CASES = [
     (17, 384, 256, 128, False, 32, 40, "own"),         # every row its own adapter
     (33, 1024, 384, 128, False, 64, 5, "runs"),
     (64, 512, 256, 128, True, 128, 3, "random"),
+    (40, 512, 256, 128, False, 16, 2, "random"),       # several 16 rows of one adapter, in any places
+    (127, 512, 384, 128, False, 64, 6, "random"),
+    (127, 256, 128, 128, True, 48, 127, "own"),
+    (90, 4096, 256, 128, False, 32, 30, "runs"),
     (130, 640, 256, 128, False, 16, 9, "random"),      # blocks of 32 rows, adapters in any order
     (300, 1024, 384, 128, False, 72, 4, "runs"),
     (257, 512, 256, 128, False, 8, 2, "none"),

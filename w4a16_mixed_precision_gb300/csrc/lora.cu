@@ -6,11 +6,11 @@
 //
 // Bound: for few rows reading the adapters in use, r (K + N) fp16 each; for
 // many rows reading x, and reading and writing y.
-//   * Rows are taken in blocks.  A block makes one pass for each different adapter
-//     among its rows (one, for the rows of a prompt), with the other rows masked,
-//     so any order of rows is right and runs of equal adapters are fast.  Which
-//     rows share an adapter is found in the kernel by votes; for small batches
-//     the passes of a block go to different clusters.
+//   * Few rows: an item is up to 16 rows of one adapter, in any places, found in the
+//     kernel; a cluster takes an item, so that every adapter in use is read once for
+//     16 rows of it.  Many rows: these are taken in blocks, and a block makes one
+//     pass for each different adapter among its rows (one, for the rows of a prompt),
+//     with the other rows masked.  So any order of rows is right in both.
 //   * mma.sync with the rows as the 16-row operand.  The k order is permuted
 //     alike in both operands so that every lane loads 16 consecutive bytes.
 //   * First product: K is split over the warps of a CTA and the CTAs of a
@@ -25,6 +25,8 @@
 #include "lora.h"
 
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -96,42 +98,20 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-// MT: 16-row tiles per block; NT: 8-rank tiles (r <= 8 NT).  Grid: blocks of rows;
-// CTAs of the cluster (parts of K, then of N); clusters that share the passes.
-// kBoth: both products (MT = 1); else v and unit go to the workspace.
-template <int MT, int NT, bool kBoth>
-__global__ void __launch_bounds__(kWarps * 32, NT <= 2 || !kBoth && NT <= 8 ? 2 : 1) lora_kernel(const LoraParams p) {
+// v and unit of blocks of rows, for the workspace.  MT: 16-row tiles per block; NT:
+// 8-rank tiles (r <= 8 NT).  Grid: blocks of rows; CTAs of the cluster (parts of K).
+template <int MT, int NT>
+__global__ void __launch_bounds__(kWarps * 32, NT <= 8 ? 2 : 1) lora_down_kernel(const LoraParams p) {
   constexpr int kRows = 16 * MT, kRanks = 8 * NT, kRp = (kRanks + 15) / 16 * 16, kAcc = MT * NT * 4;
   // half of the warps leave their sums to the other half, three times; then the CTA's sum
   __shared__ float red[kWarps / 2][kAcc][32];
   __shared__ float total[kRows][kRanks + 1];
-  __shared__ __half v[kRows][kRp + 8];
-  __shared__ float unit[kRows];
   if (threadIdx.x == 0) griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int row0 = blockIdx.x * kRows, rank = blockIdx.y;
   const Block k = block_adapters(p, row0, kRows);
   const int count = __popc(k.leaders);
-  if ((int)blockIdx.z >= count) return;  // alike in all CTAs of the cluster
-  // this cluster's passes: lane i holds the adapter of the i-th and its rows
-  const int passes = (count - (int)blockIdx.z + p.passes - 1) / p.passes;
-  int pass_ad = 0;
-  uint32_t pass_rows = 0;
-  {
-    uint32_t left = k.leaders;
-    for (int q = 0; q < count; ++q, left &= left - 1) {
-      const int ad = __shfl_sync(0xffffffffu, k.mine, __ffs(left) - 1);
-      const uint32_t rows = __ballot_sync(0xffffffffu, k.mine == ad);
-      if (q % p.passes == (int)blockIdx.z && q / p.passes == lane) {
-        pass_ad = ad;
-        pass_rows = rows;
-      }
-    }
-  }
-  const bool row_mine = k.pass >= 0 && k.pass % p.passes == (int)blockIdx.z;  // this lane's row
-  const uint32_t rows_mine = __ballot_sync(0xffffffffu, row_mine);
-
   // ---- x . A^T: this warp's 32-wide K steps --------------------------------------------
   {
     const int steps = p.K / 32, parts = p.splits * kWarps, part = rank * kWarps + warp;
@@ -143,9 +123,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 2 || !kBoth && NT <= 8 ? 2 
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-    for (int q = 0; q < passes; ++q) {
-      const int ad = __shfl_sync(0xffffffffu, pass_ad, q);
-      const uint32_t rows = __shfl_sync(0xffffffffu, pass_rows, q);
+    uint32_t left = k.leaders;
+    for (int q = 0; q < count; ++q, left &= left - 1) {
+      const int ad = __shfl_sync(0xffffffffu, k.mine, __ffs(left) - 1);
+      const uint32_t rows = __ballot_sync(0xffffffffu, k.mine == ad);
       const uint16_t* a = p.a + (long long)ad * p.r * p.K + c * 8;
       const uint16_t* x = p.x + (long long)row0 * p.K + c * 8;
       constexpr int kTogether = 2 * MT + NT <= 4 ? 4 : 2 * MT + NT <= 8 ? 2 : 1;  // steps whose loads go out together
@@ -201,12 +182,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 2 || !kBoth && NT <= 8 ? 2 
   } else {
     __syncthreads();
   }
-  // ---- v: the sum over the cluster, scaled, normalised, fp16 (every CTA for itself, or
-  // each a share of the rows for the workspace) --------------------------------------------
-  const int by = kBoth ? kWarps : kWarps * p.splits;
-  for (int row = kBoth ? warp : rank * kWarps + warp; row < kRows; row += by) {
+  // ---- v: the sum over the cluster, scaled, normalised, fp16; each CTA a share of the rows ----
+  for (int row = rank * kWarps + warp; row < kRows; row += kWarps * p.splits) {
     const int ad = __shfl_sync(0xffffffffu, k.mine, row);
-    const bool on = (rows_mine >> row) & 1u;
+    const bool on = ad >= 0;
     const float scaling = on ? p.scaling[ad] : 0.f;
     float s[(kRp + 31) / 32], top = 0.f;
 #pragma unroll
@@ -233,40 +212,193 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 2 || !kBoth && NT <= 8 ? 2 
     const float u = top > 1e-30f ? __uint_as_float(__float_as_uint(top) & 0x7F800000u) : 1.f;
 #pragma unroll
     for (int i = 0; i < (kRp + 31) / 32; ++i)
-      if (kBoth) {
-        if (32 * i + lane < kRp) v[row][32 * i + lane] = __float2half_rn(s[i] / u);
-      } else if (on && 32 * i + lane < p.rp) {
+      if (on && 32 * i + lane < p.rp)
         p.v[(long long)(row0 + row) * p.rp + 32 * i + lane] = __half_as_ushort(__float2half_rn(s[i] / u));
-      }
-    if (lane == 0 && kBoth) unit[row] = u;
-    if (lane == 0 && !kBoth && on) p.unit[row0 + row] = u;
+    if (lane == 0 && on) p.unit[row0 + row] = u;
   }
-  if (p.splits > 1) cluster_arrive();  // this CTA has read the others' sums
-  if constexpr (!kBoth) {
-    if (p.splits > 1) cluster_wait();
-    return;
+  if (p.splits > 1) {  // nobody reads this CTA's shared memory any more
+    cluster_arrive();
+    cluster_wait();
+  }
+}
+
+// Both products for up to 127 rows.  An item is up to 16 rows of one adapter, in any
+// places; a cluster takes an item (or the items z, z + gridDim.z, ...), so that every
+// adapter in use is read once.  Where there are fewer items than clusters, several
+// clusters share one: each sums the whole first product, and takes a share of the
+// columns of the second.  NT: 8-rank tiles (r <= 8 NT).  Grid: CTAs of the cluster
+// (parts of K, then of N); clusters.
+template <int NT>
+__global__ void __launch_bounds__(kWarps * 32, NT <= 2 ? 2 : 1) lora_few_kernel(const LoraParams p) {
+  constexpr int kRanks = 8 * NT, kRp = (kRanks + 15) / 16 * 16, kAcc = NT * 4;
+  // half of the warps leave their sums to the other half, three times; then the CTA's sum
+  __shared__ float red[kWarps / 2][kAcc][32];
+  __shared__ float total[16][kRanks + 1];
+  __shared__ __align__(16) __half v[16][kRp + 8];
+  __shared__ float unit[16];
+  __shared__ __align__(16) int adapter[128];  // of each row, -1 for none
+  __shared__ int starts[4];                   // items that begin in each 32 rows
+  __shared__ int item_rows[16], item_ad, item_at;
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  griddep_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int rank = blockIdx.y;
+
+  // ---- the items: a row begins one if 16 n rows before it have its adapter -----------------
+  int mine = -1, at = 0, item_of = -1;  // this thread's row: its adapter, its place among that one's rows
+  if (tid < 128) {
+    mine = tid < p.M ? p.index[tid] : -1;
+    if (mine >= p.adapters) {
+      atomicCAS(p.status + 1, 0, kLoraSite);
+      atomicOr(p.status, kStatusBounds);
+      mine = -1;
+    }
+    if (mine < 0) mine = -1;
+    adapter[tid] = mine;
   }
   __syncthreads();
+  if (tid < 128) {
+    for (int j = 0; j < (p.M + 3) / 4; ++j) {
+      const int4 q = reinterpret_cast<const int4*>(adapter)[j];
+      at += (q.x == mine && 4 * j < tid) + (q.y == mine && 4 * j + 1 < tid) + (q.z == mine && 4 * j + 2 < tid) +
+            (q.w == mine && 4 * j + 3 < tid);
+    }
+    const uint32_t begins = __ballot_sync(0xffffffffu, mine >= 0 && at % 16 == 0);
+    item_of = mine >= 0 && at % 16 == 0 ? __popc(begins & ((1u << lane) - 1)) : -1;
+    if (lane == 0) starts[warp] = __popc(begins);
+  }
+  __syncthreads();
+  const int items = starts[0] + starts[1] + starts[2] + starts[3];
+  if (items == 0) return;
+  if (item_of >= 0)
+    for (int w = 0; w < warp; ++w) item_of += starts[w];
+  const int clusters = gridDim.z, z = blockIdx.z;
+  const int shares = items <= clusters ? min(clusters / items, p.shares) : 1;
+  const int share = items <= clusters ? z / items : 0;
+  if (share >= shares) return;  // alike in all CTAs of the cluster
 
-  // ---- y += v . B^T: this warp's groups of 32 columns ------------------------------------
-  if constexpr (kBoth) {
-    constexpr int kAhead = 4;                  // (group, pass, step) triples whose loads are in flight
+  for (int item = items <= clusters ? z % items : z; item < items; item += clusters) {
+    if (item_of == item) {
+      item_ad = mine;
+      item_at = at;
+    }
+    if (tid < 16) item_rows[tid] = -1;
+    __syncthreads();
+    const int ad = item_ad;
+    if (mine == ad && tid < 128 && at >= item_at && at < item_at + 16) item_rows[at - item_at] = tid;
+    __syncthreads();
+    const int row0 = item_rows[g], row1 = item_rows[g + 8];  // of this lane, -1 where there is none
+
+    // ---- x . A^T: this warp's 32-wide K steps ------------------------------------------
+    {
+      const int steps = p.K / 32, parts = p.splits * kWarps, part = rank * kWarps + warp;
+      const int s0 = steps * part / parts, s1 = steps * (part + 1) / parts;
+      float acc[NT][4];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+      const uint16_t* a = p.a + (long long)ad * p.r * p.K + c * 8;
+      const uint16_t* x0 = p.x + (long long)row0 * p.K + c * 8;
+      const uint16_t* x1 = p.x + (long long)row1 * p.K + c * 8;
+      constexpr int kTogether = NT <= 4 ? 4 : NT <= 8 ? 2 : 1;  // steps whose loads go out together
+#pragma unroll kTogether
+      for (int s = s0; s < s1; ++s) {
+        uint4 xr[2], ar[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          ar[j] = j * 8 + g < p.r ? __ldg(reinterpret_cast<const uint4*>(a + (long long)(j * 8 + g) * p.K + s * 32))
+                                  : make_uint4(0u, 0u, 0u, 0u);
+        xr[0] = row0 >= 0 ? *reinterpret_cast<const uint4*>(x0 + s * 32) : make_uint4(0u, 0u, 0u, 0u);
+        xr[1] = row1 >= 0 ? *reinterpret_cast<const uint4*>(x1 + s * 32) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          mma16816(acc[j], xr[0].x, xr[1].x, xr[0].y, xr[1].y, ar[j].x, ar[j].y);
+          mma16816(acc[j], xr[0].z, xr[1].z, xr[0].w, xr[1].w, ar[j].z, ar[j].w);
+        }
+      }
+      // the sum over the warps, in a fixed order
+#pragma unroll
+      for (int half = kWarps / 2; half >= 1; half >>= 1) {
+        if (warp >= half && warp < 2 * half) {
+#pragma unroll
+          for (int t = 0; t < kAcc; ++t) red[warp - half][t][lane] = acc[t / 4][t % 4];
+        }
+        __syncthreads();
+        if (warp < half) {
+#pragma unroll
+          for (int t = 0; t < kAcc; ++t) acc[t / 4][t % 4] += red[warp][t][lane];
+        }
+        __syncthreads();
+      }
+      if (warp == 0) {
+#pragma unroll
+        for (int t = 0; t < kAcc; ++t) {
+          const int j = t / 4, e = t % 4;
+          total[g + 8 * (e >> 1)][8 * j + 2 * c + (e & 1)] = acc[j][e];
+        }
+      }
+    }
+    if (p.splits > 1) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
+    // ---- v: the sum over the cluster, scaled, normalised, fp16; every CTA for itself -----------
+    const float scaling = p.scaling[ad];
+    for (int row = warp; row < 16; row += kWarps) {
+      const bool on = item_rows[row] >= 0;
+      float s[(kRp + 31) / 32], top = 0.f;
+#pragma unroll
+      for (int i = 0; i < (kRp + 31) / 32; ++i) {
+        const int j = 32 * i + lane;
+        s[i] = 0.f;
+        if (on && j < p.r) {
+          if (p.splits == 1) {
+            s[i] = total[row][j];
+          } else {
+            float part[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              part[q] = q < p.splits ? ld_cluster(smem_addr(&total[row][j]), (uint32_t)q) : 0.f;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) s[i] += part[q];
+          }
+          s[i] *= scaling;
+        }
+        top = fmaxf(top, fabsf(s[i]));
+      }
+#pragma unroll
+      for (int q = 1; q < 32; q <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, q));
+      // 2^exponent of the row's largest magnitude
+      const float u = top > 1e-30f ? __uint_as_float(__float_as_uint(top) & 0x7F800000u) : 1.f;
+#pragma unroll
+      for (int i = 0; i < (kRp + 31) / 32; ++i)
+        if (32 * i + lane < kRp) v[row][32 * i + lane] = __float2half_rn(s[i] / u);
+      if (lane == 0) unit[row] = u;
+    }
+    if (p.splits > 1) cluster_arrive();  // this CTA has read the others' sums
+    __syncthreads();
+
+    // ---- y += v . B^T: this warp's groups of 32 columns ------------------------------------
+    constexpr int kAhead = 4;                  // (group, step) pairs whose loads are in flight
     constexpr int kRanksStep = NT >= 4 ? 32 : 16, kHalves = kRanksStep / 16;  // ranks of a step: 8 or 16 bytes a lane
-    const int groups = p.N / 32, parts = p.splits * kWarps, part = rank * kWarps + warp;
+    const int groups = p.N / 32, parts = shares * p.splits * kWarps, part = (share * p.splits + rank) * kWarps + warp;
     const int n_first = groups * part / parts, n_last = groups * (part + 1) / parts;
     const int steps = (p.r + kRanksStep - 1) / kRanksStep;
     // operand column g of tile t is output column 8 (g / 2) + 2 t + g % 2 of the
     // group's 32, so that a lane's results are 8 consecutive columns of y
-    const uint16_t* b = p.b + (long long)(8 * (g >> 1) + (g & 1)) * p.r + 4 * kHalves * c;
-    uint16_t* y0 = p.y + (long long)row0 * p.N + 8 * c;
+    const uint16_t* b = p.b + ((long long)ad * p.N + 8 * (g >> 1) + (g & 1)) * p.r + 4 * kHalves * c;
+    uint16_t* const y_at[2] = {p.y + (long long)row0 * p.N + 8 * c, p.y + (long long)row1 * p.N + 8 * c};
+    const bool on[2] = {row0 >= 0, row1 >= 0};
     uint32_t br[kAhead][4][2 * kHalves];
-    uint4 y[kAhead][2];  // with a group's last triple: its rows g and g + 8
-    int load_n = n_first, load_pass = 0, load_step = 0;
+    uint4 y[kAhead][2];  // with a group's last step: its rows g and g + 8
+    int load_n = n_first, load_step = 0;
     auto load = [&](uint32_t(&bq)[4][2 * kHalves], uint4(&yq)[2]) {
       if (load_n >= n_last) return;
-      const int ad = __shfl_sync(0xffffffffu, pass_ad, load_pass);
       const bool in = kRanksStep * load_step + 4 * kHalves * c < p.r;
-      const uint16_t* src = b + ((long long)ad * p.N + 32 * load_n) * p.r + kRanksStep * load_step;
+      const uint16_t* src = b + (long long)(32 * load_n) * p.r + kRanksStep * load_step;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         if constexpr (kHalves == 2) {
@@ -279,17 +411,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 2 || !kBoth && NT <= 8 ? 2 
       }
       if (++load_step < steps) return;
       load_step = 0;
-      if (++load_pass < passes) return;
-      load_pass = 0;
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        if ((rows_mine >> (8 * e + g)) & 1u)
-          yq[e] = *reinterpret_cast<const uint4*>(y0 + (long long)(8 * e + g) * p.N + 32 * load_n);
+        if (on[e]) yq[e] = *reinterpret_cast<const uint4*>(y_at[e] + 32 * load_n);
       ++load_n;
     };
 #pragma unroll
     for (int q = 0; q < kAhead; ++q) load(br[q], y[q]);
-    int n = n_first, pass = 0, step = 0;
+    int n = n_first, step = 0;
     float acc[4][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t)
@@ -299,38 +428,33 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 2 || !kBoth && NT <= 8 ? 2 
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
         if (n < n_last) {  // uniform
-          const uint32_t rows = __shfl_sync(0xffffffffu, pass_rows, pass);
 #pragma unroll
           for (int d = 0; d < kHalves; ++d) {
-            const int at = kRanksStep * step + 4 * kHalves * c + 4 * d;
-            uint2 v0 = make_uint2(0u, 0u), v1 = v0;
-            if ((rows >> g) & 1u) v0 = *reinterpret_cast<const uint2*>(&v[g][at]);
-            if ((rows >> (g + 8)) & 1u) v1 = *reinterpret_cast<const uint2*>(&v[g + 8][at]);
+            const int at_rank = kRanksStep * step + 4 * kHalves * c + 4 * d;
+            const uint2 v0 = *reinterpret_cast<const uint2*>(&v[g][at_rank]);
+            const uint2 v1 = *reinterpret_cast<const uint2*>(&v[g + 8][at_rank]);
 #pragma unroll
             for (int t = 0; t < 4; ++t)
               mma16816(acc[t], v0.x, v1.x, v0.y, v1.y, br[q][t][2 * d], br[q][t][2 * d + 1]);
           }
           if (++step == steps) {
             step = 0;
-            if (++pass == passes) {
-              pass = 0;
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if ((rows_mine >> (8 * e + g)) & 1u)
-                  add_row(y0 + (long long)(8 * e + g) * p.N + 32 * n, y[q][e], acc, e, unit[8 * e + g]);
+            for (int e = 0; e < 2; ++e)
+              if (on[e]) add_row(y_at[e] + 32 * n, y[q][e], acc, e, unit[8 * e + g]);
 #pragma unroll
-              for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
-              ++n;
-            }
+              for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+            ++n;
           }
           load(br[q], y[q]);
         }
       }
     }
+    if (p.splits > 1) cluster_wait();  // nobody reads this CTA's sums any more
+    __syncthreads();                   // nor its v, its rows
   }
-  if (p.splits > 1) cluster_wait();  // nobody reads this CTA's shared memory any more
 }
 
 // y += v . B^T for blocks of 128 rows: a warp keeps 32 columns of B in registers
@@ -447,31 +571,43 @@ bool lora_two_kernels(int M) { return M >= 128; }
 
 cudaError_t launch_lora(LoraParams p, int half, int sms, cudaStream_t stream) {
   const int nt = p.r <= 8 ? 1 : p.r <= 16 ? 2 : p.r <= 32 ? 4 : p.r <= 64 ? 8 : 16;
-  const bool both = !lora_two_kernels(p.M);
-  if (!both && half == 1) {
+  const int most = p.K / 32 / kWarps < 1 ? 1 : p.K / 32 / kWarps < 8 ? p.K / 32 / kWarps : 8;  // a step for every warp
+  if (!lora_two_kernels(p.M)) {
+    // items at most: every adapter in use begins one, and every 16 rows more of it
+    const int used = std::min(p.M, p.adapters), items = used + (p.M - used) / 16;
+    // clusters of s CTAs that the card holds at a time, where they do not fill its parts: as
+    // many as measured (rank 64, 8 rows of 4 adapters beside 4096 x 12288: 14 clusters of 8
+    // 18.3 us, 16 of them 23.9; 48 rows of 21 adapters: clusters of 6 29.3 us, of 4 32.6)
+    auto clusters = [&](int s) { return std::max(1, (nt <= 2 ? 2 : 1) * (s == 8 ? sms / 10 : sms * 7 / 8 / s)); };
+    p.splits = most;
+    while (p.splits > 1 && clusters(p.splits) < items) --p.splits;
+    p.shares = std::max(1, p.N / 32 / (p.splits * kWarps));
+    const long long wanted = (long long)items * p.shares;
+    const dim3 grid(1, p.splits, (unsigned)std::min(wanted, (long long)clusters(p.splits)));
+    return nt == 1   ? launch(lora_few_kernel<1>, grid, p.splits, p, stream)
+           : nt == 2 ? launch(lora_few_kernel<2>, grid, p.splits, p, stream)
+           : nt == 4 ? launch(lora_few_kernel<4>, grid, p.splits, p, stream)
+           : nt == 8 ? launch(lora_few_kernel<8>, grid, p.splits, p, stream)
+                     : launch(lora_few_kernel<16>, grid, p.splits, p, stream);
+  }
+  if (half == 1) {
     const dim3 grid((p.M + 127) / 128, (p.N / 32 + kWarps - 1) / kWarps);
     return p.r <= 16   ? launch(lora_up_kernel<1>, grid, 1, p, stream)
            : p.r <= 32 ? launch(lora_up_kernel<2>, grid, 1, p, stream)
            : p.r <= 64 ? launch(lora_up_kernel<4>, grid, 1, p, stream)
                        : launch(lora_up_kernel<8>, grid, 1, p, stream);
   }
-  const int mt = both || p.r > 64 ? 1 : 2;  // 32 rows where the registers hold their sums
+  const int mt = p.r > 64 ? 1 : 2;  // 32 rows where the registers hold their sums
   const int blocks = (p.M + 16 * mt - 1) / (16 * mt);
-  int most = p.M < 16 ? p.M : 16;  // different adapters in a block
-  if (p.adapters < most) most = p.adapters;
-  p.passes = both ? most : 1;
-  // clusters of up to 8 CTAs, while there is room on the card and a step for every warp
+  // clusters of up to 8 CTAs, while there is room on the card
   p.splits = 1;
-  while (p.splits < 8 && 2 * p.splits * blocks * p.passes <= 2 * sms && p.K / 32 >= 2 * p.splits * kWarps)
-    p.splits *= 2;
-  const dim3 grid(blocks, p.splits, p.passes);
-#define W4A16_LORA(MT, NT, BOTH) \
-  if (mt == MT && nt == NT && both == BOTH) return launch(lora_kernel<MT, NT, BOTH>, grid, p.splits, p, stream);
-  W4A16_LORA(1, 1, true) W4A16_LORA(1, 2, true) W4A16_LORA(1, 4, true) W4A16_LORA(1, 8, true)
-  W4A16_LORA(1, 16, true) W4A16_LORA(2, 1, false) W4A16_LORA(2, 2, false) W4A16_LORA(2, 4, false)
-  W4A16_LORA(2, 8, false) W4A16_LORA(1, 16, false)
-#undef W4A16_LORA
-  return cudaErrorInvalidValue;
+  while (2 * p.splits <= most && 2 * p.splits * blocks <= 2 * sms) p.splits *= 2;
+  const dim3 grid(blocks, p.splits);
+  return nt == 1   ? launch(lora_down_kernel<2, 1>, grid, p.splits, p, stream)
+         : nt == 2 ? launch(lora_down_kernel<2, 2>, grid, p.splits, p, stream)
+         : nt == 4 ? launch(lora_down_kernel<2, 4>, grid, p.splits, p, stream)
+         : nt == 8 ? launch(lora_down_kernel<2, 8>, grid, p.splits, p, stream)
+                   : launch(lora_down_kernel<1, 16>, grid, p.splits, p, stream);
 }
 
 }  // namespace w4a16

@@ -18,8 +18,8 @@ struct LoraParams {
   int rp;                  // r rounded up to 16
   int* status;
   int M, K, N, r, adapters;
-  int splits;              // CTAs of a cluster (filled in by launch_lora, like passes)
-  int passes;              // clusters that share the adapters of a block of rows
+  int splits;              // CTAs of a cluster (filled in by launch_lora, like shares)
+  int shares;              // clusters at most that share the columns of an item
 };
 
 constexpr int kLoraMaxRank = 128;
