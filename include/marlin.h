@@ -340,7 +340,7 @@ marlin_status_t marlin_lora_workspace_bytes(int M, int K, int N, int group, int 
 
 /*
  * The product with adapters: marlin_gemm and the adapters' part, added to Y (one
- * launch after it; from 128 rows on X . A^T has a launch before it).
+ * launch after it; for more than a few hundred rows X . A^T has a launch before it).
  *
  * X, packed, scales, zeros, Y, M, K, N, group  as for marlin_gemm, except that
  *            Y is 16-byte aligned.

@@ -71,6 +71,11 @@ CASES = [
     (300, 1024, 384, 128, False, 72, 4, "runs"),
     (257, 512, 256, 128, False, 8, 2, "none"),
     (128, 256, 128, 128, False, 40, 200, "own"),
+    (256, 512, 128, 128, False, 16, 3, "random"),      # the most rows of one kernel, and one more
+    (257, 512, 128, 128, False, 24, 3, "random"),
+    (320, 256, 128, 128, False, 32, 400, "own"),       # more items than clusters
+    (321, 512, 128, 128, False, 64, 9, "random"),
+    (600, 512, 256, 128, False, 16, 30, "random"),
 ]
 
 

@@ -1,8 +1,8 @@
 // lora.cu -- low-rank adapters of many requests beside a shared product:
 //     y[m] += scaling[a] * (x[m] . A[a]^T) . B[a]^T,   a = index[m] (none if negative),
-// A[a] r x K and B[a] N x r in fp16.  Below 128 rows one kernel after the product,
-// v = scaling x . A^T staying in shared memory between its two halves; from 128
-// rows on two, so that the second can take 128 rows at a time.
+// A[a] r x K and B[a] N x r in fp16.  Up to a few hundred rows one kernel after the
+// product, v = scaling x . A^T staying in shared memory between its two halves; for
+// more rows two, so that the second can take 128 rows at a time.
 //
 // Bound: for few rows reading the adapters in use, r (K + N) fp16 each; for
 // many rows reading x, and reading and writing y.
@@ -36,6 +36,7 @@ namespace w4a16 {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kFewRows = 512;  // of the kernel that does both products: room
 constexpr int kLoraSite = 104;  // the word after the status word: an adapter index out of range
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 8 ? 2 : 1) lora_down_kernel
   }
 }
 
-// Both products for up to 127 rows.  An item is up to 16 rows of one adapter, in any
+// Both products for few rows.  An item is up to 16 rows of one adapter, in any
 // places; a cluster takes an item (or the items z, z + gridDim.z, ...), so that every
 // adapter in use is read once.  Where there are fewer items than clusters, several
 // clusters share one: each sums the whole first product, and takes a share of the
@@ -236,8 +237,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 2 ? 2 : 1) lora_few_kernel(
   __shared__ float total[16][kRanks + 1];
   __shared__ __align__(16) __half v[16][kRp + 8];
   __shared__ float unit[16];
-  __shared__ __align__(16) int adapter[128];  // of each row, -1 for none
-  __shared__ int starts[4];                   // items that begin in each 32 rows
+  __shared__ __align__(16) int adapter[kFewRows];        // of each row, -1 for none
+  __shared__ int starts[kFewRows / 32];                  // items that begin in each 32 rows
   __shared__ int item_rows[16], item_ad, item_at;
   if (threadIdx.x == 0) griddep_launch_dependents();
   griddep_wait();
@@ -245,47 +246,66 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 2 ? 2 : 1) lora_few_kernel(
   const int rank = blockIdx.y;
 
   // ---- the items: a row begins one if 16 n rows before it have its adapter -----------------
-  int mine = -1, at = 0, item_of = -1;  // this thread's row: its adapter, its place among that one's rows
-  if (tid < 128) {
-    mine = tid < p.M ? p.index[tid] : -1;
-    if (mine >= p.adapters) {
+  // this thread's rows, tid + 256 i: their adapters, places among those ones' rows, and the
+  // items they begin
+  constexpr int kMine = kFewRows / (kWarps * 32);
+  int mine[kMine], at[kMine], item_of[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int row = tid + kWarps * 32 * i;
+    mine[i] = row < p.M ? p.index[row] : -1;
+    if (mine[i] >= p.adapters) {
       atomicCAS(p.status + 1, 0, kLoraSite);
       atomicOr(p.status, kStatusBounds);
-      mine = -1;
+      mine[i] = -1;
     }
-    if (mine < 0) mine = -1;
-    adapter[tid] = mine;
+    if (mine[i] < 0) mine[i] = -1;
+    adapter[row] = mine[i];
+    at[i] = 0;
   }
   __syncthreads();
-  if (tid < 128) {
-    for (int j = 0; j < (p.M + 3) / 4; ++j) {
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int row = tid + kWarps * 32 * i, word = i * kWarps + warp;
+    item_of[i] = -1;
+    if (32 * word >= p.M) continue;  // alike in the warp
+    for (int j = 0; j <= 8 * word + 7 && 4 * j < p.M; ++j) {  // up to the warp's last row
       const int4 q = reinterpret_cast<const int4*>(adapter)[j];
-      at += (q.x == mine && 4 * j < tid) + (q.y == mine && 4 * j + 1 < tid) + (q.z == mine && 4 * j + 2 < tid) +
-            (q.w == mine && 4 * j + 3 < tid);
+      at[i] += (q.x == mine[i] && 4 * j < row) + (q.y == mine[i] && 4 * j + 1 < row) +
+               (q.z == mine[i] && 4 * j + 2 < row) + (q.w == mine[i] && 4 * j + 3 < row);
     }
-    const uint32_t begins = __ballot_sync(0xffffffffu, mine >= 0 && at % 16 == 0);
-    item_of = mine >= 0 && at % 16 == 0 ? __popc(begins & ((1u << lane) - 1)) : -1;
-    if (lane == 0) starts[warp] = __popc(begins);
+    const bool begin = mine[i] >= 0 && at[i] % 16 == 0;
+    const uint32_t begins = __ballot_sync(0xffffffffu, begin);
+    if (begin) item_of[i] = __popc(begins & ((1u << lane) - 1));
+    if (lane == 0) starts[word] = __popc(begins);
   }
   __syncthreads();
-  const int items = starts[0] + starts[1] + starts[2] + starts[3];
+  int items = 0;
+  for (int w = 0; 32 * w < p.M; ++w) {
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+      if (item_of[i] >= 0 && w < i * kWarps + warp) item_of[i] += starts[w];
+    items += starts[w];
+  }
   if (items == 0) return;
-  if (item_of >= 0)
-    for (int w = 0; w < warp; ++w) item_of += starts[w];
   const int clusters = gridDim.z, z = blockIdx.z;
   const int shares = items <= clusters ? min(clusters / items, p.shares) : 1;
   const int share = items <= clusters ? z / items : 0;
   if (share >= shares) return;  // alike in all CTAs of the cluster
 
   for (int item = items <= clusters ? z % items : z; item < items; item += clusters) {
-    if (item_of == item) {
-      item_ad = mine;
-      item_at = at;
-    }
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+      if (item_of[i] == item) {
+        item_ad = mine[i];
+        item_at = at[i];
+      }
     if (tid < 16) item_rows[tid] = -1;
     __syncthreads();
     const int ad = item_ad;
-    if (mine == ad && tid < 128 && at >= item_at && at < item_at + 16) item_rows[at - item_at] = tid;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+      if (mine[i] == ad && at[i] >= item_at && at[i] < item_at + 16) item_rows[at[i] - item_at] = tid + kWarps * 32 * i;
     __syncthreads();
     const int row0 = item_rows[g], row1 = item_rows[g + 8];  // of this lane, -1 where there is none
 
@@ -565,14 +585,18 @@ cudaError_t launch(F kernel, dim3 grid, int cluster, const LoraParams& p, cudaSt
 
 }  // namespace
 
-// From 128 rows on the first product is before marlin_gemm in the stream (its
-// launch and tail overlap the product's start) and only the second after it.
-bool lora_two_kernels(int M) { return M >= 128; }
+// Few rows, both products in one kernel after marlin_gemm; many, the first product before
+// it in the stream (its launch and tail overlap the product's start) and the second after
+// it.  Measured with the product, one kernel against two: 128 rows of 21 adapters of rank
+// 16 (4096 x 12288) 34 against 98 us, 200 of 2, rank 64, 47 against 56, 276 of 5, rank 64
+// (4096 x 4096) 42 against 56; 276 of 3, rank 16, 41 against 38, 400 of 2, rank 64
+// (4096 x 12288) 84 against 80.
+bool lora_two_kernels(int M, int r) { return M > (r >= 32 ? 320 : 256); }
 
 cudaError_t launch_lora(LoraParams p, int half, int sms, cudaStream_t stream) {
   const int nt = p.r <= 8 ? 1 : p.r <= 16 ? 2 : p.r <= 32 ? 4 : p.r <= 64 ? 8 : 16;
   const int most = p.K / 32 / kWarps < 1 ? 1 : p.K / 32 / kWarps < 8 ? p.K / 32 / kWarps : 8;  // a step for every warp
-  if (!lora_two_kernels(p.M)) {
+  if (!lora_two_kernels(p.M, p.r)) {
     // items at most: every adapter in use begins one, and every 16 rows more of it
     const int used = std::min(p.M, p.adapters), items = used + (p.M - used) / 16;
     // clusters of s CTAs that the card holds at a time, where they do not fill its parts: as

@@ -13,7 +13,7 @@ struct LoraParams {
   const float* scaling;    // [adapters]
   const int* index;        // [M]: the row's adapter, negative for none
   uint16_t* y;             // fp16 [M][N], the base product; the adapters' part is added to it
-  uint16_t* v;             // workspace, from 128 rows on: fp16 [M][rp], scaling * x . A^T of the row over unit[m]
+  uint16_t* v;             // workspace, for many rows: fp16 [M][rp], scaling * x . A^T of the row over unit[m]
   float* unit;             // workspace: [M], a power of two
   int rp;                  // r rounded up to 16
   int* status;
@@ -26,7 +26,7 @@ constexpr int kLoraMaxRank = 128;
 
 // half: 0 the first product, 1 the second; where lora_two_kernels is false half 0
 // is not launched and half 1 does both.
-bool lora_two_kernels(int M);
+bool lora_two_kernels(int M, int r);
 cudaError_t launch_lora(LoraParams p, int half, int sms, cudaStream_t stream);
 
 }  // namespace w4a16

@@ -180,7 +180,7 @@ marlin_status_t marlin_lora_gemm(const uint16_t* X, const void* packed, const ui
   p.r = r;
   p.adapters = adapters;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (lora_two_kernels(M) && launch_lora(p, 0, sms, st) != cudaSuccess) return MARLIN_ERR_CUDA;
+  if (lora_two_kernels(M, r) && launch_lora(p, 0, sms, st) != cudaSuccess) return MARLIN_ERR_CUDA;
   s = marlin_gemm(X, packed, scales, zeros, Y, M, K, N, group, workspace, z.gemm, stream);
   if (s != MARLIN_OK) return s;
   return launch_lora(p, 1, sms, st) == cudaSuccess ? MARLIN_OK : MARLIN_ERR_CUDA;
