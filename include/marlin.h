@@ -350,7 +350,8 @@ marlin_status_t marlin_lora_workspace_bytes(int M, int K, int N, int group, int 
  * index      device, int32 [M]: the row's adapter, negative for none.  An entry
  *            >= adapters gives the row no adapter and is reported by
  *            marlin_last_device_status as MARLIN_ERR_BOUNDS.  Rows may come in
- *            any order; blocks of 16 or 32 rows that share adapters are fastest.
+ *            any order; beyond a few hundred, blocks of 32 rows that share an
+ *            adapter are fastest.
  * r          a multiple of 8 up to 128, else MARLIN_ERR_UNSUPPORTED (pad A and B
  *            with zeros).
  * workspace  device, >= marlin_lora_workspace_bytes(...) bytes; else as for

@@ -28,6 +28,16 @@
 // is finished by whichever of them arrives last, summing all parts in stripe
 // order (so the result does not depend on the order of arrival).  Nothing waits
 // for another CTA.
+//
+// Measured: 40 requests of up to 7900 tokens, 64 query heads on 8 of 128 channels,
+// 55.8 us, 222 MB, 4.0 TB/s (60% of the card's copy rate); one request of 131,001
+// tokens 39 us, 143 MB, 3.6 TB/s; one of 700 tokens, 32 heads, 10.5 us, which is
+// latency: 2.5 us to the first copy, about 4 for the first block, 2 and 3 for the
+// joins within and between CTAs.  The stream alone, without the arithmetic, takes
+// 28 us of the first; the arithmetic, 122 instructions of two cycles and 26 mma of
+// eight for a granule and warp, takes most of the rest.  Blocks of 64 tokens,
+// eight warps, rings of two blocks (four at 64 channels): more warps, longer rings
+// and smaller blocks measured the same or up to 10% slower.
 #include <type_traits>
 
 #include "kv.cuh"
@@ -73,7 +83,7 @@ __device__ __forceinline__ void load_words(const uint8_t* at, uint32_t (&w)[N]) 
 // that sees no token is zero.
 __device__ __forceinline__ void store_row(const KvAttnParams& p, const KvSeq& s, int h, int rr, int ch, int D,
                                           float4 acc, float sum) {
-  const int i = rr / p.group, head = h * p.group + rr - i * p.group;
+  const int i = kv_div_group(p, rr), head = h * p.group + rr - i * p.group;
   const float inv = s.len - s.nq + i >= 0 ? 1.f / sum : 0.f;
   if (inv == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
   uint2 v;
@@ -402,7 +412,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
       const int row = rb * RB + nb * 8 + g;
       float sum = 0.f;
       if (row < rows) {
-        const int i = row / p.group, head = h * p.group + row - i * p.group;
+        const int i = kv_div_group(p, row), head = h * p.group + row - i * p.group;
         const uint4* src = reinterpret_cast<const uint4*>(
             p.q + (long long)(w.s.q0 + i) * p.q_ts + (long long)head * p.q_hs + c * (D / 4));
 #pragma unroll
@@ -430,13 +440,13 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int rr = rb * RB + nb * 8 + 2 * c + e;
-        const int pos = first + rr / p.group;
+        const int pos = first + kv_div_group(p, rr);
         hi_pos[nb][e] = rr < rows ? pos + 1 : 0;
         lo_pos[nb][e] = p.window > 0 ? pos - p.window + 1 : 0;
       }
     }
     // tokens every row sees, [all_lo, all_hi), and tokens any row sees
-    const int i_first = rb * RB / p.group, i_last = (min(rows, (rb + 1) * RB) - 1) / p.group;
+    const int i_first = kv_div_group(p, rb * RB), i_last = kv_div_group(p, min(rows, (rb + 1) * RB) - 1);
     const int all_hi = first + i_first + 1, any_hi = first + i_last + 1;
     const int all_lo = p.window > 0 ? first + i_last - p.window + 1 : 0;
     const int any_lo = p.window > 0 ? first + i_first - p.window + 1 : 0;

@@ -25,6 +25,17 @@
 //     block, are in the order in which the codes unpack, in both operands alike.
 //   * A row's reference R is chosen so that p_t s_t starts at 2^6 at most; it is
 //     only moved, and O rescaled, when some p_t s_t would pass 2^14.
+//
+// Measured: 1000 new tokens on 9000, 64 query heads on 8 of 128 channels, 355 us,
+// 785 TFLOP/s (40% of the card's bf16 rate); the prompts of 5 requests of 682 to
+// 1900 tokens, 32 heads, 183 us, 404 TFLOP/s.  A block of 64 tokens for 256 rows
+// takes about 2700 cycles, of which shared memory needs 1950 (Q and K for S, V, the
+// dequantised block's writes, scales and offsets), the softmax warps' instructions
+// 1650 and the products 1540 (N is 64 for S, and costs nearly what 128 would): no one
+// of them is the bound alone.  Short items also pay about 6 us each for their
+// start, their first (longer) block and their rows' results.  Tried and slower: one
+// tile per CTA (the block dequantised for 128 rows only), S = Q K^T with Q in
+// tensor memory, products issued by the softmax warps.
 #include <type_traits>
 
 #include "kv.cuh"

@@ -22,6 +22,12 @@
 //   * v is normalised by a power of two per row (so that no magnitude of x leaves
 //     fp16's range) and rounded to fp16 for the second product: one rounding of
 //     2^-12 per term of a sum that is itself an addition to y.
+//
+// Measured beside the product (its own time first), 4096 x 12288: 32 rows of 21
+// adapters of rank 16 13.9 + 9.3 us; 48 of 21, rank 64 (44 MB) 15.7 + 14, 3.2 TB/s; of
+// rank 128 15.7 + 28, 3.1 TB/s; one row, 4096 x 4096, rank 16, 5.9 + 5.2; 2000 rows of
+// prompts 162 + 41 (15 of them reading and writing y).  A single row's time is three
+// trips to memory (index, A and x, B) and a barrier of the cluster.
 #include "lora.h"
 
 #include <cuda_fp16.h>
