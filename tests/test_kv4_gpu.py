@@ -160,6 +160,10 @@ ATTENTION = [
     # many requests: more than threads of a CTA; several whole requests in a warp's stripe
     ([i * 7 % 50 + 1 for i in range(300)], [1] * 300, 4, 1, 64, 16, 0),
     ([i * 37 % 400 + 1 for i in range(60)], [1] * 60, 8, 2, 128, 32, 0),
+    # whole segments for every warp: one or none of equal ones, several of unequal ones, two row groups
+    ([130] * 40, [1] * 40, 8, 8, 128, 32, 0),
+    ([i * 11 % 120 + 3 for i in range(100)], [1, 2, 0, 3] * 25, 32, 16, 64, 16, 0),
+    ([100 + i % 3 for i in range(50)], [9] * 50, 16, 8, 128, 16, 64),
 ]
 
 

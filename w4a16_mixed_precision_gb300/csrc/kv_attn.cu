@@ -192,6 +192,20 @@ __device__ __forceinline__ void advance(const KvAttnParams& p, Cursor& c, int by
   }
 }
 
+// Moves on by k segments, to the beginning of one.
+template <typename Sh>
+__device__ __forceinline__ void skip_segments(const KvAttnParams& p, Cursor& c, int k) {
+  c.g = 0;
+  c.seg += k;
+  while (c.seg >= p.kv.hkv * c.w.rbs) {
+    c.seg -= p.kv.hkv * c.w.rbs;
+    do {
+      if (++c.b >= p.kv.B) return;
+      c.w = seq_work<Sh>(p, c.b, false);
+    } while (c.w.rbs == 0);
+  }
+}
+
 // What a warp left in shared memory: the end of a segment that began before its
 // stripe (or a middle of one), and the beginning of one that goes on after it.
 struct Segment {
@@ -302,27 +316,34 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
     longest = max(longest, ctrl->longest[w]);
   }
   if (U == 0) return;
-  // Few segments of moderate length: a CTA each (by_seg), so that none is cut
-  // between CTAs.  Publishing and joining parts costs about as much as six
-  // blocks of a warp.
-  const long long even = (U + (long long)gridDim.x * W - 1) / ((long long)gridDim.x * W);
-  const bool by_seg = segs <= (long long)gridDim.x && (longest + W - 1) / W <= even + 6;
+  // Few short segments: a CTA each (by_seg), so that none is cut between CTAs.  Many: a
+  // run of whole ones for every warp (by_warp), so that none is cut at all.  What that
+  // may cost a warp in blocks is what publishing and joining parts costs: 2 between CTAs,
+  // 4 with those between warps, half of it where a block is of 16 rows.  Measured with
+  // 128 channels, whole against cut: 32 segments of 32 blocks (4 a warp, cut 1) 14.4
+  // against 12.2 us, 64 of 65 (9, 3) 23.4 against 18.7; 256 of 4 blocks (4, 1) 13.7
+  // against 14.9, 1536 of 2 (4, 3) 16.4 against 23.5.
+  constexpr int kCutSeg = NB == 1 ? 2 : 1, kCutWarp = NB == 1 ? 4 : 2;
+  const long long warps = (long long)gridDim.x * W, even = (U + warps - 1) / warps;
+  const bool by_seg = segs <= (long long)gridDim.x && (longest + W - 1) / W <= even + kCutSeg;
+  const bool by_warp = segs > (long long)gridDim.x && (segs + warps - 1) / warps * longest <= even + kCutWarp;
+  const bool uncut = by_seg || by_warp;
   // otherwise an equal share of all blocks for every warp, at least one
-  const long long G = by_seg ? segs : min((long long)gridDim.x, (U + W - 1) / W);
+  const long long G = by_seg ? segs : by_warp ? gridDim.x : min((long long)gridDim.x, (U + W - 1) / W);
   if (blockIdx.x >= G) return;
   const long long u_cta = begin_of(blockIdx.x, U, G);
   {
-    const long long at = by_seg ? blockIdx.x : u_cta;
-    const long long from = by_seg ? before_segs : before;
-    if (at >= from && at < from + (by_seg ? mine_segs : mine)) {
+    const long long at = by_seg ? blockIdx.x : by_warp ? begin_of(blockIdx.x, segs, G) : u_cta;
+    const long long from = uncut ? before_segs : before;
+    if (at >= from && at < from + (uncut ? mine_segs : mine)) {
       long long off = at - from;
       for (int b = b0; b < b1; ++b) {
         const SeqWork w = seq_work<Sh>(p, b, false);
-        const long long n = (long long)p.kv.hkv * w.rbs * (by_seg ? 1 : w.n);
+        const long long n = (long long)p.kv.hkv * w.rbs * (uncut ? 1 : w.n);
         if (off < n) {
           ctrl->start_b = b;
           ctrl->start_w = w;
-          ctrl->start_off = by_seg ? off * w.n : off;
+          ctrl->start_off = uncut ? off * w.n : off;
           break;
         }
         off -= n;
@@ -342,6 +363,19 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
     from = (long long)cur.w.n * warp / W;
     total = (int)((long long)cur.w.n * (warp + 1) / W - from);
     cur.g += (int)from;  // inside the segment, or at its end where there is nothing left to do
+  } else if (by_warp) {
+    const long long gw = (long long)blockIdx.x * W + warp, s0 = begin_of(gw, segs, G * W);
+    int left = (int)(begin_of(gw + 1, segs, G * W) - s0);
+    total = 0;
+    if (left > 0) {
+      skip_segments<Sh>(p, cur, (int)(s0 - begin_of(blockIdx.x, segs, G)));
+      for (Cursor c = cur; left > 0;) {
+        const int take = min(left, p.kv.hkv * c.w.rbs - c.seg);
+        total += take * c.w.n;
+        left -= take;
+        if (left > 0) skip_segments<Sh>(p, c, take);
+      }
+    }
   } else {
     const long long gw = (long long)blockIdx.x * W + warp;
     from = begin_of(gw, U, G * W);
