@@ -339,7 +339,7 @@ __device__ __forceinline__ void find_item(const KvAttnParams& p, CtrlP& ctrl) {
   __syncwarp();
   const long long S = p.stripes, mean = U / S;
   const long long whole = min((items + S - 1) / S * longest, mean + longest / 2);
-  if (whole <= mean + kCutCost + kCutItemCost * items / S) {
+  if (items <= (long long)gridDim.x && whole <= mean + kCutCost + kCutItemCost * items / S) {
     if (lane == 0) ctrl.by_item = 1;
   } else if (lane == 0) {
     ctrl.start_b = -1;
@@ -398,6 +398,10 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
   tc_fence_after();
   const uint32_t tmem = ctrl.tmem;
   bool by_item = ctrl.by_item;
+  if (by_item && ctrl.start_b < 0) {  // no item for this CTA
+    if (warp == kSoftmaxWarps + kDequantWarps) tmem_dealloc(tmem, kTmem);
+    return;
+  }
   long long U = 0, G = 0, u_begin = 0, u_end = 0;
   if (!by_item) {
     // every warp sums a run of requests; the warp whose run holds the CTA's first block finds it
