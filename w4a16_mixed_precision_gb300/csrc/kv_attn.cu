@@ -143,7 +143,7 @@ struct Shape {
   static constexpr int BB = GB * GR;            // bytes of a block
   static constexpr int kOStride = D + 4;        // floats of a row of a part in shared memory
   static constexpr int kPart = RB * (kOStride + 2) * 4;  // rows, then (maximum, sum) of each
-  static constexpr int kRing = 3072;           // after the control block
+  static constexpr int kRing = 3 * 1024;          // after the control block
   static constexpr int kSmem = kRing + W * S * BB;
   static_assert(kPart <= S * BB && kPart % 16 == 0, "a part has to fit a warp's ring");
   static_assert(W <= kKvAttnWarps && W * S <= 64, "the control block's and the workspace's room");
@@ -253,7 +253,7 @@ struct AttnCtrl {
   SeqWork start_w;
   Parts parts[kKvAttnWarps];
 };
-static_assert(sizeof(AttnCtrl) <= 3072, "control block too large");
+static_assert(sizeof(AttnCtrl) <= 3 * 1024, "control block too large");
 
 template <int D, int NB>
 __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const KvAttnParams p) {
