@@ -1,0 +1,58 @@
+"""Prompt attention where a CTA's stripe runs through several items (256 query rows of a key head
+each), against the formula in 64 bits.
+
+Tolerances are those of test_kv4_gpu.py, derived there.
+"""
+import numpy as np
+import pytest
+
+import kv_ref
+from test_kv4_gpu import _built, close, make, split  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+def exact(q, k, v, scale, window=0):
+    """kv_ref.attention's formula for the last rows of one request, head by head in 64 bits on the GPU."""
+    cu = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda().double()  # noqa: E731
+    q, k, v = cu(q), cu(k), cu(v)
+    n, hq, _ = q.shape
+    length, hkv, _ = k.shape
+    pos = torch.arange(length - n, length, device="cuda")[:, None]
+    t = torch.arange(length, device="cuda")
+    hide = t > pos
+    if window:
+        hide = hide | (t + window <= pos)
+    out = torch.empty_like(q)
+    for h in range(hq):
+        s = (q[:, h] @ k[:, h // (hq // hkv)].t() * scale).masked_fill(hide, -float("inf"))
+        out[:, h] = torch.softmax(s, -1) @ v[:, h // (hq // hkv)]
+    return out.cpu().numpy()
+
+
+STRIPES = [
+    # lens, nq, hq, hkv, D, page, window
+    ([4400], [1000], 40, 40, 128, 64, 0),       # more long items than SMs, about one a stripe: most stripes cross an end
+    ([4400], [1000], 24, 24, 128, 32, 0),       # fewer items than SMs, each cut in two or three
+    ([3800, 4100], [350, 350], 64, 8, 128, 16, 0),
+    ([4400], [1000], 40, 40, 64, 64, 0),
+    ([6000], [1000], 24, 24, 128, 128, 4000),
+]
+
+
+@pytest.mark.parametrize("lens,nq,hq,hkv,D,page,window", STRIPES)
+def test_stripes_through_several_items(lens, nq, hq, hkv, D, page, window):
+    import w4a16_mixed_precision_gb300 as w4
+    k, v, cache, batch, hist = make(lens, nq, hkv, D, page, seed=sum(lens) + hq)
+    ws = w4.Kv4Workspace(batch, hq, cache)
+    w4.kv4_append(torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), cache, hist, ws)
+    q = np.random.default_rng(50).standard_normal((sum(nq), hq, D)).astype(np.float16)
+    dq = torch.from_numpy(q).cuda()
+    y = w4.kv4_attention(dq, cache, batch, ws, window=window)
+    for _ in range(20):
+        assert torch.equal(w4.kv4_attention(dq, cache, batch, ws, window=window), y)
+    assert w4.device_status(ws) == 0
+    kv, vv = split(kv_ref.values(k), lens), split(kv_ref.values(v), lens)
+    for b, (qq, yy) in enumerate(zip(split(q, nq), split(y.cpu().numpy(), nq))):
+        close(yy, exact(qq, kv[b], vv[b], D ** -0.5, window), vv[b])

@@ -678,14 +678,19 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
     const bool whole = at.x == 0 && x1 == at.span.n;
     const float sum = l.x + l.y, off = pz.x + pz.y;
     const bool any = half_.to > half_.from;  // else there is nothing of this tile in tensor memory
-    // a finished row's channels 32 part .. + 31 into Q's place, which no product reads any more
-    const uint32_t ot = base + Sh::kOffQ + tile * Sh::kQ;
+    // a finished row's channels 32 part .. + 31 into Q's room, which no product of this item reads any
+    // more.  A warp keeps its 32 rows in the bytes that hold its own rows of Q, as no barrier orders
+    // the tile's warps between these rows and the next item's Q: 128 bytes of a row, of 128 channels
+    // in two panels, so that rows 0 to 15 of a warp are in the first panel and 16 to 31 in the second.
+    // (In the order of Q itself the code of the whole loop came out 5% slower: registers.)
+    const uint32_t ot = base + Sh::kOffQ + tile * Sh::kQ - (D == 128 ? wrow * 128 : 0);
+    auto place = [&](int r) { return ot + r * (D * 2) + (D == 128 && (r & 16) ? kTile * 128 - 16 * (D * 2) : 0); };
     auto keep = [&](int part, const float (&v)[32]) {
       const int r = wrow + lane;
 #pragma unroll
       for (int t = 0; t < 32; t += 8) {
         const int u = part * 4 + t / 8;
-        sts128(ot + r * (D * 2) + ((u ^ (r & 7)) << 4), make_uint4(pack(v[t], v[t + 1]), pack(v[t + 2], v[t + 3]),
+        sts128(place(r) + ((u ^ (r & 7)) << 4), make_uint4(pack(v[t], v[t + 1]), pack(v[t + 2], v[t + 3]),
                                                                    pack(v[t + 4], v[t + 5]), pack(v[t + 6], v[t + 7])));
       }
     };
@@ -697,7 +702,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       for (int it = 0; it < kRounds; ++it) {
         const int r = it * kPerRound + lane / kLanes, u = lane % kLanes;
         const long long to = __shfl_sync(0xffffffffu, out_at, r);
-        const uint4 v = lds128(ot + (wrow + r) * (D * 2) + ((u ^ (r & 7)) << 4));
+        const uint4 v = lds128(place(wrow + r) + ((u ^ (r & 7)) << 4));
         if (to >= 0) *reinterpret_cast<uint4*>(p.out + to + 8 * u) = v;
       }
       __syncwarp();
