@@ -485,14 +485,15 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 2 ? 2 : 1) lora_few_kernel(
 
 // y += v . B^T for blocks of 128 rows: a warp keeps 32 columns of B in registers
 // (a step of 16 ranks at a time beyond 64) and passes over the rows.  ST: steps
-// of 16 ranks (r <= 16 ST).
+// of 16 ranks (r <= 16 ST).  v and unit lie where the product's partial tiles are
+// when the workspace serves another call, and those have to be zero between calls:
+// the last warp of a block of rows to finish zeroes what the block has read.
 template <int ST>
 __global__ void __launch_bounds__(kWarps * 32, ST <= 4 ? 2 : 1) lora_up_kernel(const LoraParams p) {
   if (threadIdx.x == 0) griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int row0 = blockIdx.x * 128, n0 = (blockIdx.y * kWarps + warp) * 32;
-  if (n0 >= p.N) return;
   int mine[4];  // the adapters of rows lane, lane + 32, ...
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -501,7 +502,7 @@ __global__ void __launch_bounds__(kWarps * 32, ST <= 4 ? 2 : 1) lora_up_kernel(c
     mine[i] = ad < 0 || ad >= p.adapters ? -1 : ad;  // out of range: reported by the first kernel
   }
   const uint16_t* b = p.b + ((long long)n0 + 8 * (g >> 1) + (g & 1)) * p.r + 4 * c;
-  while (true) {
+  while (n0 < p.N) {
     // the next adapter, and its rows
     int ad = -1;
     uint32_t rows[4];
@@ -569,6 +570,17 @@ __global__ void __launch_bounds__(kWarps * 32, ST <= 4 ? 2 : 1) lora_up_kernel(c
       }
     }
   }
+  // release and acquire at the card's scope, for the whole warp by way of its barriers
+  int arrived = 0;
+  __syncwarp();
+  if (lane == 0)
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(arrived) : "l"(p.arrived + blockIdx.x) : "memory");
+  if (__shfl_sync(0xffffffffu, arrived, 0) != (int)gridDim.y * kWarps - 1) return;
+  if (lane == 0) p.arrived[blockIdx.x] = 0;
+  const int rows = min(128, p.M - row0);
+  uint4* v = reinterpret_cast<uint4*>(p.v + (long long)row0 * p.rp);
+  for (int i = lane; i < rows * p.rp / 8; i += 32) v[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = lane; i < rows; i += 32) p.unit[row0 + i] = 0.f;
 }
 
 template <typename F>

@@ -15,6 +15,7 @@ struct LoraParams {
   uint16_t* y;             // fp16 [M][N], the base product; the adapters' part is added to it
   uint16_t* v;             // workspace, for many rows: fp16 [M][rp], scaling * x . A^T of the row over unit[m]
   float* unit;             // workspace: [M], a power of two
+  int* arrived;            // workspace: warps done with each 128 rows; like v and unit zero between calls
   int rp;                  // r rounded up to 16
   int* status;
   int M, K, N, r, adapters;

@@ -28,10 +28,11 @@ marlin_status_t current_sms(int* sms) {
 
 // ---- adapters ---------------------------------------------------------------------
 
-// ---- adapters: the product's workspace, then v and unit for many rows ---------------
-
+// The product's workspace, then for many rows v, unit and arrivals.  All of it is zero
+// between calls: for another M (or shape) the product's partial tiles lie elsewhere in the
+// same buffer, and its reducers take a non-zero word for a sum that has been written.
 struct LoraSizes {
-  size_t gemm, v_off, unit_off, total;
+  size_t gemm, v_off, unit_off, arrived_off, total;
 };
 
 marlin_status_t lora_sizes(int M, int K, int N, int group, int r, int device, LoraSizes* z) {
@@ -39,7 +40,8 @@ marlin_status_t lora_sizes(int M, int K, int N, int group, int r, int device, Lo
   if (s != MARLIN_OK) return s;
   z->v_off = round_up(z->gemm, 256);
   z->unit_off = z->v_off + round_up((size_t)M * round_up(r, 16) * sizeof(uint16_t), 256);
-  z->total = z->unit_off + (size_t)M * sizeof(float);
+  z->arrived_off = z->unit_off + round_up((size_t)M * sizeof(float), 256);
+  z->total = z->arrived_off + ((size_t)M + 127) / 128 * sizeof(int);
   return MARLIN_OK;
 }
 
@@ -172,6 +174,7 @@ marlin_status_t marlin_lora_gemm(const uint16_t* X, const void* packed, const ui
   p.y = Y;
   p.v = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + z.v_off);
   p.unit = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + z.unit_off);
+  p.arrived = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + z.arrived_off);
   p.rp = (int)round_up(r, 16);
   p.status = static_cast<int*>(workspace);
   p.M = M;
