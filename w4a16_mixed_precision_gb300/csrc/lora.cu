@@ -576,6 +576,7 @@ __global__ void __launch_bounds__(kWarps * 32, ST <= 4 ? 2 : 1) lora_up_kernel(c
   if (lane == 0)
     asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(arrived) : "l"(p.arrived + blockIdx.x) : "memory");
   if (__shfl_sync(0xffffffffu, arrived, 0) != (int)gridDim.y * kWarps - 1) return;
+  __syncwarp();
   if (lane == 0) p.arrived[blockIdx.x] = 0;
   const int rows = min(128, p.M - row0);
   uint4* v = reinterpret_cast<uint4*>(p.v + (long long)row0 * p.rp);
