@@ -1,5 +1,5 @@
 """Prompt attention where a CTA's stripe runs through several items (256 query rows of a key head
-each), against the formula in 64 bits.
+each), and where value vectors have a scale of zero, against the formula in 64 bits.
 
 Tolerances are those of test_kv4_gpu.py, derived there.
 """
@@ -56,3 +56,38 @@ def test_stripes_through_several_items(lens, nq, hq, hkv, D, page, window):
     kv, vv = split(kv_ref.values(k), lens), split(kv_ref.values(v), lens)
     for b, (qq, yy) in enumerate(zip(split(q, nq), split(y.cpu().numpy(), nq))):
         close(yy, exact(qq, kv[b], vv[b], D ** -0.5, window), vv[b])
+
+
+@pytest.mark.parametrize("far", [12, 84, 200])
+@pytest.mark.parametrize("kind", ["zero", "constant", "all"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("nq", [1, 80])
+def test_constant_values_with_large_scores(nq, D, kind, far):
+    """A value vector whose channels are all equal has a scale of 0, so its probability enters no product with
+    codes: a score far above the earlier ones (by `far` nats) must move a row's reference all the same.
+    Tolerance: as in test_kv4_gpu.py, and 2^-20 of a score's products' magnitudes (fp32 sums of them, 2^-24
+    each) on either of two scores."""
+    import w4a16_mixed_precision_gb300 as w4
+    lens, hq, hkv, page = [400], 4, 2, 16
+    k, v, cache, batch, hist = make(lens, [nq], hkv, D, page, seed=60)
+    # every query has 1 in its last channel beside small numbers; keys have 0 there but for a few tokens
+    q = (0.05 * np.random.default_rng(61).standard_normal((nq, hq, D))).astype(np.float16)
+    q[:, :, D - 1] = 1
+    k *= np.float16(0.5)
+    k[:, :, D - 1] = 0
+    lifted = [200, 231, 257, 300, 301, 302, 303]
+    k[lifted, :, D - 1] = np.float16(far)
+    k[302, :, D - 1] = np.float16(far + 1)
+    v[lifted] = np.float16(0 if kind == "zero" else 0.75)
+    v[303] = np.float16(-1.5)
+    if kind == "all":
+        v[:] = (np.arange(400) % 7 - 3).astype(np.float16)[:, None, None] * np.float16(0.25)
+    ws = w4.Kv4Workspace(batch, hq, cache)
+    w4.kv4_append(torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), cache, hist, ws)
+    y = w4.kv4_attention(torch.from_numpy(q).cuda(), cache, batch, ws, scale=1.0).cpu().numpy().astype(np.float64)
+    assert w4.device_status(ws) == 0
+    vals = kv_ref.values(v)
+    ref = exact(q, kv_ref.values(k), vals, 1.0)
+    mag = np.abs(q.astype(np.float64)).sum(-1)[:, :, None] * 15 * np.abs(k.astype(np.float64)).max()
+    tol = 2.0 ** -11 * np.abs(ref) + (2.0 ** -12 + 2.0 ** -20 * mag) * np.abs(vals).max() + 2.0 ** -24
+    assert (np.abs(y - ref) <= tol).all()   # NaN fails too

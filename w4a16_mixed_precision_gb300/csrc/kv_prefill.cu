@@ -47,6 +47,7 @@ namespace {
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kUnset = -1e30f;   // a row's reference before it has seen a token
 constexpr float kMost = 16384.f;   // 2^14
+constexpr float kLeastScale = 9.313225746154785e-10f;  // 2^-30
 constexpr int kTile = 128, kTiles = 2, kRows = kTile * kTiles;  // query rows of a tile and of a CTA
 constexpr int kBlock = 64;         // tokens of a block
 constexpr int kTileWarps = 4, kSoftmaxWarps = kTiles * kTileWarps, kDequantWarps = 4;
@@ -903,7 +904,10 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
           float* dst = par0 + stage * (Sh::kPar / 4) + (16 * dw + (lane & ~1)) * 4 + (lane & 1);
           dst[0] = kf.x * p.scale_log2;
           dst[2] = kf.y * p.scale_log2;
-          dst[4] = vf.x;
+          // no less than 2^-30, so that p s shows how far a row's reference is behind: a vector of
+          // scale 0 has codes less 8 of 0, whose product with any p s is none, and no other
+          // scale is below fp16's 2^-24
+          dst[4] = fmaxf(vf.x, kLeastScale);
           dst[6] = vf.y;
         }
         if (lane == 0) ctrl.vmax[stage][dw] = big;
