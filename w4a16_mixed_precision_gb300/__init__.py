@@ -51,6 +51,12 @@ def _need_cuda(t: torch.Tensor, name: str, dtype=None) -> None:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
 
 
+def _need_dense(w) -> None:
+    # the dense kernels would read past the end of the 2:4 layout's shorter codes
+    if isinstance(w, SparsePackedWeights):
+        raise ValueError("w holds 2:4 weights: this call takes dense ones (PackedWeights), sparse_gemm takes 2:4 ones")
+
+
 def packed_layout(K: int, N: int, group: int, has_zeros: bool):
     return _binding.packed_layout(K, N, group, has_zeros)
 
@@ -126,6 +132,7 @@ def gemm_into(x: torch.Tensor, w: PackedWeights, ws: Workspace, y: torch.Tensor,
               kernel: str = "auto") -> torch.Tensor:
     """y[M, N] = x[M, K] . dequant(W), fp16, on the current stream.  kernel:
     "auto" (by M), "warp" (warp-level kernel, M <= 32) or "tcgen05"."""
+    _need_dense(w)
     _need_cuda(x, "x", torch.float16)
     _need_cuda(y, "y", torch.float16)
     M, K = x.shape
@@ -154,6 +161,7 @@ def gemm_host(x_host: torch.Tensor, x_dev: torch.Tensor, w: PackedWeights, ws: W
     all on the current stream (one library call: copy in, multiply, copy out).
     Host tensors should be pinned; y_host is complete once the stream is
     synchronised."""
+    _need_dense(w)
     for t, n in ((x_host, "x_host"), (y_host, "y_host")):
         if t.device.type != "cpu" or t.dtype != torch.float16 or not t.is_contiguous():
             raise ValueError(f"{n} must be a contiguous fp16 host tensor")

@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import torch
 
-from . import Workspace, _binding, _need_cuda, _on_current_device
+from . import PackedWeights, Workspace, _binding, _need_cuda, _need_dense, _on_current_device
 from ._binding import MarlinError
 
 MAX_RANK = 128
@@ -67,10 +67,11 @@ class LoraWorkspace(Workspace):
         return _binding.lora_workspace_bytes(M, K, N, group, self.r, device)
 
 
-def lora_gemm_into(x: torch.Tensor, w, bank: LoraBank, index: torch.Tensor, ws: LoraWorkspace,
+def lora_gemm_into(x: torch.Tensor, w: PackedWeights, bank: LoraBank, index: torch.Tensor, ws: LoraWorkspace,
                    y: torch.Tensor) -> torch.Tensor:
     """y[M, N] = x[M, K] . dequant(W) + the part of each row's adapter, fp16, on
     the current stream.  index: int32 [M], negative for no adapter."""
+    _need_dense(w)
     f16, K = torch.float16, w.K
     M = x.shape[0]
     if x.dtype is not f16 or y.dtype is not f16 or index.dtype is not torch.int32 or not (
@@ -95,6 +96,7 @@ def lora_gemm_into(x: torch.Tensor, w, bank: LoraBank, index: torch.Tensor, ws: 
     return y
 
 
-def lora_gemm(x: torch.Tensor, w, bank: LoraBank, index: torch.Tensor, ws: LoraWorkspace) -> torch.Tensor:
+def lora_gemm(x: torch.Tensor, w: PackedWeights, bank: LoraBank, index: torch.Tensor,
+              ws: LoraWorkspace) -> torch.Tensor:
     y = torch.empty((x.shape[0], w.N), dtype=torch.float16, device=x.device)
     return lora_gemm_into(x, w, bank, index, ws, y)
