@@ -51,6 +51,21 @@ def _need_cuda(t: torch.Tensor, name: str, dtype=None) -> None:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
 
 
+class _Handle:
+    """What a call reads of an object of several tensors, checked once: `_args`, by `_check`.  Replacing
+    one of `_fields` drops it, and the next call checks again; so does a copy's first call."""
+    _fields = ()
+    _args = None
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name in self._fields:
+            object.__setattr__(self, "_args", None)
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_args"}
+
+
 def _need_dense(w) -> None:
     # the dense kernels would read past the end of the 2:4 layout's shorter codes
     if isinstance(w, SparsePackedWeights):

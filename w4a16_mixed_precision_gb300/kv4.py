@@ -13,41 +13,52 @@ from dataclasses import dataclass
 
 import torch
 
-from . import _binding, _on_current_device
+from . import _binding, _Handle, _on_current_device
 from ._binding import MarlinError
 
 
-class Kv4Cache:
+class Kv4Cache(_Handle):
     """n_pages pages of page_size tokens of every key head, keys and values in
     4 bits (head_dim + 8 bytes per token and head)."""
+    _fields = ("buf", "n_pages", "kv_heads", "head_dim", "page_size")
 
     def __init__(self, n_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, device=None):
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         if dev.type != "cuda":
             raise ValueError("a cache lives on a CUDA device")
-        self.nbytes = _binding.kv_cache_bytes(n_pages, kv_heads, head_dim, page_size)
         self.n_pages, self.kv_heads, self.head_dim, self.page_size = n_pages, kv_heads, head_dim, page_size
-        self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=dev)
+        self.buf = torch.zeros(_binding.kv_cache_bytes(n_pages, kv_heads, head_dim, page_size), dtype=torch.uint8,
+                               device=dev)
+        self._check()
+
+    def _check(self):
+        self.nbytes = _binding.kv_cache_bytes(self.n_pages, self.kv_heads, self.head_dim, self.page_size)
+        _need_bytes(self.buf, "the cache's buf", self.nbytes)
         self._device = self.buf.get_device()
-        self._scale = 1.0 / math.sqrt(head_dim)
-        self._args = (self.buf.data_ptr(), n_pages, kv_heads, head_dim, page_size)
+        self._scale = 1.0 / math.sqrt(self.head_dim)
+        self._args = (self.buf.data_ptr(), self.n_pages, self.kv_heads, self.head_dim, self.page_size)
+        return self._args
 
 
 @dataclass
-class Kv4Batch:
+class Kv4Batch(_Handle):
     """One step's requests.  page_table int32 [B, pages], lengths int32 [B]
     (cached tokens, the new ones included), q_start int32 [B + 1] (the new
     tokens of request b are rows q_start[b] .. q_start[b+1] - 1, its last
     positions); tokens = q_start[B] rows in all, at most max_q of one request.
     The tensors are read by the kernels at each call: they may be updated in
-    place between steps."""
+    place between steps, or replaced (not resized in place)."""
     page_table: torch.Tensor
     lengths: torch.Tensor
     q_start: torch.Tensor
     tokens: int
     max_q: int = 1
+    _fields = ("page_table", "lengths", "q_start", "tokens", "max_q")
 
     def __post_init__(self):
+        self._check()
+
+    def _check(self):
         for name in ("page_table", "lengths", "q_start"):
             t = getattr(self, name)
             if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous():
@@ -61,22 +72,35 @@ class Kv4Batch:
         self._device = self.lengths.get_device()
         self._args = (self.page_table.data_ptr(), self.page_table.shape[1], self.lengths.data_ptr(),
                       self.q_start.data_ptr(), B, self.tokens)
+        return self._args
 
 
-class Kv4Workspace:
+class Kv4Workspace(_Handle):
     """Device workspace of the cache's calls for this number of query heads and
     batches of up to this one's requests and tokens; zeroed once."""
+    _fields = ("buf",)
 
     def __init__(self, batch: Kv4Batch, heads: int, cache: Kv4Cache):
         dev = cache.buf.device
-        self.nbytes = _binding.kv_workspace_bytes(heads, cache.kv_heads, cache.head_dim, batch.lengths.shape[0],
-                                                  batch.tokens, dev.index)
-        self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=dev)
-        self._device, self._ptr = self.buf.get_device(), self.buf.data_ptr()
+        nbytes = _binding.kv_workspace_bytes(heads, cache.kv_heads, cache.head_dim, batch.lengths.shape[0],
+                                             batch.tokens, dev.index)
+        self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        self._check()
+
+    def _check(self):
+        _need_bytes(self.buf, "the workspace's buf", 256)
+        self.nbytes, self._device = self.buf.numel(), self.buf.get_device()
+        self._args = (self.buf.data_ptr(), self.nbytes)
+        return self._args
 
     @property
     def ptr(self) -> int:
-        return self._ptr
+        return self.buf.data_ptr()
+
+
+def _need_bytes(t: torch.Tensor, name: str, nbytes: int) -> None:
+    if not t.is_cuda or t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < nbytes:
+        raise ValueError(f"{name} must be a contiguous uint8 CUDA tensor of at least {nbytes} bytes")
 
 
 def _explain(name: str, t: torch.Tensor, tokens: int, heads, cache: Kv4Cache) -> None:
@@ -101,6 +125,7 @@ def kv4_append(k: torch.Tensor, v: torch.Tensor, cache: Kv4Cache, batch: Kv4Batc
     """Quantise the batch's new keys and values, fp16 [tokens, kv_heads,
     head_dim] (views of one QKV product are fine), into the cache, on the
     current stream."""
+    cached, rows, work = cache._args or cache._check(), batch._args or batch._check(), ws._args or ws._check()
     want = (batch.tokens, cache.kv_heads, cache.head_dim)
     ks, vs = k.stride(), v.stride()
     for name, t, st in (("k", k, ks), ("v", v, vs)):
@@ -108,7 +133,7 @@ def kv4_append(k: torch.Tensor, v: torch.Tensor, cache: Kv4Cache, batch: Kv4Batc
             _explain(name, t, batch.tokens, cache.kv_heads, cache)
     cur = _on_device(cache, batch, ws, ("k", k), ("v", v))
     rc = (_binding._lib or _binding.load()).marlin_kv_append(
-        k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], *cache._args, *batch._args, ws._ptr,
+        k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], *cached, *rows, work[0],
         torch._C._cuda_getCurrentRawStream(cur))
     if rc:
         raise MarlinError(rc, "marlin_kv_append")
@@ -117,12 +142,13 @@ def kv4_append(k: torch.Tensor, v: torch.Tensor, cache: Kv4Cache, batch: Kv4Batc
 def kv4_read(cache: Kv4Cache, batch: Kv4Batch, ws: Kv4Workspace):
     """(k, v), fp16 [tokens, kv_heads, head_dim]: the values the cache holds for
     the batch's new tokens."""
+    cached, rows, work = cache._args or cache._check(), batch._args or batch._check(), ws._args or ws._check()
     cur = _on_device(cache, batch, ws)
     shape = (batch.tokens, cache.kv_heads, cache.head_dim)
     k = torch.empty(shape, dtype=torch.float16, device=cache.buf.device)
     v = torch.empty_like(k)
     rc = (_binding._lib or _binding.load()).marlin_kv_read(
-        k.data_ptr(), v.data_ptr(), *cache._args, *batch._args, ws._ptr, torch._C._cuda_getCurrentRawStream(cur))
+        k.data_ptr(), v.data_ptr(), *cached, *rows, work[0], torch._C._cuda_getCurrentRawStream(cur))
     if rc:
         raise MarlinError(rc, "marlin_kv_read")
     return k, v
@@ -134,6 +160,7 @@ def kv4_attention_into(q: torch.Tensor, cache: Kv4Cache, batch: Kv4Batch, ws: Kv
     over the cache, which holds their own keys and values already.  scale:
     1 / sqrt(head_dim) by default; window > 0: a token sees that many positions,
     its own included."""
+    cached, rows, work = cache._args or cache._check(), batch._args or batch._check(), ws._args or ws._check()
     qs, shape = q.stride(), q.shape
     if (q.dtype is not torch.float16 or len(shape) != 3 or shape[0] != batch.tokens or shape[2] != cache.head_dim
             or qs[2] != 1 or not q.is_cuda):
@@ -143,8 +170,8 @@ def kv4_attention_into(q: torch.Tensor, cache: Kv4Cache, batch: Kv4Batch, ws: Kv
         raise ValueError("out must be contiguous")
     cur = _on_device(cache, batch, ws, ("q", q), ("out", out))
     rc = (_binding._lib or _binding.load()).marlin_kv_attention(
-        q.data_ptr(), qs[0], qs[1], shape[1], *cache._args, *batch._args, batch.max_q,
-        cache._scale if scale is None else scale, window, out.data_ptr(), ws._ptr, ws.nbytes,
+        q.data_ptr(), qs[0], qs[1], shape[1], *cached, *rows, batch.max_q,
+        cache._scale if scale is None else scale, window, out.data_ptr(), *work,
         torch._C._cuda_getCurrentRawStream(cur))
     if rc:
         raise MarlinError(rc, "marlin_kv_attention")

@@ -8,18 +8,30 @@ from __future__ import annotations
 
 import torch
 
-from . import PackedWeights, Workspace, _binding, _need_cuda, _need_dense, _on_current_device
+from . import PackedWeights, Workspace, _binding, _Handle, _need_cuda, _need_dense, _on_current_device
 from ._binding import MarlinError
 
 MAX_RANK = 128
 
 
-class LoraBank:
+class LoraBank(_Handle):
     """The adapters of one projection, on the device: a fp16 [n, r, K], b fp16
     [n, N, r], scaling fp32 [n].  A rank that is not a multiple of 8 is padded
-    with zeros (a copy)."""
+    with zeros (a copy).  n, r (padded), K and N follow from the tensors, which
+    may be updated in place or replaced between calls (not resized in place)."""
+    _fields = ("a", "b", "scaling")
 
     def __init__(self, a: torch.Tensor, b: torch.Tensor, scaling: torch.Tensor):
+        self.a, self.b, self.scaling = a, b, scaling
+        self._check()
+
+    def __setattr__(self, name, value):
+        if name in ("n", "r", "K", "N"):
+            raise AttributeError(f"{name} follows from the adapters' tensors")
+        super().__setattr__(name, value)
+
+    def _check(self):
+        a, b, scaling = self.a, self.b, self.scaling
         if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
             raise ValueError(f"expected a [n, r, K] and b [n, N, r], got {tuple(a.shape)} and {tuple(b.shape)}")
         if tuple(scaling.shape) != (a.shape[0],):
@@ -38,9 +50,10 @@ class LoraBank:
         if pad:
             a, b = torch.nn.functional.pad(a, (0, 0, 0, pad)), torch.nn.functional.pad(b, (0, pad))
         self.a, self.b, self.scaling = a.contiguous(), b.contiguous(), scaling.contiguous()
-        self.n, self.r, self.K, self.N = n, r + pad, K, b.shape[1]
+        self.__dict__.update(n=n, r=r + pad, K=K, N=b.shape[1])
         self._device = self.a.get_device()
         self._args = (self.a.data_ptr(), self.b.data_ptr(), self.scaling.data_ptr(), n, self.r)
+        return self._args
 
     @classmethod
     def stack(cls, adapters) -> "LoraBank":
@@ -72,6 +85,7 @@ def lora_gemm_into(x: torch.Tensor, w: PackedWeights, bank: LoraBank, index: tor
     """y[M, N] = x[M, K] . dequant(W) + the part of each row's adapter, fp16, on
     the current stream.  index: int32 [M], negative for no adapter."""
     _need_dense(w)
+    adapters = bank._args or bank._check()
     f16, K = torch.float16, w.K
     M = x.shape[0]
     if x.dtype is not f16 or y.dtype is not f16 or index.dtype is not torch.int32 or not (
@@ -89,7 +103,7 @@ def lora_gemm_into(x: torch.Tensor, w: PackedWeights, bank: LoraBank, index: tor
         _on_current_device(("x", x), ("weights", w.buf), ("adapters", bank.a), ("index", index), ("workspace", ws.buf),
                            ("y", y))
     rc = (_binding._lib or _binding.load()).marlin_lora_gemm(
-        x.data_ptr(), w.codes_ptr, w.scales_ptr, w.zeros_ptr, *bank._args[:3], index.data_ptr(), *bank._args[3:],
+        x.data_ptr(), w.codes_ptr, w.scales_ptr, w.zeros_ptr, *adapters[:3], index.data_ptr(), *adapters[3:],
         y.data_ptr(), M, K, w.N, w.group, ws.buf.data_ptr(), ws.nbytes, torch._C._cuda_getCurrentRawStream(cur))
     if rc:
         raise MarlinError(rc, "marlin_lora_gemm")
