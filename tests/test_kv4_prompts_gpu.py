@@ -91,3 +91,24 @@ def test_constant_values_with_large_scores(nq, D, kind, far):
     mag = np.abs(q.astype(np.float64)).sum(-1)[:, :, None] * 15 * np.abs(k.astype(np.float64)).max()
     tol = 2.0 ** -11 * np.abs(ref) + (2.0 ** -12 + 2.0 ** -20 * mag) * np.abs(vals).max() + 2.0 ** -24
     assert (np.abs(y - ref) <= tol).all()   # NaN fails too
+
+
+@pytest.mark.parametrize("window", [2**31 - 1, 2**30, 18])
+@pytest.mark.parametrize("length,nq", [(2, 5), (20, 23), (100, 164)])
+def test_largest_windows_and_more_new_tokens_than_the_length(length, nq, window):
+    """A window that hides nothing, up to the largest number, leaves the rows that see tokens as they are,
+    in a request whose first new tokens have negative positions too."""
+    import w4a16_mixed_precision_gb300 as w4
+    hq, hkv, D, page = 4, 2, 64, 16
+    k, v, cache, batch, hist = make([length], [length], hkv, D, page, seed=70)
+    ws = w4.Kv4Workspace(w4.Kv4Batch(batch.page_table, batch.lengths, batch.q_start, nq, nq), hq, cache)
+    w4.kv4_append(torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), cache, hist, ws)
+    q = np.random.default_rng(71).standard_normal((nq, hq, D)).astype(np.float16)
+    start = torch.tensor([0, nq], dtype=torch.int32, device="cuda")
+    y = w4.kv4_attention(torch.from_numpy(q).cuda(), cache, w4.Kv4Batch(batch.page_table, batch.lengths, start, nq, nq),
+                         ws, window=window).cpu().numpy()
+    assert w4.device_status(ws) == 7   # MARLIN_ERR_BOUNDS: reported
+    none = nq - length
+    assert (y[:none] == 0).all()
+    close(y[none:], kv_ref.attention(q[none:], kv_ref.values(k), kv_ref.values(v), length, D ** -0.5,
+                                     window if window < length else 0), kv_ref.values(v))

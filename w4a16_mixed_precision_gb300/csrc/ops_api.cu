@@ -268,7 +268,9 @@ marlin_status_t marlin_kv_attention(const uint16_t* q, int64_t q_token_stride, i
   p.heads = heads;
   p.group = group;
   p.group_magic = group == 1 ? 0ull : ~0ull / (unsigned)group + 1;
-  p.window = window;
+  // positions are below 2^30: a window beyond that hides nothing, and position - window stays in 32 bits
+  // for the negative positions of a request with more new tokens than its length, too
+  p.window = std::min(window, 1 << 30);
   p.scale_log2 = scale * 1.4426950408889634f;
   p.whole_blocks = p.kv.page16 % 4 == 0;
   p.min_rows = 0;
