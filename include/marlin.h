@@ -358,7 +358,9 @@ marlin_status_t marlin_lora_workspace_bytes(int M, int K, int N, int group, int 
  *            marlin_gemm.
  * X . A^T is summed in fp32, scaled, and rounded once to fp16 (normalised row by
  * row, so that its range is fp32's) for the product with B; that is summed in
- * fp32 and added to the fp16 base product, so Y is rounded twice.
+ * fp32 and added to the fp16 base product, so Y is rounded twice (its error
+ * against 64 bits is 1.4 times that of one rounding), and where the base product
+ * alone leaves fp16's range Y is infinite whatever the adapter adds.
  * Deterministic.  Errors: INVALID_ARG, UNSUPPORTED (r), MISALIGNED,
  * WORKSPACE_TOO_SMALL (host checks, nothing launched); CUDA.
  */
@@ -378,7 +380,8 @@ marlin_status_t marlin_lora_gemm(const uint16_t* X, const void* packed, const ui
  *     s * (c - 8) + o,   s = fp16((max - min) * fp32(1/15)),  o = fp16(min + 8 s),
  *     c = 8 + clamp(round_to_even((x - o) / s), -8, 7)   (8 where s = 0),
  * in fp32 arithmetic.  A vector that holds an infinity or a NaN reads back as
- * NaN in every channel.
+ * NaN in every channel.  A value near fp16's largest may stand for one up to half
+ * a step beyond it, which marlin_kv_read rounds to infinity.
  *
  * Arguments the entry points share
  *   cache       device, marlin_kv_cache_bytes(...) bytes, 16-byte aligned.  Its
@@ -394,7 +397,8 @@ marlin_status_t marlin_lora_gemm(const uint16_t* X, const void* packed, const ui
  *               the [tokens][heads][head_dim] tensors, and they are its last ones:
  *               row q_start[b] + i is at position lengths[b] - new + i.
  *   workspace   device, marlin_kv_workspace_bytes(...) bytes, 16-byte aligned, zeroed
- *               once; ordering as for marlin_gemm.
+ *               once (and after a call that reports MARLIN_ERR_TIMEOUT); ordering as
+ *               for marlin_gemm.
  * Entries of page_table, lengths and q_start that contradict each other or lie
  * out of range are found on the device, skipped, and reported by
  * marlin_last_device_status as MARLIN_ERR_BOUNDS (that call's results are not
@@ -446,12 +450,15 @@ marlin_status_t marlin_kv_read(uint16_t* k, uint16_t* v, const void* cache, int 
  * q       device, fp16 [tokens][heads][head_dim], 16-byte aligned, strides
  *         multiples of 8.
  * out     device, fp16 [tokens][heads][head_dim] contiguous, 16-byte aligned,
- *         written.  A row that sees no token (more new tokens than the length)
- *         is zero, and reported as above.
+ *         written (rows that no request owns are left alone).  A row that sees no
+ *         token (more new tokens than the length) is zero, and reported as above.
  * max_q   most new tokens of any request; a request with more is served too, but
  *         may be slower.
  * Scores, softmax statistics and sums are fp32; q, the codes, scales and offsets
- * enter the products exactly.  Deterministic for given lengths.
+ * enter the products exactly.  A probability times its value's scale enters as two
+ * fp16 numbers (22 bits) where a request has few query rows per key head (64 at
+ * most), as one (11 bits, error against 64 bits 1.3 to 1.5 times that of the
+ * output's rounding alone) where it has more.  Deterministic for given lengths.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE_TOO_SMALL; CUDA.
  */
 marlin_status_t marlin_kv_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
@@ -468,8 +475,9 @@ marlin_status_t marlin_kv_attention(const uint16_t* q, int64_t q_token_stride, i
  * marlin_gemm keeps in `workspace`, and returns MARLIN_OK,
  * MARLIN_ERR_TIMEOUT (a bounded wait in a kernel expired; that call's Y is
  * not valid) or MARLIN_ERR_BOUNDS: the adapter or cache kernels met an index
- * out of range, or a library built with -DMARLIN_DEBUG (which checks
- * every address its kernels form against the extent of its buffer and skips
+ * out of range (checked in every build), or a library built with
+ * -DMARLIN_DEBUG (which checks every address that the kernels of marlin_gemm
+ * and marlin_sparse_gemm form against the extent of its buffer and skips
  * the access instead of faulting) met such an address; the 32-bit word at byte
  * 4 of the workspace then names the first failed check (cleared too).
  * workspace: device, as passed to marlin_gemm or to the adapter and cache calls.

@@ -19,8 +19,10 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "libw4a16_gb300.so")
-# the bounds-checked build: every address the kernels form is checked against
-# its buffer's extent (MARLIN_DEBUG, see csrc/common.cuh); slower, for tests
+# the bounds-checked build: every address the product's kernels form is checked
+# against its buffer's extent (MARLIN_DEBUG, see csrc/common.cuh); slower, for
+# tests.  The adapter and cache kernels check the indexes they read from the
+# device (adapters, pages, lengths, starts) in either build, and no addresses.
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(LIB_DIR, "libw4a16_gb300_debug.so")
 

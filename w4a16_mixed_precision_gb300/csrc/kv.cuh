@@ -105,7 +105,7 @@ struct KvAttnParams {
   uint16_t* out;            // fp16 [T][heads][D]
   int heads, group;         // query heads, and of them per key head
   int stripes;              // CTAs that share all items of the prompt kernel where these are cut
-  unsigned long long group_magic;  // floor(2^64 / group) + 1, 0 for group = 1
+  unsigned long long group_magic;  // ceil(2^64 / group), 0 for group = 1
   int window;               // > 0: a query sees that many positions, its own included
   float scale_log2;         // softmax scale * log2(e)
   int whole_blocks;         // pages hold whole blocks: one copy each

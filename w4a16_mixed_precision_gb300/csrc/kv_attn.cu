@@ -17,10 +17,11 @@
 //     subnormal c * 2^-24 (one AND per pair; the nibble four bits up is
 //     16 c * 2^-24): the products are exact and scales, offsets and the powers
 //     of two are applied to the fp32 results (kv.cuh has the algebra).
-//   * p_t s_t is fed as the sum of two fp16 numbers (22 bits): with one, the
-//     rounding of the probabilities times uncentred codes would be three times
-//     the rounding of the fp16 output.  s_t is normalised by a running power of
-//     two so that neither half falls below fp16's range.
+//   * p_t s_t is fed as the sum of two fp16 numbers (22 bits): the result is then
+//     as near to 64 bits as its own rounding leaves it (2.1e-4 of it in root mean
+//     square, 2.3e-4 at 131,001 tokens), where one fp16 number, as in the prompt
+//     kernel, gives 2.7 to 3.0e-4.  s_t is normalised by a running power of two so
+//     that neither half falls below fp16's range.
 //   * The maximum is only moved when a score exceeds it by 2^8 (one vote per
 //     block instead of shuffles and a rescaling).
 // A segment that is one warp's alone is written by that warp; the parts of one
@@ -31,10 +32,12 @@
 //
 // Measured: 40 requests of up to 7900 tokens, 64 query heads on 8 of 128 channels,
 // 55.8 us, 222 MB, 4.0 TB/s (60% of the card's copy rate); one request of 131,001
-// tokens 39 us, 143 MB, 3.6 TB/s; one of 700 tokens, 32 heads, 10.5 us, which is
-// latency: 2.5 us to the first copy, about 4 for the first block, 2 and 3 for the
-// joins within and between CTAs.  The stream alone, without the arithmetic, takes
-// 28 us of the first; the arithmetic, 122 instructions of two cycles and 26 mma of
+// tokens 39 us, 143 MB, 3.6 TB/s; one of 700 tokens, 32 heads (32 segments of 11
+// blocks, a CTA each), 10.5 us, which is latency: the look-ups and the first copy, a
+// block or two a warp, the join of its eight warps.  40 requests with 16 query rows a
+// key head (two row groups an instruction): 98 us under ncu, where 8 rows take 61.
+// The stream alone, without the arithmetic, takes
+// 28 us of the first case; the arithmetic, 122 instructions of two cycles and 26 mma of
 // eight for a granule and warp, takes most of the rest.  Blocks of 64 tokens,
 // eight warps, rings of two blocks (four at 64 channels): more warps, longer rings
 // and smaller blocks measured the same or up to 10% slower.

@@ -9,7 +9,7 @@
 // before the look-ups of their places; two tokens that share a word of values
 // write it together.  Measured with 128 channels, 8 heads: 10,740 tokens (56 MB) are
 // written in 19.3 us, 2.9 TB/s, and read back in 13.9 us, 4.0 TB/s (43 and 60% of the
-// card's copy rate); 48 tokens in 4.1 and 3.3 us.  Writing issues an instruction in 58%
+// card's copy rate); 48 tokens in 4.1 and 3.3 us.  Writing issues an instruction in 68%
 // of the cycles; fewer for the codes (sums instead of shifts) changed nothing, so what
 // is left is the loads' latency under one short task per warp.
 #include "kv.cuh"

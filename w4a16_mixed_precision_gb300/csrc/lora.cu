@@ -26,7 +26,7 @@
 // Measured beside the product (its own time first), 4096 x 12288: 32 rows of 21
 // adapters of rank 16 13.9 + 9.3 us; 48 of 21, rank 64 (44 MB) 15.7 + 14, 3.2 TB/s; of
 // rank 128 15.7 + 28, 3.1 TB/s; one row, 4096 x 4096, rank 16, 5.9 + 5.2; 2000 rows of
-// prompts 162 + 41 (15 of them reading and writing y).  A single row's time is three
+// prompts 162 + 43 (15 of them reading and writing y, 3 leaving the workspace zero).  A single row's time is three
 // trips to memory (index, A and x, B) and a barrier of the cluster.
 #include "lora.h"
 
@@ -42,7 +42,7 @@ namespace w4a16 {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kFewRows = 512;  // of the kernel that does both products: room
+constexpr int kFewRows = 512;  // room of the kernel that does both products: 320 rows at most, two for each thread
 constexpr int kLoraSite = 104;  // the word after the status word: an adapter index out of range
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,

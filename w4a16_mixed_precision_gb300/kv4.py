@@ -159,7 +159,8 @@ def kv4_attention_into(q: torch.Tensor, cache: Kv4Cache, batch: Kv4Batch, ws: Kv
     """out[tokens, heads, head_dim] = causal attention of the batch's new tokens
     over the cache, which holds their own keys and values already.  scale:
     1 / sqrt(head_dim) by default; window > 0: a token sees that many positions,
-    its own included."""
+    its own included.  Rows that no request owns are left alone (kv4_attention's
+    are not initialised)."""
     cached, rows, work = cache._args or cache._check(), batch._args or batch._check(), ws._args or ws._check()
     qs, shape = q.stride(), q.shape
     if (q.dtype is not torch.float16 or len(shape) != 3 or shape[0] != batch.tokens or shape[2] != cache.head_dim
