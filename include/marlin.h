@@ -470,6 +470,125 @@ marlin_status_t marlin_kv_attention(const uint16_t* q, int64_t q_token_stride, i
                                     marlin_stream_t stream);
 
 /*
+ * ---- Drafted trees over the 4-bit cache ---------------------------------------------
+ *
+ * A step that verifies proposed tokens: the new tokens of a request are a tree, each
+ * with its parent among them, rather than a run.  They take consecutive positions of
+ * the cache like any new tokens (append); their rotary positions go by their depth, a
+ * token sees the cached tokens before the new ones and its own ancestors, and the
+ * entries of those that are kept are moved together.  The pages have no counterpart.
+ * Arguments shared with the calls above are as there.
+ */
+
+/*
+ * From the tokens' parents to what they see.
+ * parents    device, int32 [tokens]: the parent's index among the new tokens of the
+ *            same request, less than the token's own; negative for a token whose
+ *            parent is the last cached token before the new ones.  A parent that does
+ *            not come before its child is reported as MARLIN_ERR_BOUNDS, and counts as none.
+ * mask       device, int32 [tokens][words], written: bit j % 32 of word j / 32 is set
+ *            where the request's j-th new token is the row's own or one of its
+ *            ancestors.  A request of more than 32 * words new tokens is reported as above.
+ * positions  device, int32 [tokens], written: lengths[b] - new + the row's number of ancestors.
+ * Rows that no request owns are left alone.  lengths up to 2^30.  Of the workspace the
+ * first 256 bytes are used.  Errors: INVALID_ARG, MISALIGNED; CUDA.
+ */
+marlin_status_t marlin_kv_tree(const int32_t* parents, const int32_t* lengths, const int32_t* q_start, int requests,
+                               int tokens, int words, int32_t* mask, int32_t* positions, void* workspace,
+                               marlin_stream_t stream);
+
+/*
+ * marlin_kv_attention where the new tokens see each other as bits say: row i sees the
+ * cached tokens before its request's new ones, and the j-th new one where bit j of
+ * its row of mask is set (its own included: there is no order among them).
+ * mask       device, int32 [tokens][words], as marlin_kv_tree writes it or any other.
+ *            Bits beyond a request's new tokens are ignored; a request of more than
+ *            32 * words new tokens is reported as MARLIN_ERR_BOUNDS.
+ * window     > 0: of the tokens before the new ones a row sees those within the last
+ *            `window` positions up to its own, which is lengths[b] - new + its set
+ *            bits - 1.  (All positions from lengths[b] - new - window on have to be in
+ *            valid pages, and those that share a block of 64 with them.)
+ * A row that sees nothing at all is zero.  Everything else, the workspace too, is as for
+ * marlin_kv_attention.
+ */
+marlin_status_t marlin_kv_tree_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, int heads,
+                                         const void* cache, int n_pages, int kv_heads, int head_dim, int page_size,
+                                         const int32_t* page_table, int max_pages, const int32_t* lengths,
+                                         const int32_t* q_start, int requests, int tokens, int max_q,
+                                         const int32_t* mask, int words, float scale, int window, uint16_t* out,
+                                         void* workspace, size_t workspace_bytes, marlin_stream_t stream);
+
+/*
+ * Rotary positions, and marlin_kv_append: pairs (x1, x2) of the first `rot` channels of
+ * every query and key become (x1 c - x2 s, x2 c + x1 s), each product and sum rounded
+ * to fp32, the result to fp16; the rotated queries are written to q_out, the rotated
+ * keys and the values into the cache.  One launch.
+ * q, k, v, q_out  device, fp16 [tokens][heads or kv_heads][head_dim], 16-byte aligned,
+ *            strides multiples of 8.  q_out may be q with the same strides; else it
+ *            overlaps none of the inputs.
+ * rot        channels that are rotated, the first ones: a multiple of head_dim / 8 (else
+ *            MARLIN_ERR_UNSUPPORTED), at most head_dim.
+ * interleaved  0: pair j < rot / 2 is channels (j, j + rot / 2); else (2 j, 2 j + 1).
+ * positions  device, int32 [axes][tokens]: rows of the table.  One outside it is reported
+ *            as MARLIN_ERR_BOUNDS, and the token is skipped.
+ * axes       1 to 4 (more -> MARLIN_ERR_UNSUPPORTED).
+ * table      device, fp32 [table_rows][rot / 2][2], 16-byte aligned: (c, s) of every
+ *            position and pair.
+ * axis_of_pair  host, [rot / 2]: which of the axes a pair's position is on; NULL: all on
+ *            the first (axes must be 1).
+ * Rows that no request owns are left alone.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED; CUDA.
+ */
+marlin_status_t marlin_kv_rope_append(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, int heads,
+                                      const uint16_t* k, int64_t k_token_stride, int64_t k_head_stride, const uint16_t* v,
+                                      int64_t v_token_stride, int64_t v_head_stride, const int32_t* positions, int axes,
+                                      const float* table, int table_rows, int rot, int interleaved,
+                                      const uint8_t* axis_of_pair, uint16_t* q_out, int64_t out_token_stride,
+                                      int64_t out_head_stride, void* cache, int n_pages, int kv_heads, int head_dim,
+                                      int page_size, const int32_t* page_table, int max_pages, const int32_t* lengths,
+                                      const int32_t* q_start, int requests, int tokens, void* workspace,
+                                      marlin_stream_t stream);
+
+/*
+ * Keeps some of each request's new tokens, in the caches of all layers: with first =
+ * lengths[b] - new, position first + i takes what position first + index[q_start[b] + i]
+ * holds, keys and values of every head, for i < kept[b].  One launch for 128 caches.
+ * caches     host, [count] device pointers to caches that are alike and do not overlap
+ *            (else INVALID_ARG); pages, lengths and indexes are those of every one.
+ * into       NULL: the tokens stay in their request's pages.  index must then ascend
+ *            strictly within a request: one that does not is left as it was and
+ *            reported as MARLIN_ERR_BOUNDS.
+ *            Else device, int32 [requests][into_pages]: the kept tokens' pages, position
+ *            by position as in page_table, none of which is read in this call.  index may
+ *            then name any new tokens in any order.
+ * index      device, int32 [tokens]; kept device, int32 [requests], 0 to the request's new
+ *            tokens; others are reported as above, and nothing of the request is moved.
+ * new_lengths  device, int32 [requests], written: first + kept[b] (lengths[b] where nothing
+ *            was moved for an error); overlaps none of the inputs.
+ * max_q      most new tokens of any request; a request with more is served too, slower.
+ * Positions other than those named are not touched, so that pages that several requests
+ * share are safe where they hold none.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED; CUDA.
+ */
+marlin_status_t marlin_kv_compact(void* const* caches, int count, int n_pages, int kv_heads, int head_dim, int page_size,
+                                  const int32_t* page_table, int max_pages, const int32_t* into, int into_pages,
+                                  const int32_t* lengths, const int32_t* q_start, const int32_t* index,
+                                  const int32_t* kept, int32_t* new_lengths, int requests, int tokens, int max_q,
+                                  void* workspace, marlin_stream_t stream);
+
+/*
+ * Page dst[i] takes what page src[i] holds, in the caches of all layers (as above), for
+ * i < pairs.  A pair whose source is negative is left out; one that names a page that does
+ * not exist is skipped and reported as MARLIN_ERR_BOUNDS.  src, dst: device, int32 [pairs].
+ * A page that is written must be named once only in a call, as source or destination
+ * (what it holds is not specified otherwise).
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED; CUDA.
+ */
+marlin_status_t marlin_kv_copy_pages(void* const* caches, int count, int n_pages, int kv_heads, int head_dim,
+                                     int page_size, const int32_t* src, const int32_t* dst, int pairs, void* workspace,
+                                     marlin_stream_t stream);
+
+/*
  * No page passage: failure reporting of this library's bounded waits.
  * Synchronises `stream`, reads and clears the device status word that
  * marlin_gemm keeps in `workspace`, and returns MARLIN_OK,

@@ -24,7 +24,8 @@ __all__ = ["PackedWeights", "Workspace", "repack", "gemm", "gemm_into", "gemm_ho
            "MarlinError", "status_string", "packed_layout", "SparsePackedWeights", "sparse_repack",
            "sparse_gemm", "sparse_gemm_into", "LoraBank", "LoraWorkspace", "lora_gemm", "lora_gemm_into",
            "Kv4Cache", "Kv4Batch", "Kv4Workspace", "kv4_append", "kv4_read", "kv4_attention",
-           "kv4_attention_into"]
+           "kv4_attention_into", "kv4_tree", "kv4_tree_attention", "kv4_tree_attention_into", "Kv4Rope",
+           "kv4_rope_append", "kv4_rope_append_into", "kv4_compact", "kv4_copy_pages", "Kv4Pages"]
 
 
 def _stream() -> int:
@@ -281,5 +282,6 @@ def sparse_gemm(x: torch.Tensor, w: SparsePackedWeights, ws: Workspace) -> torch
 # ---- operators beside the product ------------------------------------------------
 
 from .lora import LoraBank, LoraWorkspace, lora_gemm, lora_gemm_into  # noqa: E402
-from .kv4 import (Kv4Batch, Kv4Cache, Kv4Workspace, kv4_append, kv4_attention, kv4_attention_into,  # noqa: E402
-                  kv4_read)
+from .kv4 import (Kv4Batch, Kv4Cache, Kv4Pages, Kv4Rope, Kv4Workspace, kv4_append, kv4_attention,  # noqa: E402
+                  kv4_attention_into, kv4_compact, kv4_copy_pages, kv4_read, kv4_rope_append, kv4_rope_append_into,
+                  kv4_tree, kv4_tree_attention, kv4_tree_attention_into)

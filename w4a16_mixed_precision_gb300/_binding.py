@@ -46,6 +46,11 @@ EXPORTS = (
     "marlin_kv_append",
     "marlin_kv_read",
     "marlin_kv_attention",
+    "marlin_kv_rope_append",
+    "marlin_kv_tree",
+    "marlin_kv_tree_attention",
+    "marlin_kv_compact",
+    "marlin_kv_copy_pages",
 )
 
 
@@ -106,7 +111,12 @@ def open_library(path: str) -> ctypes.CDLL:
         lib.marlin_kv_append.argtypes = [P, L, L, P, L, L] + kv + [P, P]
         lib.marlin_kv_read.argtypes = [P, P] + kv + [P, P]
         lib.marlin_kv_attention.argtypes = [P, L, L, I] + kv + [I, F, I, P, P, SZ, P]
-        for f in EXPORTS[-7:]:
+        lib.marlin_kv_rope_append.argtypes = ([P, L, L, I, P, L, L, P, L, L, P, I, P, I, I, I, P, P, L, L] + kv + [P, P])
+        lib.marlin_kv_tree.argtypes = [P, P, P, I, I, I, P, P, P, P]
+        lib.marlin_kv_tree_attention.argtypes = [P, L, L, I] + kv + [I, P, I, F, I, P, P, SZ, P]
+        lib.marlin_kv_compact.argtypes = [P, I, I, I, I, I, P, I, P, I, P, P, P, P, P, I, I, I, P, P]
+        lib.marlin_kv_copy_pages.argtypes = [P, I, I, I, I, I, P, P, I, P, P]
+        for f in EXPORTS[-12:]:
             getattr(lib, f).restype = I
         for f in ("marlin_packed_layout", "marlin_repack", "marlin_workspace_bytes", "marlin_gemm",
                   "marlin_last_device_status"):

@@ -51,7 +51,10 @@ __device__ __forceinline__ void kv_fail(const KvParams& p, int site) {
 }
 
 // Sites of failed checks of device-side inputs (the word after the status word).
-enum KvSite { kKvSiteQStart = 101, kKvSiteLen = 102, kKvSitePage = 103, kKvSiteAdapter = 104 };
+enum KvSite {
+  kKvSiteQStart = 101, kKvSiteLen = 102, kKvSitePage = 103, kKvSiteAdapter = 104, kKvSitePosition = 105, kKvSiteTree = 106,
+  kKvSiteIndex = 107
+};
 
 // Brings the lengths, starts and page table towards L2 before the wait for the
 // previous kernel (which may still be writing them: a prefetch takes no value).
@@ -98,6 +101,17 @@ __device__ __forceinline__ KvSeq kv_seq(const KvParams& p, int b, bool report) {
   return s;
 }
 
+// The request that owns row t of the new tokens (by its starts: the last one that does not begin after it).
+__device__ __forceinline__ int kv_owner(const KvParams& p, int t) {
+  int lo = 0, hi = p.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.q_start[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
 struct KvAttnParams {
   KvParams kv;
   const uint16_t* q;        // fp16 [T][heads][D] with strides
@@ -115,7 +129,39 @@ struct KvAttnParams {
   float* partials;          // [2 grid] parts of segments cut between CTAs, kv_attn_part_floats(D) at most
   float* firsts;            // [grid][warps] parts that a warp leaves before its stripe is done
   unsigned long long timeout_ns;
+  const int* tree;          // for trees: int32 [T][tree_words], bit j of a row: it sees its request's j-th new token
+  int tree_words;
 };
+
+// Trees: a row sees all cached tokens before the new ones (the last `window` up to its position, which is the last of
+// those plus the new tokens that it sees), and the new ones whose bits are set.
+
+// A row's first visible token among those before the new ones, the first new token where it sees none of them.
+__device__ __forceinline__ int kv_tree_lo(const KvAttnParams& p, const KvSeq& s, int i) {
+  const int first = s.len - s.nq;
+  if (p.window <= 0) return 0;
+  const int* row = p.tree + (long long)(s.q0 + i) * p.tree_words;
+  int seen = 0;
+  for (int w = 0; w < p.tree_words && w * 32 < s.nq; ++w) {
+    const int left = s.nq - w * 32;
+    seen += __popc((uint32_t)row[w] & (left < 32 ? (1u << left) - 1u : ~0u));
+  }
+  return min(max(first + seen - p.window, 0), first);
+}
+
+// Which of the tokens t0 .. t0 + 31 row i of a request sees; lo as above.
+__device__ __forceinline__ uint32_t kv_tree_see(const KvAttnParams& p, const KvSeq& s, int i, int lo, int t0) {
+  const int j0 = t0 - (s.len - s.nq);  // the first of them among the new tokens; all before these count as set bits
+  const int w = j0 >> 5;
+  const int* row = p.tree + (long long)(s.q0 + i) * p.tree_words;
+  const uint32_t a = w < 0 ? ~0u : w < p.tree_words ? (uint32_t)row[w] : 0u;
+  const uint32_t b = w + 1 < 0 ? ~0u : w + 1 < p.tree_words ? (uint32_t)row[w + 1] : 0u;
+  uint32_t see = __funnelshift_r(a, b, (uint32_t)j0);
+  const int left = s.nq - j0, hidden = lo - t0;
+  if (left < 32) see &= left <= 0 ? 0u : (1u << left) - 1u;
+  if (hidden > 0) see &= hidden >= 32 ? 0u : ~0u << hidden;
+  return see;
+}
 
 // row / group, exact for 32-bit rows.
 __device__ __forceinline__ int kv_div_group(const KvAttnParams& p, int row) {
@@ -126,7 +172,8 @@ cudaError_t launch_kv_append(const KvParams& p, int D, const uint16_t* k, const 
                              cudaStream_t stream);
 cudaError_t launch_kv_read(const KvParams& p, int D, uint16_t* k, uint16_t* v, const long long (&st)[4],
                            cudaStream_t stream);
-// nb: blocks of 8 query rows that share a pass over the cache (1 or 2)
+// nb: blocks of 8 query rows that share a pass over the cache (1 or 2).  Where p.tree is set the new
+// tokens see each other as its bits say, else causally; of the prompt kernel too.
 cudaError_t launch_kv_attn(const KvAttnParams& p, int D, int nb, int grid, cudaStream_t stream);
 cudaError_t kv_attn_set_smem_limit();
 cudaError_t launch_kv_prefill(const KvAttnParams& p, int D, int grid, cudaStream_t stream);
@@ -137,6 +184,41 @@ constexpr long long kv_prefill_items(long long tokens, int requests, int hkv, in
 // Floats of a part of an item (256 rows) that stripes cut; two for every CTA.
 constexpr int kv_prefill_part_floats(int D) { return 256 * (D + 4); }
 cudaError_t kv_prefill_set_smem_limit();
+
+// ---- rotary positions and append (kv_cache.cu) ----
+constexpr int kRopeAxes = 4;
+struct KvRopeParams {
+  KvParams kv;
+  const uint16_t *q, *k, *v;  // fp16 [T][heads or hkv][D] with strides
+  uint16_t* q_out;
+  long long q_ts, q_hs, o_ts, o_hs, k_ts, k_hs, v_ts, v_hs;  // elements
+  int heads;
+  const int* positions;       // [axes][T]
+  const float* table;         // [table_rows][rot / 2] of (cos, sin)
+  int axes, table_rows, rot;
+  int grouped;                // the pairs of every D / 32 consecutive ones share an axis
+  unsigned long long axis[2];  // two bits a pair
+};
+cudaError_t launch_kv_rope_append(const KvRopeParams& p, int D, bool interleaved, cudaStream_t stream);
+
+// ---- trees, compaction, page copies (kv_tree.cu, kv_move.cu) ----
+cudaError_t launch_kv_tree(const KvParams& p, const int* parents, int words, int* mask, int* positions, cudaStream_t stream);
+constexpr int kMoveCaches = 128;  // of a launch
+struct KvCaches {
+  uint8_t* at[kMoveCaches];
+};
+struct KvCompactParams {
+  KvParams kv;          // its cache is not used
+  int caches;
+  const int* into;      // [B][into_pages], the kept tokens' pages; nullptr: where they are
+  int into_pages;
+  const int *index, *kept;
+  int* new_lens;        // nullptr where another launch writes them
+  int max_q;
+};
+cudaError_t launch_kv_compact(const KvCompactParams& p, const KvCaches& c, int D, cudaStream_t stream);
+cudaError_t launch_kv_copy_pages(const KvCaches& c, int caches, int n_pages, long long page_bytes, const int* src,
+                                 const int* dst, int pairs, int* status, cudaStream_t stream);
 // Warps of a CTA at most, and floats of a part in the workspace at most (16 rows).
 constexpr int kKvAttnWarps = 8;
 constexpr int kv_attn_part_floats(int D) { return 16 * (D + 4 + 2); }

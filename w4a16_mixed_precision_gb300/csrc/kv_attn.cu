@@ -83,11 +83,12 @@ __device__ __forceinline__ void load_words(const uint8_t* at, uint32_t (&w)[N]) 
 }
 
 // Four channels of an output row: row rr of key head h, normalised.  A row
-// that sees no token is zero.
+// that sees no token is zero (its sum is 0, exactly: all its scores are minus infinity).
+template <bool kTree>
 __device__ __forceinline__ void store_row(const KvAttnParams& p, const KvSeq& s, int h, int rr, int ch, int D,
                                           float4 acc, float sum) {
   const int i = kv_div_group(p, rr), head = h * p.group + rr - i * p.group;
-  const float inv = s.len - s.nq + i >= 0 ? 1.f / sum : 0.f;
+  const float inv = (kTree ? sum != 0.f : s.len - s.nq + i >= 0) ? 1.f / sum : 0.f;
   if (inv == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
   uint2 v;
   v.x = h2_bits(__floats2half2_rn(acc.x * inv, acc.y * inv));
@@ -136,8 +137,10 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 }
 
 // W warps; blocks of GB granules, GI of them taken together; S blocks in a warp's ring.
-template <int D, int NB>
+// kT: the new tokens are trees.
+template <int D, int NB, bool kT>
 struct Shape {
+  static constexpr bool kTree = kT;
   static constexpr int W = 8, GB = 4, GI = NB == 1 ? 4 : 2, S = D == 128 ? 2 : 4;
   static constexpr int kBlock = GB * kGranule;  // tokens
   static constexpr int kStep = GI * kGranule;  // tokens taken together
@@ -164,10 +167,12 @@ __device__ __forceinline__ SeqWork seq_work(const KvAttnParams& p, int b, bool r
   SeqWork w;
   w.s = kv_seq(p.kv, b, report);
   if (w.s.nq > w.s.len && report) kv_fail(p.kv, kKvSiteLen);
+  if (Sh::kTree && report && w.s.nq > 32ll * p.tree_words) kv_fail(p.kv, kKvSiteTree);
   const int rows = w.s.nq * p.group;
   w.rbs = rows > p.max_rows ? 0 : (rows + Sh::RB - 1) / Sh::RB;
   const int first = w.s.len - w.s.nq;  // position of the first query token
-  const int lo = p.window > 0 ? max(0, first - p.window + 1) : 0;
+  // (a row of a tree that saw no new token would be at first - 1)
+  const int lo = p.window > 0 ? max(0, first - p.window + (Sh::kTree ? 0 : 1)) : 0;
   w.lo = lo / Sh::kBlock;
   w.n = max(1, (w.s.len + Sh::kBlock - 1) / Sh::kBlock - w.lo);
   return w;
@@ -258,9 +263,9 @@ struct AttnCtrl {
 };
 static_assert(sizeof(AttnCtrl) <= 3 * 1024, "control block too large");
 
-template <int D, int NB>
-__global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const KvAttnParams p) {
-  using Sh = Shape<D, NB>;
+template <int D, int NB, bool kTree>
+__global__ void __launch_bounds__(Shape<D, NB, kTree>::W * 32, 1) kv_attn_kernel(const KvAttnParams p) {
+  using Sh = Shape<D, NB, kTree>;
   constexpr int W = Sh::W, S = Sh::S, GB = Sh::GB, GI = Sh::GI, RB = Sh::RB, GR = Sh::GR, BB = Sh::BB, CW = D / 32;
   extern __shared__ __align__(128) uint8_t smem[];
   AttnCtrl* ctrl = reinterpret_cast<AttnCtrl*>(smem);
@@ -443,7 +448,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
     // ---- queries: B operands in the channel order of the codes, and their sums ----
     uint32_t qf[NB][CW * 4];
     F2 qs[NB];
-    int hi_pos[NB][2], lo_pos[NB][2];  // tokens seen by rows 2c, 2c + 1: [lo, hi)
+    int hi_pos[NB][2], lo_pos[NB][2];  // tokens seen by rows 2c, 2c + 1: [lo, hi); of trees: hi is the row's new token
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int row = rb * RB + nb * 8 + g;
@@ -477,16 +482,21 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int rr = rb * RB + nb * 8 + 2 * c + e;
-        const int pos = first + kv_div_group(p, rr);
-        hi_pos[nb][e] = rr < rows ? pos + 1 : 0;
-        lo_pos[nb][e] = p.window > 0 ? pos - p.window + 1 : 0;
+        if constexpr (kTree) {
+          hi_pos[nb][e] = rr < rows ? kv_div_group(p, rr) : -1;
+          lo_pos[nb][e] = rr < rows ? kv_tree_lo(p, w.s, hi_pos[nb][e]) : 0;
+        } else {
+          const int pos = first + kv_div_group(p, rr);
+          hi_pos[nb][e] = rr < rows ? pos + 1 : 0;
+          lo_pos[nb][e] = p.window > 0 ? pos - p.window + 1 : 0;
+        }
       }
     }
     // tokens every row sees, [all_lo, all_hi), and tokens any row sees
     const int i_first = kv_div_group(p, rb * RB), i_last = kv_div_group(p, min(rows, (rb + 1) * RB) - 1);
-    const int all_hi = first + i_first + 1, any_hi = first + i_last + 1;
-    const int all_lo = p.window > 0 ? first + i_last - p.window + 1 : 0;
-    const int any_lo = p.window > 0 ? first + i_first - p.window + 1 : 0;
+    const int all_hi = kTree ? first : first + i_first + 1, any_hi = kTree ? w.s.len : first + i_last + 1;
+    const int all_lo = p.window > 0 ? first + (kTree ? w.s.nq - 1 : i_last) - p.window + 1 : 0;
+    const int any_lo = p.window > 0 ? first + (kTree ? -1 : i_first) - p.window + 1 : 0;
 
     F2 m[NB], l[NB], pz[NB], o[CW * 2][NB][2];  // o: rows g and g + 8 of the tile
     float sref = kMinSref;
@@ -500,6 +510,23 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
 
     auto block = [&](auto masked, const int t0, const uint8_t* st) {
       using Masked = decltype(masked);
+
+      // trees: which tokens rows 2c, 2c + 1 see; bit 16 (q & 1) + 8 e of word q / 2 is this lane's token g + 8 e of granule q
+      uint32_t see[NB][2][Sh::kStep / 32];
+      if constexpr (kTree && Masked::value) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int k = 0; k < Sh::kStep / 32; ++k)
+              see[nb][r][k] = hi_pos[nb][r] >= 0 ? kv_tree_see(p, w.s, hi_pos[nb][r], lo_pos[nb][r], t0 + 32 * k) >> g : 0u;
+      }
+      auto hidden = [&](int nb, int r, int q, int e) {
+        if constexpr (kTree && Masked::value) return !((see[nb][r][q / 2] >> (16 * (q & 1) + 8 * e)) & 1u);
+        const int t = t0 + 16 * q + g + 8 * e;
+        return t >= hi_pos[nb][r] || t < lo_pos[nb][r];
+      };
 
       // ---- S^T = K Q^T on the codes: low nibbles and high (x 16) apart -----------
       // x: scores in units of log2; element (q, nb, e) is token g + 8 e of granule
@@ -553,8 +580,8 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
             const F2 raw = fma2(sh[q][nb][e], dup(0.0625f), sl[q][nb][e]);
             F2 v = {fmaf(ks, raw.x, kz * qs[nb].x), fmaf(ks, raw.y, kz * qs[nb].y)};
             if (Masked::value) {
-              if (t >= hi_pos[nb][0] || t < lo_pos[nb][0]) v.x = kNegInf;
-              if (t >= hi_pos[nb][1] || t < lo_pos[nb][1]) v.y = kNegInf;
+              if (hidden(nb, 0, q, e)) v.x = kNegInf;
+              if (hidden(nb, 1, q, e)) v.y = kNegInf;
             }
             x[q][nb][e] = v;
             top[nb].x = fmaxf(top[nb].x, v.x);
@@ -624,10 +651,9 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
             if (!Masked::value) {
               pz[nb] = {fmaf(pe.x, vo[q][e], pz[nb].x), fmaf(pe.y, vo[q][e], pz[nb].y)};
             } else {  // a token that is masked for one row alone may have a NaN scale
-              const int t = t0 + 16 * q + g + 8 * e;
-              if (t >= hi_pos[nb][0] || t < lo_pos[nb][0]) y.x = 0.f;
+              if (hidden(nb, 0, q, e)) y.x = 0.f;
               else pz[nb].x = fmaf(pe.x, vo[q][e], pz[nb].x);
-              if (t >= hi_pos[nb][1] || t < lo_pos[nb][1]) y.y = 0.f;
+              if (hidden(nb, 1, q, e)) y.y = 0.f;
               else pz[nb].y = fmaf(pe.y, vo[q][e], pz[nb].y);
             }
             const __half2 hi = __floats2half2_rn(y.x, y.y);
@@ -729,7 +755,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
           if (!whole)
             *reinterpret_cast<float4*>(part + row * Sh::kOStride + g * (D / 8) + 4 * j) = v;
           else if (rb * RB + row < rows)
-            store_row(p, w.s, h, rb * RB + row, g * (D / 8) + 4 * j, D, v, ll);
+            store_row<kTree>(p, w.s, h, rb * RB + row, g * (D / 8) + 4 * j, D, v, ll);
         }
       }
     }
@@ -807,7 +833,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
       __stcg(reinterpret_cast<float4*>(part + row * D + ch), acc);
       if (ch == 0) __stcg(reinterpret_cast<float2*>(part + RB * D + 2 * row), make_float2(top, sum));
     } else if (sg.rb * RB + row < sg.s.nq * p.group) {
-      store_row(p, sg.s, sg.h, sg.rb * RB + row, ch, D, acc, sum);
+      store_row<kTree>(p, sg.s, sg.h, sg.rb * RB + row, ch, D, acc, sum);
     }
   }
   if (shared == 0) return;
@@ -862,41 +888,47 @@ __global__ void __launch_bounds__(Shape<D, NB>::W * 32, 1) kv_attn_kernel(const 
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) join(ml[i], a[i], top, sum, acc);
       }
-      store_row(p, sg.s, sg.h, sg.rb * RB + row, ch, D, acc, sum);
+      store_row<kTree>(p, sg.s, sg.h, sg.rb * RB + row, ch, D, acc, sum);
     }
   }
 }
 
-template <int D, int NB>
+template <int D, int NB, bool kTree>
 cudaError_t launch(const KvAttnParams& p, int grid, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(Shape<D, NB>::W * 32);
-  cfg.dynamicSmemBytes = Shape<D, NB>::kSmem;
+  cfg.blockDim = dim3(Shape<D, NB, kTree>::W * 32);
+  cfg.dynamicSmemBytes = Shape<D, NB, kTree>::kSmem;
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_attn_kernel<D, NB>, p);
+  return cudaLaunchKernelEx(&cfg, kv_attn_kernel<D, NB, kTree>, p);
 }
 
 }  // namespace
 
 cudaError_t kv_attn_set_smem_limit() {
   cudaError_t e = cudaSuccess;
-#define W4A16_SET(D, NB)                                                                                        \
-  if (e == cudaSuccess)                                                                                         \
-    e = cudaFuncSetAttribute(kv_attn_kernel<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D, NB>::kSmem);
-  W4A16_SET(128, 1) W4A16_SET(128, 2) W4A16_SET(64, 1) W4A16_SET(64, 2)
+#define W4A16_SET(D, NB, T)                                                                                   \
+  if (e == cudaSuccess)                                                                                       \
+    e = cudaFuncSetAttribute(kv_attn_kernel<D, NB, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D, NB, T>::kSmem);
+  W4A16_SET(128, 1, false) W4A16_SET(128, 2, false) W4A16_SET(64, 1, false) W4A16_SET(64, 2, false)
+  W4A16_SET(128, 1, true) W4A16_SET(128, 2, true) W4A16_SET(64, 1, true) W4A16_SET(64, 2, true)
 #undef W4A16_SET
   return e;
 }
 
+template <bool kTree>
+static cudaError_t launch_shape(const KvAttnParams& p, int D, int nb, int grid, cudaStream_t stream) {
+  if (D == 128) return nb == 1 ? launch<128, 1, kTree>(p, grid, stream) : launch<128, 2, kTree>(p, grid, stream);
+  return nb == 1 ? launch<64, 1, kTree>(p, grid, stream) : launch<64, 2, kTree>(p, grid, stream);
+}
+
 cudaError_t launch_kv_attn(const KvAttnParams& p, int D, int nb, int grid, cudaStream_t stream) {
-  if (D == 128) return nb == 1 ? launch<128, 1>(p, grid, stream) : launch<128, 2>(p, grid, stream);
-  return nb == 1 ? launch<64, 1>(p, grid, stream) : launch<64, 2>(p, grid, stream);
+  return p.tree ? launch_shape<true>(p, D, nb, grid, stream) : launch_shape<false>(p, D, nb, grid, stream);
 }
 
 }  // namespace w4a16

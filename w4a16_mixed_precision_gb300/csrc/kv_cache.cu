@@ -1,5 +1,6 @@
-// kv_cache.cu -- writing new keys and values into the 4-bit paged cache, and
-// reading cached values back as fp16.
+// kv_cache.cu -- writing new keys and values into the 4-bit paged cache, with or
+// without rotating queries and keys by their positions first, and reading cached
+// values back as fp16.
 //
 // Bound: both are streams, 4 D bytes of fp16 in (or out) and D + 8 bytes of
 // cache per token and head.  Quantising costs about ten operations a channel,
@@ -21,18 +22,10 @@ namespace {
 constexpr int kKvThreads = 256;
 constexpr int kTokens = 4;  // of a warp
 
-// Where token t (of all new tokens) of head h lives: its granule, and its
-// place in it; nullptr if the inputs give it none.
+// Where row t of the new tokens, of request b, lives at head h: its granule, and its place in it;
+// nullptr if the inputs give it none.
 template <int D>
-__device__ __forceinline__ uint8_t* kv_place(const KvParams& p, int t, int h, int* in_granule) {
-  // the request that owns token t: the last b with q_start[b] <= t
-  int lo = 0, hi = p.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.q_start[mid] <= t) lo = mid;
-    else hi = mid;
-  }
-  const KvSeq s = kv_seq(p, lo, true);
+__device__ __forceinline__ uint8_t* kv_place_of(const KvParams& p, int t, int b, const KvSeq& s, int h, int* in_granule) {
   if (t < s.q0 || t >= s.q0 + s.nq) return nullptr;
   const int pos = s.len - (s.q0 + s.nq - t);
   if (pos < 0) {
@@ -41,13 +34,18 @@ __device__ __forceinline__ uint8_t* kv_place(const KvParams& p, int t, int h, in
   }
   const int g16 = pos >> 4;
   const int pi = kv_div_page(p, g16);
-  const int page = p.table[(long long)lo * p.max_pages + pi];
+  const int page = p.table[(long long)b * p.max_pages + pi];
   if (page < 0 || page >= p.n_pages) {
     kv_fail(p, kKvSitePage);
     return nullptr;
   }
   *in_granule = pos & 15;
   return p.cache + page * p.page_bytes + h * p.head_bytes + (long long)(g16 - pi * p.page16) * kv_granule_bytes(D);
+}
+template <int D>
+__device__ __forceinline__ uint8_t* kv_place(const KvParams& p, int t, int h, int* in_granule) {
+  const int b = kv_owner(p, t);
+  return kv_place_of<D>(p, t, b, kv_seq(p, b, true), h, in_granule);
 }
 
 __device__ __forceinline__ __half2 h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
@@ -131,13 +129,60 @@ __device__ __forceinline__ void store_vec(void* at, const uint32_t (&x)[N]) {
     reinterpret_cast<uint4*>(at)[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
 }
 
+// A token's values into its granule (place i; base nullptr for none), by all lanes of a warp whose four
+// groups of eight hold a token each: lane g of a group has channels g D/8 .. + D/8 - 1.
+template <int D>
+__device__ __forceinline__ void put_values(uint8_t* base, int i, const uint32_t (&vc)[D / 64], int lane) {
+  constexpr int CW = D / 32;  // words of a lane's values (paired with another token's)
+  const int g = lane & 7, mine = lane >> 3;
+  // the token that shares this one's words of values, if it is in this warp: the
+  // even one writes the first half of them, the odd one the second
+  const int other = (lane + (i & 1 ? -8 : 8)) & 31;
+  const bool wraps = i & 1 ? mine == 0 : mine == kTokens - 1;
+  const unsigned long long there =
+      __shfl_sync(0xffffffffu, base ? (unsigned long long)(uintptr_t)base + i : 0ull, other);
+  const bool pair = base && !wraps && there == ((unsigned long long)(uintptr_t)base + i + (i & 1 ? -1 : 1));
+  // 16-bit pieces of this token: piece w is channels 4w .. 4w + 3
+  uint32_t give, take;
+  if constexpr (D == 128) {
+    give = i & 1 ? vc[0] : vc[1];
+    take = __shfl_sync(0xffffffffu, give, other);
+  } else {
+    give = vc[0];
+    take = __shfl_sync(0xffffffffu, give, other);
+  }
+  if (!base) return;
+  uint8_t* vrow = base + 8 * D + (i >> 3) * (4 * D) + (4 * g + ((i & 7) >> 1)) * (D / 8);
+  if constexpr (D == 128) {
+    if (pair) {
+      // even: pieces 0, 1 of both tokens; odd: pieces 2, 3
+      const uint32_t even = i & 1 ? take : vc[0], odd = i & 1 ? vc[1] : take;
+      *reinterpret_cast<uint2*>(vrow + (i & 1 ? 8 : 0)) =
+          make_uint2(__byte_perm(even, odd, 0x5410), __byte_perm(even, odd, 0x7632));
+    } else {
+#pragma unroll
+      for (int w = 0; w < CW; ++w)
+        *reinterpret_cast<uint16_t*>(vrow + 4 * w + 2 * (i & 1)) = (uint16_t)(vc[w / 2] >> (16 * (w & 1)));
+    }
+  } else {
+    if (pair) {
+      const uint32_t even = i & 1 ? take : vc[0], odd = i & 1 ? vc[0] : take;
+      *reinterpret_cast<uint32_t*>(vrow + (i & 1 ? 4 : 0)) = __byte_perm(even, odd, i & 1 ? 0x7632 : 0x5410);
+    } else {
+#pragma unroll
+      for (int w = 0; w < CW; ++w)
+        *reinterpret_cast<uint16_t*>(vrow + 4 * w + 2 * (i & 1)) = (uint16_t)(vc[0] >> (16 * w));
+    }
+  }
+}
+
 // kAppend: quantise k, v into the cache; else dequantise the cache into k, v.
 template <int D, bool kAppend>
 __global__ void __launch_bounds__(kKvThreads) kv_copy_kernel(const KvParams p, __half* k, __half* v, long long k_ts,
                                                              long long k_hs, long long v_ts, long long v_hs) {
   if (threadIdx.x == 0) griddep_launch_dependents();
   griddep_wait();
-  constexpr int CPL = D / 8, CW = D / 32;  // channels per lane; words of a lane's values (paired with another token's)
+  constexpr int CPL = D / 8;  // channels per lane
   const int lane = threadIdx.x & 31, g = lane & 7, mine = lane >> 3;
   const long long warp = (long long)blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5);
   const int h = (int)(warp % p.hkv);
@@ -160,47 +205,12 @@ __global__ void __launch_bounds__(kKvThreads) kv_copy_kernel(const KvParams p, _
     __half ks, ko, vs, vo;
     quantise<CPL>(kx, kc, ks, ko);
     quantise<CPL>(vx, vc, vs, vo);
-    // the token that shares this one's words of values, if it is in this warp: the
-    // even one writes the first half of them, the odd one the second
-    const int other = (lane + (i & 1 ? -8 : 8)) & 31;
-    const bool wraps = i & 1 ? mine == 0 : mine == kTokens - 1;
-    const unsigned long long there =
-        __shfl_sync(0xffffffffu, base ? (unsigned long long)(uintptr_t)base + i : 0ull, other);
-    const bool pair = base && !wraps && there == ((unsigned long long)(uintptr_t)base + i + (i & 1 ? -1 : 1));
-    // 16-bit pieces of this token: piece w is channels 4w .. 4w + 3
-    uint32_t give, take;
-    if constexpr (D == 128) {
-      give = i & 1 ? vc[0] : vc[1];
-      take = __shfl_sync(0xffffffffu, give, other);
-    } else {
-      give = vc[0];
-      take = __shfl_sync(0xffffffffu, give, other);
-    }
+    put_values<D>(base, i, vc, lane);
     if (!base) return;
-    uint8_t* vrow = base + 8 * D + (i >> 3) * (4 * D) + (4 * g + ((i & 7) >> 1)) * (D / 8);
-    if constexpr (D == 128) {
+    if constexpr (D == 128)
       *reinterpret_cast<uint2*>(base + i * (D / 2) + g * (CPL / 2)) = make_uint2(kc[0], kc[1]);
-      if (pair) {
-        // even: pieces 0, 1 of both tokens; odd: pieces 2, 3
-        const uint32_t even = i & 1 ? take : vc[0], odd = i & 1 ? vc[1] : take;
-        *reinterpret_cast<uint2*>(vrow + (i & 1 ? 8 : 0)) =
-            make_uint2(__byte_perm(even, odd, 0x5410), __byte_perm(even, odd, 0x7632));
-      } else {
-#pragma unroll
-        for (int w = 0; w < CW; ++w)
-          *reinterpret_cast<uint16_t*>(vrow + 4 * w + 2 * (i & 1)) = (uint16_t)(vc[w / 2] >> (16 * (w & 1)));
-      }
-    } else {
+    else
       *reinterpret_cast<uint32_t*>(base + i * (D / 2) + g * (CPL / 2)) = kc[0];
-      if (pair) {
-        const uint32_t even = i & 1 ? take : vc[0], odd = i & 1 ? vc[0] : take;
-        *reinterpret_cast<uint32_t*>(vrow + (i & 1 ? 4 : 0)) = __byte_perm(even, odd, i & 1 ? 0x7632 : 0x5410);
-      } else {
-#pragma unroll
-        for (int w = 0; w < CW; ++w)
-          *reinterpret_cast<uint16_t*>(vrow + 4 * w + 2 * (i & 1)) = (uint16_t)(vc[0] >> (16 * w));
-      }
-    }
     if (g == 0) *reinterpret_cast<uint2*>(base + 16 * D + 8 * i) = make_uint2(pair_bits(ks, ko), pair_bits(vs, vo));
   } else {
     const uint8_t* base = live ? kv_place<D>(p, t, h, &i) : nullptr;
@@ -244,7 +254,194 @@ cudaError_t launch_copy(const KvParams& p, uint16_t* k, uint16_t* v, const long 
                             reinterpret_cast<__half*>(v), st[0], st[1], st[2], st[3]);
 }
 
+// ---- rotary positions and append --------------------------------------------------------------
+// (x1, x2) -> (x1 c - x2 s, x2 c + x1 s) for the rot / 2 pairs of the first rot channels, (c, s) the table's
+// entry for the pair at the position of its axis: products and sums rounded to fp32 one by one, the
+// result to fp16.  Queries go to q_out; keys, and values as they are, into the cache like above.
+//
+// Bound: the stream, 4 D bytes a query head, 4 D + 2 (D/2 + 4) a key head and token.  A warp takes four
+// tokens like above, eight lanes each, and keeps the tokens' cosines and sines in registers for kQHeads
+// query heads or one key head.  A lane holds two chunks of D/16 channels, such that both channels of its
+// pairs are its own: chunks g and g + rot/2 of the rotated ones, two neighbours of the rest.
+constexpr int kQHeads = 4;  // of a warp
+
+template <int N>  // 4-byte words
+__device__ __forceinline__ void load_chunk(const uint16_t* at, uint32_t* x) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(at);
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(at);
+    x[0] = v.x; x[1] = v.y;
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_chunk(uint16_t* at, const uint32_t* x) {
+  if constexpr (N == 4) *reinterpret_cast<uint4*>(at) = make_uint4(x[0], x[1], x[2], x[3]);
+  else *reinterpret_cast<uint2*>(at) = make_uint2(x[0], x[1]);
+}
+
+__device__ __forceinline__ void rotate(float& x1, float& x2, float2 cs) {
+  const float a = x1, b = x2;
+  x1 = __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
+  x2 = __fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, cs.y));
+}
+
+// x: a lane's two chunks, CH / 2 words each; cs: of its CH pairs.
+template <int CH, bool kInterleaved>
+__device__ __forceinline__ void rotate_chunks(uint32_t (&x)[CH], const float2 (&cs)[CH]) {
+  if constexpr (kInterleaved) {
+#pragma unroll
+    for (int w = 0; w < CH; ++w) {
+      float2 f = __half22float2(h2(x[w]));
+      rotate(f.x, f.y, cs[w]);
+      x[w] = bits(__floats2half2_rn(f.x, f.y));
+    }
+  } else {
+#pragma unroll
+    for (int w = 0; w < CH / 2; ++w) {
+      float2 f = __half22float2(h2(x[w])), s = __half22float2(h2(x[CH / 2 + w]));
+      rotate(f.x, s.x, cs[2 * w]);
+      rotate(f.y, s.y, cs[2 * w + 1]);
+      x[w] = bits(__floats2half2_rn(f.x, f.y));
+      x[CH / 2 + w] = bits(__floats2half2_rn(s.x, s.y));
+    }
+  }
+}
+
+template <int D, bool kInterleaved>
+__global__ void __launch_bounds__(kKvThreads) kv_rope_append_kernel(const KvRopeParams p) {
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  griddep_wait();
+  constexpr int CH = D / 16;  // channels of a chunk, pairs of a lane
+  const int lane = threadIdx.x & 31, g = lane & 7, mine = lane >> 3;
+  const int q_tasks = (p.heads + kQHeads - 1) / kQHeads, tasks = q_tasks + p.kv.hkv;
+  const long long warp = (long long)blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5);
+  const long long tile = warp / tasks;
+  const int task = (int)(warp - tile * tasks);
+  const bool live = tile * kTokens + mine < p.kv.T;
+  const int t = live ? (int)(tile * kTokens) + mine : 0;
+  const bool keys = task >= q_tasks;
+  const int h = keys ? task - q_tasks : task * kQHeads;
+  const int heads = keys ? 2 : min(kQHeads, p.heads - h);  // vectors that are loaded: a key and a value
+
+  const int half = p.rot / (2 * CH);  // chunks that hold the pairs' first channels (or half of the pairs)
+  const bool rotated = g < half;
+  const int ca = (rotated ? g : 2 * half + 2 * (g - half)) * CH, cb = rotated ? ca + half * CH : ca + CH;
+
+  // the vectors first, then what their places and positions need
+  uint32_t x[kQHeads][CH];
+  const uint16_t* value = p.v + t * p.v_ts + h * p.v_hs + g * (D / 8);
+#pragma unroll
+  for (int i = 0; i < kQHeads; ++i) {
+#pragma unroll
+    for (int w = 0; w < CH; ++w) x[i][w] = 0u;
+    if (!live || i >= heads) continue;
+    if (keys && i == 1) {
+      load_chunk<CH / 2>(value, x[i]);
+      load_chunk<CH / 2>(value + CH, x[i] + CH / 2);
+    } else {
+      const uint16_t* from = keys ? p.k + t * p.k_ts + h * p.k_hs : p.q + t * p.q_ts + (h + i) * p.q_hs;
+      load_chunk<CH / 2>(from + ca, x[i]);
+      load_chunk<CH / 2>(from + cb, x[i] + CH / 2);
+    }
+  }
+  const int b = kv_owner(p.kv, t);
+  const KvSeq s = kv_seq(p.kv, b, true);
+  bool mine_ok = live && t >= s.q0 && t < s.q0 + s.nq;
+  int pos[kRopeAxes];
+#pragma unroll
+  for (int a = 0; a < kRopeAxes; ++a) {
+    pos[a] = 0;
+    if (a < p.axes && mine_ok) pos[a] = p.positions[(long long)a * p.kv.T + t];
+  }
+  bool bad = false;
+#pragma unroll
+  for (int a = 0; a < kRopeAxes; ++a) bad = bad || (uint32_t)pos[a] >= (uint32_t)p.table_rows;
+  if (bad) {
+    if (g == 0 && task == 0) kv_fail(p.kv, kKvSitePosition);
+    mine_ok = false;
+  }
+  float2 cs[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) cs[i] = make_float2(1.f, 0.f);
+  if (mine_ok && rotated) {
+    auto entry = [&](int pair) {
+      const int axis = (int)(p.axis[pair >> 5] >> (2 * (pair & 31))) & 3;
+      const int at = axis == 0 ? pos[0] : axis == 1 ? pos[1] : axis == 2 ? pos[2] : pos[3];
+      return reinterpret_cast<const float2*>(p.table) + (long long)at * (p.rot / 2) + pair;
+    };
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      const int pair0 = kInterleaved ? (part ? cb : ca) / 2 : ca + part * (CH / 2);
+      if (p.grouped) {  // CH / 2 pairs lie together
+        const float4* from = reinterpret_cast<const float4*>(entry(pair0));
+#pragma unroll
+        for (int i = 0; i < CH / 4; ++i) {
+          const float4 v = from[i];
+          cs[part * (CH / 2) + 2 * i] = make_float2(v.x, v.y);
+          cs[part * (CH / 2) + 2 * i + 1] = make_float2(v.z, v.w);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < CH / 2; ++i) cs[part * (CH / 2) + i] = *entry(pair0 + i);
+      }
+    }
+  }
+  if (!keys) {
+    if (!mine_ok) return;
+#pragma unroll
+    for (int i = 0; i < kQHeads; ++i) {
+      if (i >= heads) break;
+      if (rotated) rotate_chunks<CH, kInterleaved>(x[i], cs);
+      uint16_t* to = p.q_out + t * p.o_ts + (h + i) * p.o_hs;
+      store_chunk<CH / 2>(to + ca, x[i]);
+      store_chunk<CH / 2>(to + cb, x[i] + CH / 2);
+    }
+    return;
+  }
+  int i = 0;
+  uint8_t* base = mine_ok ? kv_place_of<D>(p.kv, t, b, s, h, &i) : nullptr;
+  if (rotated) rotate_chunks<CH, kInterleaved>(x[0], cs);
+  uint32_t kc[CH / 4], vc[CH / 4];
+  __half ks, ko, vs, vo;
+  quantise<2 * CH>(x[0], kc, ks, ko);
+  quantise<2 * CH>(x[1], vc, vs, vo);
+  put_values<D>(base, i, vc, lane);
+  if (!base) return;
+  uint8_t* krow = base + i * (D / 2);
+  if constexpr (D == 128) {
+    *reinterpret_cast<uint32_t*>(krow + ca / 2) = kc[0];
+    *reinterpret_cast<uint32_t*>(krow + cb / 2) = kc[1];
+  } else {
+    *reinterpret_cast<uint16_t*>(krow + ca / 2) = (uint16_t)kc[0];
+    *reinterpret_cast<uint16_t*>(krow + cb / 2) = (uint16_t)(kc[0] >> 16);
+  }
+  if (g == 0) *reinterpret_cast<uint2*>(base + 16 * D + 8 * i) = make_uint2(pair_bits(ks, ko), pair_bits(vs, vo));
+}
+
+template <int D, bool kInterleaved>
+cudaError_t launch_rope(const KvRopeParams& p, cudaStream_t stream) {
+  const long long warps = ((long long)p.kv.T + kTokens - 1) / kTokens * ((p.heads + kQHeads - 1) / kQHeads + p.kv.hkv);
+  constexpr int per = kKvThreads / 32;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3((unsigned)((warps + per - 1) / per));
+  cfg.blockDim = dim3(kKvThreads);
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_rope_append_kernel<D, kInterleaved>, p);
+}
+
 }  // namespace
+
+cudaError_t launch_kv_rope_append(const KvRopeParams& p, int D, bool interleaved, cudaStream_t stream) {
+  if (D == 128) return interleaved ? launch_rope<128, true>(p, stream) : launch_rope<128, false>(p, stream);
+  return interleaved ? launch_rope<64, true>(p, stream) : launch_rope<64, false>(p, stream);
+}
 
 cudaError_t launch_kv_append(const KvParams& p, int D, const uint16_t* k, const uint16_t* v, const long long (&st)[4],
                              cudaStream_t stream) {

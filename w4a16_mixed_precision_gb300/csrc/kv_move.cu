@@ -1,0 +1,313 @@
+// kv_move.cu -- moving what the caches of a model's layers hold: the kept ones of a request's new tokens
+// together (after a tree of drafted tokens was verified, or to drop tokens of a long context), and whole
+// pages.  One launch serves the caches of all layers, which share pages, lengths and indexes.
+#include "kv.cuh"
+
+namespace w4a16 {
+
+namespace {
+
+// ---- kept tokens ---------------------------------------------------------------------------------
+// Position first + i of request b takes what position first + index[i] held, for i < kept[b], first the
+// position of the first new token.
+//
+// Bound: the stream, kept entries of 2 (D/2 + 4) bytes out of and into every head of every cache, and the
+// latency of a chain of three loads (index, page, entry).  A warp builds a granule of 16 positions in
+// registers, all of its loads in flight, and writes it in whole lines: keys are moved in 16-byte pieces;
+// a word of values pairs two tokens, so that a lane loads the words of both its tokens and takes a half of
+// each (kv.cuh).  Where the kept tokens stay in their pages, W warps (a unit) take a request's head in
+// rounds of W granules, loads before stores: index[i] ascends, so no round reads what one before has
+// written, and a barrier between a round's loads and stores keeps it from overwriting what is still read.
+constexpr int kMoveThreads = 256, kMoveWarps = kMoveThreads / 32;
+
+// What warps read of a request, checked.
+struct Kept {
+  KvSeq s;
+  int first, kept;
+};
+__device__ __forceinline__ Kept kept_of(const KvCompactParams& p, int b, bool report) {
+  Kept k;
+  k.s = kv_seq(p.kv, b, report);
+  k.first = k.s.len - k.s.nq;
+  k.kept = p.kept[b];
+  if (k.first < 0) {
+    if (report) kv_fail(p.kv, kKvSiteLen);
+    k.kept = -1;
+  } else if (k.kept < 0 || k.kept > k.s.nq) {
+    if (report) kv_fail(p.kv, kKvSiteIndex);
+    k.kept = -1;
+  }
+  return k;  // kept < 0: nothing is moved
+}
+
+// By a warp: whether index ascends strictly, within the new tokens.
+__device__ __forceinline__ bool ascends(const KvCompactParams& p, const Kept& k) {
+  const int lane = threadIdx.x & 31;
+  bool ok = true;
+  for (int i = lane; i < k.kept; i += 32) {
+    const int at = p.index[k.s.q0 + i], before = i ? p.index[k.s.q0 + i - 1] : -1;
+    ok = ok && at > before && at < k.s.nq;
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Byte offset of a position's granule in a cache, of key head 0; -1 for a page that does not exist.
+template <int D>
+__device__ __forceinline__ long long granule_at(const KvParams& p, const int* row, int pages, int pos) {
+  const int g16 = pos >> 4, pi = kv_div_page(p, g16);
+  const int page = pi < pages ? row[pi] : -1;
+  if (page < 0 || page >= p.n_pages) {
+    kv_fail(p, kKvSitePage);
+    return -1;
+  }
+  return page * p.page_bytes + (long long)(g16 - pi * p.page16) * kv_granule_bytes(D);
+}
+
+// Where the 16 tokens of a granule come from: lane s < 16 has token s; lanes of tokens that are not
+// written have from < 0.
+struct Plan {
+  long long from, to;  // offsets of this lane's source granule, of the granule itself
+  int tok;             // the source's place in its granule
+};
+
+template <int D>
+__device__ __forceinline__ Plan plan_granule(const KvCompactParams& p, const Kept& k, int b, int granule) {
+  const int lane = threadIdx.x & 31, pos = granule * 16 + lane, i = pos - k.first;
+  Plan m{-1, -1, 0};
+  const bool mine = lane < 16 && i >= 0 && i < k.kept;
+  if (mine) {
+    const int at = p.index[k.s.q0 + i];
+    if (at < 0 || at >= k.s.nq) {
+      kv_fail(p.kv, kKvSiteIndex);
+    } else {
+      m.from = granule_at<D>(p.kv, p.kv.table + (long long)b * p.kv.max_pages, p.kv.max_pages, k.first + at);
+      m.tok = (k.first + at) & 15;
+    }
+  }
+  const int lead = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+  if (lead >= 0) {
+    if (lane == lead)
+      m.to = p.into ? granule_at<D>(p.kv, p.into + (long long)b * p.into_pages, p.into_pages, pos)
+                    : granule_at<D>(p.kv, p.kv.table + (long long)b * p.kv.max_pages, p.kv.max_pages, pos);
+    m.to = __shfl_sync(0xffffffffu, m.to, lead);
+  }
+  return m;
+}
+
+template <int N>
+__device__ __forceinline__ void get_words(const uint8_t* at, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(at);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(at);
+    w[0] = v.x; w[1] = v.y;
+  }
+}
+
+// A granule's bytes in a warp's registers.
+template <int D>
+struct Granule {
+  static constexpr int NK = D / 64, CW = D / 32;  // 16-byte pieces of keys, words of a lane's values in a half
+  uint4 k[NK];
+  uint32_t v[2][CW];
+  uint2 s;
+  uint32_t live;  // tokens that are written
+};
+
+template <int D>
+__device__ __forceinline__ void load_granule(const uint8_t* head, const Plan& m, Granule<D>& r) {
+  constexpr int PK = D / 32;  // 16-byte pieces of a token's keys
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  r.live = __ballot_sync(0xffffffffu, m.from >= 0 && m.to >= 0);
+#pragma unroll
+  for (int j = 0; j < Granule<D>::NK; ++j) {
+    const int piece = j * 32 + lane, s = piece / PK;
+    const long long from = __shfl_sync(0xffffffffu, m.from, s);
+    const int tok = __shfl_sync(0xffffffffu, m.tok, s);
+    if ((r.live >> s) & 1u) r.k[j] = *reinterpret_cast<const uint4*>(head + from + tok * (D / 2) + (piece % PK) * 16);
+  }
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    uint32_t w[2][Granule<D>::CW];
+    int odd[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int s = 8 * hf + 2 * c + e;
+      const long long from = __shfl_sync(0xffffffffu, m.from, s);
+      const int tok = __shfl_sync(0xffffffffu, m.tok, s);
+      odd[e] = tok & 1;
+#pragma unroll
+      for (int i = 0; i < Granule<D>::CW; ++i) w[e][i] = 0u;
+      if ((r.live >> s) & 1u)
+        get_words<Granule<D>::CW>(head + from + 8 * D + (tok >> 3) * (4 * D) + (4 * g + ((tok & 7) >> 1)) * (D / 8), w[e]);
+    }
+    const uint32_t pick = (odd[0] ? 0x32u : 0x10u) | (odd[1] ? 0x7600u : 0x5400u);
+#pragma unroll
+    for (int i = 0; i < Granule<D>::CW; ++i) r.v[hf][i] = __byte_perm(w[0][i], w[1][i], pick);
+  }
+  if (lane < 16 && ((r.live >> lane) & 1u)) r.s = *reinterpret_cast<const uint2*>(head + m.from + 16 * D + 8 * m.tok);
+}
+
+template <int D>
+__device__ __forceinline__ void store_granule(uint8_t* head, long long at, const Granule<D>& r) {
+  constexpr int PK = D / 32, CW = Granule<D>::CW;
+  const int lane = threadIdx.x & 31, c = lane & 3;
+  if (r.live == 0) return;
+  uint8_t* to = head + at;
+#pragma unroll
+  for (int j = 0; j < Granule<D>::NK; ++j) {
+    const int piece = j * 32 + lane;
+    if ((r.live >> (piece / PK)) & 1u) *reinterpret_cast<uint4*>(to + piece * 16) = r.k[j];
+  }
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    const uint32_t both = (r.live >> (8 * hf + 2 * c)) & 3u;
+    uint8_t* row = to + 8 * D + hf * (4 * D) + lane * (D / 8);
+    if (both == 3u) {
+      if constexpr (CW == 4) *reinterpret_cast<uint4*>(row) = make_uint4(r.v[hf][0], r.v[hf][1], r.v[hf][2], r.v[hf][3]);
+      else *reinterpret_cast<uint2*>(row) = make_uint2(r.v[hf][0], r.v[hf][1]);
+    } else if (both) {  // the other token of the words is not to be touched
+      const int e = both >> 1;
+#pragma unroll
+      for (int i = 0; i < CW; ++i) *reinterpret_cast<uint16_t*>(row + 4 * i + 2 * e) = (uint16_t)(r.v[hf][i] >> (16 * e));
+    }
+  }
+  if (lane < 16 && ((r.live >> lane) & 1u)) *reinterpret_cast<uint2*>(to + 16 * D + 8 * lane) = r.s;
+}
+
+// The kept tokens stay in their pages.  W warps a unit: (request, cache, head), heads fastest.
+template <int D, int W>
+__global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const KvCompactParams p, const __grid_constant__ KvCaches caches) {
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long unit = (long long)blockIdx.x * (kMoveWarps / W) + warp / W;
+  const long long per = (long long)p.caches * p.kv.hkv;
+  if (unit >= per * p.kv.B) return;  // a whole unit
+  const int b = (int)(unit / per), at = (int)(unit - b * per), cache = at / p.kv.hkv, h = at - cache * p.kv.hkv;
+  const bool speaks = at == 0 && warp % W == 0;  // one warp of the request
+  Kept k = kept_of(p, b, speaks && lane == 0);
+  if (k.kept > 0 && !ascends(p, k)) {
+    if (speaks && lane == 0) kv_fail(p.kv, kKvSiteIndex);
+    k.kept = -1;
+  }
+  if (speaks && lane == 0 && p.new_lens) p.new_lens[b] = k.kept < 0 ? p.kv.lens[b] : k.first + k.kept;
+  if (k.kept <= 0) return;
+  uint8_t* head = caches.at[cache] + h * p.kv.head_bytes;
+  const int g_end = (k.first + k.kept + 15) >> 4;
+  for (int g0 = k.first >> 4; g0 < g_end; g0 += W) {
+    const int granule = g0 + warp % W;
+    Granule<D> r;
+    r.live = 0;
+    Plan m{-1, -1, 0};
+    if (granule < g_end) {
+      m = plan_granule<D>(p, k, b, granule);
+      load_granule<D>(head, m, r);
+    }
+    if constexpr (W == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / W), "n"(W * 32) : "memory");
+    store_granule<D>(head, m.to, r);
+  }
+}
+
+// The kept tokens go to other pages: every granule is a warp's.
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads) kv_gather_kernel(const KvCompactParams p, const __grid_constant__ KvCaches caches,
+                                                                 int ctas) {
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  griddep_wait();
+  const int warp = threadIdx.x >> 5;
+  const int x = blockIdx.x % ctas, unit = blockIdx.x / ctas;  // of a head's CTAs
+  const int per = p.caches * p.kv.hkv, b = unit / per, at = unit - b * per, cache = at / p.kv.hkv, h = at - cache * p.kv.hkv;
+  const bool speaks = at == 0 && x == 0 && threadIdx.x == 0;
+  const Kept k = kept_of(p, b, speaks);
+  if (speaks && p.new_lens) p.new_lens[b] = k.kept < 0 ? p.kv.lens[b] : k.first + k.kept;
+  if (k.kept <= 0) return;
+  uint8_t* head = caches.at[cache] + h * p.kv.head_bytes;
+  const int g_end = (k.first + k.kept + 15) >> 4;
+  for (int granule = (k.first >> 4) + x * kMoveWarps + warp; granule < g_end; granule += ctas * kMoveWarps) {
+    const Plan m = plan_granule<D>(p, k, b, granule);
+    Granule<D> r;
+    load_granule<D>(head, m, r);
+    store_granule<D>(head, m.to, r);
+  }
+}
+
+// ---- pages -------------------------------------------------------------------------------------------
+// Bound: the stream, a page's bytes in and out for every pair and cache.  A CTA copies 16 KB, four loads
+// of 16 bytes in flight a thread.
+constexpr int kPageThreads = 256, kPageVecs = 4, kPageChunk = kPageThreads * kPageVecs * 16;
+
+__global__ void __launch_bounds__(kPageThreads) kv_copy_pages_kernel(const __grid_constant__ KvCaches caches, int n_caches,
+                                                                     int n_pages, long long page_bytes, int chunks,
+                                                                     const int* src, const int* dst, int* status) {
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  griddep_wait();
+  const int chunk = blockIdx.x % chunks, rest = blockIdx.x / chunks, cache = rest % n_caches, pair = rest / n_caches;
+  const int from = src[pair], to = dst[pair];
+  if (from < 0) return;  // no pair
+  if (from >= n_pages || to < 0 || to >= n_pages) {
+    if (chunk == 0 && cache == 0 && threadIdx.x == 0) {
+      atomicCAS(status + 1, 0, kKvSitePage);
+      atomicOr(status, kStatusBounds);
+    }
+    return;
+  }
+  const uint4* in = reinterpret_cast<const uint4*>(caches.at[cache] + from * page_bytes);
+  uint4* out = reinterpret_cast<uint4*>(caches.at[cache] + to * page_bytes);
+  const int vecs = (int)(page_bytes / 16), v0 = chunk * (kPageChunk / 16) + threadIdx.x;
+  uint4 v[kPageVecs];
+#pragma unroll
+  for (int i = 0; i < kPageVecs; ++i)
+    if (v0 + i * kPageThreads < vecs) v[i] = in[v0 + i * kPageThreads];
+#pragma unroll
+  for (int i = 0; i < kPageVecs; ++i)
+    if (v0 + i * kPageThreads < vecs) out[v0 + i * kPageThreads] = v[i];
+}
+
+template <typename... Args>
+cudaError_t launch(void (*kernel)(Args...), long long ctas, int threads, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int D>
+cudaError_t compact(const KvCompactParams& p, const KvCaches& c, cudaStream_t stream) {
+  const long long units = (long long)p.kv.B * p.caches * p.kv.hkv;
+  const long long granules = ((long long)p.max_q + 15) / 16 + 1;  // at most, of a request
+  if (p.into) {
+    const int ctas = (int)((granules + kMoveWarps - 1) / kMoveWarps);
+    if (units * ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    return launch(kv_gather_kernel<D>, units * ctas, kMoveThreads, stream, p, c, ctas);
+  }
+  const auto go = [&](auto kernel, int w) {
+    return launch(kernel, (units * w + kMoveWarps - 1) / kMoveWarps, kMoveThreads, stream, p, c);
+  };
+  if (granules <= 2) return go(kv_compact_kernel<D, 1>, 1);
+  return granules <= 8 ? go(kv_compact_kernel<D, 2>, 2) : go(kv_compact_kernel<D, 8>, 8);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_compact(const KvCompactParams& p, const KvCaches& c, int D, cudaStream_t stream) {
+  return D == 128 ? compact<128>(p, c, stream) : compact<64>(p, c, stream);
+}
+
+cudaError_t launch_kv_copy_pages(const KvCaches& c, int caches, int n_pages, long long page_bytes, const int* src,
+                                 const int* dst, int pairs, int* status, cudaStream_t stream) {
+  const int chunks = (int)((page_bytes + kPageChunk - 1) / kPageChunk);
+  const long long ctas = (long long)chunks * caches * pairs;
+  if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  return launch(kv_copy_pages_kernel, ctas, kPageThreads, stream, c, caches, n_pages, page_bytes, chunks, src, dst, status);
+}
+
+}  // namespace w4a16

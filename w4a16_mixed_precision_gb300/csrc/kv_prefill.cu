@@ -168,6 +168,17 @@ __device__ __forceinline__ void load_words(const uint8_t* at, uint32_t (&w)[N]) 
   }
 }
 
+// Of an item that stripes cut: the CTA whose stripe it begins in notes it in a part of its slot 1 that
+// holds no sums, for the kernel that joins the parts.
+struct PartNote {
+  int q0, rows, tile, h;  // h < 0: no such item
+  int last;               // CTA of its last block
+};
+template <int D>
+__device__ __forceinline__ PartNote* part_note(const KvAttnParams& p, int cta) {
+  return reinterpret_cast<PartNote*>(p.partials + (2ll * cta + 1) * (kRows * (D + 4)) + (D + 2) * kRows);
+}
+
 template <int D>
 struct ShapeP {
   static constexpr int kK = kBlock * D * 2, kV = D * kBlock * 2;  // bytes of a block's operands
@@ -202,7 +213,12 @@ struct CtrlP {
 struct Span {
   int lo, n;
 };
+template <bool kTree>
 __device__ __forceinline__ Span item_span(const KvAttnParams& p, const KvSeq& s, int rows, int tile) {
+  if constexpr (kTree) {  // all tokens (a row that saw no new token would be at s.len - s.nq - 1)
+    const int lo = p.window > 0 ? max(0, s.len - s.nq - p.window) / kBlock : 0;
+    return {lo, max(1, (s.len + kBlock - 1) / kBlock - lo)};
+  }
   const int r0 = tile * kRows, r1 = min(rows, r0 + kRows) - 1, first = s.len - s.nq;
   const int lo = p.window > 0 ? max(0, first + kv_div_group(p, r0) - p.window + 1) / kBlock : 0;
   const int hi = (max(0, first + kv_div_group(p, r1) + 1) + kBlock - 1) / kBlock;
@@ -216,12 +232,13 @@ __device__ __forceinline__ int item_rows(const KvAttnParams& p, const KvSeq& s) 
 }
 
 // Blocks of all items of a request and one key head, by a warp; and its longest item's.
+template <bool kTree>
 __device__ __forceinline__ long long request_blocks(const KvAttnParams& p, const KvSeq& s, int* longest) {
   const int rows = item_rows(p, s), tiles = (rows + kRows - 1) / kRows;
   long long sum = 0;
   int most = 0;
   for (int t = threadIdx.x & 31; t < tiles; t += 32) {
-    const int n = item_span(p, s, rows, t).n;
+    const int n = item_span<kTree>(p, s, rows, t).n;
     sum += n;
     most = max(most, n);
   }
@@ -244,17 +261,29 @@ struct Place {
   Span span;           // of the item
 };
 
-__device__ __forceinline__ void enter_item(const KvAttnParams& p, Place& c) { c.span = item_span(p, c.seq, c.rows, c.tile); }
+template <bool kTree>
+__device__ __forceinline__ void enter_item(const KvAttnParams& p, Place& c) {
+  c.span = item_span<kTree>(p, c.seq, c.rows, c.tile);
+}
 
 // One of an item's two tiles, in blocks [from, to) of the piece [blk0, end): those
 // that any of its rows sees; and the tokens that all of them see.
 struct Half {
   int from, to, all_lo, all_hi;
 };
+template <bool kTree>
 __device__ __forceinline__ Half tile_half(const KvAttnParams& p, const Place& c, int t, int blk0, int end) {
   const int r0 = c.tile * kRows + t * kTile, r1 = min(c.rows, r0 + kTile) - 1, first = c.seq.len - c.seq.nq;
   const int i0 = kv_div_group(p, r0), i1 = kv_div_group(p, r1);
   Half f;
+  if constexpr (kTree) {
+    f.all_lo = p.window > 0 ? first + c.seq.nq - p.window : 0;
+    f.all_hi = first;
+    f.from = max(blk0, p.window > 0 ? max(0, first - p.window) / kBlock : 0);
+    f.to = r0 < c.rows ? min(end, max(1, (c.seq.len + kBlock - 1) / kBlock)) : f.from;
+    if (f.to < f.from) f.to = f.from;
+    return f;
+  }
   f.all_lo = p.window > 0 ? first + i1 - p.window + 1 : 0;
   f.all_hi = first + i0 + 1;
   f.from = max(blk0, p.window > 0 ? max(0, first + i0 - p.window + 1) / kBlock : 0);
@@ -264,6 +293,7 @@ __device__ __forceinline__ Half tile_half(const KvAttnParams& p, const Place& c,
 }
 
 // Moves on by `by` blocks, to the end of the item at most.
+template <bool kTree>
 __device__ __forceinline__ void move_on(const KvAttnParams& p, Place& c, int by) {
   c.x += by;
   c.left -= by;
@@ -283,7 +313,7 @@ __device__ __forceinline__ void move_on(const KvAttnParams& p, Place& c, int by)
     }
     c.tile = (c.rows + kRows - 1) / kRows - 1;
   }
-  enter_item(p, c);
+  enter_item<kTree>(p, c);
 }
 
 // The blockIdx.x-th item, each request's longest first, by a warp, where the grid has
@@ -296,6 +326,7 @@ __device__ __forceinline__ void move_on(const KvAttnParams& p, Place& c, int by)
 // against 355, 376 of 94 to 141 506 against 462, 504 of 94 to 125 629 against 573.
 // The mean is taken as if a request's items grew evenly.
 constexpr int kCutCost = 20, kCutItemCost = 4;  // blocks
+template <bool kTree>
 __device__ __forceinline__ void find_item(const KvAttnParams& p, CtrlP& ctrl) {
   const int lane = threadIdx.x & 31;
   long long left = blockIdx.x, U = 0, items = 0;
@@ -307,11 +338,12 @@ __device__ __forceinline__ void find_item(const KvAttnParams& p, CtrlP& ctrl) {
     if (b0 + lane < p.kv.B) {
       const KvSeq s = kv_seq(p.kv, b0 + lane, blockIdx.x == 0);
       if (s.nq > s.len && blockIdx.x == 0) kv_fail(p.kv, kKvSiteLen);
+      if (kTree && s.nq > 32ll * p.tree_words && blockIdx.x == 0) kv_fail(p.kv, kKvSiteTree);
       const int rows = item_rows(p, s);
       tiles = (rows + kRows - 1) / kRows;
       n = (long long)tiles * p.kv.hkv;
       if (tiles > 0) {
-        const int n0 = item_span(p, s, rows, 0).n, n1 = item_span(p, s, rows, tiles - 1).n;
+        const int n0 = item_span<kTree>(p, s, rows, 0).n, n1 = item_span<kTree>(p, s, rows, tiles - 1).n;
         longest = max(longest, max(n0, n1));
         U += n * (n0 + n1) / 2;
       }
@@ -350,7 +382,11 @@ __device__ __forceinline__ void find_item(const KvAttnParams& p, CtrlP& ctrl) {
   }
 }
 
-template <int D>
+// kTree: the new tokens are trees (kv.cuh).  Their items are short of rows and long, so that stripes cut
+// them into many parts: these are joined by the next kernel, with a CTA for 8 channels of every item,
+// instead of by the last CTA to arrive.  One request of 8000 tokens, 512 rows a key head of 128
+// channels, is cut into 152 parts.
+template <int D, bool kTree>
 __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnParams p) {
   using Sh = ShapeP<D>;
   constexpr int CW = D / 32, GR = kv_granule_bytes(D);
@@ -396,7 +432,10 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
   }
   // ---- this CTA's work: an item, or a stripe of all items ----------------------------------
   const bool many = (int)gridDim.x > p.stripes;
-  if (many && warp == 0) find_item(p, ctrl);
+  if constexpr (kTree) {  // no item begins in this stripe and goes on behind it, so far
+    if (tid == 0 && (int)blockIdx.x < p.stripes) part_note<D>(p, blockIdx.x)->h = -1;
+  }
+  if (many && warp == 0) find_item<kTree>(p, ctrl);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -416,7 +455,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
     for (int b = b_from; b < b_to; ++b) {
       const KvSeq q = kv_seq(p.kv, b, blockIdx.x == 0 && lane == 0);
       if (q.nq > q.len && blockIdx.x == 0 && lane == 0) kv_fail(p.kv, kKvSiteLen);
-      mine += p.kv.hkv * request_blocks(p, q, &longest);
+      if (kTree && q.nq > 32ll * p.tree_words && blockIdx.x == 0 && lane == 0) kv_fail(p.kv, kKvSiteTree);
+      mine += p.kv.hkv * request_blocks<kTree>(p, q, &longest);
       mine_items += (long long)p.kv.hkv * ((item_rows(p, q) + kRows - 1) / kRows);
     }
     if (lane == 0) {
@@ -450,7 +490,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       for (int b = b_from; b < b_to; ++b) {
         const KvSeq q = kv_seq(p.kv, b, false);
         const int rows = item_rows(p, q), tiles = (rows + kRows - 1) / kRows;
-        const long long one = by_item ? tiles : request_blocks(p, q, &longest);
+        const long long one = by_item ? tiles : request_blocks<kTree>(p, q, &longest);
         if (off >= one * p.kv.hkv) {
           off -= one * p.kv.hkv;
           continue;
@@ -467,7 +507,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
           break;
         }
         for (int top = tiles - 1; top >= 0; top -= 32) {  // 32 tiles at a time, downwards
-          const int n = top >= lane ? item_span(p, q, rows, top - lane).n : 0;
+          const int n = top >= lane ? item_span<kTree>(p, q, rows, top - lane).n : 0;
           int upto = n;
 #pragma unroll
           for (int m = 1; m < 32; m <<= 1) {
@@ -500,7 +540,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
     at.x = ctrl.start_x;
     at.seq = kv_seq(p.kv, at.b, false);
     at.rows = item_rows(p, at.seq);
-    enter_item(p, at);
+    enter_item<kTree>(p, at);
     at.left = by_item ? at.span.n : (int)(u_end - u_begin);
   }
 
@@ -523,8 +563,9 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
     const int i = live ? kv_div_group(p, row) : 0;
     const int head = at.h * p.group + (live ? row - i * p.group : 0);
     const int pos = first + i;
-    const int hi = live ? pos + 1 : 0, lo = p.window > 0 ? pos - p.window + 1 : 0;  // tokens seen
-    const Half half_ = tile_half(p, at, tile, at.span.lo + at.x, at.span.lo + x1);
+    const int hi = live ? pos + 1 : 0;  // tokens seen; of trees by their bits
+    const int lo = kTree ? (live ? kv_tree_lo(p, seq, i) : 0) : p.window > 0 ? pos - p.window + 1 : 0;
+    const Half half_ = tile_half<kTree>(p, at, tile, at.span.lo + at.x, at.span.lo + x1);
 
     // Q to shared memory, channels in the codes' order: the warp's 32 rows, kLanes lanes a
     // row (whole lines of global memory); then every row's sum
@@ -580,6 +621,13 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       uint32_t P[32];
       F2 lt, pzt;
       float over;
+      uint32_t see[2] = {0u, 0u};
+      if constexpr (kTree) {
+        if (!full && live) {
+          see[0] = kv_tree_see(p, seq, i, lo, t0);
+          see[1] = kv_tree_see(p, seq, i, lo, t0 + 32);
+        }
+      }
       // one pass over the block's scores; Masked: some row does not see all of it.  A
       // second one where a reference had to be moved.
       auto pass = [&](auto masked) {
@@ -600,7 +648,11 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
             const float4 kp = par[(half * 32 + t)], vp = par[(half * 32 + t) + 1];  // (ks, ks, ko, ko), (vs, vs, vo, vo)
             F2 x = fma2({kp.x, kp.y}, {__uint_as_float(s[t]), __uint_as_float(s[t + 1])}, fma2({kp.z, kp.w}, qs, nr));
             const int at = t0 + half * 32 + t;
-            const bool see0 = !Masked::value || (at < hi && at >= lo), see1 = !Masked::value || (at + 1 < hi && at + 1 >= lo);
+            bool see0 = !Masked::value || (at < hi && at >= lo), see1 = !Masked::value || (at + 1 < hi && at + 1 >= lo);
+            if constexpr (kTree && Masked::value) {
+              see0 = (see[half] >> t) & 1u;
+              see1 = (see[half] >> (t + 1)) & 1u;
+            }
             if (!see0) x.x = kNegInf;
             if (!see1) x.y = kNegInf;
             const F2 e = {ex2(x.x), ex2(x.y)};
@@ -633,8 +685,14 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
             const float4 kp = par[half * 32 + t];
             const F2 x = fma2({kp.x, kp.y}, {__uint_as_float(s[t]), __uint_as_float(s[t + 1])}, mul2({kp.z, kp.w}, qs));
             const int at = t0 + half * 32 + t;
-            if (at < hi && at >= lo) top = fmaxf(top, x.x);
-            if (at + 1 < hi && at + 1 >= lo) top = fmaxf(top, x.y);
+            if constexpr (kTree) {
+              const uint32_t seen = full ? ~0u : half ? see[1] : see[0];
+              if ((seen >> t) & 1u) top = fmaxf(top, x.x);
+              if ((seen >> (t + 1)) & 1u) top = fmaxf(top, x.y);
+            } else {
+              if (at < hi && at >= lo) top = fmaxf(top, x.x);
+              if (at + 1 < hi && at + 1 >= lo) top = fmaxf(top, x.y);
+            }
           }
         }
         const float4 vm = *reinterpret_cast<const float4*>(ctrl.vmax[st]);
@@ -712,7 +770,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       __syncwarp();
     };
     if (whole) {
-      const float inv = hi > 0 ? 1.f / sum : 0.f, add = off * inv;  // a row that sees no token is zero
+      const float inv = (kTree ? sum != 0.f : hi > 0) ? 1.f / sum : 0.f, add = off * inv;  // a row that sees no token is zero
 #pragma unroll 1
       for (int part = 0; part < D / 32; ++part) {
         uint32_t v[32];
@@ -744,6 +802,11 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       }
       __stcg(slot + D * kRows, R);
       __stcg(slot + (D + 1) * kRows, sum);
+      if constexpr (kTree) {  // the next kernel joins them
+        if (tid == 0 && at.x == 0)
+          *part_note<D>(p, blockIdx.x) = {seq.q0, at.rows, at.tile, at.h,
+                                          (int)stripe_owner(u - at.x + at.span.n - 1, U, G)};
+      } else {
       // all warps have written; one thread counts this CTA in, with release and acquire for all of them
       const long long s0 = u - at.x;  // the item's first block among all
       const int c0 = (int)stripe_owner(s0, U, G), c1 = (int)stripe_owner(s0 + at.span.n - 1, U, G);
@@ -794,13 +857,14 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
         }
         write_rows();
       }
+      }
     }
     // on to the next item; its Q may replace this one's: o_full followed all products
     tc_fence_before();
     ++items;
     stage = (stage + pieces) % Sh::kStages;
     u += pieces;
-    move_on(p, at, pieces);
+    move_on<kTree>(p, at, pieces);
     }
   } else if (warp < kSoftmaxWarps + kDequantWarps) {
     // ================= dequantisation =================
@@ -831,7 +895,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
                      (gi - kv_div_page(p.kv, gi) * p.kv.page16) * GR,
                  p.whole_blocks ? copies * GR : GR, bar(ctrl.raw_full[slot]), policy);
       if (++issued < n) {
-        move_on(p, ahead, 1);
+        move_on<kTree>(p, ahead, 1);
         look_up();
       }
     };
@@ -929,7 +993,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
         }
         issue();
       }
-      move_on(p, at, 1);
+      move_on<kTree>(p, at, 1);
       if (++stage == Sh::kStages) {
         stage = 0;
         ph ^= 1u;
@@ -962,7 +1026,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       const int pieces = min(at.span.n - at.x, at.left), blk0 = at.span.lo + at.x, end = blk0 + pieces;
       Half half_[kTiles];
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) half_[t] = tile_half(p, at, t, blk0, end);
+      for (int t = 0; t < kTiles; ++t) half_[t] = tile_half<kTree>(p, at, t, blk0, end);
       // Q of this item, which the softmax warps write after the item before is done
       if (!(ok = wait_warp(bar(ctrl.q_full), (uint32_t)(items & 1), wc))) break;
       if (!(ok = wait_warp(bar(ctrl.kv_full[stage]), ph, wc))) break;
@@ -1007,7 +1071,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       if (!ok) break;
       mma_commit_elect(bar(ctrl.o_full));
       ++items;
-      move_on(p, at, pieces);
+      move_on<kTree>(p, at, pieces);
     }
     mma_commit_elect(bar(ctrl.drain));
     wait_drain(bar(ctrl.drain), 0, wc);
@@ -1018,28 +1082,87 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
   if (warp == kSoftmaxWarps + kDequantWarps) tmem_dealloc(tmem, kTmem);
 }
 
+// Joins the parts of the items that stripes cut, in stripe order: CTA (q, x) channels 8 x .. 8 x + 7 of the
+// item that begins in stripe q, a row a thread.  A part's row is scaled to the largest reference.
 template <int D>
-cudaError_t launch(const KvAttnParams& p, int grid, cudaStream_t stream) {
+__global__ void __launch_bounds__(kRows) kv_join_kernel(const KvAttnParams p) {
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  griddep_wait();
+  constexpr int kSlot = kRows * (D + 4), kAhead = 4;
+  const int c0 = blockIdx.x / (D / 8), ch = (blockIdx.x % (D / 8)) * 8;
+  const PartNote note = *part_note<D>(p, c0);
+  if (note.h < 0) return;
+  const int row = note.tile * kRows + threadIdx.x;
+  if (row >= note.rows) return;
+  float top = kUnset, all = 0.f, o[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) o[k] = 0.f;
+  for (int q0 = c0; q0 <= note.last; q0 += kAhead) {
+    float r[kAhead], l[kAhead], v[kAhead][8];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      r[i] = kUnset;
+      l[i] = 0.f;
+      const float* part = p.partials + (2ll * (q0 + i) + (q0 + i == c0 ? 1 : 0)) * kSlot + threadIdx.x;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
+      if (q0 + i <= note.last) {
+        r[i] = __ldcg(part + D * kRows);
+        l[i] = __ldcg(part + (D + 1) * kRows);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] = __ldcg(part + (ch + k) * kRows);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const float nt = l[i] == 0.f ? top : fmaxf(top, r[i]);
+      const float fo = top == nt ? 1.f : ex2(top - nt), fn = l[i] == 0.f ? 0.f : r[i] == nt ? 1.f : ex2(r[i] - nt);
+      top = nt;
+      all = fmaf(all, fo, l[i] * fn);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = fmaf(o[k], fo, l[i] == 0.f ? 0.f : v[i][k] * fn);
+    }
+  }
+  const float inv = all != 0.f ? 1.f / all : 0.f;
+  const int i = kv_div_group(p, row), head = note.h * p.group + row - i * p.group;
+  uint4 out = make_uint4(0u, 0u, 0u, 0u);
+  if (inv != 0.f)
+    out = make_uint4(pack(o[0] * inv, o[1] * inv), pack(o[2] * inv, o[3] * inv), pack(o[4] * inv, o[5] * inv),
+                     pack(o[6] * inv, o[7] * inv));
+  *reinterpret_cast<uint4*>(p.out + ((long long)(note.q0 + i) * p.heads + head) * D + ch) = out;
+}
+
+template <typename Kernel>
+cudaError_t launch_one(Kernel kernel, const KvAttnParams& p, int grid, int threads, int smem, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreadsP);
-  cfg.dynamicSmemBytes = ShapeP<D>::kSmem;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_prefill_kernel<D>, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int D>
+cudaError_t launch(const KvAttnParams& p, int grid, cudaStream_t stream) {
+  if (!p.tree) return launch_one(kv_prefill_kernel<D, false>, p, grid, kThreadsP, ShapeP<D>::kSmem, stream);
+  const cudaError_t e = launch_one(kv_prefill_kernel<D, true>, p, grid, kThreadsP, ShapeP<D>::kSmem, stream);
+  return e != cudaSuccess ? e : launch_one(kv_join_kernel<D>, p, p.stripes * (D / 8), kRows, 0, stream);
 }
 
 }  // namespace
 
 cudaError_t kv_prefill_set_smem_limit() {
-  cudaError_t e = cudaFuncSetAttribute(kv_prefill_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       ShapeP<128>::kSmem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kv_prefill_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, ShapeP<64>::kSmem);
+  cudaError_t e = cudaSuccess;
+#define W4A16_SET(D, T)   \
+  if (e == cudaSuccess) \
+    e = cudaFuncSetAttribute(kv_prefill_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, ShapeP<D>::kSmem);
+  W4A16_SET(128, false) W4A16_SET(64, false) W4A16_SET(128, true) W4A16_SET(64, true)
+#undef W4A16_SET
   return e;
 }
 

@@ -139,6 +139,115 @@ AttnPlan attn_plan(int sms, int D, int group, int max_q, int tokens) {
   return a;
 }
 
+// Attention of both kinds; words > 0: the new tokens are trees.
+marlin_status_t attention(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, int heads, const void* cache,
+                          int n_pages, int kv_heads, int head_dim, int page_size, const int32_t* page_table, int max_pages,
+                          const int32_t* lengths, const int32_t* q_start, int requests, int tokens, int max_q,
+                          const int32_t* tree, int words, float scale, int window, uint16_t* out, void* workspace,
+                          size_t workspace_bytes, marlin_stream_t stream) {
+  KvAttnParams p{};
+  if (heads <= 0 || kv_heads <= 0 || heads % kv_heads != 0 || window < 0 || max_q < 0 || !std::isfinite(scale))
+    return MARLIN_ERR_INVALID_ARG;
+  marlin_status_t s = make_kv(&p.kv, cache, n_pages, kv_heads, head_dim, page_size, page_table, max_pages, lengths,
+                              q_start, requests, tokens, workspace);
+  if (s != MARLIN_OK || requests == 0 || tokens == 0) return s;
+  if (!q || !out || (words > 0 && !tree)) return MARLIN_ERR_INVALID_ARG;
+  if (!aligned(tree, 4)) return MARLIN_ERR_MISALIGNED;
+  if (!aligned(q, 16) || !aligned(out, 16) || !strides_ok(q_token_stride, q_head_stride, 8))
+    return MARLIN_ERR_MISALIGNED;
+  int sms;
+  if ((s = current_sms(&sms)) != MARLIN_OK) return s;
+  const int group = heads / kv_heads;
+  if ((long long)tokens * group > 0x7FFFFFFF) return MARLIN_ERR_UNSUPPORTED;
+  const AttnPlan a = attn_plan(sms, head_dim, group, max_q, tokens);
+  if (workspace_bytes < a.bytes) return MARLIN_ERR_WORKSPACE_TOO_SMALL;
+  {
+    static std::mutex lock;
+    static bool set[64] = {};
+    int dev;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MARLIN_ERR_CUDA;
+    std::lock_guard<std::mutex> hold(lock);
+    if (dev < 0 || dev >= 64) return MARLIN_ERR_INVALID_ARG;
+    if (!set[dev]) {
+      if (kv_attn_set_smem_limit() != cudaSuccess || kv_prefill_set_smem_limit() != cudaSuccess) return MARLIN_ERR_CUDA;
+      set[dev] = true;
+    }
+  }
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.q = q;
+  p.q_ts = q_token_stride;
+  p.q_hs = q_head_stride;
+  p.out = out;
+  p.heads = heads;
+  p.group = group;
+  p.group_magic = group == 1 ? 0ull : ~0ull / (unsigned)group + 1;
+  // positions are below 2^30: a window beyond that hides nothing, and position - window stays in 32 bits
+  // for the negative positions of a request with more new tokens than its length, too
+  p.window = std::min(window, 1 << 30);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.whole_blocks = p.kv.page16 % 4 == 0;
+  p.min_rows = 0;
+  p.max_rows = 0x7FFFFFFF;
+  p.counters = reinterpret_cast<int*>(ws + a.counters_off);
+  p.partials = reinterpret_cast<float*>(ws + a.partials_off);
+  p.firsts = reinterpret_cast<float*>(ws + a.firsts_off);
+  p.timeout_ns = kTimeoutNs;
+  p.tree = tree;
+  p.tree_words = words;
+  // Which kernel: by the query rows that share a key head.  The streaming kernel
+  // takes 8 or 16 rows a pass over the cache, the tcgen05 kernel 128.  Where every
+  // request has the same number of new tokens one launch serves them all (each
+  // kernel is right for any number); else both are launched and each takes its
+  // side of the bound, request by request.
+  const bool uniform = requests == 1 || (long long)requests * max_q == tokens;
+  // (the workspace holds the tcgen05 kernel's parts where all tokens together have enough rows)
+  const bool some_large = (long long)(requests == 1 ? tokens : std::min(max_q, tokens)) * group > kPrefillRows;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (some_large) {
+    if (!uniform) p.min_rows = kPrefillRows;
+    KvAttnParams f = p;
+    f.counters = p.counters + a.grid;
+    f.partials = reinterpret_cast<float*>(ws + a.prompt_off);
+    f.stripes = a.grid;
+    const long long items = kv_prefill_items(tokens, requests, kv_heads, group);
+    if (items > 0x7FFFFFFF) return MARLIN_ERR_UNSUPPORTED;
+    if (launch_kv_prefill(f, head_dim, std::max((int)items, a.grid), st) != cudaSuccess) return MARLIN_ERR_CUDA;
+    if (uniform) return MARLIN_OK;
+    p.max_rows = kPrefillRows;
+  }
+  return launch_kv_attn(p, head_dim, a.nb, a.grid, st) == cudaSuccess ? MARLIN_OK : MARLIN_ERR_CUDA;
+}
+
+// ---- caches of several layers ---------------------------------------------------------
+
+// Launches `go` for up to kMoveCaches caches at a time.
+template <typename Go>
+marlin_status_t for_caches(void* const* caches, int count, Go go) {
+  for (int c0 = 0; c0 < count; c0 += kMoveCaches) {
+    KvCaches c{};
+    const int n = std::min(kMoveCaches, count - c0);
+    for (int i = 0; i < n; ++i) c.at[i] = static_cast<uint8_t*>(caches[c0 + i]);
+    if (go(c, n, c0) != cudaSuccess) return MARLIN_ERR_CUDA;
+  }
+  return MARLIN_OK;
+}
+
+// The layers' caches are all there and do not overlap.
+marlin_status_t check_caches(void* const* caches, int count, int n_pages, int hkv, int D, int page) {
+  size_t bytes;
+  if (count <= 0 || !caches) return MARLIN_ERR_INVALID_ARG;
+  if (const marlin_status_t c = marlin_kv_cache_bytes(n_pages, hkv, D, page, &bytes)) return c;
+  for (int i = 0; i < count; ++i) {
+    if (!caches[i]) return MARLIN_ERR_INVALID_ARG;
+    if (!aligned(caches[i], 16)) return MARLIN_ERR_MISALIGNED;
+  }
+  const auto at = [&](int i) { return reinterpret_cast<uintptr_t>(caches[i]); };
+  for (int i = 1; i < count; ++i)
+    for (int j = 0; j < i; ++j)
+      if ((at(i) > at(j) ? at(i) - at(j) : at(j) - at(i)) < bytes) return MARLIN_ERR_INVALID_ARG;
+  return MARLIN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -239,73 +348,145 @@ marlin_status_t marlin_kv_attention(const uint16_t* q, int64_t q_token_stride, i
                                     const int32_t* q_start, int requests, int tokens, int max_q, float scale,
                                     int window, uint16_t* out, void* workspace, size_t workspace_bytes,
                                     marlin_stream_t stream) {
-  KvAttnParams p{};
-  if (heads <= 0 || kv_heads <= 0 || heads % kv_heads != 0 || window < 0 || max_q < 0 || !std::isfinite(scale))
-    return MARLIN_ERR_INVALID_ARG;
-  marlin_status_t s = make_kv(&p.kv, cache, n_pages, kv_heads, head_dim, page_size, page_table, max_pages, lengths,
-                              q_start, requests, tokens, workspace);
-  if (s != MARLIN_OK || requests == 0 || tokens == 0) return s;
-  if (!q || !out) return MARLIN_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(out, 16) || !strides_ok(q_token_stride, q_head_stride, 8))
+  return attention(q, q_token_stride, q_head_stride, heads, cache, n_pages, kv_heads, head_dim, page_size, page_table,
+                   max_pages, lengths, q_start, requests, tokens, max_q, nullptr, 0, scale, window, out, workspace,
+                   workspace_bytes, stream);
+}
+
+marlin_status_t marlin_kv_tree_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, int heads,
+                                         const void* cache, int n_pages, int kv_heads, int head_dim, int page_size,
+                                         const int32_t* page_table, int max_pages, const int32_t* lengths,
+                                         const int32_t* q_start, int requests, int tokens, int max_q,
+                                         const int32_t* mask, int words, float scale, int window, uint16_t* out,
+                                         void* workspace, size_t workspace_bytes, marlin_stream_t stream) {
+  if (words <= 0) return MARLIN_ERR_INVALID_ARG;
+  return attention(q, q_token_stride, q_head_stride, heads, cache, n_pages, kv_heads, head_dim, page_size, page_table,
+                   max_pages, lengths, q_start, requests, tokens, max_q, mask, words, scale, window, out, workspace,
+                   workspace_bytes, stream);
+}
+
+marlin_status_t marlin_kv_tree(const int32_t* parents, const int32_t* lengths, const int32_t* q_start, int requests,
+                               int tokens, int words, int32_t* mask, int32_t* positions, void* workspace,
+                               marlin_stream_t stream) {
+  if (requests < 0 || tokens < 0 || words <= 0) return MARLIN_ERR_INVALID_ARG;
+  if (requests == 0 || tokens == 0) return MARLIN_OK;
+  if (!parents || !lengths || !q_start || !mask || !positions || !workspace) return MARLIN_ERR_INVALID_ARG;
+  if (!aligned(parents, 4) || !aligned(lengths, 4) || !aligned(q_start, 4) || !aligned(mask, 4) || !aligned(positions, 4) ||
+      !aligned(workspace, 16))
     return MARLIN_ERR_MISALIGNED;
-  int sms;
-  if ((s = current_sms(&sms)) != MARLIN_OK) return s;
-  const int group = heads / kv_heads;
-  if ((long long)tokens * group > 0x7FFFFFFF) return MARLIN_ERR_UNSUPPORTED;
-  const AttnPlan a = attn_plan(sms, head_dim, group, max_q, tokens);
-  if (workspace_bytes < a.bytes) return MARLIN_ERR_WORKSPACE_TOO_SMALL;
-  {
-    static std::mutex lock;
-    static bool set[64] = {};
-    int dev;
-    if (cudaGetDevice(&dev) != cudaSuccess) return MARLIN_ERR_CUDA;
-    std::lock_guard<std::mutex> hold(lock);
-    if (dev < 0 || dev >= 64) return MARLIN_ERR_INVALID_ARG;
-    if (!set[dev]) {
-      if (kv_attn_set_smem_limit() != cudaSuccess || kv_prefill_set_smem_limit() != cudaSuccess) return MARLIN_ERR_CUDA;
-      set[dev] = true;
-    }
+  KvParams p{};
+  p.B = requests;
+  p.T = tokens;
+  p.lens = lengths;
+  p.q_start = q_start;
+  p.status = static_cast<int*>(workspace);
+  p.max_pages = 1;  // lengths up to 2^30, as in any cache
+  p.page = 1 << 30;
+  return launch_kv_tree(p, parents, words, mask, positions, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MARLIN_OK
+             : MARLIN_ERR_CUDA;
+}
+
+marlin_status_t marlin_kv_rope_append(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, int heads,
+                                      const uint16_t* k, int64_t k_token_stride, int64_t k_head_stride, const uint16_t* v,
+                                      int64_t v_token_stride, int64_t v_head_stride, const int32_t* positions, int axes,
+                                      const float* table, int table_rows, int rot, int interleaved,
+                                      const uint8_t* axis_of_pair, uint16_t* q_out, int64_t out_token_stride,
+                                      int64_t out_head_stride, void* cache, int n_pages, int kv_heads, int head_dim,
+                                      int page_size, const int32_t* page_table, int max_pages, const int32_t* lengths,
+                                      const int32_t* q_start, int requests, int tokens, void* workspace,
+                                      marlin_stream_t stream) {
+  KvRopeParams p{};
+  if (heads <= 0 || axes <= 0 || table_rows <= 0 || rot <= 0 || rot > head_dim) return MARLIN_ERR_INVALID_ARG;
+  const marlin_status_t s = make_kv(&p.kv, cache, n_pages, kv_heads, head_dim, page_size, page_table, max_pages, lengths,
+                                    q_start, requests, tokens, workspace);
+  if (s != MARLIN_OK) return s;
+  if (axes > kRopeAxes || rot % (head_dim / 8) != 0) return MARLIN_ERR_UNSUPPORTED;
+  if (axes > 1 && !axis_of_pair) return MARLIN_ERR_INVALID_ARG;
+  p.grouped = 1;
+  for (int j = 0; axis_of_pair && j < rot / 2; ++j) {
+    if (axis_of_pair[j] >= axes) return MARLIN_ERR_INVALID_ARG;
+    p.axis[j / 32] |= (unsigned long long)axis_of_pair[j] << (2 * (j % 32));
+    if (j % (head_dim / 32) != 0 && axis_of_pair[j] != axis_of_pair[j - 1]) p.grouped = 0;
   }
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (requests == 0 || tokens == 0) return MARLIN_OK;
+  if (!q || !k || !v || !positions || !table || !q_out) return MARLIN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(positions, 4) ||
+      !aligned(table, 16) || !strides_ok(q_token_stride, q_head_stride, 8) || !strides_ok(k_token_stride, k_head_stride, 8) ||
+      !strides_ok(v_token_stride, v_head_stride, 8) || !strides_ok(out_token_stride, out_head_stride, 8))
+    return MARLIN_ERR_MISALIGNED;
   p.q = q;
   p.q_ts = q_token_stride;
   p.q_hs = q_head_stride;
-  p.out = out;
   p.heads = heads;
-  p.group = group;
-  p.group_magic = group == 1 ? 0ull : ~0ull / (unsigned)group + 1;
-  // positions are below 2^30: a window beyond that hides nothing, and position - window stays in 32 bits
-  // for the negative positions of a request with more new tokens than its length, too
-  p.window = std::min(window, 1 << 30);
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.whole_blocks = p.kv.page16 % 4 == 0;
-  p.min_rows = 0;
-  p.max_rows = 0x7FFFFFFF;
-  p.counters = reinterpret_cast<int*>(ws + a.counters_off);
-  p.partials = reinterpret_cast<float*>(ws + a.partials_off);
-  p.firsts = reinterpret_cast<float*>(ws + a.firsts_off);
-  p.timeout_ns = kTimeoutNs;
-  // Which kernel: by the query rows that share a key head.  The streaming kernel
-  // takes 8 or 16 rows a pass over the cache, the tcgen05 kernel 128.  Where every
-  // request has the same number of new tokens one launch serves them all (each
-  // kernel is right for any number); else both are launched and each takes its
-  // side of the bound, request by request.
-  const bool uniform = requests == 1 || (long long)requests * max_q == tokens;
-  const bool some_large = (long long)(requests == 1 ? tokens : max_q) * group > kPrefillRows;
+  p.k = k;
+  p.k_ts = k_token_stride;
+  p.k_hs = k_head_stride;
+  p.v = v;
+  p.v_ts = v_token_stride;
+  p.v_hs = v_head_stride;
+  p.q_out = q_out;
+  p.o_ts = out_token_stride;
+  p.o_hs = out_head_stride;
+  p.positions = positions;
+  p.axes = axes;
+  p.table = table;
+  p.table_rows = table_rows;
+  p.rot = rot;
+  return launch_kv_rope_append(p, head_dim, interleaved != 0, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MARLIN_OK
+             : MARLIN_ERR_CUDA;
+}
+
+marlin_status_t marlin_kv_compact(void* const* caches, int count, int n_pages, int kv_heads, int head_dim, int page_size,
+                                  const int32_t* page_table, int max_pages, const int32_t* into, int into_pages,
+                                  const int32_t* lengths, const int32_t* q_start, const int32_t* index,
+                                  const int32_t* kept, int32_t* new_lengths, int requests, int tokens, int max_q,
+                                  void* workspace, marlin_stream_t stream) {
+  KvCompactParams p{};
+  if (max_q < 0 || (into && into_pages <= 0)) return MARLIN_ERR_INVALID_ARG;
+  if (const marlin_status_t c = check_caches(caches, count, n_pages, kv_heads, head_dim, page_size)) return c;
+  const marlin_status_t s = make_kv(&p.kv, caches[0], n_pages, kv_heads, head_dim, page_size, page_table, max_pages, lengths,
+                                    q_start, requests, tokens, workspace);
+  if (s != MARLIN_OK) return s;
+  if (into && (long long)into_pages * page_size > (1ll << 30)) return MARLIN_ERR_UNSUPPORTED;
+  if (requests == 0) return MARLIN_OK;
+  if (!lengths || !q_start || !page_table || !workspace || (!index && tokens > 0) || !kept || !new_lengths)
+    return MARLIN_ERR_INVALID_ARG;
+  if (!aligned(into, 4) || !aligned(index, 4) || !aligned(kept, 4) || !aligned(new_lengths, 4) || !aligned(lengths, 4))
+    return MARLIN_ERR_MISALIGNED;
+  if (tokens == 0)
+    return cudaMemcpyAsync(new_lengths, lengths, (size_t)requests * sizeof(int32_t), cudaMemcpyDeviceToDevice,
+                           reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MARLIN_OK
+               : MARLIN_ERR_CUDA;
+  p.into = into;
+  p.into_pages = into_pages;
+  p.index = index;
+  p.kept = kept;
+  p.max_q = std::min(max_q, tokens);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (some_large) {
-    if (!uniform) p.min_rows = kPrefillRows;
-    KvAttnParams f = p;
-    f.counters = p.counters + a.grid;
-    f.partials = reinterpret_cast<float*>(ws + a.prompt_off);
-    f.stripes = a.grid;
-    const long long items = kv_prefill_items(tokens, requests, kv_heads, group);
-    if (items > 0x7FFFFFFF) return MARLIN_ERR_UNSUPPORTED;
-    if (launch_kv_prefill(f, head_dim, std::max((int)items, a.grid), st) != cudaSuccess) return MARLIN_ERR_CUDA;
-    if (uniform) return MARLIN_OK;
-    p.max_rows = kPrefillRows;
-  }
-  return launch_kv_attn(p, head_dim, a.nb, a.grid, st) == cudaSuccess ? MARLIN_OK : MARLIN_ERR_CUDA;
+  return for_caches(caches, count, [&](const KvCaches& c, int n, int c0) {
+    p.caches = n;
+    p.new_lens = c0 == 0 ? new_lengths : nullptr;
+    return launch_kv_compact(p, c, head_dim, st);
+  });
+}
+
+marlin_status_t marlin_kv_copy_pages(void* const* caches, int count, int n_pages, int kv_heads, int head_dim,
+                                     int page_size, const int32_t* src, const int32_t* dst, int pairs, void* workspace,
+                                     marlin_stream_t stream) {
+  if (pairs < 0) return MARLIN_ERR_INVALID_ARG;
+  if (const marlin_status_t c = check_caches(caches, count, n_pages, kv_heads, head_dim, page_size)) return c;
+  size_t bytes;
+  if (const marlin_status_t c = marlin_kv_cache_bytes(1, kv_heads, head_dim, page_size, &bytes)) return c;
+  if (pairs == 0) return MARLIN_OK;
+  if (!src || !dst || !workspace) return MARLIN_ERR_INVALID_ARG;
+  if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(workspace, 16)) return MARLIN_ERR_MISALIGNED;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return for_caches(caches, count, [&](const KvCaches& c, int n, int) {
+    return launch_kv_copy_pages(c, n, n_pages, (long long)bytes, src, dst, pairs, static_cast<int*>(workspace), st);
+  });
 }
 
 }  // extern "C"

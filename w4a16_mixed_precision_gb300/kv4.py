@@ -8,6 +8,7 @@
 """
 from __future__ import annotations
 
+import ctypes
 import math
 from dataclasses import dataclass
 
@@ -103,6 +104,12 @@ def _need_bytes(t: torch.Tensor, name: str, nbytes: int) -> None:
         raise ValueError(f"{name} must be a contiguous uint8 CUDA tensor of at least {nbytes} bytes")
 
 
+def _need_i32(t: torch.Tensor, name: str, shape) -> None:
+    if (not t.is_cuda or t.dtype is not torch.int32 or not t.is_contiguous() or t.dim() != len(shape)
+            or any(n is not None and n != m for n, m in zip(shape, t.shape))):
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
 def _explain(name: str, t: torch.Tensor, tokens: int, heads, cache: Kv4Cache) -> None:
     """Raises for a tensor that is not fp16 [tokens, heads, head_dim] on the cache's device."""
     if not t.is_cuda or t.dtype != torch.float16:
@@ -183,3 +190,253 @@ def kv4_attention(q: torch.Tensor, cache: Kv4Cache, batch: Kv4Batch, ws: Kv4Work
                   window: int = 0) -> torch.Tensor:
     out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
     return kv4_attention_into(q, cache, batch, ws, out, scale, window)
+
+
+# ---- drafted trees ------------------------------------------------------------------------------
+
+def kv4_tree(parents: torch.Tensor, batch: Kv4Batch, ws: Kv4Workspace):
+    """(mask, positions) of the batch's new tokens, where those of a request are a tree: parents int32
+    [tokens], each token's parent among its request's new tokens (0 is the first), which comes before it,
+    negative for none.  mask int32 [tokens, words], words = max_q / 32 rounded up: bit j (of word j / 32) of a row is
+    set where the request's j-th new token is the row's own or one of its ancestors.  positions int32
+    [tokens]: the cached tokens before the new ones and the row's ancestors, counted.  Rows that no request
+    owns are not initialised."""
+    rows, work = batch._args or batch._check(), ws._args or ws._check()
+    _need_i32(parents, "parents", (batch.tokens,))
+    cur = torch._C._cuda_getDevice()
+    if not batch._device == ws._device == parents.get_device() == cur:
+        _on_current_device(("page_table", batch.page_table), ("workspace", ws.buf), ("parents", parents))
+    words = max(1, (batch.max_q + 31) // 32)
+    mask = torch.empty((batch.tokens, words), dtype=torch.int32, device=parents.device)
+    positions = torch.empty((batch.tokens,), dtype=torch.int32, device=parents.device)
+    rc = (_binding._lib or _binding.load()).marlin_kv_tree(
+        parents.data_ptr(), rows[2], rows[3], rows[4], rows[5], words, mask.data_ptr(), positions.data_ptr(), work[0],
+        torch._C._cuda_getCurrentRawStream(cur))
+    if rc:
+        raise MarlinError(rc, "marlin_kv_tree")
+    return mask, positions
+
+
+def kv4_tree_attention_into(q: torch.Tensor, cache: Kv4Cache, batch: Kv4Batch, tree: torch.Tensor, ws: Kv4Workspace,
+                            out: torch.Tensor, scale: float | None = None, window: int = 0) -> torch.Tensor:
+    """out[tokens, heads, head_dim] = attention of the batch's new tokens over the cache, which holds their own keys and
+    values already: a token sees the cached tokens before the new ones, and of its request's new ones those whose bit is
+    set in its row of tree (int32 [tokens, words], as kv4_tree makes it, or any other).  scale: 1 / sqrt(head_dim) by
+    default; window > 0: of the tokens before the new ones a row sees those among the last `window` up to its position,
+    which is the number of them and of the new tokens that it sees, less 1.  Rows that no request owns are left alone
+    (kv4_tree_attention's are not initialised)."""
+    cached, rows, work = cache._args or cache._check(), batch._args or batch._check(), ws._args or ws._check()
+    qs, shape = q.stride(), q.shape
+    if (q.dtype is not torch.float16 or len(shape) != 3 or shape[0] != batch.tokens or shape[2] != cache.head_dim
+            or qs[2] != 1 or not q.is_cuda):
+        _explain("q", q, batch.tokens, None, cache)
+    if out.dtype is not torch.float16 or out.shape != shape or not out.is_contiguous() or not out.is_cuda:
+        _explain("out", out, batch.tokens, shape[1], cache)
+        raise ValueError("out must be contiguous")
+    _need_i32(tree, "tree", (batch.tokens, None))
+    cur = _on_device(cache, batch, ws, ("q", q), ("out", out), ("tree", tree))
+    rc = (_binding._lib or _binding.load()).marlin_kv_tree_attention(
+        q.data_ptr(), qs[0], qs[1], shape[1], *cached, *rows, batch.max_q, tree.data_ptr(), tree.shape[1],
+        cache._scale if scale is None else scale, window, out.data_ptr(), *work,
+        torch._C._cuda_getCurrentRawStream(cur))
+    if rc:
+        raise MarlinError(rc, "marlin_kv_tree_attention")
+    return out
+
+
+def kv4_tree_attention(q: torch.Tensor, cache: Kv4Cache, batch: Kv4Batch, tree: torch.Tensor, ws: Kv4Workspace,
+                       scale: float | None = None, window: int = 0) -> torch.Tensor:
+    out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+    return kv4_tree_attention_into(q, cache, batch, tree, ws, out, scale, window)
+
+
+# ---- rotary positions ----------------------------------------------------------------------------
+
+class Kv4Rope(_Handle):
+    """Cosines and sines of rotary positions, once per model: cos, sin fp32 [positions, rot / 2], the entry for a
+    position and a pair of channels; rot, a multiple of head_dim / 8, is how many channels of a head are rotated, its first.
+    interleaved: pair j is channels (2 j, 2 j + 1), else (j, j + rot / 2).  axes: for positions on up to 4 axes (time,
+    height, width) the axis of each pair, rot / 2 numbers; None for one axis."""
+    _fields = ("table", "rot", "interleaved", "axes")
+
+    def __init__(self, cos: torch.Tensor, sin: torch.Tensor, axes=None, interleaved: bool = False):
+        if (not cos.is_cuda or cos.dtype != torch.float32 or cos.dim() != 2 or sin.shape != cos.shape
+                or sin.dtype != torch.float32 or sin.device != cos.device):
+            raise ValueError("cos and sin must be fp32 CUDA tensors [positions, rot / 2] on one device")
+        self.table = torch.stack([cos, sin], dim=-1).contiguous()
+        self.rot, self.interleaved = 2 * cos.shape[1], bool(interleaved)
+        self.axes = None if axes is None else tuple(int(a) for a in axes)
+        self._check()
+
+    @classmethod
+    def from_theta(cls, rot: int, positions: int, theta: float = 10000.0, axes=None, interleaved: bool = False, device=None):
+        """Angles position * theta^(-2 j / rot) for pair j, in 64 bits up to their cosines and sines."""
+        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        freq = theta ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=dev) / rot)
+        angle = torch.arange(positions, dtype=torch.float64, device=dev)[:, None] * freq
+        return cls(angle.cos().float(), angle.sin().float(), axes, interleaved)
+
+    def _check(self):
+        t = self.table
+        if not t.is_cuda or t.dtype != torch.float32 or not t.is_contiguous() or t.dim() != 3 or t.shape[1:] != (self.rot // 2, 2):
+            raise ValueError("the rope's table must be a contiguous fp32 CUDA tensor [positions, rot / 2, 2]")
+        if t.shape[0] < 1 or t.shape[1] < 1:
+            raise ValueError("the rope's table is empty")
+        axes = self.axes if self.axes is not None else (0,) * (self.rot // 2)
+        if len(axes) != self.rot // 2 or any(a < 0 or a > 3 for a in axes):
+            raise ValueError(f"axes: expected {self.rot // 2} numbers from 0 to 3")
+        self.n_axes = max(axes) + 1
+        self._device = t.get_device()
+        self._args = (t.data_ptr(), t.shape[0], self.rot, int(self.interleaved), bytes(axes))
+        return self._args
+
+
+def kv4_rope_append_into(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, rope: Kv4Rope,
+                         cache: Kv4Cache, batch: Kv4Batch, ws: Kv4Workspace, out: torch.Tensor) -> torch.Tensor:
+    """Rotate the batch's queries q, fp16 [tokens, heads, head_dim], and keys k, fp16 [tokens, kv_heads, head_dim], by
+    their positions, and quantise the rotated keys and the values v into the cache (as kv4_append does: the rotated
+    keys are rounded to fp16 first).  The rotated queries go to out, shaped like q (q itself, or anything that
+    overlaps neither q, k nor v).  positions int32 [axes, tokens], or [tokens] for one axis: rows of the rope's
+    table.  q, k, v and out may be views whose last dimension is contiguous (of one QKV product).  Rows that no
+    request owns are left alone."""
+    cached, rows, work = cache._args or cache._check(), batch._args or batch._check(), ws._args or ws._check()
+    angles = rope._args or rope._check()
+    T = batch.tokens
+    for name, t, heads in (("q", q, None), ("k", k, cache.kv_heads), ("v", v, cache.kv_heads),
+                           ("out", out, q.shape[1] if q.dim() == 3 else None)):
+        s = t.shape
+        if (t.dtype is not torch.float16 or len(s) != 3 or s[0] != T or s[2] != cache.head_dim or (heads and s[1] != heads)
+                or t.stride(2) != 1 or not t.is_cuda):
+            _explain(name, t, T, heads, cache)
+    _need_i32(positions, "positions", (T,) if positions.dim() == 1 and rope.n_axes == 1 else (rope.n_axes, T))
+    cur = _on_device(cache, batch, ws, ("q", q), ("k", k), ("v", v), ("out", out), ("positions", positions),
+                     ("rope", rope.table))
+    qs, ks, vs, os = q.stride(), k.stride(), v.stride(), out.stride()
+    rc = (_binding._lib or _binding.load()).marlin_kv_rope_append(
+        q.data_ptr(), qs[0], qs[1], q.shape[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+        positions.data_ptr(), rope.n_axes, *angles, out.data_ptr(), os[0], os[1], *cached, *rows, work[0],
+        torch._C._cuda_getCurrentRawStream(cur))
+    if rc:
+        raise MarlinError(rc, "marlin_kv_rope_append")
+    return out
+
+
+def kv4_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, rope: Kv4Rope,
+                    cache: Kv4Cache, batch: Kv4Batch, ws: Kv4Workspace) -> torch.Tensor:
+    """kv4_rope_append_into with the rotated queries in a new tensor."""
+    out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+    return kv4_rope_append_into(q, k, v, positions, rope, cache, batch, ws, out)
+
+
+# ---- moving what the caches hold -----------------------------------------------------------------
+
+def _layers(caches, ws: Kv4Workspace, *named):
+    """The addresses of the layers' caches (one or several alike), what they share, and the current device."""
+    caches = (caches,) if isinstance(caches, Kv4Cache) else tuple(caches)
+    if not caches:
+        raise ValueError("no caches")
+    args = [c._args or c._check() for c in caches]
+    if any(a[1:] != args[0][1:] for a in args):
+        raise ValueError("the caches must be alike: pages, key heads, head_dim and page size")
+    cur = torch._C._cuda_getDevice()
+    if not (all(c._device == cur for c in caches) and ws._device == cur and all(t.get_device() == cur for _, t in named)):
+        _on_current_device(*(("cache", c.buf) for c in caches), ("workspace", ws.buf), *named)
+    return (ctypes.c_void_p * len(args))(*(a[0] for a in args)), len(args), args[0][1:], cur
+
+
+def kv4_compact(caches, batch: Kv4Batch, index: torch.Tensor, kept: torch.Tensor, ws: Kv4Workspace,
+                into: torch.Tensor | None = None) -> torch.Tensor:
+    """Keep some of each request's new tokens, in the caches of all layers (one Kv4Cache or a sequence of them, all
+    alike): with first = lengths[b] - new tokens, position first + i takes what position first + index[q_start[b] + i]
+    holds, for i < kept[b].  index int32 [tokens], kept int32 [B].  Returns the new lengths, int32 [B]: first + kept.
+
+    into None: the tokens stay in their pages, and index must ascend within a request (one that does not is left as it
+    was, and reported).  into int32 [B, pages]: the kept tokens' pages, which the caller owns and which are none of
+    those that are read; index may then name any of the new tokens, in any order.  Other positions are not touched.
+    Pages that requests share must hold none of the positions that are written."""
+    rows, work = batch._args or batch._check(), ws._args or ws._check()
+    B = rows[4]
+    _need_i32(index, "index", (batch.tokens,))
+    _need_i32(kept, "kept", (B,))
+    named = [("page_table", batch.page_table), ("index", index), ("kept", kept)]
+    if into is not None:
+        _need_i32(into, "into", (B, None))
+        named.append(("into", into))
+    at, count, shape, cur = _layers(caches, ws, *named)
+    lengths = torch.empty((B,), dtype=torch.int32, device=index.device)
+    rc = (_binding._lib or _binding.load()).marlin_kv_compact(
+        at, count, *shape, rows[0], rows[1], None if into is None else into.data_ptr(),
+        0 if into is None else into.shape[1], rows[2], rows[3], index.data_ptr(), kept.data_ptr(), lengths.data_ptr(), B,
+        batch.tokens, batch.max_q, work[0], torch._C._cuda_getCurrentRawStream(cur))
+    if rc:
+        raise MarlinError(rc, "marlin_kv_compact")
+    return lengths
+
+
+def kv4_copy_pages(caches, src: torch.Tensor, dst: torch.Tensor, ws: Kv4Workspace) -> None:
+    """Page dst[i] takes what page src[i] holds, in the caches of all layers (one Kv4Cache or a sequence of them, all
+    alike); a pair whose source is negative is left out.  src, dst int32 [pairs].  A page that is written must be named
+    once only, as source or destination, in a call."""
+    work = ws._args or ws._check()
+    _need_i32(src, "src", (None,))
+    _need_i32(dst, "dst", (src.shape[0],))
+    at, count, shape, cur = _layers(caches, ws, ("src", src), ("dst", dst))
+    rc = (_binding._lib or _binding.load()).marlin_kv_copy_pages(
+        at, count, *shape, src.data_ptr(), dst.data_ptr(), src.shape[0], work[0],
+        torch._C._cuda_getCurrentRawStream(cur))
+    if rc:
+        raise MarlinError(rc, "marlin_kv_copy_pages")
+
+
+class Kv4Pages:
+    """Which pages of the caches are free, and how many requests hold each of the others (on the host)."""
+
+    def __init__(self, n_pages: int, page_size: int):
+        self.page_size = page_size
+        self._free = list(range(n_pages - 1, -1, -1))
+        self._holders = [0] * n_pages
+
+    @property
+    def free_pages(self) -> int:
+        return len(self._free)
+
+    def take(self, n: int) -> list[int]:
+        """n pages that no one holds."""
+        if n < 0 or n > len(self._free):
+            raise ValueError(f"{n} pages asked for, {len(self._free)} are free")
+        pages = [self._free.pop() for _ in range(n)]
+        for page in pages:
+            self._holders[page] = 1
+        return pages
+
+    def fork(self, pages, length: int):
+        """(pages, copies) of a request that goes on from another's first `length` tokens: it shares the pages that
+        these fill, and has one of its own for the rest of them; copies lists that (from, to), for kv4_copy_pages."""
+        full, rest = divmod(length, self.page_size)
+        if length < 0 or full + (rest > 0) > len(pages):
+            raise ValueError(f"{length} tokens do not fit {len(pages)} pages")
+        self._need_held(pages[:full + (rest > 0)])
+        own = self.take(1) if rest else []
+        for page in pages[:full]:
+            self._holders[page] += 1
+        return list(pages[:full]) + own, [(pages[full], own[0])] if rest else []
+
+    def free(self, pages) -> None:
+        """A request's pages, which it no longer holds; those that no one else holds are free again."""
+        self._need_held(pages)
+        for page in pages:
+            self._holders[page] -= 1
+            if self._holders[page] == 0:
+                self._free.append(page)
+
+    def shared(self, page: int) -> bool:
+        """Whether several requests hold the page: none of them may write into it."""
+        return self._holders[page] > 1
+
+    def _need_held(self, pages) -> None:
+        count = {}
+        for page in pages:
+            count[page] = count.get(page, 0) + 1
+        for page, n in count.items():
+            if not 0 <= page < len(self._holders) or self._holders[page] < n:
+                raise ValueError(f"page {page} is not held")
