@@ -112,6 +112,18 @@ __device__ __forceinline__ int kv_owner(const KvParams& p, int t) {
   return lo;
 }
 
+// The same by a warp, for one row: 32 starts at a time.
+__device__ __forceinline__ int kv_owner_by_warp(const KvParams& p, int t) {
+  int lo = 0, hi = p.B;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + ((int)(threadIdx.x & 31) + 1) * step;
+    const int n = __popc(__ballot_sync(0xffffffffu, at < hi && p.q_start[at] <= t));
+    lo = min(lo + n * step, hi - 1);
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
 struct KvAttnParams {
   KvParams kv;
   const uint16_t* q;        // fp16 [T][heads][D] with strides
@@ -193,6 +205,7 @@ struct KvRopeParams {
   uint16_t* q_out;
   long long q_ts, q_hs, o_ts, o_hs, k_ts, k_hs, v_ts, v_hs;  // elements
   int heads;
+  int run;                    // steps of several heads that a warp takes (filled in by launch_kv_rope_append)
   const int* positions;       // [axes][T]
   const float* table;         // [table_rows][rot / 2] of (cos, sin)
   int axes, table_rows, rot;

@@ -13,6 +13,8 @@
 // card's copy rate); 48 tokens in 4.1 and 3.3 us.  Writing issues an instruction in 68%
 // of the cycles; fewer for the codes (sums instead of shifts) changed nothing, so what
 // is left is the loads' latency under one short task per warp.
+#include <algorithm>
+
 #include "kv.cuh"
 
 namespace w4a16 {
@@ -260,10 +262,14 @@ cudaError_t launch_copy(const KvParams& p, uint16_t* k, uint16_t* v, const long 
 // result to fp16.  Queries go to q_out; keys, and values as they are, into the cache like above.
 //
 // Bound: the stream, 4 D bytes a query head, 4 D + 2 (D/2 + 4) a key head and token.  A warp takes four
-// tokens like above, eight lanes each, and keeps the tokens' cosines and sines in registers for kQHeads
-// query heads or one key head.  A lane holds two chunks of D/16 channels, such that both channels of its
-// pairs are its own: chunks g and g + rot/2 of the rotated ones, two neighbours of the rest.
-constexpr int kQHeads = 4;  // of a warp
+// tokens like above, eight lanes each, and a run of their heads, 1 KB of a token at a time: four query heads of
+// 128 channels, or two key heads with their values.  What the tokens need (their request, place, positions, cosines and sines,
+// a chain of loads) is found once, under the first vectors' loads, and kept in registers.  A lane holds two
+// chunks of D/16 channels, such that both channels of its pairs are its own: chunks g and g + rot/2 of the
+// rotated ones, two neighbours of the rest.
+template <int D>
+constexpr int kVectors = 512 / D;  // together
+constexpr long long kFullCard = 3700;  // warps: about one load of the card
 
 template <int N>  // 4-byte words
 __device__ __forceinline__ void load_chunk(const uint16_t* at, uint32_t* x) {
@@ -310,119 +316,138 @@ __device__ __forceinline__ void rotate_chunks(uint32_t (&x)[CH], const float2 (&
 }
 
 template <int D, bool kInterleaved>
-__global__ void __launch_bounds__(kKvThreads) kv_rope_append_kernel(const KvRopeParams p) {
+__global__ void __launch_bounds__(kKvThreads, 3) kv_rope_append_kernel(const KvRopeParams p) {
   if (threadIdx.x == 0) griddep_launch_dependents();
   griddep_wait();
   constexpr int CH = D / 16;  // channels of a chunk, pairs of a lane
+  constexpr int kVec = kVectors<D>;
   const int lane = threadIdx.x & 31, g = lane & 7, mine = lane >> 3;
-  const int q_tasks = (p.heads + kQHeads - 1) / kQHeads, tasks = q_tasks + p.kv.hkv;
+  const int q_steps = (p.heads + kVec - 1) / kVec, steps = q_steps + (2 * p.kv.hkv + kVec - 1) / kVec;
+  const int runs = (steps + p.run - 1) / p.run;
   const long long warp = (long long)blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5);
-  const long long tile = warp / tasks;
-  const int task = (int)(warp - tile * tasks);
+  const long long tile = warp / runs;
+  const int first = (int)(warp - tile * runs) * p.run, last = min(first + p.run, steps);
   const bool live = tile * kTokens + mine < p.kv.T;
+  if (tile * kTokens >= p.kv.T) return;
   const int t = live ? (int)(tile * kTokens) + mine : 0;
-  const bool keys = task >= q_tasks;
-  const int h = keys ? task - q_tasks : task * kQHeads;
-  const int heads = keys ? 2 : min(kQHeads, p.heads - h);  // vectors that are loaded: a key and a value
 
   const int half = p.rot / (2 * CH);  // chunks that hold the pairs' first channels (or half of the pairs)
   const bool rotated = g < half;
   const int ca = (rotated ? g : 2 * half + 2 * (g - half)) * CH, cb = rotated ? ca + half * CH : ca + CH;
+  const uint16_t *q = p.q + t * p.q_ts, *k = p.k + t * p.k_ts, *v = p.v + t * p.v_ts + g * (D / 8);
 
-  // the vectors first, then what their places and positions need
-  uint32_t x[kQHeads][CH];
-  const uint16_t* value = p.v + t * p.v_ts + h * p.v_hs + g * (D / 8);
-#pragma unroll
-  for (int i = 0; i < kQHeads; ++i) {
-#pragma unroll
-    for (int w = 0; w < CH; ++w) x[i][w] = 0u;
-    if (!live || i >= heads) continue;
-    if (keys && i == 1) {
-      load_chunk<CH / 2>(value, x[i]);
-      load_chunk<CH / 2>(value + CH, x[i] + CH / 2);
-    } else {
-      const uint16_t* from = keys ? p.k + t * p.k_ts + h * p.k_hs : p.q + t * p.q_ts + (h + i) * p.q_hs;
-      load_chunk<CH / 2>(from + ca, x[i]);
-      load_chunk<CH / 2>(from + cb, x[i] + CH / 2);
-    }
-  }
-  const int b = kv_owner(p.kv, t);
-  const KvSeq s = kv_seq(p.kv, b, true);
-  bool mine_ok = live && t >= s.q0 && t < s.q0 + s.nq;
-  int pos[kRopeAxes];
-#pragma unroll
-  for (int a = 0; a < kRopeAxes; ++a) {
-    pos[a] = 0;
-    if (a < p.axes && mine_ok) pos[a] = p.positions[(long long)a * p.kv.T + t];
-  }
-  bool bad = false;
-#pragma unroll
-  for (int a = 0; a < kRopeAxes; ++a) bad = bad || (uint32_t)pos[a] >= (uint32_t)p.table_rows;
-  if (bad) {
-    if (g == 0 && task == 0) kv_fail(p.kv, kKvSitePosition);
-    mine_ok = false;
-  }
+  bool mine_ok = false;
+  uint8_t* base = nullptr;  // the token's granule of key head 0
+  int in = 0;
   float2 cs[CH];
+  for (int step = first; step < last; ++step) {
+    const bool keys = step >= q_steps;
+    const int h = keys ? (step - q_steps) * (kVec / 2) : step * kVec;
+    const int count = min(kVec, keys ? 2 * (p.kv.hkv - h) : p.heads - h);
+    uint32_t x[kVec][CH];
 #pragma unroll
-  for (int i = 0; i < CH; ++i) cs[i] = make_float2(1.f, 0.f);
-  if (mine_ok && rotated) {
-    auto entry = [&](int pair) {
-      const int axis = (int)(p.axis[pair >> 5] >> (2 * (pair & 31))) & 3;
-      const int at = axis == 0 ? pos[0] : axis == 1 ? pos[1] : axis == 2 ? pos[2] : pos[3];
-      return reinterpret_cast<const float2*>(p.table) + (long long)at * (p.rot / 2) + pair;
-    };
+    for (int i = 0; i < kVec; ++i) {
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      const int pair0 = kInterleaved ? (part ? cb : ca) / 2 : ca + part * (CH / 2);
-      if (p.grouped) {  // CH / 2 pairs lie together
-        const float4* from = reinterpret_cast<const float4*>(entry(pair0));
-#pragma unroll
-        for (int i = 0; i < CH / 4; ++i) {
-          const float4 v = from[i];
-          cs[part * (CH / 2) + 2 * i] = make_float2(v.x, v.y);
-          cs[part * (CH / 2) + 2 * i + 1] = make_float2(v.z, v.w);
-        }
+      for (int w = 0; w < CH; ++w) x[i][w] = 0u;
+      if (!live || i >= count) continue;
+      if (keys && (i & 1)) {
+        const uint16_t* from = v + (h + i / 2) * p.v_hs;
+        load_chunk<CH / 2>(from, x[i]);
+        load_chunk<CH / 2>(from + CH, x[i] + CH / 2);
       } else {
-#pragma unroll
-        for (int i = 0; i < CH / 2; ++i) cs[part * (CH / 2) + i] = *entry(pair0 + i);
+        const uint16_t* from = keys ? k + (h + i / 2) * p.k_hs : q + (h + i) * p.q_hs;
+        load_chunk<CH / 2>(from + ca, x[i]);
+        load_chunk<CH / 2>(from + cb, x[i] + CH / 2);
       }
     }
-  }
-  if (!keys) {
-    if (!mine_ok) return;
+    if (step == first) {
+      const int b = kv_owner(p.kv, t);
+      const KvSeq s = kv_seq(p.kv, b, true);
+      mine_ok = live && t >= s.q0 && t < s.q0 + s.nq;
+      int pos[kRopeAxes];
 #pragma unroll
-    for (int i = 0; i < kQHeads; ++i) {
-      if (i >= heads) break;
-      if (rotated) rotate_chunks<CH, kInterleaved>(x[i], cs);
-      uint16_t* to = p.q_out + t * p.o_ts + (h + i) * p.o_hs;
-      store_chunk<CH / 2>(to + ca, x[i]);
-      store_chunk<CH / 2>(to + cb, x[i] + CH / 2);
+      for (int a = 0; a < kRopeAxes; ++a) {
+        pos[a] = 0;
+        if (a < p.axes && mine_ok) pos[a] = p.positions[(long long)a * p.kv.T + t];
+      }
+      bool bad = false;
+#pragma unroll
+      for (int a = 0; a < kRopeAxes; ++a) bad = bad || (uint32_t)pos[a] >= (uint32_t)p.table_rows;
+      if (bad) {
+        if (g == 0) kv_fail(p.kv, kKvSitePosition);
+        mine_ok = false;
+      }
+#pragma unroll
+      for (int i = 0; i < CH; ++i) cs[i] = make_float2(1.f, 0.f);
+      if (mine_ok && rotated) {
+        auto entry = [&](int pair) {
+          const int axis = (int)(p.axis[pair >> 5] >> (2 * (pair & 31))) & 3;
+          const int at = axis == 0 ? pos[0] : axis == 1 ? pos[1] : axis == 2 ? pos[2] : pos[3];
+          return reinterpret_cast<const float2*>(p.table) + (long long)at * (p.rot / 2) + pair;
+        };
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          const int pair0 = kInterleaved ? (part ? cb : ca) / 2 : ca + part * (CH / 2);
+          if (p.grouped) {  // CH / 2 pairs lie together
+            const float4* from = reinterpret_cast<const float4*>(entry(pair0));
+#pragma unroll
+            for (int i = 0; i < CH / 4; ++i) {
+              const float4 e = from[i];
+              cs[part * (CH / 2) + 2 * i] = make_float2(e.x, e.y);
+              cs[part * (CH / 2) + 2 * i + 1] = make_float2(e.z, e.w);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < CH / 2; ++i) cs[part * (CH / 2) + i] = *entry(pair0 + i);
+          }
+        }
+      }
+      if (last > q_steps) base = mine_ok ? kv_place_of<D>(p.kv, t, b, s, 0, &in) : nullptr;
     }
-    return;
+    if (!keys) {
+      if (!mine_ok) continue;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        if (i >= count) break;
+        if (rotated) rotate_chunks<CH, kInterleaved>(x[i], cs);
+        uint16_t* to = p.q_out + t * p.o_ts + (h + i) * p.o_hs;
+        store_chunk<CH / 2>(to + ca, x[i]);
+        store_chunk<CH / 2>(to + cb, x[i] + CH / 2);
+      }
+      continue;
+    }
+#pragma unroll
+    for (int i = 0; i < kVec; i += 2) {
+      if (i >= count) break;  // (the whole warp)
+      if (rotated) rotate_chunks<CH, kInterleaved>(x[i], cs);
+      uint32_t kc[CH / 4], vc[CH / 4];
+      __half ks, ko, vs, vo;
+      quantise<2 * CH>(x[i], kc, ks, ko);
+      quantise<2 * CH>(x[i + 1], vc, vs, vo);
+      uint8_t* at = base ? base + (h + i / 2) * p.kv.head_bytes : nullptr;
+      put_values<D>(at, in, vc, lane);
+      if (!at) continue;
+      uint8_t* krow = at + in * (D / 2);
+      if constexpr (D == 128) {
+        *reinterpret_cast<uint32_t*>(krow + ca / 2) = kc[0];
+        *reinterpret_cast<uint32_t*>(krow + cb / 2) = kc[1];
+      } else {
+        *reinterpret_cast<uint16_t*>(krow + ca / 2) = (uint16_t)kc[0];
+        *reinterpret_cast<uint16_t*>(krow + cb / 2) = (uint16_t)(kc[0] >> 16);
+      }
+      if (g == 0) *reinterpret_cast<uint2*>(at + 16 * D + 8 * in) = make_uint2(pair_bits(ks, ko), pair_bits(vs, vo));
+    }
   }
-  int i = 0;
-  uint8_t* base = mine_ok ? kv_place_of<D>(p.kv, t, b, s, h, &i) : nullptr;
-  if (rotated) rotate_chunks<CH, kInterleaved>(x[0], cs);
-  uint32_t kc[CH / 4], vc[CH / 4];
-  __half ks, ko, vs, vo;
-  quantise<2 * CH>(x[0], kc, ks, ko);
-  quantise<2 * CH>(x[1], vc, vs, vo);
-  put_values<D>(base, i, vc, lane);
-  if (!base) return;
-  uint8_t* krow = base + i * (D / 2);
-  if constexpr (D == 128) {
-    *reinterpret_cast<uint32_t*>(krow + ca / 2) = kc[0];
-    *reinterpret_cast<uint32_t*>(krow + cb / 2) = kc[1];
-  } else {
-    *reinterpret_cast<uint16_t*>(krow + ca / 2) = (uint16_t)kc[0];
-    *reinterpret_cast<uint16_t*>(krow + cb / 2) = (uint16_t)(kc[0] >> 16);
-  }
-  if (g == 0) *reinterpret_cast<uint2*>(base + 16 * D + 8 * i) = make_uint2(pair_bits(ks, ko), pair_bits(vs, vo));
 }
 
 template <int D, bool kInterleaved>
 cudaError_t launch_rope(const KvRopeParams& p, cudaStream_t stream) {
-  const long long warps = ((long long)p.kv.T + kTokens - 1) / kTokens * ((p.heads + kQHeads - 1) / kQHeads + p.kv.hkv);
+  const long long tiles = ((long long)p.kv.T + kTokens - 1) / kTokens;
+  constexpr int kVec = kVectors<D>;
+  const int steps = (p.heads + kVec - 1) / kVec + (2 * p.kv.hkv + kVec - 1) / kVec;
+  KvRopeParams f = p;
+  f.run = (int)std::min<long long>(steps, std::max<long long>(1, tiles * steps / kFullCard));
+  const long long warps = tiles * ((steps + f.run - 1) / f.run);
   constexpr int per = kKvThreads / 32;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -433,7 +458,7 @@ cudaError_t launch_rope(const KvRopeParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_rope_append_kernel<D, kInterleaved>, p);
+  return cudaLaunchKernelEx(&cfg, kv_rope_append_kernel<D, kInterleaved>, f);
 }
 
 }  // namespace

@@ -18,6 +18,8 @@ namespace {
 // each (kv.cuh).  Where the kept tokens stay in their pages, W warps (a unit) take a request's head in
 // rounds of W granules, loads before stores: index[i] ascends, so no round reads what one before has
 // written, and a barrier between a round's loads and stores keeps it from overwriting what is still read.
+// (Where tokens come from is the same for every head of every cache; warps that moved several heads, to find it
+// once, were up to 15% slower.)
 constexpr int kMoveThreads = 256, kMoveWarps = kMoveThreads / 32;
 
 // What warps read of a request, checked.
@@ -183,9 +185,9 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const KvCompac
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * (kMoveWarps / W) + warp / W;
-  const long long per = (long long)p.caches * p.kv.hkv;
-  if (unit >= per * p.kv.B) return;  // a whole unit
-  const int b = (int)(unit / per), at = (int)(unit - b * per), cache = at / p.kv.hkv, h = at - cache * p.kv.hkv;
+  const int heads = p.caches * p.kv.hkv;
+  if (unit >= (long long)heads * p.kv.B) return;  // a whole unit
+  const int b = (int)(unit / heads), at = (int)(unit - (long long)b * heads), cache = at / p.kv.hkv;
   const bool speaks = at == 0 && warp % W == 0;  // one warp of the request
   Kept k = kept_of(p, b, speaks && lane == 0);
   if (k.kept > 0 && !ascends(p, k)) {
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const KvCompac
   }
   if (speaks && lane == 0 && p.new_lens) p.new_lens[b] = k.kept < 0 ? p.kv.lens[b] : k.first + k.kept;
   if (k.kept <= 0) return;
-  uint8_t* head = caches.at[cache] + h * p.kv.head_bytes;
+  uint8_t* head = caches.at[cache] + (at - cache * p.kv.hkv) * p.kv.head_bytes;
   const int g_end = (k.first + k.kept + 15) >> 4;
   for (int g0 = k.first >> 4; g0 < g_end; g0 += W) {
     const int granule = g0 + warp % W;
@@ -211,22 +213,21 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const KvCompac
   }
 }
 
-// The kept tokens go to other pages: every granule is a warp's.
+// The kept tokens go to other pages: every granule of a head is a warp's.
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) kv_gather_kernel(const KvCompactParams p, const __grid_constant__ KvCaches caches,
                                                                  int ctas) {
   if (threadIdx.x == 0) griddep_launch_dependents();
   griddep_wait();
-  const int warp = threadIdx.x >> 5;
   const int x = blockIdx.x % ctas, unit = blockIdx.x / ctas;  // of a head's CTAs
-  const int per = p.caches * p.kv.hkv, b = unit / per, at = unit - b * per, cache = at / p.kv.hkv, h = at - cache * p.kv.hkv;
+  const int heads = p.caches * p.kv.hkv, b = unit / heads, at = unit - b * heads, cache = at / p.kv.hkv;
   const bool speaks = at == 0 && x == 0 && threadIdx.x == 0;
   const Kept k = kept_of(p, b, speaks);
   if (speaks && p.new_lens) p.new_lens[b] = k.kept < 0 ? p.kv.lens[b] : k.first + k.kept;
   if (k.kept <= 0) return;
-  uint8_t* head = caches.at[cache] + h * p.kv.head_bytes;
+  uint8_t* head = caches.at[cache] + (at - cache * p.kv.hkv) * p.kv.head_bytes;
   const int g_end = (k.first + k.kept + 15) >> 4;
-  for (int granule = (k.first >> 4) + x * kMoveWarps + warp; granule < g_end; granule += ctas * kMoveWarps) {
+  for (int granule = (k.first >> 4) + x * kMoveWarps + (threadIdx.x >> 5); granule < g_end; granule += ctas * kMoveWarps) {
     const Plan m = plan_granule<D>(p, k, b, granule);
     Granule<D> r;
     load_granule<D>(head, m, r);
@@ -285,15 +286,13 @@ cudaError_t compact(const KvCompactParams& p, const KvCaches& c, cudaStream_t st
   const long long units = (long long)p.kv.B * p.caches * p.kv.hkv;
   const long long granules = ((long long)p.max_q + 15) / 16 + 1;  // at most, of a request
   if (p.into) {
-    const int ctas = (int)((granules + kMoveWarps - 1) / kMoveWarps);
+    const long long ctas = (granules + kMoveWarps - 1) / kMoveWarps;
     if (units * ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    return launch(kv_gather_kernel<D>, units * ctas, kMoveThreads, stream, p, c, ctas);
+    return launch(kv_gather_kernel<D>, units * ctas, kMoveThreads, stream, p, c, (int)ctas);
   }
-  const auto go = [&](auto kernel, int w) {
-    return launch(kernel, (units * w + kMoveWarps - 1) / kMoveWarps, kMoveThreads, stream, p, c);
-  };
-  if (granules <= 2) return go(kv_compact_kernel<D, 1>, 1);
-  return granules <= 8 ? go(kv_compact_kernel<D, 2>, 2) : go(kv_compact_kernel<D, 8>, 8);
+  // a warp a head where few tokens can be kept (more are served by it in more rounds), else a CTA
+  if (granules <= 16) return launch(kv_compact_kernel<D, 1>, (units + kMoveWarps - 1) / kMoveWarps, kMoveThreads, stream, p, c);
+  return launch(kv_compact_kernel<D, 8>, units, kMoveThreads, stream, p, c);
 }
 
 }  // namespace

@@ -326,6 +326,7 @@ __device__ __forceinline__ void move_on(const KvAttnParams& p, Place& c, int by)
 // against 355, 376 of 94 to 141 506 against 462, 504 of 94 to 125 629 against 573.
 // The mean is taken as if a request's items grew evenly.
 constexpr int kCutCost = 20, kCutItemCost = 4;  // blocks
+constexpr int kTreeCutCost = 14;               // of trees, whose parts another kernel joins
 template <bool kTree>
 __device__ __forceinline__ void find_item(const KvAttnParams& p, CtrlP& ctrl) {
   const int lane = threadIdx.x & 31;
@@ -375,7 +376,7 @@ __device__ __forceinline__ void find_item(const KvAttnParams& p, CtrlP& ctrl) {
   __syncwarp();
   const long long S = p.stripes, mean = U / S;
   const long long whole = min((items + S - 1) / S * longest, mean + longest / 2);
-  if (items <= (long long)gridDim.x && whole <= mean + kCutCost + kCutItemCost * items / S) {
+  if (items <= (long long)gridDim.x && whole <= mean + (kTree ? kTreeCutCost : kCutCost) + kCutItemCost * items / S) {
     if (lane == 0) ctrl.by_item = 1;
   } else if (lane == 0) {
     ctrl.start_b = -1;
@@ -476,7 +477,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       longest = max(longest, ctrl.longest[w]);
     }
     // no more items than SMs: a CTA each, unless stripes would end before the longest
-    by_item = !many && all_items <= (long long)gridDim.x && longest <= U / p.stripes + kCutCost;
+    by_item = !many && all_items <= (long long)gridDim.x && longest <= U / p.stripes + (kTree ? kTreeCutCost : kCutCost);
     G = by_item ? all_items : min((long long)p.stripes, U);
     const bool works = (long long)blockIdx.x < G;
     if (works && !by_item) {

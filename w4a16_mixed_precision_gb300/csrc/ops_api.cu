@@ -117,6 +117,7 @@ marlin_status_t kv_copy(bool append, uint16_t* k, int64_t k_ts, int64_t k_hs, ui
 // rows: one request of 1000, 64 heads on 8, 160 rows 16 / 32, of 8000 43 / 126 (an item that
 // many stripes cut is joined part by part).
 constexpr int kPrefillRows = 64;
+constexpr int kTreeRows = 48;  // the same for trees
 
 struct AttnPlan {
   int grid, nb;
@@ -125,7 +126,7 @@ struct AttnPlan {
 
 // [status 256 B][arrivals of both kernels][parts of the streaming kernel][parts of the
 // tcgen05 kernel, where a request can have enough rows for it]
-AttnPlan attn_plan(int sms, int D, int group, int max_q, int tokens) {
+AttnPlan attn_plan(int sms, int D, int group, int max_q, int tokens, int most_rows) {
   AttnPlan a;
   a.grid = sms;
   a.nb = (long long)group * max_q > 8 ? 2 : 1;
@@ -135,7 +136,7 @@ AttnPlan attn_plan(int sms, int D, int group, int max_q, int tokens) {
   a.firsts_off = a.partials_off + 2 * sms * part;
   a.prompt_off = round_up(a.firsts_off + kKvAttnWarps * sms * part, 256);
   a.bytes = a.prompt_off;
-  if ((long long)group * tokens > kPrefillRows) a.bytes += 2 * sms * kv_prefill_part_floats(D) * sizeof(float);
+  if ((long long)group * tokens > most_rows) a.bytes += 2 * sms * kv_prefill_part_floats(D) * sizeof(float);
   return a;
 }
 
@@ -159,7 +160,8 @@ marlin_status_t attention(const uint16_t* q, int64_t q_token_stride, int64_t q_h
   if ((s = current_sms(&sms)) != MARLIN_OK) return s;
   const int group = heads / kv_heads;
   if ((long long)tokens * group > 0x7FFFFFFF) return MARLIN_ERR_UNSUPPORTED;
-  const AttnPlan a = attn_plan(sms, head_dim, group, max_q, tokens);
+  const int most_rows = words > 0 ? kTreeRows : kPrefillRows;
+  const AttnPlan a = attn_plan(sms, head_dim, group, max_q, tokens, most_rows);
   if (workspace_bytes < a.bytes) return MARLIN_ERR_WORKSPACE_TOO_SMALL;
   {
     static std::mutex lock;
@@ -201,10 +203,10 @@ marlin_status_t attention(const uint16_t* q, int64_t q_token_stride, int64_t q_h
   // side of the bound, request by request.
   const bool uniform = requests == 1 || (long long)requests * max_q == tokens;
   // (the workspace holds the tcgen05 kernel's parts where all tokens together have enough rows)
-  const bool some_large = (long long)(requests == 1 ? tokens : std::min(max_q, tokens)) * group > kPrefillRows;
+  const bool some_large = (long long)(requests == 1 ? tokens : std::min(max_q, tokens)) * group > most_rows;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (some_large) {
-    if (!uniform) p.min_rows = kPrefillRows;
+    if (!uniform) p.min_rows = most_rows;
     KvAttnParams f = p;
     f.counters = p.counters + a.grid;
     f.partials = reinterpret_cast<float*>(ws + a.prompt_off);
@@ -213,7 +215,7 @@ marlin_status_t attention(const uint16_t* q, int64_t q_token_stride, int64_t q_h
     if (items > 0x7FFFFFFF) return MARLIN_ERR_UNSUPPORTED;
     if (launch_kv_prefill(f, head_dim, std::max((int)items, a.grid), st) != cudaSuccess) return MARLIN_ERR_CUDA;
     if (uniform) return MARLIN_OK;
-    p.max_rows = kPrefillRows;
+    p.max_rows = most_rows;
   }
   return launch_kv_attn(p, head_dim, a.nb, a.grid, st) == cudaSuccess ? MARLIN_OK : MARLIN_ERR_CUDA;
 }
@@ -319,7 +321,7 @@ marlin_status_t marlin_kv_workspace_bytes(int heads, int kv_heads, int head_dim,
   int sms;
   const marlin_status_t s = static_cast<marlin_status_t>(device_sms(device, &sms));
   if (s != MARLIN_OK) return s;
-  *bytes = attn_plan(sms, head_dim, heads / kv_heads, 1, tokens).bytes;
+  *bytes = attn_plan(sms, head_dim, heads / kv_heads, 1, tokens, std::min(kPrefillRows, kTreeRows)).bytes;
   return MARLIN_OK;
 }
 

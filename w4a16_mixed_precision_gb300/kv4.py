@@ -8,8 +8,8 @@
 """
 from __future__ import annotations
 
-import ctypes
 import math
+from array import array
 from dataclasses import dataclass
 
 import torch
@@ -38,6 +38,7 @@ class Kv4Cache(_Handle):
         self._device = self.buf.get_device()
         self._scale = 1.0 / math.sqrt(self.head_dim)
         self._args = (self.buf.data_ptr(), self.n_pages, self.kv_heads, self.head_dim, self.page_size)
+        self._like = (self._device, *self._args[1:])  # what caches that a call takes together have in common
         return self._args
 
 
@@ -105,9 +106,9 @@ def _need_bytes(t: torch.Tensor, name: str, nbytes: int) -> None:
 
 
 def _need_i32(t: torch.Tensor, name: str, shape) -> None:
-    if (not t.is_cuda or t.dtype is not torch.int32 or not t.is_contiguous() or t.dim() != len(shape)
-            or any(n is not None and n != m for n, m in zip(shape, t.shape))):
-        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.shape != shape or t.dtype is not torch.int32 or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor {list(shape)}, got {t.dtype} {list(t.shape)} "
+                         f"on {t.device}")
 
 
 def _explain(name: str, t: torch.Tensor, tokens: int, heads, cache: Kv4Cache) -> None:
@@ -233,7 +234,9 @@ def kv4_tree_attention_into(q: torch.Tensor, cache: Kv4Cache, batch: Kv4Batch, t
     if out.dtype is not torch.float16 or out.shape != shape or not out.is_contiguous() or not out.is_cuda:
         _explain("out", out, batch.tokens, shape[1], cache)
         raise ValueError("out must be contiguous")
-    _need_i32(tree, "tree", (batch.tokens, None))
+    if tree.dim() != 2:
+        raise ValueError(f"tree: expected [{batch.tokens}, words], got {tuple(tree.shape)}")
+    _need_i32(tree, "tree", (batch.tokens, tree.shape[1]))
     cur = _on_device(cache, batch, ws, ("q", q), ("out", out), ("tree", tree))
     rc = (_binding._lib or _binding.load()).marlin_kv_tree_attention(
         q.data_ptr(), qs[0], qs[1], shape[1], *cached, *rows, batch.max_q, tree.data_ptr(), tree.shape[1],
@@ -301,19 +304,21 @@ def kv4_rope_append_into(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, posi
     request owns are left alone."""
     cached, rows, work = cache._args or cache._check(), batch._args or batch._check(), ws._args or ws._check()
     angles = rope._args or rope._check()
-    T = batch.tokens
-    for name, t, heads in (("q", q, None), ("k", k, cache.kv_heads), ("v", v, cache.kv_heads),
-                           ("out", out, q.shape[1] if q.dim() == 3 else None)):
-        s = t.shape
-        if (t.dtype is not torch.float16 or len(s) != 3 or s[0] != T or s[2] != cache.head_dim or (heads and s[1] != heads)
-                or t.stride(2) != 1 or not t.is_cuda):
-            _explain(name, t, T, heads, cache)
-    _need_i32(positions, "positions", (T,) if positions.dim() == 1 and rope.n_axes == 1 else (rope.n_axes, T))
-    cur = _on_device(cache, batch, ws, ("q", q), ("k", k), ("v", v), ("out", out), ("positions", positions),
-                     ("rope", rope.table))
     qs, ks, vs, os = q.stride(), k.stride(), v.stride(), out.stride()
+    T, shape, f16 = batch.tokens, q.shape, torch.float16
+    new = (T, cache.kv_heads, cache.head_dim)
+    if (k.shape != new or v.shape != new or len(shape) != 3 or shape[0] != T or shape[2] != new[2] or out.shape != shape
+            or not (q.dtype is k.dtype is v.dtype is out.dtype is f16) or not (qs[2] == ks[2] == vs[2] == os[2] == 1)
+            or not (q.is_cuda and k.is_cuda and v.is_cuda and out.is_cuda)):
+        for name, t, heads in (("q", q, None), ("k", k, new[1]), ("v", v, new[1]), ("out", out, shape[1] if len(shape) == 3 else None)):
+            _explain(name, t, T, heads, cache)
+    _need_i32(positions, "positions", (T,) if rope.n_axes == 1 and positions.dim() == 1 else (rope.n_axes, T))
+    cur = torch._C._cuda_getDevice()
+    if not (cache._device == batch._device == ws._device == rope._device == q.get_device() == k.get_device()
+            == v.get_device() == out.get_device() == positions.get_device() == cur):
+        _on_device(cache, batch, ws, ("q", q), ("k", k), ("v", v), ("out", out), ("positions", positions), ("rope", rope.table))
     rc = (_binding._lib or _binding.load()).marlin_kv_rope_append(
-        q.data_ptr(), qs[0], qs[1], q.shape[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+        q.data_ptr(), qs[0], qs[1], shape[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
         positions.data_ptr(), rope.n_axes, *angles, out.data_ptr(), os[0], os[1], *cached, *rows, work[0],
         torch._C._cuda_getCurrentRawStream(cur))
     if rc:
@@ -332,16 +337,16 @@ def kv4_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions
 
 def _layers(caches, ws: Kv4Workspace, *named):
     """The addresses of the layers' caches (one or several alike), what they share, and the current device."""
-    caches = (caches,) if isinstance(caches, Kv4Cache) else tuple(caches)
-    if not caches:
-        raise ValueError("no caches")
-    args = [c._args or c._check() for c in caches]
-    if any(a[1:] != args[0][1:] for a in args):
-        raise ValueError("the caches must be alike: pages, key heads, head_dim and page size")
+    caches = (caches,) if isinstance(caches, Kv4Cache) else caches
+    at = [(c._args or c._check())[0] for c in caches]
+    like = [c._like for c in caches]
+    if not at or like.count(like[0]) != len(at):
+        raise ValueError("no caches" if not at else
+                         "the caches must be alike: device, pages, key heads, head_dim and page size")
     cur = torch._C._cuda_getDevice()
-    if not (all(c._device == cur for c in caches) and ws._device == cur and all(t.get_device() == cur for _, t in named)):
+    if like[0][0] != cur or ws._device != cur or any(t.get_device() != cur for _, t in named):
         _on_current_device(*(("cache", c.buf) for c in caches), ("workspace", ws.buf), *named)
-    return (ctypes.c_void_p * len(args))(*(a[0] for a in args)), len(args), args[0][1:], cur
+    return array("Q", at), len(at), like[0][1:], cur
 
 
 def kv4_compact(caches, batch: Kv4Batch, index: torch.Tensor, kept: torch.Tensor, ws: Kv4Workspace,
@@ -360,12 +365,14 @@ def kv4_compact(caches, batch: Kv4Batch, index: torch.Tensor, kept: torch.Tensor
     _need_i32(kept, "kept", (B,))
     named = [("page_table", batch.page_table), ("index", index), ("kept", kept)]
     if into is not None:
-        _need_i32(into, "into", (B, None))
+        if into.dim() != 2:
+            raise ValueError(f"into: expected [{B}, pages], got {tuple(into.shape)}")
+        _need_i32(into, "into", (B, into.shape[1]))
         named.append(("into", into))
     at, count, shape, cur = _layers(caches, ws, *named)
     lengths = torch.empty((B,), dtype=torch.int32, device=index.device)
     rc = (_binding._lib or _binding.load()).marlin_kv_compact(
-        at, count, *shape, rows[0], rows[1], None if into is None else into.data_ptr(),
+        at.buffer_info()[0], count, *shape, rows[0], rows[1], None if into is None else into.data_ptr(),
         0 if into is None else into.shape[1], rows[2], rows[3], index.data_ptr(), kept.data_ptr(), lengths.data_ptr(), B,
         batch.tokens, batch.max_q, work[0], torch._C._cuda_getCurrentRawStream(cur))
     if rc:
@@ -378,11 +385,13 @@ def kv4_copy_pages(caches, src: torch.Tensor, dst: torch.Tensor, ws: Kv4Workspac
     alike); a pair whose source is negative is left out.  src, dst int32 [pairs].  A page that is written must be named
     once only, as source or destination, in a call."""
     work = ws._args or ws._check()
-    _need_i32(src, "src", (None,))
-    _need_i32(dst, "dst", (src.shape[0],))
+    if src.dim() != 1:
+        raise ValueError(f"src: expected [pairs], got {tuple(src.shape)}")
+    _need_i32(src, "src", src.shape)
+    _need_i32(dst, "dst", src.shape)
     at, count, shape, cur = _layers(caches, ws, ("src", src), ("dst", dst))
     rc = (_binding._lib or _binding.load()).marlin_kv_copy_pages(
-        at, count, *shape, src.data_ptr(), dst.data_ptr(), src.shape[0], work[0],
+        at.buffer_info()[0], count, *shape, src.data_ptr(), dst.data_ptr(), src.shape[0], work[0],
         torch._C._cuda_getCurrentRawStream(cur))
     if rc:
         raise MarlinError(rc, "marlin_kv_copy_pages")
