@@ -279,6 +279,22 @@ def test_pages_beyond_32_bits():
     assert int(cache.buf[:1 << 20].max()) == 0
 
 
+def test_more_caches_than_one_launch_takes():
+    import w4a16_mixed_precision_gb300 as w4
+    lens, nq, index = [9, 5], [6, 5], [np.array([1, 4]), np.array([0, 2, 3, 4])]
+    for other in (False, True):
+        caches, batch, ws, kv, into = filled(lens, nq, 1, 64, 16, 130, seed=11)
+        new = w4.kv4_compact(caches, batch, padded(index, nq), i32([2, 4]), ws, into=into if other else None)
+        assert w4.device_status(ws) == 0 and new.tolist() == [5, 4]
+        if not other:
+            check(caches, batch.page_table, ws, kv, lens, nq, index, [5, 4])
+        else:
+            for cache, (k, v) in zip(caches, kv):
+                got = w4.kv4_read(cache, w4.Kv4Batch(into, new, starts([2, 4]), 6, 4), ws)
+                assert np.array_equal(got[0].cpu().numpy(), k[[4, 7, 9, 11, 12, 13]])
+                assert np.array_equal(got[1].cpu().numpy(), v[[4, 7, 9, 11, 12, 13]])
+
+
 def test_on_another_stream_and_in_a_graph():
     import w4a16_mixed_precision_gb300 as w4
     lens, nq = [60, 45], [30, 17]

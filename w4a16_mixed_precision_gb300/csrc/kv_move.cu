@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(kPageThreads) kv_copy_pages_kernel(const __gri
 
 template <typename... Args>
 cudaError_t launch(void (*kernel)(Args...), long long ctas, int threads, cudaStream_t stream, Args... args) {
+  if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3((unsigned)ctas);
@@ -287,7 +288,6 @@ cudaError_t compact(const KvCompactParams& p, const KvCaches& c, cudaStream_t st
   const long long granules = ((long long)p.max_q + 15) / 16 + 1;  // at most, of a request
   if (p.into) {
     const long long ctas = (granules + kMoveWarps - 1) / kMoveWarps;
-    if (units * ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
     return launch(kv_gather_kernel<D>, units * ctas, kMoveThreads, stream, p, c, (int)ctas);
   }
   // a warp a head where few tokens can be kept (more are served by it in more rounds), else a CTA
@@ -305,7 +305,6 @@ cudaError_t launch_kv_copy_pages(const KvCaches& c, int caches, int n_pages, lon
                                  const int* dst, int pairs, int* status, cudaStream_t stream) {
   const int chunks = (int)((page_bytes + kPageChunk - 1) / kPageChunk);
   const long long ctas = (long long)chunks * caches * pairs;
-  if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
   return launch(kv_copy_pages_kernel, ctas, kPageThreads, stream, c, caches, n_pages, page_bytes, chunks, src, dst, status);
 }
 
