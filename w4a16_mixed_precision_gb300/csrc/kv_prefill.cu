@@ -56,6 +56,11 @@ constexpr int kBlock = 64;         // tokens of a block
 constexpr int kTileWarps = 4, kSoftmaxWarps = kTiles * kTileWarps, kDequantWarps = 4;
 constexpr int kThreadsP = (kSoftmaxWarps + kDequantWarps + 1) * 32;
 constexpr int kTmem = 512, kTileCols = kTmem / kTiles;  // columns, and of a tile
+// Trees: blocks whose products with V are summed in tensor memory at most; then they are added to the CTA's part of
+// the item, in fp32 rounded to nearest.  The tensor cores' sums are not: root mean square errors against 64 bits at 25
+// tokens on 100,000, 64 heads on 8, by the blocks of a piece: 3.0e-4 with 41, 3.1e-4 with 82, 3.9e-4 with 164, 6.7e-4
+// with 329 (3.0e-4 is what rounding p s and the output to fp16 leave).
+constexpr int kMostBlocks = 48;
 
 struct F2 {
   float x, y;
@@ -117,6 +122,24 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
   asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {" W4A16_PLACES32 "};" ::W4A16_R32(W4A16_IN), "r"(taddr)
                : "memory");
 #undef W4A16_IN
+}
+
+// 16 columns; the wait names the registers, so that nothing reads them before it.
+#define W4A16_R16(X) \
+  X(0), X(1), X(2), X(3), X(4), X(5), X(6), X(7), X(8), X(9), X(10), X(11), X(12), X(13), X(14), X(15)
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+#define W4A16_OUT(i) "=r"(v[i])
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : W4A16_R16(W4A16_OUT)
+      : "r"(taddr)
+      : "memory");
+#undef W4A16_OUT
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&v)[16]) {
+#define W4A16_BOTH(i) "+r"(v[i])
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : W4A16_R16(W4A16_BOTH)::"memory");
+#undef W4A16_BOTH
 }
 
 // One word of 8 codes -> c - 8 of its nibbles as fp16 pairs, exact: (0, 4),
@@ -376,7 +399,8 @@ __device__ __forceinline__ void find_item(const KvAttnParams& p, CtrlP& ctrl) {
   __syncwarp();
   const long long S = p.stripes, mean = U / S;
   const long long whole = min((items + S - 1) / S * longest, mean + longest / 2);
-  if (items <= (long long)gridDim.x && whole <= mean + (kTree ? kTreeCutCost : kCutCost) + kCutItemCost * items / S) {
+  // (a CTA beyond the stripes has no room for parts)
+  if (items <= (long long)gridDim.x && (!kTree || longest <= kMostBlocks) && whole <= mean + (kTree ? kTreeCutCost : kCutCost) + kCutItemCost * items / S) {
     if (lane == 0) ctrl.by_item = 1;
   } else if (lane == 0) {
     ctrl.start_b = -1;
@@ -556,9 +580,14 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
     int jt = 0;             // blocks of this tile so far: its places and phases
     int items = 0, cuts = 0;
     long long u = u_begin;  // first block of the piece
+    bool fresh = true, from0 = false;  // the stripe's first piece of the item; that begins with the item
+    float qsum = 0.f, R = 0.f, R_part = 0.f;  // the reference of the row, and at which the part's sums of products are
+    F2 l = dup(0.f), pz = dup(0.f);
     while (ok && at.left > 0) {
     const KvSeq seq = at.seq;
-    const int x1 = min(at.span.n, at.x + at.left), pieces = x1 - at.x;  // blocks at.x .. x1 - 1 of the item
+    const int x_all = min(at.span.n, at.x + at.left);  // the stripe's blocks of the item end there
+    const int x1 = kTree ? min(x_all, at.x + kMostBlocks) : x_all, pieces = x1 - at.x;  // blocks at.x .. x1 - 1 of the item
+    if (fresh) from0 = at.x == 0;
     const int first = seq.len - seq.nq, row = at.tile * kRows + warp * 32 + lane;
     const bool live = row < at.rows;
     const int i = live ? kv_div_group(p, row) : 0;
@@ -572,8 +601,10 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
     // row (whole lines of global memory); then every row's sum
     const int wrow = (warp % kTileWarps) * 32;  // the warp's first row of the tile
     const long long row_at = live ? (long long)(seq.q0 + i) * p.q_ts + (long long)head * p.q_hs : -1;
-    float qsum = 0.f;
-    {
+    if (kTree && !fresh) {  // it is there
+      if (lane == 0) mbar_arrive(bar(ctrl.q_full));
+    } else {
+      qsum = 0.f;
       const uint32_t qt = base + Sh::kOffQ + tile * Sh::kQ;
       constexpr int kTogether = 8;  // loads in flight
 #pragma unroll 1
@@ -605,8 +636,10 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
     }
     const F2 qs = dup(qsum);
 
-    float R = live ? kUnset : 0.f;
-    F2 l = dup(0.f), pz = dup(0.f);
+    if (!kTree || fresh) {
+      R = live ? kUnset : 0.f;
+      l = pz = dup(0.f);
+    }
     const int skipped = half_.to > half_.from ? half_.from - (at.span.lo + at.x) : 0;
     int st = (stage + skipped) % Sh::kStages;
     for (int blk = half_.from; ok && blk < half_.to; ++blk, ++jt) {
@@ -738,7 +771,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
     // ---- the rows' results, or this CTA's part of them ----
     if (!ok || !wait_warp(bar(ctrl.o_full), (uint32_t)(items & 1), wc)) break;
     tc_fence_after();
-    const bool whole = at.x == 0 && x1 == at.span.n;
+    const bool whole = (!kTree || fresh) && at.x == 0 && x1 == at.span.n;
     const float sum = l.x + l.y, off = pz.x + pz.y;
     const bool any = half_.to > half_.from;  // else there is nothing of this tile in tensor memory
     // a finished row's channels 32 part .. + 31 into Q's room, which no product of this item reads any
@@ -753,6 +786,15 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
 #pragma unroll
       for (int t = 0; t < 32; t += 8) {
         const int u = part * 4 + t / 8;
+        sts128(place(r) + ((u ^ (r & 7)) << 4), make_uint4(pack(v[t], v[t + 1]), pack(v[t + 2], v[t + 3]),
+                                                                   pack(v[t + 4], v[t + 5]), pack(v[t + 6], v[t + 7])));
+      }
+    };
+    auto keep16 = [&](int part, const float (&v)[16]) {  // channels 16 part .. + 15
+      const int r = wrow + lane;
+#pragma unroll
+      for (int t = 0; t < 16; t += 8) {
+        const int u = part * 2 + t / 8;
         sts128(place(r) + ((u ^ (r & 7)) << 4), make_uint4(pack(v[t], v[t + 1]), pack(v[t + 2], v[t + 3]),
                                                                    pack(v[t + 4], v[t + 5]), pack(v[t + 6], v[t + 7])));
       }
@@ -792,7 +834,55 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       // Channel-major, so that a warp's rows are written and read in whole lines.
       constexpr int kSlot = kRows * (D + 4);
       const int my_row = warp * 32 + lane;
-      float* slot = p.partials + (2ll * blockIdx.x + (at.x == 0 ? 1 : 0)) * kSlot + my_row;
+      float* slot = p.partials + (2ll * blockIdx.x + ((kTree ? from0 : at.x == 0) ? 1 : 0)) * kSlot + my_row;
+      if constexpr (kTree) {
+        // the part takes this piece's sums of products; after the stripe's last piece of the item the offsets, too,
+        // or it is the rows' results that come of both
+        const bool last = x1 == x_all, done = last && from0 && x1 == at.span.n;
+        const float inv = sum != 0.f ? 1.f / sum : 0.f;  // a row that sees no token is zero
+        const float f0 = fresh || R_part == kUnset ? 0.f : R_part == R ? 1.f : ex2(R_part - R), add = last ? off : 0.f;
+        const bool rescaled = !fresh && __any_sync(0xffffffffu, f0 != 1.f);
+        R_part = R;
+#pragma unroll 1
+        for (int part = 0; part < D / 16; ++part) {
+          float* at_ = slot + part * 16 * kRows;
+          float o[16];
+          uint32_t v[16];
+          tmem_ld16(lanes + Sh::kColO + part * 16, v);
+#pragma unroll
+          for (int t = 0; t < 16; ++t) o[t] = 0.f;
+          if (rescaled || (done && !fresh)) {
+#pragma unroll
+            for (int t = 0; t < 16; ++t) o[t] = __ldcg(at_ + t * kRows);
+          }
+          tmem_wait_ld16(v);
+#pragma unroll
+          for (int t = 0; t < 16; ++t)
+            o[t] = (f0 == 0.f ? 0.f : o[t] * f0) + (any ? __uint_as_float(v[t]) + add : add);
+          if (done) {
+#pragma unroll
+            for (int t = 0; t < 16; ++t) o[t] = inv == 0.f ? 0.f : o[t] * inv;
+            keep16(part, o);
+          } else if (fresh || rescaled) {
+#pragma unroll
+            for (int t = 0; t < 16; ++t) __stcg(at_ + t * kRows, o[t]);
+          } else {  // nobody else writes there, and the thread's own additions stay in order
+#pragma unroll
+            for (int t = 0; t < 16; ++t)
+              asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(at_ + t * kRows), "f"(o[t]) : "memory");
+          }
+        }
+        if (done) {
+          write_rows();
+        } else if (last) {
+          __stcg(slot + D * kRows, R);
+          __stcg(slot + (D + 1) * kRows, sum);
+          // the next kernel joins the stripes' parts
+          if (tid == 0 && from0)
+            *part_note<D>(p, blockIdx.x) = {seq.q0, at.rows, at.tile, at.h,
+                                            (int)stripe_owner(u - at.x + at.span.n - 1, U, G)};
+        }
+      } else {
 #pragma unroll 1
       for (int part = 0; part < D / 32; ++part) {
         uint32_t v[32];
@@ -803,11 +893,6 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       }
       __stcg(slot + D * kRows, R);
       __stcg(slot + (D + 1) * kRows, sum);
-      if constexpr (kTree) {  // the next kernel joins them
-        if (tid == 0 && at.x == 0)
-          *part_note<D>(p, blockIdx.x) = {seq.q0, at.rows, at.tile, at.h,
-                                          (int)stripe_owner(u - at.x + at.span.n - 1, U, G)};
-      } else {
       // all warps have written; one thread counts this CTA in, with release and acquire for all of them
       const long long s0 = u - at.x;  // the item's first block among all
       const int c0 = (int)stripe_owner(s0, U, G), c1 = (int)stripe_owner(s0 + at.span.n - 1, U, G);
@@ -865,6 +950,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
     ++items;
     stage = (stage + pieces) % Sh::kStages;
     u += pieces;
+    fresh = x1 == x_all;
     move_on<kTree>(p, at, pieces);
     }
   } else if (warp < kSoftmaxWarps + kDequantWarps) {
@@ -1024,7 +1110,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       mma_commit_elect(bar(ctrl.s_full[t][i & 1]));
     };
     while (ok && at.left > 0) {
-      const int pieces = min(at.span.n - at.x, at.left), blk0 = at.span.lo + at.x, end = blk0 + pieces;
+      const int pieces = min(min(at.span.n - at.x, at.left), kTree ? kMostBlocks : at.left);
+      const int blk0 = at.span.lo + at.x, end = blk0 + pieces;
       Half half_[kTiles];
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) half_[t] = tile_half<kTree>(p, at, t, blk0, end);
