@@ -60,7 +60,7 @@ constexpr int kTmem = 512, kTileCols = kTmem / kTiles;  // columns, and of a til
 // the item, in fp32 rounded to nearest.  The tensor cores' sums are not: root mean square errors against 64 bits at 25
 // tokens on 100,000, 64 heads on 8, by the blocks of a piece: 3.0e-4 with 41, 3.1e-4 with 82, 3.9e-4 with 164, 6.7e-4
 // with 329 (3.0e-4 is what rounding p s and the output to fp16 leave).
-constexpr int kMostBlocks = 48;
+constexpr int kMostBlocks = 56;
 
 struct F2 {
   float x, y;
