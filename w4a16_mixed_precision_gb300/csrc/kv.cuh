@@ -205,14 +205,14 @@ struct KvRopeParams {
   uint16_t* q_out;
   long long q_ts, q_hs, o_ts, o_hs, k_ts, k_hs, v_ts, v_hs;  // elements
   int heads;
-  int run;                    // steps of several heads that a warp takes (filled in by launch_kv_rope_append)
+  long long warps;            // that share the work (filled in by launch_kv_rope_append)
   const int* positions;       // [axes][T]
   const float* table;         // [table_rows][rot / 2] of (cos, sin)
   int axes, table_rows, rot;
   int grouped;                // the pairs of every D / 32 consecutive ones share an axis
   unsigned long long axis[2];  // two bits a pair
 };
-cudaError_t launch_kv_rope_append(const KvRopeParams& p, int D, bool interleaved, cudaStream_t stream);
+cudaError_t launch_kv_rope_append(const KvRopeParams& p, int D, bool interleaved, int sms, cudaStream_t stream);
 
 // ---- trees, compaction, page copies (kv_tree.cu, kv_move.cu) ----
 cudaError_t launch_kv_tree(const KvParams& p, const int* parents, int words, int* mask, int* positions, cudaStream_t stream);

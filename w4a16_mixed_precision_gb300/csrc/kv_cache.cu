@@ -261,15 +261,16 @@ cudaError_t launch_copy(const KvParams& p, uint16_t* k, uint16_t* v, const long 
 // entry for the pair at the position of its axis: products and sums rounded to fp32 one by one, the
 // result to fp16.  Queries go to q_out; keys, and values as they are, into the cache like above.
 //
-// Bound: the stream, 4 D bytes a query head, 4 D + 2 (D/2 + 4) a key head and token.  A warp takes four
-// tokens like above, eight lanes each, and a run of their heads, 1 KB of a token at a time: four query heads of
-// 128 channels, or two key heads with their values.  What the tokens need (their request, place, positions, cosines and sines,
-// a chain of loads) is found once, under the first vectors' loads, and kept in registers.  A lane holds two
+// Bound: the stream, 4 D bytes a query head, 4 D + 2 (D/2 + 4) a key head and token.  The work is steps: four
+// tokens like above, eight lanes each, and 1 KB of each: four query heads of 128 channels, or two key heads
+// with their values.  Every warp takes an equal run of all steps, in the order of the tokens: what these need
+// (their request, place, positions, cosines and sines, a chain of loads) is found once for the steps of the
+// same tokens, under the first vectors' loads, and kept in registers.  A lane holds two
 // chunks of D/16 channels, such that both channels of its pairs are its own: chunks g and g + rot/2 of the
 // rotated ones, two neighbours of the rest.
 template <int D>
 constexpr int kVectors = 512 / D;  // together
-constexpr long long kFullCard = 3700;  // warps: about one load of the card
+constexpr int kRopeCtas = 3;  // of an SM
 
 template <int N>  // 4-byte words
 __device__ __forceinline__ void load_chunk(const uint16_t* at, uint32_t* x) {
@@ -316,31 +317,35 @@ __device__ __forceinline__ void rotate_chunks(uint32_t (&x)[CH], const float2 (&
 }
 
 template <int D, bool kInterleaved>
-__global__ void __launch_bounds__(kKvThreads, 3) kv_rope_append_kernel(const KvRopeParams p) {
+__global__ void __launch_bounds__(kKvThreads, kRopeCtas) kv_rope_append_kernel(const KvRopeParams p) {
   if (threadIdx.x == 0) griddep_launch_dependents();
   griddep_wait();
   constexpr int CH = D / 16;  // channels of a chunk, pairs of a lane
   constexpr int kVec = kVectors<D>;
   const int lane = threadIdx.x & 31, g = lane & 7, mine = lane >> 3;
   const int q_steps = (p.heads + kVec - 1) / kVec, steps = q_steps + (2 * p.kv.hkv + kVec - 1) / kVec;
-  const int runs = (steps + p.run - 1) / p.run;
+  const long long all = ((long long)p.kv.T + kTokens - 1) / kTokens * steps;
   const long long warp = (long long)blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5);
-  const long long tile = warp / runs;
-  const int first = (int)(warp - tile * runs) * p.run, last = min(first + p.run, steps);
-  const bool live = tile * kTokens + mine < p.kv.T;
-  if (tile * kTokens >= p.kv.T) return;
-  const int t = live ? (int)(tile * kTokens) + mine : 0;
+  if (warp >= p.warps) return;
+  const long long begin = stripe_begin(warp, all, p.warps), end = stripe_begin(warp + 1, all, p.warps);
+  long long tile = begin / steps;
+  int step = (int)(begin - tile * steps);
 
   const int half = p.rot / (2 * CH);  // chunks that hold the pairs' first channels (or half of the pairs)
   const bool rotated = g < half;
   const int ca = (rotated ? g : 2 * half + 2 * (g - half)) * CH, cb = rotated ? ca + half * CH : ca + CH;
-  const uint16_t *q = p.q + t * p.q_ts, *k = p.k + t * p.k_ts, *v = p.v + t * p.v_ts + g * (D / 8);
-
+  int t = 0;
+  bool live = false, fresh = true;  // whether there is a token; whether its places and angles are to be found
   bool mine_ok = false;
   uint8_t* base = nullptr;  // the token's granule of key head 0
   int in = 0;
   float2 cs[CH];
-  for (int step = first; step < last; ++step) {
+  for (long long at = begin; at < end; ++at) {
+    if (fresh) {
+      live = tile * kTokens + mine < p.kv.T;
+      t = live ? (int)(tile * kTokens) + mine : 0;
+    }
+    const uint16_t *q = p.q + t * p.q_ts, *k = p.k + t * p.k_ts, *v = p.v + t * p.v_ts + g * (D / 8);
     const bool keys = step >= q_steps;
     const int h = keys ? (step - q_steps) * (kVec / 2) : step * kVec;
     const int count = min(kVec, keys ? 2 * (p.kv.hkv - h) : p.heads - h);
@@ -360,7 +365,8 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv_rope_append_kernel(const KvR
         load_chunk<CH / 2>(from + cb, x[i] + CH / 2);
       }
     }
-    if (step == first) {
+    if (fresh) {
+      fresh = false;
       const int b = kv_owner(p.kv, t);
       const KvSeq s = kv_seq(p.kv, b, true);
       mine_ok = live && t >= s.q0 && t < s.q0 + s.nq;
@@ -402,7 +408,13 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv_rope_append_kernel(const KvR
           }
         }
       }
-      if (last > q_steps) base = mine_ok ? kv_place_of<D>(p.kv, t, b, s, 0, &in) : nullptr;
+      base = nullptr;
+      if (mine_ok && step + (end - at) > q_steps) base = kv_place_of<D>(p.kv, t, b, s, 0, &in);
+    }
+    if (++step == steps) {
+      step = 0;
+      ++tile;
+      fresh = true;
     }
     if (!keys) {
       if (!mine_ok) continue;
@@ -424,10 +436,10 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv_rope_append_kernel(const KvR
       __half ks, ko, vs, vo;
       quantise<2 * CH>(x[i], kc, ks, ko);
       quantise<2 * CH>(x[i + 1], vc, vs, vo);
-      uint8_t* at = base ? base + (h + i / 2) * p.kv.head_bytes : nullptr;
-      put_values<D>(at, in, vc, lane);
-      if (!at) continue;
-      uint8_t* krow = at + in * (D / 2);
+      uint8_t* to = base ? base + (h + i / 2) * p.kv.head_bytes : nullptr;
+      put_values<D>(to, in, vc, lane);
+      if (!to) continue;
+      uint8_t* krow = to + in * (D / 2);
       if constexpr (D == 128) {
         *reinterpret_cast<uint32_t*>(krow + ca / 2) = kc[0];
         *reinterpret_cast<uint32_t*>(krow + cb / 2) = kc[1];
@@ -435,23 +447,24 @@ __global__ void __launch_bounds__(kKvThreads, 3) kv_rope_append_kernel(const KvR
         *reinterpret_cast<uint16_t*>(krow + ca / 2) = (uint16_t)kc[0];
         *reinterpret_cast<uint16_t*>(krow + cb / 2) = (uint16_t)(kc[0] >> 16);
       }
-      if (g == 0) *reinterpret_cast<uint2*>(at + 16 * D + 8 * in) = make_uint2(pair_bits(ks, ko), pair_bits(vs, vo));
+      if (g == 0) *reinterpret_cast<uint2*>(to + 16 * D + 8 * in) = make_uint2(pair_bits(ks, ko), pair_bits(vs, vo));
     }
   }
 }
 
 template <int D, bool kInterleaved>
-cudaError_t launch_rope(const KvRopeParams& p, cudaStream_t stream) {
-  const long long tiles = ((long long)p.kv.T + kTokens - 1) / kTokens;
+cudaError_t launch_rope(const KvRopeParams& p, int sms, cudaStream_t stream) {
   constexpr int kVec = kVectors<D>;
   const int steps = (p.heads + kVec - 1) / kVec + (2 * p.kv.hkv + kVec - 1) / kVec;
   KvRopeParams f = p;
-  f.run = (int)std::min<long long>(steps, std::max<long long>(1, tiles * steps / kFullCard));
-  const long long warps = tiles * ((steps + f.run - 1) / f.run);
+  // as many warps as are on the card at a time; a step each, up to twice as many (1290 tokens, 32 heads on 8: 13.7
+  // against 14.9 us with the read back)
+  const long long all = ((long long)p.kv.T + kTokens - 1) / kTokens * steps, full = (long long)sms * kRopeCtas * (kKvThreads / 32);
+  f.warps = all <= 2 * full ? all : full;
   constexpr int per = kKvThreads / 32;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3((unsigned)((warps + per - 1) / per));
+  cfg.gridDim = dim3((unsigned)((f.warps + per - 1) / per));
   cfg.blockDim = dim3(kKvThreads);
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -463,9 +476,9 @@ cudaError_t launch_rope(const KvRopeParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_kv_rope_append(const KvRopeParams& p, int D, bool interleaved, cudaStream_t stream) {
-  if (D == 128) return interleaved ? launch_rope<128, true>(p, stream) : launch_rope<128, false>(p, stream);
-  return interleaved ? launch_rope<64, true>(p, stream) : launch_rope<64, false>(p, stream);
+cudaError_t launch_kv_rope_append(const KvRopeParams& p, int D, bool interleaved, int sms, cudaStream_t stream) {
+  if (D == 128) return interleaved ? launch_rope<128, true>(p, sms, stream) : launch_rope<128, false>(p, sms, stream);
+  return interleaved ? launch_rope<64, true>(p, sms, stream) : launch_rope<64, false>(p, sms, stream);
 }
 
 cudaError_t launch_kv_append(const KvParams& p, int D, const uint16_t* k, const uint16_t* v, const long long (&st)[4],

@@ -435,7 +435,9 @@ marlin_status_t marlin_kv_rope_append(const uint16_t* q, int64_t q_token_stride,
   p.table = table;
   p.table_rows = table_rows;
   p.rot = rot;
-  return launch_kv_rope_append(p, head_dim, interleaved != 0, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  int sms;
+  if (const marlin_status_t c = current_sms(&sms)) return c;
+  return launch_kv_rope_append(p, head_dim, interleaved != 0, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MARLIN_OK
              : MARLIN_ERR_CUDA;
 }
