@@ -265,9 +265,11 @@ cudaError_t launch_copy(const KvParams& p, uint16_t* k, uint16_t* v, const long 
 // tokens like above, eight lanes each, and 1 KB of each: four query heads of 128 channels, or two key heads
 // with their values.  Every warp takes an equal run of all steps, in the order of the tokens: what these need
 // (their request, place, positions, cosines and sines, a chain of loads) is found once for the steps of the
-// same tokens, under the first vectors' loads, and kept in registers.  A lane holds two
-// chunks of D/16 channels, such that both channels of its pairs are its own: chunks g and g + rot/2 of the
-// rotated ones, two neighbours of the rest.
+// same tokens, under the first vectors' loads, and kept in registers.  A lane holds two chunks of D/16
+// channels, such that both channels of its pairs are its own: chunks g and g + rot/2 of the rotated ones, two
+// neighbours of the rest.
+// Measured: 9880 tokens, 32 heads on 8 of 128 channels, three axes, 40.9 us, 5.3 TB/s (79% of the card's copy
+// rate; the append alone takes 15.2); 208 tokens, 64 heads on 8, 6.0 us.
 template <int D>
 constexpr int kVectors = 512 / D;  // together
 constexpr int kRopeCtas = 3;  // of an SM

@@ -19,7 +19,9 @@ namespace {
 // rounds of W granules, loads before stores: index[i] ascends, so no round reads what one before has
 // written, and a barrier between a round's loads and stores keeps it from overwriting what is still read.
 // (Where tokens come from is the same for every head of every cache; warps that moved several heads, to find it
-// once, were up to 15% slower.)
+// once, were up to 15% slower.)  A kept token's values share their 32-byte sectors with up to 15 others, so that
+// more is read than kept.  Measured with 8 heads of 128 channels: 5 tokens of each of 40 requests in 32 caches
+// 11.3 us (7 MB kept, 34 read); 38,668 of 76,825 tokens into other pages 26.3 us, 84 MB out and in, 3.2 TB/s.
 constexpr int kMoveThreads = 256, kMoveWarps = kMoveThreads / 32;
 
 // What warps read of a request, checked.
@@ -237,7 +239,8 @@ __global__ void __launch_bounds__(kMoveThreads) kv_gather_kernel(const KvCompact
 
 // ---- pages -------------------------------------------------------------------------------------------
 // Bound: the stream, a page's bytes in and out for every pair and cache.  A CTA copies 16 KB, four loads
-// of 16 bytes in flight a thread.
+// of 16 bytes in flight a thread.  Measured: 45 pages of 70 KB in 32 caches 31.3 us, 6.4 TB/s (94% of the card's
+// copy rate); one page in 32 caches 2.2 us.
 constexpr int kPageThreads = 256, kPageVecs = 4, kPageChunk = kPageThreads * kPageVecs * 16;
 
 __global__ void __launch_bounds__(kPageThreads) kv_copy_pages_kernel(const __grid_constant__ KvCaches caches, int n_caches,
