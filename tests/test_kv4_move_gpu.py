@@ -132,6 +132,16 @@ def test_gathers_tokens_into_other_pages(lens, nq, hkv, D, page, layers):
     assert w4.device_status(ws) == 0
 
 
+@pytest.mark.parametrize("lens,nq,hkv,D,page,layers", [
+    ([1990, 27, 1201, 0, 64], [1985, 7, 1200, 0, 64], 5, 64, 16, 7),   # 4 of 35 heads together, across the caches' ends
+    ([4000, 133, 1600], [4000, 33, 1590], 3, 128, 64, 17),             # 7 of 51
+    ([300] * 50, [290] * 50, 4, 128, 48, 5),                           # 4 of 20
+])
+def test_gathers_several_heads_together(lens, nq, hkv, D, page, layers):
+    """With so much to move that a warp takes several heads (on 152 SMs as many as said)."""
+    test_gathers_tokens_into_other_pages(lens, nq, hkv, D, page, layers)
+
+
 def test_bytes_that_are_not_named_stay():
     """In a cache of random bytes nothing but the kept positions' entries changes."""
     import w4a16_mixed_precision_gb300 as w4

@@ -229,7 +229,7 @@ struct KvCompactParams {
   int* new_lens;        // nullptr where another launch writes them
   int max_q;
 };
-cudaError_t launch_kv_compact(const KvCompactParams& p, const KvCaches& c, int D, cudaStream_t stream);
+cudaError_t launch_kv_compact(const KvCompactParams& p, const KvCaches& c, int D, int sms, cudaStream_t stream);
 cudaError_t launch_kv_copy_pages(const KvCaches& c, int caches, int n_pages, long long page_bytes, const int* src,
                                  const int* dst, int pairs, int* status, cudaStream_t stream);
 // Warps of a CTA at most, and floats of a part in the workspace at most (16 rows).

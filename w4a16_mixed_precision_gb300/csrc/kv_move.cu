@@ -1,6 +1,8 @@
 // kv_move.cu -- moving what the caches of a model's layers hold: the kept ones of a request's new tokens
 // together (after a tree of drafted tokens was verified, or to drop tokens of a long context), and whole
 // pages.  One launch serves the caches of all layers, which share pages, lengths and indexes.
+#include <algorithm>
+
 #include "kv.cuh"
 
 namespace w4a16 {
@@ -18,10 +20,13 @@ namespace {
 // each (kv.cuh).  Where the kept tokens stay in their pages, W warps (a unit) take a request's head in
 // rounds of W granules, loads before stores: index[i] ascends, so no round reads what one before has
 // written, and a barrier between a round's loads and stores keeps it from overwriting what is still read.
-// (Where tokens come from is the same for every head of every cache; warps that moved several heads, to find it
-// once, were up to 15% slower.)  A kept token's values share their 32-byte sectors with up to 15 others, so that
-// more is read than kept.  Measured with 8 heads of 128 channels: 5 tokens of each of 40 requests in 32 caches
-// 11.3 us (7 MB kept, 34 read); 38,668 of 76,825 tokens into other pages 26.3 us, 84 MB out and in, 3.2 TB/s.
+// Where tokens come from is the same for every head of every cache.  Where they go to other pages and there is
+// work for every warp, a warp finds it once for up to 8 heads, two of them in flight: 38,668 of 76,825 tokens, 8 heads
+// of 128 channels, 20 us (84 MB out and in, 4.2 TB/s); 23 with one in flight, 26 a head a warp, 27 with four in flight
+// (their registers leave fewer warps).  Of few tokens a head a warp is faster: 500 of 2 requests 5 against 8 us, and
+// in place, where warps that moved several were up to 15% slower.  A kept token's values share their 32-byte
+// sectors with up to 15 others, so that more is read than kept: 5 tokens of each of 40 requests in place, in 32 caches,
+// 11 us (7 MB kept, 34 read).
 constexpr int kMoveThreads = 256, kMoveWarps = kMoveThreads / 32;
 
 // What warps read of a request, checked.
@@ -119,21 +124,29 @@ struct Granule {
   uint32_t live;  // tokens that are written
 };
 
+// Where a lane's pieces of a granule come from, offsets from the beginning of a head.
 template <int D>
-__device__ __forceinline__ void load_granule(const uint8_t* head, const Plan& m, Granule<D>& r) {
-  constexpr int PK = D / 32;  // 16-byte pieces of a token's keys
+struct Source {
+  static constexpr int PK = D / 32;  // 16-byte pieces of a token's keys
+  long long k[D / 64], v[2][2], s;
+  uint32_t pick[2];  // which halves of the two tokens' words
+  uint32_t live;     // tokens that are written
+};
+
+template <int D>
+__device__ __forceinline__ Source<D> source_of(const Plan& m) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  r.live = __ballot_sync(0xffffffffu, m.from >= 0 && m.to >= 0);
+  Source<D> o;
+  o.live = __ballot_sync(0xffffffffu, m.from >= 0 && m.to >= 0);
 #pragma unroll
-  for (int j = 0; j < Granule<D>::NK; ++j) {
-    const int piece = j * 32 + lane, s = piece / PK;
+  for (int j = 0; j < D / 64; ++j) {
+    const int piece = j * 32 + lane, s = piece / o.PK;
     const long long from = __shfl_sync(0xffffffffu, m.from, s);
     const int tok = __shfl_sync(0xffffffffu, m.tok, s);
-    if ((r.live >> s) & 1u) r.k[j] = *reinterpret_cast<const uint4*>(head + from + tok * (D / 2) + (piece % PK) * 16);
+    o.k[j] = from + tok * (D / 2) + (piece % o.PK) * 16;
   }
 #pragma unroll
   for (int hf = 0; hf < 2; ++hf) {
-    uint32_t w[2][Granule<D>::CW];
     int odd[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -141,16 +154,34 @@ __device__ __forceinline__ void load_granule(const uint8_t* head, const Plan& m,
       const long long from = __shfl_sync(0xffffffffu, m.from, s);
       const int tok = __shfl_sync(0xffffffffu, m.tok, s);
       odd[e] = tok & 1;
+      o.v[hf][e] = from + 8 * D + (tok >> 3) * (4 * D) + (4 * g + ((tok & 7) >> 1)) * (D / 8);
+    }
+    o.pick[hf] = (odd[0] ? 0x32u : 0x10u) | (odd[1] ? 0x7600u : 0x5400u);
+  }
+  o.s = m.from + 16 * D + 8 * m.tok;
+  return o;
+}
+
+template <int D>
+__device__ __forceinline__ void load_granule(const uint8_t* head, const Source<D>& o, Granule<D>& r) {
+  const int lane = threadIdx.x & 31, c = lane & 3;
+  r.live = o.live;
+#pragma unroll
+  for (int j = 0; j < Granule<D>::NK; ++j)
+    if ((o.live >> ((j * 32 + lane) / o.PK)) & 1u) r.k[j] = *reinterpret_cast<const uint4*>(head + o.k[j]);
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    uint32_t w[2][Granule<D>::CW];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
 #pragma unroll
       for (int i = 0; i < Granule<D>::CW; ++i) w[e][i] = 0u;
-      if ((r.live >> s) & 1u)
-        get_words<Granule<D>::CW>(head + from + 8 * D + (tok >> 3) * (4 * D) + (4 * g + ((tok & 7) >> 1)) * (D / 8), w[e]);
+      if ((o.live >> (8 * hf + 2 * c + e)) & 1u) get_words<Granule<D>::CW>(head + o.v[hf][e], w[e]);
     }
-    const uint32_t pick = (odd[0] ? 0x32u : 0x10u) | (odd[1] ? 0x7600u : 0x5400u);
 #pragma unroll
-    for (int i = 0; i < Granule<D>::CW; ++i) r.v[hf][i] = __byte_perm(w[0][i], w[1][i], pick);
+    for (int i = 0; i < Granule<D>::CW; ++i) r.v[hf][i] = __byte_perm(w[0][i], w[1][i], o.pick[hf]);
   }
-  if (lane < 16 && ((r.live >> lane) & 1u)) r.s = *reinterpret_cast<const uint2*>(head + m.from + 16 * D + 8 * m.tok);
+  if (lane < 16 && ((o.live >> lane) & 1u)) r.s = *reinterpret_cast<const uint2*>(head + o.s);
 }
 
 template <int D>
@@ -207,7 +238,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const KvCompac
     Plan m{-1, -1, 0};
     if (granule < g_end) {
       m = plan_granule<D>(p, k, b, granule);
-      load_granule<D>(head, m, r);
+      load_granule<D>(head, source_of<D>(m), r);
     }
     if constexpr (W == 1) __syncwarp();
     else asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / W), "n"(W * 32) : "memory");
@@ -215,25 +246,42 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const KvCompac
   }
 }
 
-// The kept tokens go to other pages: every granule of a head is a warp's.
-template <int D>
+// The kept tokens go to other pages: a warp has granules of `run` of all caches' heads, H in flight.
+constexpr int kMostHeads = 8;
+
+template <int D, int H>
 __global__ void __launch_bounds__(kMoveThreads) kv_gather_kernel(const KvCompactParams p, const __grid_constant__ KvCaches caches,
-                                                                 int ctas) {
+                                                                 int ctas, int run) {
   if (threadIdx.x == 0) griddep_launch_dependents();
   griddep_wait();
-  const int x = blockIdx.x % ctas, unit = blockIdx.x / ctas;  // of a head's CTAs
-  const int heads = p.caches * p.kv.hkv, b = unit / heads, at = unit - b * heads, cache = at / p.kv.hkv;
+  const int x = blockIdx.x % ctas, unit = blockIdx.x / ctas;  // of a run's CTAs
+  const int heads = p.caches * p.kv.hkv, runs = (heads + run - 1) / run, b = unit / runs, at = (unit - b * runs) * run;
   const bool speaks = at == 0 && x == 0 && threadIdx.x == 0;
   const Kept k = kept_of(p, b, speaks);
   if (speaks && p.new_lens) p.new_lens[b] = k.kept < 0 ? p.kv.lens[b] : k.first + k.kept;
   if (k.kept <= 0) return;
-  uint8_t* head = caches.at[cache] + (at - cache * p.kv.hkv) * p.kv.head_bytes;
-  const int g_end = (k.first + k.kept + 15) >> 4;
+  const int g_end = (k.first + k.kept + 15) >> 4, first_cache = at / p.kv.hkv, first_head = at - first_cache * p.kv.hkv;
   for (int granule = (k.first >> 4) + x * kMoveWarps + (threadIdx.x >> 5); granule < g_end; granule += ctas * kMoveWarps) {
     const Plan m = plan_granule<D>(p, k, b, granule);
-    Granule<D> r;
-    load_granule<D>(head, m, r);
-    store_granule<D>(head, m.to, r);
+    const Source<D> o = source_of<D>(m);
+    int cache = first_cache, h = first_head;
+    for (int left = min(run, heads - at); left > 0; left -= H) {
+      uint8_t* head[H];
+      Granule<D> r[H];
+#pragma unroll
+      for (int i = 0; i < H; ++i)
+        if (i < left) {
+          head[i] = caches.at[cache] + h * p.kv.head_bytes;
+          load_granule<D>(head[i], o, r[i]);
+          if (++h == p.kv.hkv) {
+            h = 0;
+            ++cache;
+          }
+        }
+#pragma unroll
+      for (int i = 0; i < H; ++i)
+        if (i < left) store_granule<D>(head[i], m.to, r[i]);
+    }
   }
 }
 
@@ -286,12 +334,16 @@ cudaError_t launch(void (*kernel)(Args...), long long ctas, int threads, cudaStr
 }
 
 template <int D>
-cudaError_t compact(const KvCompactParams& p, const KvCaches& c, cudaStream_t stream) {
+cudaError_t compact(const KvCompactParams& p, const KvCaches& c, int sms, cudaStream_t stream) {
   const long long units = (long long)p.kv.B * p.caches * p.kv.hkv;
   const long long granules = ((long long)p.max_q + 15) / 16 + 1;  // at most, of a request
   if (p.into) {
     const long long ctas = (granules + kMoveWarps - 1) / kMoveWarps;
-    return launch(kv_gather_kernel<D>, units * ctas, kMoveThreads, stream, p, c, (int)ctas);
+    const int heads = p.caches * p.kv.hkv;
+    // 32 warps an SM at least, as many as fit where a head is a warp's
+    const int run = (int)std::min<long long>(std::max<long long>(units * granules / (32ll * sms), 1), kMostHeads);
+    return launch(run == 1 ? kv_gather_kernel<D, 1> : kv_gather_kernel<D, 2>, p.kv.B * ((heads + run - 1ll) / run) * ctas,
+                  kMoveThreads, stream, p, c, (int)ctas, run);
   }
   // a warp a head where few tokens can be kept (more are served by it in more rounds), else a CTA
   if (granules <= 16) return launch(kv_compact_kernel<D, 1>, (units + kMoveWarps - 1) / kMoveWarps, kMoveThreads, stream, p, c);
@@ -300,8 +352,8 @@ cudaError_t compact(const KvCompactParams& p, const KvCaches& c, cudaStream_t st
 
 }  // namespace
 
-cudaError_t launch_kv_compact(const KvCompactParams& p, const KvCaches& c, int D, cudaStream_t stream) {
-  return D == 128 ? compact<128>(p, c, stream) : compact<64>(p, c, stream);
+cudaError_t launch_kv_compact(const KvCompactParams& p, const KvCaches& c, int D, int sms, cudaStream_t stream) {
+  return D == 128 ? compact<128>(p, c, sms, stream) : compact<64>(p, c, sms, stream);
 }
 
 cudaError_t launch_kv_copy_pages(const KvCaches& c, int caches, int n_pages, long long page_bytes, const int* src,

@@ -472,11 +472,13 @@ marlin_status_t marlin_kv_compact(void* const* caches, int count, int n_pages, i
   p.index = index;
   p.kept = kept;
   p.max_q = std::min(max_q, tokens);
+  int sms;
+  if (const marlin_status_t c = current_sms(&sms)) return c;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return for_caches(caches, count, [&](const KvCaches& c, int n, int c0) {
     p.caches = n;
     p.new_lens = c0 == 0 ? new_lengths : nullptr;
-    return launch_kv_compact(p, c, head_dim, st);
+    return launch_kv_compact(p, c, head_dim, sms, st);
   });
 }
 
