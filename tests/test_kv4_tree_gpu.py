@@ -115,6 +115,18 @@ def test_tree_attention(lens, nq, hq, hkv, D, page, window):
     check(y, q, k, v, lens, nq, see, D, window)
 
 
+@pytest.mark.parametrize("lens,nq,hq,hkv,D,page,window", [
+    ([5000] + [70 + i for i in range(30)], [3] * 31, 24, 8, 64, 16, 0),        # a long cut one and many short
+    ([70 + i for i in range(30)] + [5000], [2] * 31, 24, 8, 128, 32, 0),
+    ([900 + 131 * i for i in range(24)], [5] * 24, 24, 8, 64, 16, 700),
+    ([3000, 4, 5, 2000, 6, 900], [2, 4, 5, 1, 6, 3], 6, 3, 128, 64, 0),         # fewer blocks than warps
+    ([65, 129, 700], [1, 1, 1], 2, 2, 64, 16, 0),
+    ([10 + i * 61 % 2500 for i in range(100)], [1 + i % 4 for i in range(100)], 4, 2, 64, 48, 0),
+])
+def test_shares_that_begin_and_end_anywhere(lens, nq, hq, hkv, D, page, window):
+    test_tree_attention(lens, nq, hq, hkv, D, page, window)
+
+
 ANY = [([300, 40], [20, 40], 4, 2, 128, 16, 0), ([70, 66], [70, 66], 8, 1, 128, 64, 0), ([30, 5], [30, 5], 2, 2, 64, 32, 0),
        ([260], [100], 4, 1, 64, 16, 30), ([4000, 100], [33, 100], 8, 1, 64, 128, 0)]
 

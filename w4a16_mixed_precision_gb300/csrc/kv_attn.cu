@@ -139,7 +139,7 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 // W warps; blocks of GB granules, GI of them taken together; S blocks in a warp's ring.
 // kT: the new tokens are trees: blocks that hold some of them, or where a window begins, take their masks from the
 // rows' bits (kv.cuh).  Measured: a tree of 8 on 692 tokens, 32 heads of 128 channels, 10.6 us; 24 of 5, window
-// 2048, 24 heads on 8 of 64 channels, 29 us.
+// 2048, 24 heads on 8 of 64 channels, 27 us.
 template <int D, int NB, bool kT>
 struct Shape {
   static constexpr bool kTree = kT;
@@ -151,6 +151,11 @@ struct Shape {
   static constexpr int BB = GB * GR;            // bytes of a block
   static constexpr int kOStride = D + 4;        // floats of a row of a part in shared memory
   static constexpr int kPart = RB * (kOStride + 2) * 4;  // rows, then (maximum, sum) of each
+  // Units that a segment's start counts for beside its blocks where the work is cut into equal shares: the queries,
+  // the masks where a window begins and new tokens are, the parts.  Of trees alone: measured with 15 rows a key head
+  // of 64 channels, window 2048, 20 requests 23.7 us, 26.5 without, 24 26.6 / 28.8, 38 34.6 / 36.0, 100 70.1 / 70.1;
+  // 20 trees of 8 on 692 tokens, 32 heads of 128 channels, 26.8 / 29.3; 24 of 5 on 500 16.0 / 15.6 (finding the shares).
+  static constexpr int kStart = kTree ? 3 : 0;
   static constexpr int kRing = 3 * 1024;          // after the control block
   static constexpr int kSmem = kRing + W * S * BB;
   static_assert(kPart <= S * BB && kPart % 16 == 0, "a part has to fit a warp's ring");
@@ -187,11 +192,11 @@ struct Cursor {
   SeqWork w;
 };
 
-template <typename Sh>
+template <typename Sh, int kStart = 0>
 __device__ __forceinline__ void advance(const KvAttnParams& p, Cursor& c, int by) {
   c.g += by;
-  while (c.g >= c.w.n) {
-    c.g -= c.w.n;
+  while (c.g >= c.w.n + kStart) {
+    c.g -= c.w.n + kStart;
     if (++c.seg == p.kv.hkv * c.w.rbs) {
       c.seg = 0;
       do {
@@ -294,7 +299,7 @@ __global__ void __launch_bounds__(Shape<D, NB, kTree>::W * 32, 1) kv_attn_kernel
   for (int b = b0; b < b1; ++b) {
     const SeqWork w = seq_work<Sh>(p, b, blockIdx.x == 0);
     const long long segs = (long long)p.kv.hkv * w.rbs;
-    mine += segs * w.n;
+    mine += segs * (w.n + Sh::kStart);
     mine_segs += segs;
     if (segs) longest = max(longest, w.n);
   }
@@ -334,11 +339,11 @@ __global__ void __launch_bounds__(Shape<D, NB, kTree>::W * 32, 1) kv_attn_kernel
   // against 12.2 us, 64 of 65 (9, 3) 23.4 against 18.7; 256 of 4 blocks (4, 1) 13.7
   // against 14.9, 1536 of 2 (4, 3) 16.4 against 23.5.
   constexpr int kCutSeg = NB == 1 ? 2 : 1, kCutWarp = NB == 1 ? 4 : 2;
-  const long long warps = (long long)gridDim.x * W, even = (U + warps - 1) / warps;
+  const long long warps = (long long)gridDim.x * W, even = (U - segs * Sh::kStart + warps - 1) / warps;
   const bool by_seg = segs <= (long long)gridDim.x && (longest + W - 1) / W <= even + kCutSeg;
   const bool by_warp = segs > (long long)gridDim.x && (segs + warps - 1) / warps * longest <= even + kCutWarp;
   const bool uncut = by_seg || by_warp;
-  // otherwise an equal share of all blocks for every warp, at least one
+  // otherwise an equal share of all units for every warp, at least one
   const long long G = by_seg ? segs : by_warp ? gridDim.x : min((long long)gridDim.x, (U + W - 1) / W);
   if (blockIdx.x >= G) return;
   const long long u_cta = begin_of(blockIdx.x, U, G);
@@ -349,7 +354,7 @@ __global__ void __launch_bounds__(Shape<D, NB, kTree>::W * 32, 1) kv_attn_kernel
       long long off = at - from;
       for (int b = b0; b < b1; ++b) {
         const SeqWork w = seq_work<Sh>(p, b, false);
-        const long long n = (long long)p.kv.hkv * w.rbs * (uncut ? 1 : w.n);
+        const long long n = (long long)p.kv.hkv * w.rbs * (uncut ? 1 : w.n + Sh::kStart);
         if (off < n) {
           ctrl->start_b = b;
           ctrl->start_w = w;
@@ -365,10 +370,11 @@ __global__ void __launch_bounds__(Shape<D, NB, kTree>::W * 32, 1) kv_attn_kernel
   cur.b = ctrl->start_b;
   cur.w = ctrl->start_w;
   const long long start_off = ctrl->start_off;
-  cur.seg = start_off < (1ll << 32) ? (int)((uint32_t)start_off / (uint32_t)cur.w.n) : (int)(start_off / cur.w.n);
-  cur.g = (int)(start_off - (long long)cur.seg * cur.w.n);
+  const int weight = cur.w.n + (uncut ? 0 : Sh::kStart);
+  cur.seg = start_off < (1ll << 32) ? (int)((uint32_t)start_off / (uint32_t)weight) : (int)(start_off / weight);
+  cur.g = (int)(start_off - (long long)cur.seg * weight);
   int total;           // this warp's blocks
-  long long from = 0;  // and the first of them
+  long long from = 0;  // and the first of them; of trees' equal shares: the first unit of its first segment
   if (by_seg) {
     from = (long long)cur.w.n * warp / W;
     total = (int)((long long)cur.w.n * (warp + 1) / W - from);
@@ -390,7 +396,19 @@ __global__ void __launch_bounds__(Shape<D, NB, kTree>::W * 32, 1) kv_attn_kernel
     const long long gw = (long long)blockIdx.x * W + warp;
     from = begin_of(gw, U, G * W);
     total = (int)(begin_of(gw + 1, U, G * W) - from);
-    if (total > 0) advance<Sh>(p, cur, (int)(from - u_cta));
+    if (total > 0) advance<Sh, Sh::kStart>(p, cur, (int)(from - u_cta));
+    if constexpr (Sh::kStart > 0) {  // from units to blocks
+      int left = total;
+      total = 0;
+      for (Cursor c = cur; left > 0;) {
+        const int take = min(left, c.w.n + Sh::kStart - c.g);
+        total += max(c.g + take - max(c.g, Sh::kStart), 0);
+        left -= take;
+        if (left > 0) advance<Sh, Sh::kStart>(p, c, take);
+      }
+      from -= cur.g;  // the segment's first unit
+      cur.g = max(cur.g - Sh::kStart, 0);
+    }
   }
 
   if (lane == 0) ctrl->parts[warp].idle = total == 0;
@@ -770,8 +788,9 @@ __global__ void __launch_bounds__(Shape<D, NB, kTree>::W * 32, 1) kv_attn_kernel
       } else {
         q.last = 1;
       }
-      q.seg[tail ? 0 : 1] = {w.s, h, rb, w.n, from + done - cnt - cur.g};
+      q.seg[tail ? 0 : 1] = {w.s, h, rb, w.n, Sh::kStart ? from : from + done - cnt - cur.g};
     }
+    if constexpr (Sh::kStart > 0) from += w.n + Sh::kStart;
     advance<Sh>(p, cur, cnt);
   }
   // nothing may still be in flight into this CTA's shared memory
@@ -850,8 +869,8 @@ __global__ void __launch_bounds__(Shape<D, NB, kTree>::W * 32, 1) kv_attn_kernel
 #pragma unroll
   for (int k = 0; k < 2; ++k)
     if (on[k]) {
-      c0[k] = (int)owner_of(seg[k]->s0, U, G);
-      c1[k] = (int)owner_of(seg[k]->s0 + seg[k]->n - 1, U, G);
+      c0[k] = (int)owner_of(seg[k]->s0 + Sh::kStart, U, G);
+      c1[k] = (int)owner_of(seg[k]->s0 + Sh::kStart + seg[k]->n - 1, U, G);
     }
   __syncthreads();
   if (tid < 2 && on[tid]) {
