@@ -94,6 +94,23 @@ def test_compact_checks(lib):
           ok=[dict(B=0), dict(B=0, T=0), dict(B=0, caches=(G, G + size))])
 
 
+def test_caches_that_overlap_in_any_order(lib):
+    """Refused wherever the two stand; any order of caches that touch is taken.  (No requests: nothing is launched.)"""
+    import random
+    from w4a16_mixed_precision_gb300 import _binding as b
+    size, rng = 4 * 2 * 16 * 136, random.Random(3)
+    for n in (2, 3, 7, 40, 129):
+        for _ in range(30):
+            at = [G + size * i for i in range(n)]
+            order = rng.choice([at, at[::-1], rng.sample(at, n)])
+            assert compact(lib, caches=order, B=0) == b.OK
+            i, j = rng.sample(range(n), 2)
+            bad = list(order)
+            bad[i] = bad[j] + rng.choice([0, 16, -16, size - 16, 16 - size])
+            if bad[i] > 0:
+                assert compact(lib, caches=bad, B=0) == b.ERR_INVALID_ARG
+
+
 def copy(lib, caches=FAR, count=None, n_pages=4, hkv=2, D=128, page=16, src=G, dst=G, pairs=1, ws=G):
     at = None if caches is None else pointers(*caches)
     return lib.marlin_kv_copy_pages(at, len(caches or ()) if count is None else count, n_pages, hkv, D, page, src, dst, pairs, ws, None)

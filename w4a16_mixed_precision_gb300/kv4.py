@@ -9,6 +9,7 @@
 from __future__ import annotations
 
 import math
+import sys
 from array import array
 from dataclasses import dataclass
 
@@ -38,7 +39,8 @@ class Kv4Cache(_Handle):
         self._device = self.buf.get_device()
         self._scale = 1.0 / math.sqrt(self.head_dim)
         self._args = (self.buf.data_ptr(), self.n_pages, self.kv_heads, self.head_dim, self.page_size)
-        self._like = (self._device, *self._args[1:])  # what caches that a call takes together have in common
+        # what caches that a call takes together have in common, in a form that is quick to compare
+        self._like = sys.intern(repr((self._device, *self._args[1:])))
         return self._args
 
 
@@ -344,9 +346,9 @@ def _layers(caches, ws: Kv4Workspace, *named):
         raise ValueError("no caches" if not at else
                          "the caches must be alike: device, pages, key heads, head_dim and page size")
     cur = torch._C._cuda_getDevice()
-    if like[0][0] != cur or ws._device != cur or any(t.get_device() != cur for _, t in named):
+    if caches[0]._device != cur or ws._device != cur or any(t.get_device() != cur for _, t in named):
         _on_current_device(*(("cache", c.buf) for c in caches), ("workspace", ws.buf), *named)
-    return array("Q", at), len(at), like[0][1:], cur
+    return array("Q", at), len(at), caches[0]._args[1:], cur
 
 
 def kv4_compact(caches, batch: Kv4Batch, index: torch.Tensor, kept: torch.Tensor, ws: Kv4Workspace,
