@@ -1,6 +1,9 @@
 """Masks and positions of drafted trees, and attention of trees over the 4-bit cache, against plain implementations.
 
-Tolerances are those of test_kv4_gpu.py, derived there.
+Tolerances are those of test_kv4_gpu.py, derived there, and where a request has more than 48 query rows per key
+head one rounding more: that kernel rounds every p s (a probability times its value vector's scale) to fp16, by at
+most 2^-11 of itself.  The result is sum p (s (c - 8) + o) / sum p over codes c from 0 to 15, so that it moves by at
+most 2^-11 of the largest |s (c - 8)|, which is 8 s = 8/15 of the vector's range.
 """
 import numpy as np
 import pytest
@@ -96,10 +99,22 @@ def setup(lens, nq, hq, hkv, D, page, seed, see):
     return k, v, q, cache, batch, ws, tree
 
 
+def near(y, ref, v, rows):
+    """test_kv4_gpu.close, with the rounding of p s counted where the kernel for many rows served the request."""
+    if rows <= 48 or not v.size:
+        return close(y, ref, v)
+    y = np.asarray(y, np.float64)
+    assert np.array_equal(np.isnan(y), np.isnan(ref))
+    tol = 2.0 ** -11 * np.abs(ref) + 2.0 ** -12 * np.nanmax(np.abs(v)) + 2.0 ** -24
+    tol = tol + 2.0 ** -11 * 8 / 15 * np.nanmax(np.nanmax(v, -1) - np.nanmin(v, -1))
+    err = np.abs(y - ref)[~np.isnan(ref)]
+    assert (err <= tol[~np.isnan(ref)]).all(), f"max error {err.max()}"
+
+
 def check(y, q, k, v, lens, nq, see, D, window=0):
     kv, vv = split(kv_ref.values(k), lens), split(kv_ref.values(v), lens)
     for b, (qq, yy) in enumerate(zip(split(q, nq), split(y.cpu().numpy(), nq))):
-        close(yy, tree_ref.attention(qq, kv[b], vv[b], see[b], D ** -0.5, window), vv[b])
+        near(yy, tree_ref.attention(qq, kv[b], vv[b], see[b], D ** -0.5, window), vv[b], nq[b] * q.shape[1] // k.shape[1])
 
 
 @pytest.mark.parametrize("lens,nq,hq,hkv,D,page,window", TREES)
@@ -178,7 +193,7 @@ def test_nan_stays_where_it_is_seen(nq, hq):
     assert bad.any() and not bad.all()
     assert np.array_equal(np.isnan(y).any((1, 2)), bad) and np.array_equal(np.isnan(y).all((1, 2)), bad)
     ref = tree_ref.attention(q, kv_ref.values(k), kv_ref.values(v), see, D ** -0.5)
-    close(y[~bad], ref[~bad], kv_ref.values(v)[:first + 3])
+    near(y[~bad], ref[~bad], kv_ref.values(v)[:first + 3], nq * hq)
 
 
 def test_a_run_of_tokens_is_causal_attention():
@@ -280,10 +295,10 @@ def test_bad_entries_are_reported_and_not_followed(nq):
         y = w4.kv4_tree_attention(dq, cache, w4.Kv4Batch(table, length, start, 2 * nq, nq), bits, ws)
         assert w4.device_status(ws) == 7, change
         if change != "words":
-            close(y[:nq].cpu().numpy(), ref, kv_ref.values(v))
+            near(y[:nq].cpu().numpy(), ref, kv_ref.values(v), nq * 2)
     y = w4.kv4_tree_attention(dq, cache, batch, tree, ws)
     assert w4.device_status(ws) == 0
-    close(y[:nq].cpu().numpy(), ref, kv_ref.values(v))
+    near(y[:nq].cpu().numpy(), ref, kv_ref.values(v), nq * 2)
 
 
 def test_refusals():
