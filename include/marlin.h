@@ -552,7 +552,8 @@ marlin_status_t marlin_kv_rope_append(const uint16_t* q, int64_t q_token_stride,
 /*
  * Keeps some of each request's new tokens, in the caches of all layers: with first =
  * lengths[b] - new, position first + i takes what position first + index[q_start[b] + i]
- * holds, keys and values of every head, for i < kept[b].  One launch for 128 caches.
+ * holds, keys and values of every head, for i < kept[b].  One launch for 128 caches, with
+ * `into` and max_q > 1024 another one before them.
  * caches     host, [count] device pointers to caches that are alike and do not overlap
  *            (else INVALID_ARG); pages, lengths and indexes are those of every one.
  * into       NULL: the tokens stay in their request's pages.  index must then ascend
@@ -562,7 +563,9 @@ marlin_status_t marlin_kv_rope_append(const uint16_t* q, int64_t q_token_stride,
  *            by position as in page_table, none of which is read in this call.  index may
  *            then name any new tokens in any order.
  * index      device, int32 [tokens]; kept device, int32 [requests], 0 to the request's new
- *            tokens; others are reported as above, and nothing of the request is moved.
+ *            tokens; others are reported as above, and nothing of the request is moved.  (A
+ *            position whose page does not exist, or whose source's does not, is reported and
+ *            left as it is; new_lengths counts it.)
  * new_lengths  device, int32 [requests], written: first + kept[b] (lengths[b] where nothing
  *            was moved for an error); overlaps none of the inputs.
  * max_q      most new tokens of any request; a request with more is served too, slower.

@@ -228,6 +228,7 @@ struct KvCompactParams {
   const int *index, *kept;
   int* new_lens;        // nullptr where another launch writes them
   int max_q;
+  int look;             // into: every CTA looks at its request's indexes (filled in by launch_kv_compact)
 };
 cudaError_t launch_kv_compact(const KvCompactParams& p, const KvCaches& c, int D, int sms, cudaStream_t stream);
 cudaError_t launch_kv_copy_pages(const KvCaches& c, int caches, int n_pages, long long page_bytes, const int* src,

@@ -86,7 +86,7 @@ __device__ __forceinline__ Plan plan_granule(const KvCompactParams& p, const Kep
   const bool mine = lane < 16 && i >= 0 && i < k.kept;
   if (mine) {
     const int at = p.index[k.s.q0 + i];
-    if (at < 0 || at >= k.s.nq) {
+    if (at < 0 || at >= k.s.nq) {  // (not unless it has changed since all indexes were looked at)
       kv_fail(p.kv, kKvSiteIndex);
     } else {
       m.from = granule_at<D>(p.kv, p.kv.table + (long long)b * p.kv.max_pages, p.kv.max_pages, k.first + at);
@@ -246,8 +246,40 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const KvCompac
   }
 }
 
-// The kept tokens go to other pages: a warp has granules of `run` of all caches' heads, H in flight.
+// The kept tokens go to other pages: a warp has granules of `run` of all caches' heads, H in flight.  Nothing of a
+// request with an index outside its new tokens is moved, so that all of its indexes are looked at before a warp's first
+// store, under its first loads: by every warp (p.look) where they are few, else by a kernel before (kv_index_kernel),
+// which reports what is outside; while nothing is reported there is nothing to find, and until what was reported is
+// read every warp looks.
 constexpr int kMostHeads = 8;
+// New tokens of a request.  Half of the tokens of 2 requests of 250 3.5 us where every warp looks, 4.5 with a kernel
+// before; of 1000 4.5 / 5.0, of 2000 5.8 / 5.2, of 4000 9.0 / 6.4, of 38,000 58.7 / 21.7 (20.0 if nobody looked); 8 heads
+// of 128 channels.
+constexpr int kLookMost = 1024;
+
+constexpr int kIndexes = 8;  // of a thread, in flight
+__device__ __forceinline__ bool inside(const KvCompactParams& p, const Kept& k, long long i0, int step) {
+  bool ok = true;
+#pragma unroll
+  for (int j = 0; j < kIndexes; ++j) {
+    const long long i = i0 + j * step;
+    const int at = i < k.kept ? p.index[k.s.q0 + i] : 0;
+    ok &= (uint32_t)at < (uint32_t)k.s.nq;
+  }
+  return ok;
+}
+
+__global__ void __launch_bounds__(kMoveThreads) kv_index_kernel(const KvCompactParams p, int ctas) {
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  griddep_wait();
+  const int b = blockIdx.x / ctas;
+  const Kept k = kept_of(p, b, false);  // (counts and lengths that do not fit are the next kernel's to report)
+  constexpr long long kChunk = kMoveThreads * kIndexes;
+  bool ok = true;
+  for (long long i = blockIdx.x % ctas * kChunk + threadIdx.x; i < k.kept; i += ctas * kChunk)
+    ok &= inside(p, k, i, kMoveThreads);
+  if (!ok) kv_fail(p.kv, kKvSiteIndex);
+}
 
 template <int D, int H>
 __global__ void __launch_bounds__(kMoveThreads) kv_gather_kernel(const KvCompactParams p, const __grid_constant__ KvCaches caches,
@@ -257,10 +289,14 @@ __global__ void __launch_bounds__(kMoveThreads) kv_gather_kernel(const KvCompact
   const int x = blockIdx.x % ctas, unit = blockIdx.x / ctas;  // of a run's CTAs
   const int heads = p.caches * p.kv.hkv, runs = (heads + run - 1) / run, b = unit / runs, at = (unit - b * runs) * run;
   const bool speaks = at == 0 && x == 0 && threadIdx.x == 0;
+  const int reported = p.look ? 1 : __ldcg(p.kv.status);
   const Kept k = kept_of(p, b, speaks);
-  if (speaks && p.new_lens) p.new_lens[b] = k.kept < 0 ? p.kv.lens[b] : k.first + k.kept;
-  if (k.kept <= 0) return;
+  if (k.kept <= 0) {
+    if (speaks && p.new_lens) p.new_lens[b] = k.kept < 0 ? p.kv.lens[b] : k.first;
+    return;
+  }
   const int g_end = (k.first + k.kept + 15) >> 4, first_cache = at / p.kv.hkv, first_head = at - first_cache * p.kv.hkv;
+  bool sure = false;  // that all indexes are inside
   for (int granule = (k.first >> 4) + x * kMoveWarps + (threadIdx.x >> 5); granule < g_end; granule += ctas * kMoveWarps) {
     const Plan m = plan_granule<D>(p, k, b, granule);
     const Source<D> o = source_of<D>(m);
@@ -278,6 +314,15 @@ __global__ void __launch_bounds__(kMoveThreads) kv_gather_kernel(const KvCompact
             ++cache;
           }
         }
+      if (!sure) {
+        bool ok = true;
+        if (__any_sync(0xffffffffu, reported != 0))
+          for (long long i = threadIdx.x & 31; i < k.kept; i += 32 * kIndexes) ok &= inside(p, k, i, 32);
+        sure = __all_sync(0xffffffffu, ok);
+        if (speaks && !sure) kv_fail(p.kv, kKvSiteIndex);
+        if (speaks && p.new_lens) p.new_lens[b] = sure ? k.first + k.kept : p.kv.lens[b];  // (its warp has the first granule)
+        if (!sure) return;
+      }
 #pragma unroll
       for (int i = 0; i < H; ++i)
         if (i < left) store_granule<D>(head[i], m.to, r[i]);
@@ -340,10 +385,17 @@ cudaError_t compact(const KvCompactParams& p, const KvCaches& c, int sms, cudaSt
   if (p.into) {
     const long long ctas = (granules + kMoveWarps - 1) / kMoveWarps;
     const int heads = p.caches * p.kv.hkv;
+    KvCompactParams f = p;
+    f.look = p.max_q <= kLookMost;
+    if (!f.look && p.new_lens) {  // the first of several launches
+      const long long looks = (p.max_q + kMoveThreads * kIndexes - 1ll) / (kMoveThreads * kIndexes);
+      const cudaError_t e = launch(kv_index_kernel, p.kv.B * looks, kMoveThreads, stream, p, (int)looks);
+      if (e != cudaSuccess) return e;
+    }
     // 32 warps an SM at least, as many as fit where a head is a warp's
     const int run = (int)std::min<long long>(std::max<long long>(units * granules / (32ll * sms), 1), kMostHeads);
     return launch(run == 1 ? kv_gather_kernel<D, 1> : kv_gather_kernel<D, 2>, p.kv.B * ((heads + run - 1ll) / run) * ctas,
-                  kMoveThreads, stream, p, c, (int)ctas, run);
+                  kMoveThreads, stream, f, c, (int)ctas, run);
   }
   // a warp a head where few tokens can be kept (more are served by it in more rounds), else a CTA
   if (granules <= 16) return launch(kv_compact_kernel<D, 1>, (units + kMoveWarps - 1) / kMoveWarps, kMoveThreads, stream, p, c);
