@@ -532,15 +532,24 @@ __global__ void __launch_bounds__(Shape<D, NB, kTree>::W * 32, 1) kv_attn_kernel
       using Masked = decltype(masked);
 
       // trees: which tokens rows 2c, 2c + 1 see; bit 16 (q & 1) + 8 e of word q / 2 is this lane's token g + 8 e of granule q
-      uint32_t see[NB][2][Sh::kStep / 32];
+      // of `any`: whether some row of the warp's sees it
+      uint32_t see[NB][2][Sh::kStep / 32], any[Sh::kStep / 32];
       if constexpr (kTree && Masked::value) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int k = 0; k < Sh::kStep / 32; ++k) {
+          any[k] = 0u;
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int k = 0; k < Sh::kStep / 32; ++k)
-              see[nb][r][k] = hi_pos[nb][r] >= 0 ? kv_tree_see(p, w.s, hi_pos[nb][r], lo_pos[nb][r], t0 + 32 * k) >> g : 0u;
+            for (int r = 0; r < 2; ++r) {
+              const uint32_t all = hi_pos[nb][r] >= 0 ? kv_tree_see(p, w.s, hi_pos[nb][r], lo_pos[nb][r], t0 + 32 * k) : 0u;
+              any[k] |= all;
+              see[nb][r][k] = all >> g;
+            }
+          any[k] |= __shfl_xor_sync(0xffffffffu, any[k], 1);
+          any[k] |= __shfl_xor_sync(0xffffffffu, any[k], 2);
+          any[k] >>= g;
+        }
       }
       auto hidden = [&](int nb, int r, int q, int e) {
         if constexpr (kTree && Masked::value) return !((see[nb][r][q / 2] >> (16 * (q & 1) + 8 * e)) & 1u);
@@ -593,7 +602,9 @@ __global__ void __launch_bounds__(Shape<D, NB, kTree>::W * 32, 1) kv_attn_kernel
           vs[q][e] = vf.x;
           vo[q][e] = vf.y;
           const int t = t0 + 16 * q + g + 8 * e;
-          if (Masked::value && (t >= any_hi || t < any_lo)) ks = kz = vs[q][e] = vo[q][e] = 0.f;
+          bool unseen = Masked::value && (t >= any_hi || t < any_lo);
+          if constexpr (kTree && Masked::value) unseen = !((any[q / 2] >> (16 * (q & 1) + 8 * e)) & 1u);
+          if (unseen) ks = kz = vs[q][e] = vo[q][e] = 0.f;
           big = fmaxf(big, vs[q][e]);
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
