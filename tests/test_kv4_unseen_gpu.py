@@ -1,15 +1,15 @@
 """What no row sees has no part in any row: unwritten tokens may hold anything (infinite and NaN scales and offsets, large
 finite ones), new tokens whose bit no row has and tokens before every row's window among them.
 
-The results have to be the same bits whatever the unseen tokens hold, and within the tolerances of test_kv4_tree_gpu.py,
-derived there.
+The results have to be the same bits whatever the unseen tokens hold, and within the tolerances of test_kv4_gpu.py and
+test_kv4_tree_gpu.py, derived there.
 """
 import numpy as np
 import pytest
 
 import kv_ref
 import tree_ref
-from test_kv4_gpu import _built, make  # noqa: F401
+from test_kv4_gpu import _built, close, make  # noqa: F401
 from test_kv4_tree_gpu import near
 
 pytestmark = pytest.mark.gpu
@@ -43,6 +43,9 @@ CASES = [
     ([90], [6], 2, 2, 128, 16, 0),             # up to 16 rows a key head
     ([200], [5], 8, 2, 64, 16, 40),
     ([200], [3], 16, 1, 128, 32, 70),          # 48
+    ([150], [40], 4, 1, 128, 16, 0),           # many
+    ([300], [30], 8, 1, 64, 48, 75),
+    ([400], [33], 8, 2, 128, 64, 130),
 ]
 
 
@@ -66,4 +69,21 @@ def test_trees(lens, nq, hq, hkv, D, page, window):
     for params in GARBAGE:
         overwrite(cache, batch.page_table[0].tolist(), unseen, params)
         assert torch.equal(w4.kv4_tree_attention(q, cache, batch, tree, ws, window=window), y), [hex(x) for x in params]
+    assert w4.device_status(ws) == 0
+
+
+@pytest.mark.parametrize("lens,nq,hq,hkv,D,page,window", [([200], [2], 4, 2, 128, 16, 70), ([300], [100], 4, 2, 128, 16, 75),
+                                                          ([700], [66], 2, 2, 64, 64, 130)])
+def test_runs_under_a_window(lens, nq, hq, hkv, D, page, window):
+    import w4a16_mixed_precision_gb300 as w4
+    k, v, cache, batch, hist = make(lens, nq, hkv, D, page, seed=lens[0] + 1)
+    ws = w4.Kv4Workspace(batch, hq, cache)
+    w4.kv4_append(cuda(k), cuda(v), cache, hist, ws)
+    q = cuda(np.random.default_rng(lens[0]).standard_normal((nq[0], hq, D)).astype(np.float16))
+    y = w4.kv4_attention(q, cache, batch, ws, window=window)
+    close(y.cpu().numpy(), kv_ref.attention(q.cpu().numpy(), kv_ref.values(k), kv_ref.values(v), nq[0], D ** -0.5, window),
+          kv_ref.values(v))
+    for params in GARBAGE:
+        overwrite(cache, batch.page_table[0].tolist(), range(lens[0] - nq[0] - window + 1), params)
+        assert torch.equal(w4.kv4_attention(q, cache, batch, ws, window=window), y), [hex(x) for x in params]
     assert w4.device_status(ws) == 0

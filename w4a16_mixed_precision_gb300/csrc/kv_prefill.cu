@@ -737,7 +737,22 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
           }
         }
         const float4 vm = *reinterpret_cast<const float4*>(ctrl.vmax[st]);
-        const float big = fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w));
+        float big = fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w));
+        if (!full) {  // of the tokens that the row sees: others may hold anything
+          big = 0.f;
+#pragma unroll 16
+          for (int t = 0; t < kBlock; t += 2) {
+            const float2 vp = *reinterpret_cast<const float2*>(par + t + 1);
+            const int at = t0 + t;
+            bool see0 = at < hi && at >= lo, see1 = at + 1 < hi && at + 1 >= lo;
+            if constexpr (kTree) {
+              const uint32_t seen = (t < 32 ? see[0] : see[1]) >> (t & 31);
+              see0 = seen & 1u;
+              see1 = seen & 2u;
+            }
+            big = fmaxf(big, fmaxf(see0 ? vp.x : 0.f, see1 ? vp.y : 0.f));
+          }
+        }
         const float scale = (float)max((int)(__float_as_uint(big) >> 23) - 126, -30);  // log2 of a power of two above it
         float f = 1.f;
         if (top > kNegInf && over > kMost) {
@@ -1054,8 +1069,10 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       // scales and offsets, by pairs of tokens: (ks, ks, ko, ko, vs, vs, vo, vo), keys' in log2 units
       {
         float2 kf = unpack(pr.x), vf = unpack(pr.y);
-        if (!(fabsf(vf.x) <= 65504.f)) {  // a value that holds NaN: by way of its score, which masks can take out
-          kf.x = vf.x;
+        // a value that holds NaN: by way of its score, which masks can take out.  (A slot that was never written may hold
+        // any scale and offset, and rows that do not see it take nothing from it.)
+        if (!(fabsf(vf.x) <= 65504.f && fabsf(vf.y) <= 65504.f)) {
+          kf.x = __int_as_float(0x7FFFFFFF);
           vf.x = vf.y = 0.f;
         }
         float big = lane < 16 ? vf.x : 0.f;
