@@ -175,6 +175,17 @@ __device__ __forceinline__ uint32_t kv_tree_see(const KvAttnParams& p, const KvS
   return see;
 }
 
+// What a row's sum of probabilities is divided by, for a row that sees no token nothing (0).  One that sees some
+// and whose scores are all minus infinity has a sum of 0, too: its softmax is not defined, and the result is NaN.
+__device__ __forceinline__ float kv_tree_inverse(const KvAttnParams& p, const KvSeq& s, int i, float sum) {
+  if (sum == 0.f) {
+    bool sees = kv_tree_lo(p, s, i) < s.len - s.nq;
+    for (int t0 = max(s.len - s.nq, 0); !sees && t0 < s.len; t0 += 32) sees = kv_tree_see(p, s, i, 0, t0) != 0u;
+    if (!sees) return 0.f;
+  }
+  return 1.f / sum;
+}
+
 // row / group, exact for 32-bit rows.
 __device__ __forceinline__ int kv_div_group(const KvAttnParams& p, int row) {
   return p.group_magic ? (int)__umul64hi((unsigned long long)(uint32_t)row, p.group_magic) : row;

@@ -83,12 +83,13 @@ __device__ __forceinline__ void load_words(const uint8_t* at, uint32_t (&w)[N]) 
 }
 
 // Four channels of an output row: row rr of key head h, normalised.  A row
-// that sees no token is zero (its sum is 0, exactly: all its scores are minus infinity).
+// that sees no token is zero.
 template <bool kTree>
 __device__ __forceinline__ void store_row(const KvAttnParams& p, const KvSeq& s, int h, int rr, int ch, int D,
                                           float4 acc, float sum) {
   const int i = kv_div_group(p, rr), head = h * p.group + rr - i * p.group;
-  const float inv = (kTree ? sum != 0.f : s.len - s.nq + i >= 0) ? 1.f / sum : 0.f;
+  float inv = s.len - s.nq + i >= 0 ? 1.f / sum : 0.f;
+  if constexpr (kTree) inv = kv_tree_inverse(p, s, i, sum);
   if (inv == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
   uint2 v;
   v.x = h2_bits(__floats2half2_rn(acc.x * inv, acc.y * inv));

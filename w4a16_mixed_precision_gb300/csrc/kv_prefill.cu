@@ -194,7 +194,8 @@ __device__ __forceinline__ void load_words(const uint8_t* at, uint32_t (&w)[N]) 
 // Of an item that stripes cut: the CTA whose stripe it begins in notes it in a part of its slot 1 that
 // holds no sums, for the kernel that joins the parts.
 struct PartNote {
-  int q0, rows, tile, h;  // h < 0: no such item
+  KvSeq seq;
+  int rows, tile, h;      // h < 0: no such item
   int last;               // CTA of its last block
 };
 template <int D>
@@ -835,7 +836,12 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       __syncwarp();
     };
     if (whole) {
-      const float inv = (kTree ? sum != 0.f : hi > 0) ? 1.f / sum : 0.f, add = off * inv;  // a row that sees no token is zero
+      float inv = hi > 0 ? 1.f / sum : 0.f;  // a row that sees no token is zero
+      if constexpr (kTree) {
+        inv = live ? kv_tree_inverse(p, seq, i, sum) : 0.f;
+        __syncwarp();
+      }
+      const float add = off * inv;
 #pragma unroll 1
       for (int part = 0; part < D / 32; ++part) {
         uint32_t v[32];
@@ -861,7 +867,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
         // the part takes this piece's sums of products; after the stripe's last piece of the item the offsets, too,
         // or it is the rows' results that come of both
         const bool last = x1 == x_all, done = last && from0 && x1 == at.span.n;
-        const float inv = sum != 0.f ? 1.f / sum : 0.f;  // a row that sees no token is zero
+        const float inv = done && live ? kv_tree_inverse(p, seq, i, sum) : 0.f;
+        __syncwarp();
         const float f0 = fresh || R_part == kUnset ? 0.f : R_part == R ? 1.f : ex2(R_part - R), add = last ? off : 0.f;
         const bool rescaled = !fresh && __any_sync(0xffffffffu, f0 != 1.f);
         R_part = R;
@@ -901,7 +908,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
           __stcg(slot + (D + 1) * kRows, sum);
           // the next kernel joins the stripes' parts
           if (tid == 0 && from0)
-            *part_note<D>(p, blockIdx.x) = {seq.q0, at.rows, at.tile, at.h,
+            *part_note<D>(p, blockIdx.x) = {seq, at.rows, at.tile, at.h,
                                             (int)stripe_owner(u - at.x + at.span.n - 1, U, G)};
         }
       } else {
@@ -1235,13 +1242,13 @@ __global__ void __launch_bounds__(kRows) kv_join_kernel(const KvAttnParams p) {
       for (int k = 0; k < 8; ++k) o[k] = fmaf(o[k], fo, l[i] == 0.f ? 0.f : v[i][k] * fn);
     }
   }
-  const float inv = all != 0.f ? 1.f / all : 0.f;
   const int i = kv_div_group(p, row), head = note.h * p.group + row - i * p.group;
+  const float inv = kv_tree_inverse(p, note.seq, i, all);
   uint4 out = make_uint4(0u, 0u, 0u, 0u);
   if (inv != 0.f)
     out = make_uint4(pack(o[0] * inv, o[1] * inv), pack(o[2] * inv, o[3] * inv), pack(o[4] * inv, o[5] * inv),
                      pack(o[6] * inv, o[7] * inv));
-  *reinterpret_cast<uint4*>(p.out + ((long long)(note.q0 + i) * p.heads + head) * D + ch) = out;
+  *reinterpret_cast<uint4*>(p.out + ((long long)(note.seq.q0 + i) * p.heads + head) * D + ch) = out;
 }
 
 template <typename Kernel>
