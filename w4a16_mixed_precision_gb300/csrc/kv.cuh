@@ -175,15 +175,22 @@ __device__ __forceinline__ uint32_t kv_tree_see(const KvAttnParams& p, const KvS
   return see;
 }
 
-// What a row's sum of probabilities is divided by, for a row that sees no token nothing (0).  One that sees some
-// and whose scores are all minus infinity has a sum of 0, too: its softmax is not defined, and the result is NaN.
-__device__ __forceinline__ float kv_tree_inverse(const KvAttnParams& p, const KvSeq& s, int i, float sum) {
-  if (sum == 0.f) {
-    bool sees = kv_tree_lo(p, s, i) < s.len - s.nq;
-    for (int t0 = max(s.len - s.nq, 0); !sees && t0 < s.len; t0 += 32) sees = kv_tree_see(p, s, i, 0, t0) != 0u;
-    if (!sees) return 0.f;
+// A row's sum of probabilities, infinite for a row that sees no token, so that its result is zero.  One that sees some
+// and whose scores are all minus infinity has a sum of 0, too: its softmax is not defined, and the result NaN.
+// (The look at the bits is not inlined: hardly ever made, its code at every row's end made short trees 10% slower.)
+__device__ __noinline__ static bool kv_tree_sees(const int* row, int words, int nq, int len, int window) {
+  const int first = len - nq;
+  int seen = 0, there = 0;  // bits of new tokens, and of those at positions from 0 on
+  for (int j = 0; j < nq && j < 32 * words; ++j) {
+    const int bit = ((uint32_t)row[j >> 5] >> (j & 31)) & 1u;
+    seen += bit;
+    if (first + j >= 0) there += bit;
   }
-  return 1.f / sum;
+  return there > 0 || (window > 0 ? min(max(first + seen - window, 0), first) : 0) < first;
+}
+__device__ __forceinline__ float kv_tree_sum(const KvAttnParams& p, const KvSeq& s, int i, float sum) {
+  const bool empty = sum == 0.f && !kv_tree_sees(p.tree + (long long)(s.q0 + i) * p.tree_words, p.tree_words, s.nq, s.len, p.window);
+  return empty ? __builtin_huge_valf() : sum;
 }
 
 // row / group, exact for 32-bit rows.

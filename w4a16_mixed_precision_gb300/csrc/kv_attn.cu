@@ -83,13 +83,12 @@ __device__ __forceinline__ void load_words(const uint8_t* at, uint32_t (&w)[N]) 
 }
 
 // Four channels of an output row: row rr of key head h, normalised.  A row
-// that sees no token is zero.
+// that sees no token is zero; of trees' rows kv_tree_sum tells by their sum.
 template <bool kTree>
 __device__ __forceinline__ void store_row(const KvAttnParams& p, const KvSeq& s, int h, int rr, int ch, int D,
                                           float4 acc, float sum) {
   const int i = kv_div_group(p, rr), head = h * p.group + rr - i * p.group;
-  float inv = s.len - s.nq + i >= 0 ? 1.f / sum : 0.f;
-  if constexpr (kTree) inv = kv_tree_inverse(p, s, i, sum);
+  const float inv = kTree || s.len - s.nq + i >= 0 ? 1.f / sum : 0.f;
   if (inv == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
   uint2 v;
   v.x = h2_bits(__floats2half2_rn(acc.x * inv, acc.y * inv));
@@ -771,11 +770,13 @@ __global__ void __launch_bounds__(Shape<D, NB, kTree>::W * 32, 1) kv_attn_kernel
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int row = nb * 8 + 2 * c + e;
-        const float ll = e ? l[nb].y : l[nb].x, zz = e ? pz[nb].y : pz[nb].x;
+        float ll = e ? l[nb].y : l[nb].x;
+        const float zz = e ? pz[nb].y : pz[nb].x;
         if (!whole && g == 0) {
           part[RB * Sh::kOStride + 2 * row] = e ? m[nb].y : m[nb].x;
           part[RB * Sh::kOStride + 2 * row + 1] = ll;
         }
+        if (kTree && whole && rb * RB + row < rows) ll = kv_tree_sum(p, w.s, kv_div_group(p, rb * RB + row), ll);
 #pragma unroll
         for (int j = 0; j < CW; ++j) {
           const F2 a = o[2 * j][nb][0], b = o[2 * j + 1][nb][0], d = o[2 * j][nb][1], f = o[2 * j + 1][nb][1];
@@ -866,6 +867,7 @@ __global__ void __launch_bounds__(Shape<D, NB, kTree>::W * 32, 1) kv_attn_kernel
       __stcg(reinterpret_cast<float4*>(part + row * D + ch), acc);
       if (ch == 0) __stcg(reinterpret_cast<float2*>(part + RB * D + 2 * row), make_float2(top, sum));
     } else if (sg.rb * RB + row < sg.s.nq * p.group) {
+      if (kTree) sum = kv_tree_sum(p, sg.s, kv_div_group(p, sg.rb * RB + row), sum);
       store_row<kTree>(p, sg.s, sg.h, sg.rb * RB + row, ch, D, acc, sum);
     }
   }
@@ -921,6 +923,7 @@ __global__ void __launch_bounds__(Shape<D, NB, kTree>::W * 32, 1) kv_attn_kernel
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) join(ml[i], a[i], top, sum, acc);
       }
+      if (kTree) sum = kv_tree_sum(p, sg.s, kv_div_group(p, sg.rb * RB + row), sum);
       store_row<kTree>(p, sg.s, sg.h, sg.rb * RB + row, ch, D, acc, sum);
     }
   }

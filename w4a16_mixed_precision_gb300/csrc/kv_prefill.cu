@@ -796,6 +796,11 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
     tc_fence_after();
     const bool whole = (!kTree || fresh) && at.x == 0 && x1 == at.span.n;
     const float sum = l.x + l.y, off = pz.x + pz.y;
+    float total = sum;
+    if constexpr (kTree) {
+      if (from0 && x1 == at.span.n && live) total = kv_tree_sum(p, seq, i, sum);
+      __syncwarp();
+    }
     const bool any = half_.to > half_.from;  // else there is nothing of this tile in tensor memory
     // a finished row's channels 32 part .. + 31 into Q's room, which no product of this item reads any
     // more.  A warp keeps its 32 rows in the bytes that hold its own rows of Q, as no barrier orders
@@ -836,12 +841,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
       __syncwarp();
     };
     if (whole) {
-      float inv = hi > 0 ? 1.f / sum : 0.f;  // a row that sees no token is zero
-      if constexpr (kTree) {
-        inv = live ? kv_tree_inverse(p, seq, i, sum) : 0.f;
-        __syncwarp();
-      }
-      const float add = off * inv;
+      const float inv = kTree || hi > 0 ? 1.f / total : 0.f, add = off * inv;  // a row that sees no token is zero
 #pragma unroll 1
       for (int part = 0; part < D / 32; ++part) {
         uint32_t v[32];
@@ -867,8 +867,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv_prefill_kernel(const KvAttnPa
         // the part takes this piece's sums of products; after the stripe's last piece of the item the offsets, too,
         // or it is the rows' results that come of both
         const bool last = x1 == x_all, done = last && from0 && x1 == at.span.n;
-        const float inv = done && live ? kv_tree_inverse(p, seq, i, sum) : 0.f;
-        __syncwarp();
+        const float inv = 1.f / total;
         const float f0 = fresh || R_part == kUnset ? 0.f : R_part == R ? 1.f : ex2(R_part - R), add = last ? off : 0.f;
         const bool rescaled = !fresh && __any_sync(0xffffffffu, f0 != 1.f);
         R_part = R;
@@ -1243,7 +1242,7 @@ __global__ void __launch_bounds__(kRows) kv_join_kernel(const KvAttnParams p) {
     }
   }
   const int i = kv_div_group(p, row), head = note.h * p.group + row - i * p.group;
-  const float inv = kv_tree_inverse(p, note.seq, i, all);
+  const float inv = 1.f / kv_tree_sum(p, note.seq, i, all);
   uint4 out = make_uint4(0u, 0u, 0u, 0u);
   if (inv != 0.f)
     out = make_uint4(pack(o[0] * inv, o[1] * inv), pack(o[2] * inv, o[3] * inv), pack(o[4] * inv, o[5] * inv),
