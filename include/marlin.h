@@ -509,7 +509,7 @@ marlin_status_t marlin_kv_tree(const int32_t* parents, const int32_t* lengths, c
  *            bits - 1.  (All positions from lengths[b] - new - window on have to be in
  *            valid pages, and those that share a block of 64 with them.)
  * A row that sees nothing at all is zero.  Everything else, the workspace too, is as for
- * marlin_kv_attention, except that a request has few query rows per key head up to 48 of them.
+ * marlin_kv_attention.
  */
 marlin_status_t marlin_kv_tree_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride, int heads,
                                          const void* cache, int n_pages, int kv_heads, int head_dim, int page_size,

@@ -116,11 +116,11 @@ marlin_status_t kv_copy(bool append, uint16_t* k, int64_t k_ts, int64_t k_hs, ui
 // of 4000, 80 51 / 59, 96 59 / 59, 128 75 / 59.  Few items are the exception, whatever the
 // rows: one request of 1000, 64 heads on 8, 160 rows 16 / 32, of 8000 43 / 126 (an item that
 // many stripes cut is joined part by part).
+// Trees have the same bound, although their parts, which a second kernel joins, would allow 48: it is also where a
+// probability times its value's scale goes from two fp16 numbers to one.  Streaming against tcgen05: 8 requests of 8000
+// tokens, 64 heads on 8, 32 rows 50 against 63 us, 64 82 / 64; 32 of 2000, 32 58 / 78, 64 89 / 78; one of 8000, 32
+// 26 / 25, 64 30 / 25; one of 100,000, 32 86 / 113, 64 150 / 113; 64 channels, 8 of 4000, 32 25 / 35, 64 37 / 35.
 constexpr int kPrefillRows = 64;
-// The same for trees (whose parts a second kernel joins): 8 requests of 8000 tokens, 64 heads on 8, 32 rows 50 against
-// 63 us, 64 82 / 64; 32 of 2000, 32 58 / 78, 64 89 / 78; one of 8000, 32 26 / 25, 64 30 / 25; one of 100,000, 32 86 / 113,
-// 64 150 / 113; 64 channels, 8 of 4000, 32 25 / 35, 64 37 / 35.
-constexpr int kTreeRows = 48;
 
 struct AttnPlan {
   int grid, nb;
@@ -129,7 +129,7 @@ struct AttnPlan {
 
 // [status 256 B][arrivals of both kernels][parts of the streaming kernel][parts of the
 // tcgen05 kernel, where a request can have enough rows for it]
-AttnPlan attn_plan(int sms, int D, int group, int max_q, int tokens, int most_rows) {
+AttnPlan attn_plan(int sms, int D, int group, int max_q, int tokens) {
   AttnPlan a;
   a.grid = sms;
   a.nb = (long long)group * max_q > 8 ? 2 : 1;
@@ -139,7 +139,7 @@ AttnPlan attn_plan(int sms, int D, int group, int max_q, int tokens, int most_ro
   a.firsts_off = a.partials_off + 2 * sms * part;
   a.prompt_off = round_up(a.firsts_off + kKvAttnWarps * sms * part, 256);
   a.bytes = a.prompt_off;
-  if ((long long)group * tokens > most_rows) a.bytes += 2 * sms * kv_prefill_part_floats(D) * sizeof(float);
+  if ((long long)group * tokens > kPrefillRows) a.bytes += 2 * sms * kv_prefill_part_floats(D) * sizeof(float);
   return a;
 }
 
@@ -163,8 +163,7 @@ marlin_status_t attention(const uint16_t* q, int64_t q_token_stride, int64_t q_h
   if ((s = current_sms(&sms)) != MARLIN_OK) return s;
   const int group = heads / kv_heads;
   if ((long long)tokens * group > 0x7FFFFFFF) return MARLIN_ERR_UNSUPPORTED;
-  const int most_rows = words > 0 ? kTreeRows : kPrefillRows;
-  const AttnPlan a = attn_plan(sms, head_dim, group, max_q, tokens, most_rows);
+  const AttnPlan a = attn_plan(sms, head_dim, group, max_q, tokens);
   if (workspace_bytes < a.bytes) return MARLIN_ERR_WORKSPACE_TOO_SMALL;
   {
     static std::mutex lock;
@@ -206,10 +205,10 @@ marlin_status_t attention(const uint16_t* q, int64_t q_token_stride, int64_t q_h
   // side of the bound, request by request.
   const bool uniform = requests == 1 || (long long)requests * max_q == tokens;
   // (the workspace holds the tcgen05 kernel's parts where all tokens together have enough rows)
-  const bool some_large = (long long)(requests == 1 ? tokens : std::min(max_q, tokens)) * group > most_rows;
+  const bool some_large = (long long)(requests == 1 ? tokens : std::min(max_q, tokens)) * group > kPrefillRows;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (some_large) {
-    if (!uniform) p.min_rows = most_rows;
+    if (!uniform) p.min_rows = kPrefillRows;
     KvAttnParams f = p;
     f.counters = p.counters + a.grid;
     f.partials = reinterpret_cast<float*>(ws + a.prompt_off);
@@ -218,7 +217,7 @@ marlin_status_t attention(const uint16_t* q, int64_t q_token_stride, int64_t q_h
     if (items > 0x7FFFFFFF) return MARLIN_ERR_UNSUPPORTED;
     if (launch_kv_prefill(f, head_dim, std::max((int)items, a.grid), st) != cudaSuccess) return MARLIN_ERR_CUDA;
     if (uniform) return MARLIN_OK;
-    p.max_rows = most_rows;
+    p.max_rows = kPrefillRows;
   }
   return launch_kv_attn(p, head_dim, a.nb, a.grid, st) == cudaSuccess ? MARLIN_OK : MARLIN_ERR_CUDA;
 }
@@ -331,7 +330,7 @@ marlin_status_t marlin_kv_workspace_bytes(int heads, int kv_heads, int head_dim,
   int sms;
   const marlin_status_t s = static_cast<marlin_status_t>(device_sms(device, &sms));
   if (s != MARLIN_OK) return s;
-  *bytes = attn_plan(sms, head_dim, heads / kv_heads, 1, tokens, std::min(kPrefillRows, kTreeRows)).bytes;
+  *bytes = attn_plan(sms, head_dim, heads / kv_heads, 1, tokens).bytes;
   return MARLIN_OK;
 }
 
