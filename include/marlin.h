@@ -525,7 +525,7 @@ marlin_status_t marlin_kv_tree_attention(const uint16_t* q, int64_t q_token_stri
  * keys and the values into the cache.  One launch.
  * q, k, v, q_out  device, fp16 [tokens][heads or kv_heads][head_dim], 16-byte aligned,
  *            strides multiples of 8.  q_out may be q with the same strides; else it
- *            overlaps none of the inputs.
+ *            overlaps none of the inputs.  Its rows do not overlap (else INVALID_ARG).
  * rot        channels that are rotated, the first ones: a multiple of head_dim / 8 (else
  *            MARLIN_ERR_UNSUPPORTED), at most head_dim.
  * interleaved  0: pair j < rot / 2 is channels (j, j + rot / 2); else (2 j, 2 j + 1).

@@ -1,0 +1,43 @@
+"""Calls for drafted trees that are refused before anything is launched: outputs whose rows overlap.  No GPU needed: as in test_handles.py and test_tree_ops_abi.py."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_handles import D, HKV, I32, card, make  # noqa: E402
+from test_tree_handles import lib, rope_of  # noqa: E402, F401
+from test_tree_ops_abi import check, rope  # noqa: E402
+from test_tree_ops_abi import lib as real_lib  # noqa: E402, F401
+
+
+def test_rotated_queries_that_overlap_are_refused(real_lib):  # noqa: F811
+    """Two rows of q_out in the same place would hold whichever came last.  (Of the calls that are taken T is 0 or B is:
+    nothing is launched.)"""
+    check(rope, real_lib,
+          invalid=[dict(out_strides=(0, 128)), dict(out_strides=(512, 0)), dict(out_strides=(0, 0)), dict(out_strides=(504, 128)),
+                   dict(out_strides=(512, 120)), dict(out_strides=(128, 512)), dict(out_strides=(1024, 64)),
+                   dict(heads=1, hkv=1, out_strides=(0, 128)), dict(T=1, out_strides=(0, 0))],
+          ok=[dict(B=0, out_strides=(0, 0)), dict(T=0, out_strides=(0, 0))])
+
+
+def test_layouts_that_do_not_overlap_are_taken(real_lib):  # noqa: F811
+    """Tokens or heads outermost, one head, one token: these pass the check on overlaps, so that the next one (a misaligned
+    table) answers."""
+    check(rope, real_lib,
+          misaligned=[dict(table=257 * 8, out_strides=s, **more) for s, more in (
+              ((512, 128), {}), ((768, 128), {}), ((128, 640), {}), ((1024, 256), {}), ((136, 680), {}),
+              ((128, 0), dict(heads=1, hkv=1)), ((0, 128), dict(T=1)), ((0, 0), dict(T=1, heads=1, hkv=1)))])
+
+
+def test_out_with_overlapping_rows(lib):  # noqa: F811
+    w4, cache, batch, ws = make()
+    r = rope_of(w4, 9, D)
+    q, k, pos = card(5, 4, D), card(5, HKV, D), card(5, dtype=I32)
+    run = lambda out: w4.kv4_rope_append_into(q, k, k, pos, r, cache, batch, ws, out)  # noqa: E731
+    for bad in (card(1, 4, D).expand(5, 4, D), card(5, 1, D).expand(5, 4, D), card(D).expand(5, 4, D),
+                card(5 * 4 * D).as_strided((5, 4, D), (3 * D, D, 1))):
+        with pytest.raises(ValueError):
+            run(bad)
+    n = len(lib.calls)
+    for good in (card(5, 4, D), card(4, 5, D).transpose(0, 1), card(5, 6, D)[:, 1:5], card(5, 4, 2 * D)[..., :D], q):
+        assert run(good) is good
+    assert len(lib.calls) == n + 5

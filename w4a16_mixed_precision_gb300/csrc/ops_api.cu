@@ -90,6 +90,14 @@ bool strides_ok(long long ts, long long hs, int align) {
   return ts >= 0 && hs >= 0 && ts % align == 0 && hs % align == 0;
 }
 
+// Whether no two of T x H rows of D elements share any, tokens or heads outermost.
+bool rows_apart(long long ts, long long hs, int T, int H, int D) {
+  const auto inside = [D](long long inner, int n, long long outer, int m) {  // n inner rows between two outer ones
+    return (n == 1 || inner >= D) && (m == 1 || (outer >= D && (n == 1 || (outer - D) / (n - 1) >= inner)));
+  };
+  return inside(hs, H, ts, T) || inside(ts, T, hs, H);
+}
+
 marlin_status_t kv_copy(bool append, uint16_t* k, int64_t k_ts, int64_t k_hs, uint16_t* v, int64_t v_ts, int64_t v_hs,
                         const void* cache, int n_pages, int hkv, int D, int page, const int32_t* table, int max_pages,
                         const int32_t* lens, const int32_t* q_start, int B, int T, void* workspace,
@@ -422,6 +430,9 @@ marlin_status_t marlin_kv_rope_append(const uint16_t* q, int64_t q_token_stride,
   }
   if (requests == 0 || tokens == 0) return MARLIN_OK;
   if (!q || !k || !v || !positions || !table || !q_out) return MARLIN_ERR_INVALID_ARG;
+  if (out_token_stride >= 0 && out_head_stride >= 0 &&
+      !rows_apart(out_token_stride, out_head_stride, tokens, heads, head_dim))
+    return MARLIN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(positions, 4) ||
       !aligned(table, 16) || !strides_ok(q_token_stride, q_head_stride, 8) || !strides_ok(k_token_stride, k_head_stride, 8) ||
       !strides_ok(v_token_stride, v_head_stride, 8) || !strides_ok(out_token_stride, out_head_stride, 8))

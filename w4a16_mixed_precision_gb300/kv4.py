@@ -296,12 +296,19 @@ class Kv4Rope(_Handle):
         return self._args
 
 
+def _rows_apart(t: torch.Tensor) -> bool:
+    """Whether no two of the rows [tokens, heads] share an element, tokens or heads outermost."""
+    (T, H, D), (ts, hs, _) = t.shape, t.stride()
+    inside = lambda inner, n, outer, m: (n <= 1 or inner >= D) and (m <= 1 or outer >= (n - 1) * inner + D)  # noqa: E731
+    return inside(hs, H, ts, T) or inside(ts, T, hs, H)
+
+
 def kv4_rope_append_into(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, rope: Kv4Rope,
                          cache: Kv4Cache, batch: Kv4Batch, ws: Kv4Workspace, out: torch.Tensor) -> torch.Tensor:
     """Rotate the batch's queries q, fp16 [tokens, heads, head_dim], and keys k, fp16 [tokens, kv_heads, head_dim], by
     their positions, and quantise the rotated keys and the values v into the cache (as kv4_append does: the rotated
     keys are rounded to fp16 first).  The rotated queries go to out, shaped like q (q itself, or anything that
-    overlaps neither q, k nor v).  positions int32 [axes, tokens], or [tokens] for one axis: rows of the rope's
+    overlaps neither q, k nor v, its rows apart).  positions int32 [axes, tokens], or [tokens] for one axis: rows of the rope's
     table.  q, k, v and out may be views whose last dimension is contiguous (of one QKV product).  Rows that no
     request owns are left alone."""
     cached, rows, work = cache._args or cache._check(), batch._args or batch._check(), ws._args or ws._check()
@@ -314,6 +321,8 @@ def kv4_rope_append_into(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, posi
             or not (q.is_cuda and k.is_cuda and v.is_cuda and out.is_cuda)):
         for name, t, heads in (("q", q, None), ("k", k, new[1]), ("v", v, new[1]), ("out", out, shape[1] if len(shape) == 3 else None)):
             _explain(name, t, T, heads, cache)
+    if (os[1] < new[2] or os[0] < (shape[1] - 1) * os[1] + new[2]) and not _rows_apart(out):
+        raise ValueError("out's rows overlap")
     _need_i32(positions, "positions", (T,) if rope.n_axes == 1 and positions.dim() == 1 else (rope.n_axes, T))
     cur = torch._C._cuda_getDevice()
     if not (cache._device == batch._device == ws._device == rope._device == q.get_device() == k.get_device()
