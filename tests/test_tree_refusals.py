@@ -1,4 +1,5 @@
-"""Calls for drafted trees that are refused before anything is launched: outputs whose rows overlap.  No GPU needed: as in test_handles.py and test_tree_ops_abi.py."""
+"""Calls for drafted trees that are refused before anything is launched: outputs whose rows overlap, odd numbers of
+rotated channels.  No GPU needed: as in test_handles.py and test_tree_ops_abi.py."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -41,3 +42,10 @@ def test_out_with_overlapping_rows(lib):  # noqa: F811
     for good in (card(5, 4, D), card(4, 5, D).transpose(0, 1), card(5, 6, D)[:, 1:5], card(5, 4, 2 * D)[..., :D], q):
         assert run(good) is good
     assert len(lib.calls) == n + 5
+
+
+def test_odd_numbers_of_rotated_channels():
+    import w4a16_mixed_precision_gb300 as w4
+    for rot in (63, 1, 0, -2):
+        with pytest.raises(ValueError):
+            w4.Kv4Rope.from_theta(rot, 10, device="cuda:0")

@@ -276,6 +276,8 @@ class Kv4Rope(_Handle):
     @classmethod
     def from_theta(cls, rot: int, positions: int, theta: float = 10000.0, axes=None, interleaved: bool = False, device=None):
         """Angles position * theta^(-2 j / rot) for pair j, in 64 bits up to their cosines and sines."""
+        if rot <= 0 or rot % 2:
+            raise ValueError(f"rot: expected an even number of channels, got {rot}")
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         freq = theta ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=dev) / rot)
         angle = torch.arange(positions, dtype=torch.float64, device=dev)[:, None] * freq
