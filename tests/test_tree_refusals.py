@@ -1,10 +1,10 @@
 """Calls for drafted trees that are refused before anything is launched: outputs whose rows overlap, odd numbers of
-rotated channels.  No GPU needed: as in test_handles.py and test_tree_ops_abi.py."""
+rotated channels; and caches in any iterable.  No GPU needed: as in test_handles.py and test_tree_ops_abi.py."""
 import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_handles import D, HKV, I32, card, make  # noqa: E402
+from test_handles import D, HKV, I32, PAGE, PAGES, card, make  # noqa: E402
 from test_tree_handles import lib, rope_of  # noqa: E402, F401
 from test_tree_ops_abi import check, rope  # noqa: E402
 from test_tree_ops_abi import lib as real_lib  # noqa: E402, F401
@@ -49,3 +49,18 @@ def test_odd_numbers_of_rotated_channels():
     for rot in (63, 1, 0, -2):
         with pytest.raises(ValueError):
             w4.Kv4Rope.from_theta(rot, 10, device="cuda:0")
+
+
+def test_caches_in_any_iterable(lib):  # noqa: F811
+    w4, cache, batch, ws = make()
+    more = [w4.Kv4Cache(PAGES, HKV, D, PAGE, device="cuda:0") for _ in range(3)]
+    index, kept, pairs = card(5, dtype=I32), card(3, dtype=I32), card(2, dtype=I32)
+    at = tuple(c.buf.data_ptr() for c in more)
+    for caches in (more, tuple(more), (c for c in more), dict(enumerate(more)).values()):
+        w4.kv4_compact(caches, batch, index, kept, ws)
+        assert lib.calls[-1][:4] == (*at, 3)
+    w4.kv4_copy_pages(iter(more), pairs, pairs, ws)
+    assert lib.calls[-1][:4] == (*at, 3)
+    for go in (lambda c: w4.kv4_compact(c, batch, index, kept, ws), lambda c: w4.kv4_copy_pages(c, pairs, pairs, ws)):
+        with pytest.raises(ValueError):
+            go(iter(()))

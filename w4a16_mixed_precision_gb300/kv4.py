@@ -350,7 +350,7 @@ def kv4_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions
 
 def _layers(caches, ws: Kv4Workspace, *named):
     """The addresses of the layers' caches (one or several alike), what they share, and the current device."""
-    caches = (caches,) if isinstance(caches, Kv4Cache) else caches
+    caches = (caches,) if isinstance(caches, Kv4Cache) else tuple(caches)
     at = [(c._args or c._check())[0] for c in caches]
     like = [c._like for c in caches]
     if not at or like.count(like[0]) != len(at):
