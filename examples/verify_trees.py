@@ -81,7 +81,8 @@ class Server:
         return w4.Kv4Batch(table.cuda(), i32([r.length + n for r, n in zip(self.requests, new)]), i32(start), start[-1], max(new))
 
     def admit(self, prompt):
-        """A new request: its prompt but the last token is a tree without branches, of which all is kept."""
+        """A new request: its prompt but the last token is a tree without branches, of which all is kept.  (Prompts are short
+        here: one of thousands of tokens is for kv4_attention, with its positions counted on.)"""
         self.requests.append(Request(prompt))
         new = [0] * (len(self.requests) - 1) + [len(prompt) - 1]
         self.model(torch.tensor(prompt[:-1], device="cuda"), self.batch(new), i32(range(-1, len(prompt) - 2)))

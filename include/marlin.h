@@ -491,7 +491,9 @@ marlin_status_t marlin_kv_attention(const uint16_t* q, int64_t q_token_stride, i
  *            ancestors.  A request of more than 32 * words new tokens is reported as above.
  * positions  device, int32 [tokens], written: lengths[b] - new + the row's number of ancestors.
  * Rows that no request owns are left alone.  lengths up to 2^30.  Of the workspace the
- * first 256 bytes are used.  Errors: INVALID_ARG, MISALIGNED; CUDA.
+ * first 256 bytes are used.  (Made for drafted trees: a token costs a step for every
+ * ancestor, and every row has the words of the longest request.  Long runs without
+ * branches are marlin_kv_attention's.)  Errors: INVALID_ARG, MISALIGNED; CUDA.
  */
 marlin_status_t marlin_kv_tree(const int32_t* parents, const int32_t* lengths, const int32_t* q_start, int requests,
                                int tokens, int words, int32_t* mask, int32_t* positions, void* workspace,
@@ -508,6 +510,9 @@ marlin_status_t marlin_kv_tree(const int32_t* parents, const int32_t* lengths, c
  *            `window` positions up to its own, which is lengths[b] - new + its set
  *            bits - 1.  (All positions from lengths[b] - new - window on have to be in
  *            valid pages, and those that share a block of 64 with them.)
+ *            New tokens are hidden by their bits alone: an ancestor `window` or more
+ *            levels up is seen where its bit is set.  Where the bits of those, and of no
+ *            others, are left out, a run of tokens sees what marlin_kv_attention lets it see.
  * A row that sees nothing at all is zero.  Everything else, the workspace too, is as for
  * marlin_kv_attention.
  */

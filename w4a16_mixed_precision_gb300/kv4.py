@@ -203,7 +203,8 @@ def kv4_tree(parents: torch.Tensor, batch: Kv4Batch, ws: Kv4Workspace):
     negative for none.  mask int32 [tokens, words], words = max_q / 32 rounded up: bit j (of word j / 32) of a row is
     set where the request's j-th new token is the row's own or one of its ancestors.  positions int32
     [tokens]: the cached tokens before the new ones and the row's ancestors, counted.  Rows that no request
-    owns are not initialised."""
+    owns are not initialised.  (A token takes a step for every ancestor, and all rows the words of the longest request:
+    long runs without branches, as prompts are, belong to kv4_attention.)"""
     rows, work = batch._args or batch._check(), ws._args or ws._check()
     _need_i32(parents, "parents", (batch.tokens,))
     cur = torch._C._cuda_getDevice()
@@ -226,7 +227,8 @@ def kv4_tree_attention_into(q: torch.Tensor, cache: Kv4Cache, batch: Kv4Batch, t
     values already: a token sees the cached tokens before the new ones, and of its request's new ones those whose bit is
     set in its row of tree (int32 [tokens, words], as kv4_tree makes it, or any other).  scale: 1 / sqrt(head_dim) by
     default; window > 0: of the tokens before the new ones a row sees those among the last `window` up to its position,
-    which is the number of them and of the new tokens that it sees, less 1.  Rows that no request owns are left alone
+    which is the number of them and of the new tokens that it sees, less 1.  New tokens are hidden by their bits alone: to
+    hide ancestors `window` or more levels up, leave their bits out.  Rows that no request owns are left alone
     (kv4_tree_attention's are not initialised)."""
     cached, rows, work = cache._args or cache._check(), batch._args or batch._check(), ws._args or ws._check()
     qs, shape = q.stride(), q.shape
