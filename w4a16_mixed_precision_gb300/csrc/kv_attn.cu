@@ -138,8 +138,8 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 
 // W warps; blocks of GB granules, GI of them taken together; S blocks in a warp's ring.
 // kT: the new tokens are trees: blocks that hold some of them, or where a window begins, take their masks from the
-// rows' bits (kv.cuh).  Measured: a tree of 8 on 692 tokens, 32 heads of 128 channels, 10.6 us; 24 of 5, window
-// 2048, 24 heads on 8 of 64 channels, 27 us.
+// rows' bits (kv.cuh).  Measured: a tree of 8 on 692 tokens, 32 heads of 128 channels, 10.9 us; 24 of 5, window
+// 2048, 24 heads on 8 of 64 channels, 26.8 us.
 template <int D, int NB, bool kT>
 struct Shape {
   static constexpr bool kTree = kT;

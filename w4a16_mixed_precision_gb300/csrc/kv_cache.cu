@@ -269,7 +269,7 @@ cudaError_t launch_copy(const KvParams& p, uint16_t* k, uint16_t* v, const long 
 // channels, such that both channels of its pairs are its own: chunks g and g + rot/2 of the rotated ones, two
 // neighbours of the rest.
 // Measured: 9880 tokens, 32 heads on 8 of 128 channels, three axes, 40.9 us, 5.3 TB/s (79% of the card's copy
-// rate; the append alone takes 15.2); 208 tokens, 64 heads on 8, 6.0 us.
+// rate; the append alone takes 15.2), 44.0 where the axes of neighbouring pairs differ; 208 tokens, 64 heads on 8, 6.0 us.
 template <int D>
 constexpr int kVectors = 512 / D;  // together
 constexpr int kRopeCtas = 3;  // of an SM

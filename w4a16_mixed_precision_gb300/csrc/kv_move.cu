@@ -22,11 +22,12 @@ namespace {
 // written, and a barrier between a round's loads and stores keeps it from overwriting what is still read.
 // Where tokens come from is the same for every head of every cache.  Where they go to other pages and there is
 // work for every warp, a warp finds it once for up to 8 heads, two of them in flight: 38,668 of 76,825 tokens, 8 heads
-// of 128 channels, 18.1 us (84 MB out and in, 4.6 TB/s); 20.5 with one in flight, 26.3 a head a warp, 23 with four in flight
-// (their registers leave fewer warps).  Of few tokens a head a warp is faster: half of 500 of 2 requests, with the read back, 6.7 against 9.2 us, and
+// of 128 channels, 20.6 us (84 MB out and in, 4.1 TB/s; 25 where nothing of it is in L2), of which the look at the indexes
+// is 2.5.  Without that look: 20.5 with one in flight, 26.3 a head a warp, 23 with four in flight (their registers leave
+// fewer warps).  Of few tokens a head a warp is faster: half of 500 of 2 requests, with the read back, 6.7 against 9.2 us, and
 // in place, where warps that moved several were up to 15% slower.  A kept token's values share their 32-byte
 // sectors with up to 15 others, so that more is read than kept: 5 tokens of each of 40 requests in place, in 32 caches,
-// 10.6 us (7 MB kept, 34 read).
+// 10.6 us (7 MB kept, 34 read).  In place few heads are few CTAs, and their rounds a chain: the 38,668 tokens 333 us.
 constexpr int kMoveThreads = 256, kMoveWarps = kMoveThreads / 32;
 
 // What warps read of a request, checked.

@@ -27,11 +27,11 @@
 //     block, are in the order in which the codes unpack, in both operands alike.
 //   * A row's reference R is chosen so that p_t s_t starts at 2^6 at most; it is
 //     only moved, and O rescaled, when some p_t s_t (s_t taken as 2^-30 at least)
-//     would pass 2^14.
+//     would pass 2^14.  It goes by the tokens that the row sees alone.
 //
-// Measured: 1000 new tokens on 9000, 64 query heads on 8 of 128 channels, 355 us,
-// 785 TFLOP/s (40% of the card's bf16 rate); the prompts of 5 requests of 682 to
-// 1900 tokens, 32 heads, 184 us, 404 TFLOP/s.  A block of 64 tokens for 256 rows
+// Measured: 1000 new tokens on 9000, 64 query heads on 8 of 128 channels, 353 us,
+// 790 TFLOP/s (40% of the card's bf16 rate); the prompts of 5 requests of 682 to
+// 1900 tokens, 32 heads, 185 us, 402 TFLOP/s.  A block of 64 tokens for 256 rows
 // takes about 2700 cycles, of which shared memory needs 1950 (Q and K for S, V, the
 // dequantised block's writes, scales and offsets), the softmax warps' instructions
 // 1650 and the products 1540 (N is 64 for S, and costs nearly what 128 would): no one
@@ -59,7 +59,8 @@ constexpr int kTmem = 512, kTileCols = kTmem / kTiles;  // columns, and of a til
 // Trees: blocks whose products with V are summed in tensor memory at most; then they are added to the CTA's part of
 // the item, in fp32 rounded to nearest.  The tensor cores' sums are not: root mean square errors against 64 bits at 25
 // tokens on 100,000, 64 heads on 8, by the blocks of a piece: 3.0e-4 with 41, 3.1e-4 with 82, 3.9e-4 with 164, 6.7e-4
-// with 329 (3.0e-4 is what rounding p s and the output to fp16 leave).
+// with 329 (3.0e-4 is what rounding p s and the output to fp16 leave).  Pieces take 4% of that call's time (144 us, 138
+// without), 1% of the 14 trees' below.
 constexpr int kMostBlocks = 56;
 
 struct F2 {
@@ -350,7 +351,10 @@ __device__ __forceinline__ void move_on(const KvAttnParams& p, Place& c, int by)
 // against 355, 376 of 94 to 141 506 against 462, 504 of 94 to 125 629 against 573.
 // The mean is taken as if a request's items grew evenly.
 constexpr int kCutCost = 20, kCutItemCost = 4;  // blocks
-constexpr int kTreeCutCost = 14;               // of trees, whose parts another kernel joins
+// Of trees, whose parts another kernel joins.  Items against stripes, by how many blocks the longest is above the mean,
+// 128 rows of 128 channels: 40 items 21 against 26 us at 6, 30 / 27 at 13, 39 / 29 at 20; 80 30 / 31 at 10, 39 / 34 at 16;
+// 120 29 / 42 at 7, 48 / 52 at 15, 65 / 65 at 23; 144 48 / 57 at 12, 65 / 69 at 18; 160 48 / 62 at 10, 65 / 81 at 15.
+constexpr int kTreeCutCost = 14;
 template <bool kTree>
 __device__ __forceinline__ void find_item(const KvAttnParams& p, CtrlP& ctrl) {
   const int lane = threadIdx.x & 31;
@@ -413,7 +417,7 @@ __device__ __forceinline__ void find_item(const KvAttnParams& p, CtrlP& ctrl) {
 // CTA for 8 channels of every item, instead of by the last CTA to arrive, part by part.  One request of 8000
 // tokens, 128 rows a key head, 64 heads on 8 of 128 channels: 26 us (126 where the last CTA joins).
 // Measured: 14 requests of 1750 to 6000 tokens with trees of 17 to 60, 64 heads on 8 of 128 channels, 167 us, 480
-// TFLOP/s (24% of the card's bf16 rate); a tree of 25 on 100,001 tokens 145 us, 565 TFLOP/s.  A block takes 2990
+// TFLOP/s (24% of the card's bf16 rate); a tree of 25 on 100,001 tokens 144 us, 569 TFLOP/s.  A block takes 2990
 // cycles where both tiles have rows, 2400 where one has (dequantisation, four warps, takes that alone), plus
 // some 6 us for every piece's start and end.  Tried and slower: both tiles on the rows of an item of one tile, in
 // turn on its blocks (114 to 120 us at 128 rows on 100,000); a warp that brings the blocks; a warp for either
