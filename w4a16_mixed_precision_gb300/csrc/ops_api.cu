@@ -126,8 +126,8 @@ marlin_status_t kv_copy(bool append, uint16_t* k, int64_t k_ts, int64_t k_hs, ui
 // many stripes cut is joined part by part).
 // Trees have the same bound, although their parts, which a second kernel joins, would allow 48: it is also where a
 // probability times its value's scale goes from two fp16 numbers to one.  Streaming against tcgen05: 8 requests of 8000
-// tokens, 64 heads on 8, 32 rows 50 against 63 us, 64 82 / 64; 32 of 2000, 32 58 / 78, 64 89 / 78; one of 8000, 32
-// 26 / 25, 64 30 / 25; one of 100,000, 32 86 / 113, 64 150 / 113; 64 channels, 8 of 4000, 32 25 / 35, 64 37 / 35.
+// tokens, 64 heads on 8, 32 rows 50 against 63 us, 64 80 / 65; 32 of 2000, 32 58 / 78, 64 89 / 77; one of 8000, 32
+// 26 / 25, 64 30 / 26; one of 100,000, 32 86 / 113, 64 149 / 117; 64 channels, 8 of 4000, 32 25 / 35, 64 36 / 37.
 constexpr int kPrefillRows = 64;
 
 struct AttnPlan {
